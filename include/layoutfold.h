@@ -335,6 +335,142 @@ lf_status gemm_nt_xent_noalloc(const void *x, const void *w, const int32_t *labe
                                float *loss, void *grad_or_null,
                                int64_t M, int64_t N, int64_t K, cudaStream_t stream);
 
+/* Element types of the feed-forward operators below. */
+typedef enum {
+    LF_BF16 = 0,
+    LF_FP16 = 1,
+    LF_FP32 = 2,
+    LF_E4M3 = 3  /* float8_e4m3fn, with fp32 scales beside it */
+} lf_dtype;
+
+/* Activations of the gated projections. */
+typedef enum {
+    LF_ACT_SILU = 0,      /* v / (1 + exp(-v)) */
+    LF_ACT_GELU = 1,      /* v Phi(v), Phi the standard normal distribution function */
+    LF_ACT_GELU_TANH = 2  /* v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) / 2 */
+} lf_act;
+
+/*
+ * add_rms_norm -- the residual addition and its root-mean-square norm, in the
+ * stream's type or in e4m3 with one scale per row, in one kernel that reads
+ * each row once.  The pages have no counterpart: the norm produces the X that
+ * the projections of this library read (and its e4m3 form the X of
+ * gated_ffn_e4m3).
+ *
+ *   dtype  : LF_BF16, LF_FP16 or LF_FP32, the type of x, residual and h.
+ *   wdtype : the type of weight: dtype, or LF_FP32.
+ *   ydtype : the type of y: dtype, or LF_E4M3.
+ *   x      : [M,D] with a row pitch of ldx elements, device.
+ *   residual_or_null : [M,D] with a row pitch of ldr elements, or NULL.
+ *   weight : [D].
+ *   h      : [M,D] contiguous, or NULL when residual_or_null is NULL;
+ *              h[m,d] = rn(x[m,d] + residual[m,d])
+ *            the stream in its own type: the norm reads h as it is kept, so the
+ *            backward pass finds the same statistics in it.  Without a residual
+ *            h is x itself and nothing is written.
+ *   y      : [M,D] contiguous, with r = 1 / sqrt(mean_d h[m,d]^2 + eps) and
+ *            f[m,d] = h[m,d] r weight[d] (statistics and products in fp32):
+ *              y = rn(f), or for LF_E4M3 y = e4m3(f / scale[m])
+ *   scale_or_null : fp32 [M], required exactly when ydtype is LF_E4M3:
+ *              scale[m] = max_d |f[m,d]| / 448, or 1 where that maximum is 0,
+ *            so y[m,d] scale[m] stands for f.  A row with a NaN (or an
+ *            infinity, whose norm is undefined) gets a NaN scale and NaN codes.
+ *   eps >= 0.  1 <= M, D < 2^31; ldx, ldr >= D (LF_ERR_SHAPE otherwise).
+ * Alignment: that of the elements; rows whose bases and pitches are multiples
+ * of 16 bytes take the vectorised kernel.  h may be the same buffer as x or
+ * residual (row pitch D) and y the same as x; other overlaps are not allowed.
+ * One launch; nothing is allocated.  A combination of types outside the above
+ * is LF_ERR_SHAPE.
+ */
+lf_status add_rms_norm(const void *x, int64_t ldx, const void *residual_or_null, int64_t ldr, const void *weight,
+                       void *h, void *y, float *scale_or_null, int dtype, int wdtype, int ydtype, float eps,
+                       int64_t M, int64_t D, cudaStream_t stream);
+
+/*
+ * add_rms_norm_backward -- the gradient of add_rms_norm.  With g = dy weight
+ * and r as above, recomputed from h (no statistics have to be kept):
+ *   dx[m,d]    = rn(r g[m,d] - h[m,d] r^3 mean_d(g h) + dh[m,d])
+ *   dweight[d] = rn(sum_m dy[m,d] h[m,d] r)
+ * dx is the gradient of x and of the residual alike.  An e4m3 output is
+ * differentiated as if it had not been rounded (dy is the gradient of f).
+ *
+ *   dy, h, dx : dtype (LF_BF16, LF_FP16, LF_FP32), [M,D] contiguous, device;
+ *               h is add_rms_norm's (or its x, where there was no residual).
+ *   weight    : wdtype [D] (dtype or LF_FP32).
+ *   dh_or_null: dtype [M,D], the gradient that arrives at h by other ways (the
+ *               stream's own), added to dx; or NULL.
+ *   dweight_or_null : wdtype [D], or NULL when it is not wanted.
+ *   scratch   : fp32, add_rms_norm_backward_scratch(M, D) bytes, 4-byte aligned,
+ *               device, owned by the caller, contents arbitrary; NULL allowed
+ *               without dweight.
+ * Sums in fp32 in a fixed order: two calls on the same inputs give the same
+ * bits.  dx may be the same buffer as dy or dh.  Two launches (one without
+ * dweight); nothing is allocated.  Errors as add_rms_norm.
+ */
+lf_status add_rms_norm_backward(const void *dy, const void *h, const void *weight, const void *dh_or_null, void *dx,
+                                void *dweight_or_null, void *scratch, int dtype, int wdtype, float eps, int64_t M,
+                                int64_t D, cudaStream_t stream);
+
+/* Bytes of scratch that add_rms_norm_backward needs (0 for M or D out of range). */
+int64_t add_rms_norm_backward_scratch(int64_t M, int64_t D);
+
+/*
+ * gated_ffn -- the gated projections of a feed-forward block in one kernel:
+ *   [g, u] = X . W^T,   out = act(g) * u
+ * The two projections are two column blocks of one NT GEMM whose epilogue has
+ * both accumulators ("Allow reductions in matmul epilogues", NVIDIA/Fuser issue
+ * 2213: work on the matmul's result inside its epilogue; "Strength reduction:
+ * fold transpose into a subsequent GEMM call", lightning-thunder issue 1252:
+ * the weight is read as it is stored).
+ *
+ *   x   : bf16 [M,K], device, row-major.
+ *   w   : bf16 [2F,K], device, row-major: the gate's F rows, then the up
+ *         projection's F rows.
+ *   act : an lf_act value.
+ *   out : bf16 [M,F]; out[m,f] = bf16_rn(act(g[m,f]) * u[m,f]), with g and u the
+ *         fp32 accumulators (not rounded in between).
+ *   gu_or_null : NULL, or bf16 [M,2F]: bf16_rn of g (columns 0..F-1) and of u
+ *         (columns F..2F-1), which gated_ffn_backward takes.  They are kept in
+ *         bf16 because the backward products read their gradients in bf16.
+ *   K % 8 == 0, F % 8 == 0 (16-byte row pitches), 1 <= M, K < 2^31, 1 <= F < 2^30;
+ *   all pointers 16-byte aligned; outputs overlap nothing.  One launch.
+ */
+lf_status gated_ffn(const void *x, const void *w, int act, void *out, void *gu_or_null, int64_t M, int64_t F,
+                    int64_t K, cudaStream_t stream);
+
+/*
+ * gated_ffn_e4m3 -- gated_ffn on e4m3 operands with a scale for each token and
+ * each output channel (applied to the fp32 accumulators):
+ *   g[m,f] = x_scale[m] w_scale[f]     sum_k x[m,k] w[f,k]
+ *   u[m,f] = x_scale[m] w_scale[F + f] sum_k x[m,k] w[F + f,k]
+ *
+ *   x : e4m3 [M,K] and x_scale : fp32 [M], as add_rms_norm writes them.
+ *   w : e4m3 [2F,K] and w_scale : fp32 [2F].
+ *   out, act as gated_ffn.  K % 16 == 0 and F % 8 == 0; x, w, w_scale and out
+ *   16-byte aligned, x_scale 4-byte aligned.  One launch.
+ */
+lf_status gated_ffn_e4m3(const void *x, const float *x_scale, const void *w, const float *w_scale, int act, void *out,
+                         int64_t M, int64_t F, int64_t K, cudaStream_t stream);
+
+/*
+ * gated_ffn_backward -- the gradient of gated_ffn, given dout and the kept
+ * pre-activations gu = [g, u]:
+ *   dgu = [dout u act'(g), dout act(g)],  dx = dgu . W,  dw = dgu^T . X
+ * Neither product transposes anything in memory: W and both operands of dw are
+ * read MN-major, as gemm_layout reads them.
+ *
+ *   dout : bf16 [M,F]; x : bf16 [M,K]; w : bf16 [2F,K]; gu : bf16 [M,2F].
+ *   dgu  : bf16 [M,2F], written (the products read it, so it is rounded to bf16
+ *          once); may be the same buffer as gu.
+ *   dx_or_null : bf16 [M,K] or NULL;  dw_or_null : bf16 [2F,K] or NULL.
+ * Sizes and alignment as gated_ffn; outputs otherwise overlap nothing.  One
+ * launch for dgu and one for each of dx and dw, which may use the stream-K
+ * split and its workspace, ordered across streams as gemm_nt's.
+ */
+lf_status gated_ffn_backward(const void *dout, const void *x, const void *w, const void *gu, int act, void *dgu,
+                             void *dx_or_null, void *dw_or_null, int64_t M, int64_t F, int64_t K,
+                             cudaStream_t stream);
+
 /* Human-readable name of a status code (static storage, never NULL). */
 const char *lf_status_string(lf_status status);
 

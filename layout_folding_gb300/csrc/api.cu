@@ -293,6 +293,22 @@ bool make_tmap(CUtensorMap *m, const void *ptr, int64_t rows, int64_t K, uint32_
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 2-D tensor [rows, K] of 1-byte elements (K contiguous), box = 128 columns x
+// box_rows rows, 128-byte swizzle, zero fill.
+bool make_tmap_e4m3(CUtensorMap *m, const void *ptr, int64_t rows, int64_t K, uint32_t box_rows)
+{
+    EncodeTiledFn enc = encode_fn();
+    if (!enc)
+        return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(K)};
+    const cuuint32_t box[2] = {128, box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(ptr), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // 2-D bf16 tensor stored [K, rows] (rows contiguous: an MN-major operand),
 // box = 64 rows x 64 K, 128-byte swizzle; out-of-range elements read as zero.
 // The same [K, rows] operand viewed as (64 rows, K, rows / 64): one box of
@@ -966,6 +982,172 @@ static lf_status fp8_cast_dual_call(const void *x, const float *scale, void *out
     return launched(lf::launch_fp8_cast_dual(x, scale, out, out_t, M, K, d->num_sms, stream), 1);
 }
 
+static bool norm_types_ok(int dtype, int wdtype)
+{
+    return dtype >= LF_BF16 && dtype <= LF_FP32 && (wdtype == dtype || wdtype == LF_FP32);
+}
+
+static bool misaligned_for(const void *p, int dtype)
+{
+    const uintptr_t size = dtype == LF_FP32 ? 4 : dtype == LF_E4M3 ? 1 : 2;
+    return (reinterpret_cast<uintptr_t>(p) & (size - 1)) != 0;
+}
+
+static lf_status add_rms_norm_call(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *weight,
+                                   void *h, void *y, float *scale, int dtype, int wdtype, int ydtype, float eps,
+                                   int64_t M, int64_t D, cudaStream_t stream)
+{
+    if (!x || !weight || !y || (residual && !h) || (ydtype == LF_E4M3 && !scale))
+        return LF_ERR_NULL;
+    if (!norm_types_ok(dtype, wdtype) || (ydtype != dtype && ydtype != LF_E4M3) || (ydtype != LF_E4M3 && scale) ||
+        !(eps >= 0.f) || M <= 0 || D <= 0 || M > MAX_DIM || D > MAX_DIM || ldx < D || (residual && ldr < D))
+        return LF_ERR_SHAPE;
+    if (misaligned_for(x, dtype) || misaligned_for(weight, wdtype) || misaligned_for(y, ydtype) ||
+        (residual && (misaligned_for(residual, dtype) || misaligned_for(h, dtype))) || (scale && !aligned4(scale)))
+        return LF_ERR_ALIGN;
+    DeviceState *d = nullptr;
+    lf_status st = current_device(&d);
+    if (st != LF_OK)
+        return st;
+    const lf::NormParams p = {x, residual, weight, h, y, scale, M, D, ldx, ldr, eps};
+    return launched(lf::launch_rms_norm(p, dtype, wdtype, ydtype == LF_E4M3, d->num_sms, stream), 1);
+}
+
+static lf_status add_rms_norm_backward_call(const void *dy, const void *h, const void *weight, const void *dh, void *dx,
+                                            void *dweight, void *scratch, int dtype, int wdtype, float eps, int64_t M,
+                                            int64_t D, cudaStream_t stream)
+{
+    if (!dy || !h || !weight || !dx || (dweight && !scratch))
+        return LF_ERR_NULL;
+    if (!norm_types_ok(dtype, wdtype) || !(eps >= 0.f) || M <= 0 || D <= 0 || M > MAX_DIM || D > MAX_DIM)
+        return LF_ERR_SHAPE;
+    if (misaligned_for(dy, dtype) || misaligned_for(h, dtype) || misaligned_for(weight, wdtype) ||
+        misaligned_for(dx, dtype) || (dh && misaligned_for(dh, dtype)) ||
+        (dweight && (misaligned_for(dweight, wdtype) || !aligned4(scratch))))
+        return LF_ERR_ALIGN;
+    DeviceState *d = nullptr;
+    lf_status st = current_device(&d);
+    if (st != LF_OK)
+        return st;
+    const lf::NormBwdParams p = {dy, h, weight, dh, dx, dweight ? static_cast<float *>(scratch) : nullptr, M, D, eps};
+    return launched(lf::launch_rms_norm_bwd(p, dweight, dtype, wdtype, stream), dweight ? 2 : 1);
+}
+
+static bool act_ok(int act) { return act >= LF_ACT_SILU && act <= LF_ACT_GELU_TANH; }
+
+static lf_status check_gated_shape(int64_t M, int64_t F, int64_t K, int act)
+{
+    if (!act_ok(act) || F > MAX_DIM / 2)
+        return LF_ERR_SHAPE;
+    return check_gemm_shape(M, 2 * F, K);
+}
+
+// gated_ffn and gated_ffn_e4m3 (x_scale and w_scale set), arguments checked.
+static lf_status gated_launch(const void *x, const float *x_scale, const void *w, const float *w_scale, int act,
+                              void *out, void *gu, int64_t M, int64_t F, int64_t K, cudaStream_t stream)
+{
+    DeviceState *d = nullptr;
+    lf_status st = current_device(&d);
+    if (st != LF_OK)
+        return st;
+    if (d->pair_clusters <= 0)
+        return LF_ERR_LAUNCH;
+    const bool e4m3 = x_scale != nullptr;
+    lf::GatedParams gp;
+    std::memset(&gp, 0, sizeof gp);
+    CUtensorMap ta, tw, to, tg, tu;
+    const bool ok = (e4m3 ? make_tmap_e4m3(&ta, x, M, K, lf::BM) && make_tmap_e4m3(&tw, w, 2 * F, K, lf::BN / 2)
+                          : make_tmap(&ta, x, M, K, lf::BM) && make_tmap(&tw, w, 2 * F, K, lf::BN / 2)) &&
+                    make_tmap_out(&to, out, M, F, F, 1, M * F, false);
+    if (!ok)
+        return LF_ERR_LAUNCH;
+    tg = tu = to;
+    if (gu) {
+        // two views of gu, so that a box past column F is clipped there
+        if (!make_tmap_out(&tg, gu, M, F, 2 * F, 1, 2 * M * F, false) ||
+            !make_tmap_out(&tu, static_cast<char *>(gu) + 2 * F, M, F, 2 * F, 1, 2 * M * F, false))
+            return LF_ERR_LAUNCH;
+    }
+    lf::GemmParams &p = gp.g;
+    const int64_t kblock = e4m3 ? 128 : 64;
+    p.M = static_cast<int>(M);
+    p.N = static_cast<int>(F);
+    p.K = static_cast<int>(K);
+    p.num_m_blocks = static_cast<int>((M + 2 * lf::BM - 1) / (2 * lf::BM));
+    p.num_n_blocks = static_cast<int>((F + lf::BN / 2 - 1) / (lf::BN / 2));
+    p.num_k_blocks = static_cast<int>((K + kblock - 1) / kblock);
+    p.num_tiles = p.num_m_blocks * p.num_n_blocks;
+    p.err = d->err_word;
+    p.timeout_ns = g_timeout_ns.load();
+    p.inject = g_inject.load();
+    // bands of M blocks whose X rows stay in L2, as plan_gemm
+    const double x_bytes = 2.0 * lf::BM * static_cast<double>(K) * (e4m3 ? 1.0 : 2.0);
+    int band = static_cast<int>(BAND_X_BYTES / x_bytes);
+    band = band < 1 ? 1 : band;
+    if (band < p.num_m_blocks) {
+        const int nbands = (p.num_m_blocks + band - 1) / band;
+        p.band_m = (p.num_m_blocks + nbands - 1) / nbands;
+    }
+    gp.x_scale = x_scale;
+    gp.w_scale = w_scale;
+    gp.save = gu ? 1 : 0;
+    const int grid = 2 * (p.num_tiles < d->pair_clusters ? p.num_tiles : d->pair_clusters);
+    return launched(lf::launch_gated_pair(e4m3, act, ta, tw, to, tg, tu, gp, grid, stream), 1);
+}
+
+static lf_status gated_ffn_call(const void *x, const void *w, int act, void *out, void *gu, int64_t M, int64_t F,
+                                int64_t K, cudaStream_t stream)
+{
+    if (!x || !w || !out)
+        return LF_ERR_NULL;
+    lf_status st = check_gated_shape(M, F, K, act);
+    if (st != LF_OK)
+        return st;
+    if (!aligned16(x) || !aligned16(w) || !aligned16(out) || (gu && !aligned16(gu)) || F % 8 != 0 || K % 8 != 0)
+        return LF_ERR_ALIGN;
+    return gated_launch(x, nullptr, w, nullptr, act, out, gu, M, F, K, stream);
+}
+
+static lf_status gated_ffn_e4m3_call(const void *x, const float *x_scale, const void *w, const float *w_scale, int act,
+                                     void *out, int64_t M, int64_t F, int64_t K, cudaStream_t stream)
+{
+    if (!x || !x_scale || !w || !w_scale || !out)
+        return LF_ERR_NULL;
+    lf_status st = check_gated_shape(M, F, K, act);
+    if (st != LF_OK)
+        return st;
+    if (!aligned16(x) || !aligned16(w) || !aligned16(out) || !aligned16(w_scale) || !aligned4(x_scale) || F % 8 != 0 ||
+        K % 16 != 0)
+        return LF_ERR_ALIGN;
+    return gated_launch(x, x_scale, w, w_scale, act, out, nullptr, M, F, K, stream);
+}
+
+static lf_status gated_ffn_backward_call(const void *dout, const void *x, const void *w, const void *gu, int act,
+                                         void *dgu, void *dx, void *dw, int64_t M, int64_t F, int64_t K,
+                                         cudaStream_t stream)
+{
+    if (!dout || !x || !w || !gu || !dgu)
+        return LF_ERR_NULL;
+    lf_status st = check_gated_shape(M, F, K, act);
+    if (st == LF_OK)
+        st = check_gemm_shape(2 * F, K, M);
+    if (st != LF_OK)
+        return st;
+    if (!aligned16(dout) || !aligned16(x) || !aligned16(w) || !aligned16(gu) || !aligned16(dgu) ||
+        (dx && !aligned16(dx)) || (dw && !aligned16(dw)) || F % 8 != 0 || K % 8 != 0)
+        return LF_ERR_ALIGN;
+    DeviceState *d = nullptr;
+    if ((st = current_device(&d)) != LF_OK)
+        return st;
+    if ((st = launched(lf::launch_gated_bwd(act, dout, gu, dgu, M, F, d->num_sms, stream), 1)) != LF_OK)
+        return st;
+    if (dx && (st = gemm_layout_call(dgu, LF_K_MAJOR, w, LF_MN_MAJOR, dx, M, K, 2 * F, stream)) != LF_OK)
+        return st;
+    if (dw && (st = gemm_layout_call(dgu, LF_MN_MAJOR, x, LF_MN_MAJOR, dw, 2 * F, K, M, stream)) != LF_OK)
+        return st;
+    return LF_OK;
+}
+
 const char *lf_status_string(lf_status s)
 {
     switch (s) {
@@ -1137,6 +1319,55 @@ lf_status fp8_cast_dual(const void *x, const float *scale, void *out, void *out_
 {
     const lf::CallRange range("fp8_cast_dual");
     return debug_sync(fp8_cast_dual_call(x, scale, out, out_t, M, K, stream), stream);
+}
+
+lf_status add_rms_norm(const void *x, int64_t ldx, const void *residual_or_null, int64_t ldr, const void *weight,
+                       void *h, void *y, float *scale_or_null, int dtype, int wdtype, int ydtype, float eps,
+                       int64_t M, int64_t D, cudaStream_t stream)
+{
+    const lf::CallRange range("add_rms_norm");
+    return debug_sync(add_rms_norm_call(x, ldx, residual_or_null, ldr, weight, h, y, scale_or_null, dtype, wdtype,
+                                        ydtype, eps, M, D, stream),
+                      stream);
+}
+
+int64_t add_rms_norm_backward_scratch(int64_t M, int64_t D)
+{
+    if (M <= 0 || D <= 0 || M > MAX_DIM || D > MAX_DIM)
+        return 0;
+    return static_cast<int64_t>(lf::rms_norm_bwd_blocks(M)) * D * static_cast<int64_t>(sizeof(float));
+}
+
+lf_status add_rms_norm_backward(const void *dy, const void *h, const void *weight, const void *dh_or_null, void *dx,
+                                void *dweight_or_null, void *scratch, int dtype, int wdtype, float eps, int64_t M,
+                                int64_t D, cudaStream_t stream)
+{
+    const lf::CallRange range("add_rms_norm_backward");
+    return debug_sync(add_rms_norm_backward_call(dy, h, weight, dh_or_null, dx, dweight_or_null, scratch, dtype,
+                                                 wdtype, eps, M, D, stream),
+                      stream);
+}
+
+lf_status gated_ffn(const void *x, const void *w, int act, void *out, void *gu_or_null, int64_t M, int64_t F,
+                    int64_t K, cudaStream_t stream)
+{
+    const lf::CallRange range("gated_ffn");
+    return debug_sync(gated_ffn_call(x, w, act, out, gu_or_null, M, F, K, stream), stream);
+}
+
+lf_status gated_ffn_e4m3(const void *x, const float *x_scale, const void *w, const float *w_scale, int act, void *out,
+                         int64_t M, int64_t F, int64_t K, cudaStream_t stream)
+{
+    const lf::CallRange range("gated_ffn_e4m3");
+    return debug_sync(gated_ffn_e4m3_call(x, x_scale, w, w_scale, act, out, M, F, K, stream), stream);
+}
+
+lf_status gated_ffn_backward(const void *dout, const void *x, const void *w, const void *gu, int act, void *dgu,
+                             void *dx_or_null, void *dw_or_null, int64_t M, int64_t F, int64_t K, cudaStream_t stream)
+{
+    const lf::CallRange range("gated_ffn_backward");
+    return debug_sync(gated_ffn_backward_call(dout, x, w, gu, act, dgu, dx_or_null, dw_or_null, M, F, K, stream),
+                      stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,479 @@
+// gated_ffn.cu -- the gated projections of a feed-forward block,
+//   out = act(x Wg^T) * (x Wu^T),   w = [2F, K]: Wg's rows, then Wu's,
+// in one kernel, and the elementwise part of their gradient.
+//
+// Both projections share x, so one tile computes 128 columns of each: the B
+// operand of the 256 x 256 MMA is 128 rows of Wg and 128 rows of Wu (one half
+// staged by each CTA of the pair), the accumulator's columns 0..127 are the gate
+// and 128..255 the up projection of the same output columns, and the epilogue
+// has both in the same TMEM lane: activation and product happen in registers
+// and neither projection is written unless the caller keeps it for the
+// backward pass.  Compute bound from a few hundred rows on (4 M F K FLOP).
+//
+// The roles, barriers and bounded waits are those of gemm_nt_pair.cu (whole
+// tiles only: nothing here waits for another pair).
+#include <atomic>
+
+#include "lf_gemm_common.cuh"
+
+namespace lf {
+namespace {
+
+constexpr int G_M = 2 * BM;                // 256 rows of x per pair tile
+constexpr int G_F = BN / 2;                // 128 output columns per pair tile
+constexpr int G_STAGES = 6;                // ring slots of one K block (128 bytes of K)
+constexpr int G_ROW = 128;                 // bytes of K per row and block
+constexpr int G_A_BYTES = BM * G_ROW;      // this CTA's 128 rows of x
+constexpr int G_B_BYTES = G_F * G_ROW;     // this CTA's 128 rows of w (gate in the leader, up in its peer)
+constexpr int G_STAGE_BYTES = G_A_BYTES + G_B_BYTES;
+constexpr int G_ACC_BUFS = 2;
+constexpr int G_TMEM_COLS = G_ACC_BUFS * BN;
+constexpr int G_NUM_BARS = 2 * G_STAGES + 2 * G_ACC_BUFS + 1;
+constexpr int G_EPI_WARPS = 8;
+constexpr int G_THREADS = 64 + 32 * G_EPI_WARPS;
+constexpr int G_STG_SLOT = 32 * 64;        // 32 rows x 32 bf16 columns
+constexpr int G_STG_WARP = 2 * G_STG_SLOT;
+constexpr int G_STG_OFF = ((G_STAGES * G_STAGE_BYTES + G_NUM_BARS * 8 + 16 + 1023) / 1024) * 1024;
+constexpr int G_SMEM = 1024 + G_STG_OFF + G_EPI_WARPS * G_STG_WARP;
+static_assert(G_SMEM <= 232448, "shared memory per CTA");
+constexpr uint64_t G_ABORT_SETTLE_NS = 100000;
+
+constexpr int ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2;
+constexpr float GELU_C2 = 1.5957691216057308f;  // 2 sqrt(2 / pi): gelu_tanh(v) = v sigmoid(GELU_C2 (v + a v^3))
+constexpr float GELU_A = 0.044715f;
+
+// 1 / (1 + exp(-v)), fp32 (about 2^-21): both ends saturate (exp overflows to
+// infinity and the quotient to 0).
+__device__ __forceinline__ float sigmoid_f(float v) { return __fdividef(1.f, 1.f + ex2_approx(-v * LOG2E)); }
+
+// act(v) = v * phi(v)
+template <int ACT>
+__device__ __forceinline__ float act_phi(float v)
+{
+    if (ACT == ACT_SILU)
+        return sigmoid_f(v);
+    if (ACT == ACT_GELU)
+        return normcdff(v);
+    return sigmoid_f(GELU_C2 * fmaf(GELU_A * v * v, v, v));
+}
+
+// d phi / d v, given p = phi(v)
+template <int ACT>
+__device__ __forceinline__ float act_dphi(float v, float p)
+{
+    if (ACT == ACT_SILU)
+        return p * (1.f - p);
+    if (ACT == ACT_GELU)
+        return 0.3989422804014327f * ex2_approx(-0.5f * LOG2E * v * v);
+    return p * (1.f - p) * GELU_C2 * fmaf(3.f * GELU_A * v, v, 1.f);
+}
+
+// Tile order: bands of band_m M blocks (M block fastest), as gemm_nt_pair.cu.
+__device__ __forceinline__ void g_tile_coords(const GemmParams &p, int tile, int &mb, int &nb)
+{
+    const int MB = p.num_m_blocks;
+    const int bm = p.band_m > 0 && p.band_m < MB ? p.band_m : MB;
+    const int per_band = bm * p.num_n_blocks;
+    const int band = tile / per_band;
+    const int local = tile - band * per_band;
+    const int rows = min(bm, MB - band * bm);
+    mb = band * bm + local % rows;
+    nb = local / rows;
+}
+
+// One 32 x 32 chunk of output (this thread's row as 16 packed pairs) through
+// staging slot k & 1 and a TMA store, as tma_store_chunk of gemm_nt_pair.cu.
+__device__ __forceinline__ void g_store_chunk(const CUtensorMap *tm, uint8_t *stg, uint32_t stg_s, int k,
+                                              const uint32_t (&pk)[16], int col, int row0, int M)
+{
+    const int lane = threadIdx.x & 31;
+    const int slot = k & 1;
+    if (k >= 2) {
+        if (lane == 0)
+            bulk_wait_group_read<1>();
+        __syncwarp();
+    }
+    uint8_t *buf = stg + slot * G_STG_SLOT;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<uint4 *>(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
+            make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0 && row0 < M) {
+        tma_store_2d(tm, stg_s + static_cast<uint32_t>(slot * G_STG_SLOT), col, row0);
+        bulk_commit_group();
+    }
+}
+
+// The warp's 32 rows x columns [c0, c1) of a finished tile.  The gate of output
+// column c is accumulator column c, its up projection accumulator column 128 + c.
+template <bool E4M3, int ACT>
+__device__ __forceinline__ void g_epilogue(const GatedParams &gp, const CUtensorMap *tmO, const CUtensorMap *tmG,
+                                           const CUtensorMap *tmU, uint32_t taddr, int row0, int nb, int c0, int c1,
+                                           uint8_t *stg, uint32_t stg_s)
+{
+    const GemmParams &p = gp.g;
+    const int lane = threadIdx.x & 31;
+    float sx = 1.f;
+    if (E4M3)
+        sx = row0 + lane < p.M ? gp.x_scale[row0 + lane] : 0.f;
+    int k = 0;
+#pragma unroll 1
+    for (int c = c0; c < c1; c += 32) {
+        const int col = nb * G_F + c;
+        if (col >= p.N)
+            break;  // warp-uniform
+        uint32_t g[32], u[32];
+        tmem_ld_32x32b_x32(taddr + static_cast<uint32_t>(c), g);
+        tmem_ld_32x32b_x32(taddr + static_cast<uint32_t>(G_F + c), u);
+        tmem_wait_ld();
+        if (E4M3) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+                if (col + i < p.N) {  // N % 8 == 0
+                    const float4 wg = *reinterpret_cast<const float4 *>(gp.w_scale + col + i);
+                    const float4 wu = *reinterpret_cast<const float4 *>(gp.w_scale + p.N + col + i);
+                    g[i] = __float_as_uint(__uint_as_float(g[i]) * (sx * wg.x));
+                    g[i + 1] = __float_as_uint(__uint_as_float(g[i + 1]) * (sx * wg.y));
+                    g[i + 2] = __float_as_uint(__uint_as_float(g[i + 2]) * (sx * wg.z));
+                    g[i + 3] = __float_as_uint(__uint_as_float(g[i + 3]) * (sx * wg.w));
+                    u[i] = __float_as_uint(__uint_as_float(u[i]) * (sx * wu.x));
+                    u[i + 1] = __float_as_uint(__uint_as_float(u[i + 1]) * (sx * wu.y));
+                    u[i + 2] = __float_as_uint(__uint_as_float(u[i + 2]) * (sx * wu.z));
+                    u[i + 3] = __float_as_uint(__uint_as_float(u[i + 3]) * (sx * wu.w));
+                }
+            }
+        }
+        uint32_t pk[16];
+        if (gp.save) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                pk[i] = pack_bf16(__uint_as_float(g[2 * i]), __uint_as_float(g[2 * i + 1]));
+            g_store_chunk(tmG, stg, stg_s, k++, pk, col, row0, p.M);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                pk[i] = pack_bf16(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+            g_store_chunk(tmU, stg, stg_s, k++, pk, col, row0, p.M);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float g0 = __uint_as_float(g[2 * i]), g1 = __uint_as_float(g[2 * i + 1]);
+            pk[i] = pack_bf16(g0 * act_phi<ACT>(g0) * __uint_as_float(u[2 * i]),
+                              g1 * act_phi<ACT>(g1) * __uint_as_float(u[2 * i + 1]));
+        }
+        g_store_chunk(tmO, stg, stg_s, k++, pk, col, row0, p.M);
+    }
+    if (lane == 0)
+        bulk_wait_group_read<0>();  // the staging slots are free for the next tile
+    __syncwarp();
+}
+
+template <bool E4M3, int ACT>
+__global__ void __launch_bounds__(G_THREADS, 1)
+    k_gated_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
+                 const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmG,
+                 const __grid_constant__ CUtensorMap tmU, const __grid_constant__ GatedParams gp)
+{
+    const GemmParams &p = gp.g;
+    constexpr int KELEMS = E4M3 ? 128 : 64;  // elements of K per block
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *gbase = smem_raw + (base - raw);
+    const uint32_t sA = base;
+    const uint32_t sB = base + G_STAGES * G_A_BYTES;
+    const uint32_t bar0 = base + G_STAGES * G_STAGE_BYTES;
+    const uint32_t drain_bar = bar0 + 8u * (2 * G_STAGES + 2 * G_ACC_BUFS);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + G_STAGES * G_STAGE_BYTES + G_NUM_BARS * 8);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+#define FULL_BAR(s) (bar0 + 8u * (s))
+#define EMPTY_BAR(s) (bar0 + 8u * (G_STAGES + (s)))
+#define TFULL_BAR(b) (bar0 + 8u * (2 * G_STAGES + (b)))
+#define TEMPTY_BAR(b) (bar0 + 8u * (2 * G_STAGES + G_ACC_BUFS + (b)))
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const int pair = blockIdx.x >> 1;
+    const int num_pairs = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < G_STAGES; ++s) {
+            mbar_init(FULL_BAR(s), 1);   // leader: its arrive.expect_tx + both CTAs' bytes
+            mbar_init(EMPTY_BAR(s), 1);  // the leader's multicast commit
+        }
+        for (int b = 0; b < G_ACC_BUFS; ++b) {
+            mbar_init(TFULL_BAR(b), 1);                 // the leader's multicast commit
+            mbar_init(TEMPTY_BAR(b), 2 * G_EPI_WARPS);  // leader: one arrive per epilogue warp of each CTA
+        }
+        mbar_init(drain_bar, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_tmap(&tmA);
+        prefetch_tmap(&tmW);
+        prefetch_tmap(&tmO);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(smem_u32(tmem_slot), G_TMEM_COLS);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // both CTAs' barriers exist before any cross-CTA signal
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const uint32_t peer_abort = mapa_shared(smem_u32(const_cast<int *>(abort_flag)), rank ^ 1u);
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer (both CTAs)
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            uint32_t armed[G_STAGES];
+#pragma unroll
+            for (int s = 0; s < G_STAGES; ++s)
+                armed[s] = 0;
+            bool ok = true, first = true;
+            for (int tile = pair; ok && tile < p.num_tiles; tile += num_pairs) {
+                int mb, nb;
+                g_tile_coords(p, tile, mb, nb);
+                const int arow = mb * G_M + static_cast<int>(rank) * BM;
+                // gate rows in the leader, up rows in its peer
+                const int brow = static_cast<int>(rank) * p.N + nb * G_F;
+                for (int kb = 0; kb < p.num_k_blocks; ++kb) {
+                    if (!wait_bar(EMPTY_BAR(stage), phase ^ 1u, abort_flag, p, ERR_PRODUCER, peer_abort)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t full_leader = mapa_shared(FULL_BAR(stage), 0u);
+                    const bool skip = first && p.inject == 1 && blockIdx.x == 0;  // test hook
+                    first = false;
+                    if (!skip) {
+                        if (leader) {
+                            mbar_arrive_expect_tx(FULL_BAR(stage), 2u * G_STAGE_BYTES);
+                            ++armed[stage];
+                        }
+                        tma_load_2d_pair(sA + stage * G_A_BYTES, &tmA, kb * KELEMS, arow, full_leader);
+                        tma_load_2d_pair(sB + stage * G_B_BYTES, &tmW, kb * KELEMS, brow, full_leader);
+                    }
+                    if (++stage == G_STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (leader)
+                for (int s = 0; s < G_STAGES; ++s)
+                    if (armed[s])
+                        wait_bar_drain(FULL_BAR(s), (armed[s] - 1u) & 1u, abort_flag, p, peer_abort);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer (leader only)
+        if (leader && lane == 0) {
+            int stage = 0, acc = 0;
+            uint32_t phase = 0, acc_phase = 0;
+            bool ok = true;
+            const uint32_t idesc = E4M3 ? idesc_e4m3_f32(G_M, BN) : idesc_bf16_f32(G_M, BN);
+            for (int tile = pair; ok && tile < p.num_tiles; tile += num_pairs) {
+                if (!wait_bar(TEMPTY_BAR(acc), acc_phase ^ 1u, abort_flag, p, ERR_MMA_ACC, peer_abort))
+                    break;
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
+                for (int kb = 0; kb < p.num_k_blocks; ++kb) {
+                    if (!wait_bar(FULL_BAR(stage), phase, abort_flag, p, ERR_MMA_FULL, peer_abort)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a0 = sA + stage * G_A_BYTES;
+                    const uint32_t b0 = sB + stage * G_B_BYTES;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {  // 32 bytes of K per MMA
+                        const uint64_t da = smem_desc_k128(a0 + k * 32), db = smem_desc_k128(b0 + k * 32);
+                        const uint32_t accumulate = (kb | k) != 0 ? 1u : 0u;
+                        if (E4M3)
+                            umma_f8_pair(d_tmem, da, db, idesc, accumulate);
+                        else
+                            umma_f16_pair(d_tmem, da, db, idesc, accumulate);
+                    }
+                    umma_commit_pair_mc(EMPTY_BAR(stage), 0x3);
+                    if (++stage == G_STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok)
+                    break;
+                umma_commit_pair_mc(TFULL_BAR(acc), 0x3);
+                if (++acc == G_ACC_BUFS) {
+                    acc = 0;
+                    acc_phase ^= 1u;
+                }
+            }
+            umma_commit_pair_mc(drain_bar, 0x1);
+            wait_bar_drain(drain_bar, 0u, abort_flag, p, peer_abort);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------ epilogue (both CTAs)
+        // warp w reads TMEM lanes 32 (w % 4) ..; warps 2..5 take output columns
+        // 0..63 of the tile, warps 6..9 columns 64..127
+        const int q = warp & 3;
+        const int c0 = ((warp - 2) >> 2) * (G_F / 2);
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        uint8_t *stg = gbase + G_STG_OFF + (warp - 2) * G_STG_WARP;
+        const uint32_t stg_s = base + static_cast<uint32_t>(G_STG_OFF + (warp - 2) * G_STG_WARP);
+        for (int tile = pair; tile < p.num_tiles; tile += num_pairs) {
+            int mb, nb;
+            g_tile_coords(p, tile, mb, nb);
+            const bool ok = wait_bar(TFULL_BAR(acc), acc_phase, abort_flag, p, ERR_EPI, peer_abort);
+            if (!__all_sync(0xffffffffu, ok))
+                break;
+            tc_fence_after();
+            g_epilogue<E4M3, ACT>(gp, &tmO, &tmG, &tmU,
+                                  tmem_base + static_cast<uint32_t>(acc * BN) + (static_cast<uint32_t>(q * 32) << 16),
+                                  mb * G_M + static_cast<int>(rank) * BM + q * 32, nb, c0, c0 + G_F / 2, stg, stg_s);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive_cluster(mapa_shared(TEMPTY_BAR(acc), 0u));
+            if (++acc == G_ACC_BUFS) {
+                acc = 0;
+                acc_phase ^= 1u;
+            }
+        }
+        if (lane == 0)
+            bulk_wait_group_all();
+    }
+#undef FULL_BAR
+#undef EMPTY_BAR
+#undef TFULL_BAR
+#undef TEMPTY_BAR
+
+    if (*abort_flag) {
+        // Copies this CTA issued complete on the leader's barrier, so nothing
+        // here can wait for them: give them a fixed, generous time to land.
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < G_ABORT_SETTLE_NS) {
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // the peer no longer touches this CTA's barriers, smem or TMEM
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, G_TMEM_COLS);
+    }
+}
+
+template <bool E4M3, int ACT>
+cudaError_t launch_gated_pair_t(const CUtensorMap &ta, const CUtensorMap &tw, const CUtensorMap &to,
+                                const CUtensorMap &tg, const CUtensorMap &tu, const GatedParams &p, int grid,
+                                cudaStream_t s)
+{
+    static std::atomic<unsigned long long> done{0};  // the shared-memory opt-in, once per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(done.load() & bit)) {
+        e = cudaFuncSetAttribute(k_gated_pair<E4M3, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, G_SMEM);
+        if (e != cudaSuccess)
+            return e;
+        done.fetch_or(bit);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.blockDim = dim3(G_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = G_SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_gated_pair<E4M3, ACT>, ta, tw, to, tg, tu, p);
+}
+
+// ---------------------------------------------------------------- gradient
+// dgu = [dout u act'(g), dout act(g)] from the kept pre-activations gu = [g, u]:
+// 8 columns per thread and step, 6 bytes read and 4 written per column.
+template <int ACT>
+__global__ void __launch_bounds__(256)
+    k_gated_bwd(const __nv_bfloat16 *dout, const __nv_bfloat16 *gu, __nv_bfloat16 *dgu, int64_t M, int64_t F)
+{
+    const int64_t packs = F / 8;
+    for (int64_t row = blockIdx.y; row < M; row += gridDim.y) {
+        for (int64_t c = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; c < packs;
+             c += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+            const uint4 dv = *reinterpret_cast<const uint4 *>(dout + row * F + c * 8);
+            const uint4 gv = *reinterpret_cast<const uint4 *>(gu + row * 2 * F + c * 8);
+            const uint4 uv = *reinterpret_cast<const uint4 *>(gu + row * 2 * F + F + c * 8);
+            const __nv_bfloat162 *d2 = reinterpret_cast<const __nv_bfloat162 *>(&dv);
+            const __nv_bfloat162 *g2 = reinterpret_cast<const __nv_bfloat162 *>(&gv);
+            const __nv_bfloat162 *u2 = reinterpret_cast<const __nv_bfloat162 *>(&uv);
+            uint32_t dg[4], du[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 d = __bfloat1622float2(d2[i]), g = __bfloat1622float2(g2[i]), u = __bfloat1622float2(u2[i]);
+                const float p0 = act_phi<ACT>(g.x), p1 = act_phi<ACT>(g.y);
+                dg[i] = pack_bf16(d.x * u.x * fmaf(g.x, act_dphi<ACT>(g.x, p0), p0),
+                                  d.y * u.y * fmaf(g.y, act_dphi<ACT>(g.y, p1), p1));
+                du[i] = pack_bf16(d.x * (g.x * p0), d.y * (g.y * p1));
+            }
+            *reinterpret_cast<uint4 *>(dgu + row * 2 * F + c * 8) = make_uint4(dg[0], dg[1], dg[2], dg[3]);
+            *reinterpret_cast<uint4 *>(dgu + row * 2 * F + F + c * 8) = make_uint4(du[0], du[1], du[2], du[3]);
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_gated_pair(bool e4m3, int act, const CUtensorMap &ta, const CUtensorMap &tw, const CUtensorMap &to,
+                              const CUtensorMap &tg, const CUtensorMap &tu, const GatedParams &p, int grid,
+                              cudaStream_t s)
+{
+    switch (act + (e4m3 ? 3 : 0)) {
+    case ACT_SILU:
+        return launch_gated_pair_t<false, ACT_SILU>(ta, tw, to, tg, tu, p, grid, s);
+    case ACT_GELU:
+        return launch_gated_pair_t<false, ACT_GELU>(ta, tw, to, tg, tu, p, grid, s);
+    case ACT_GELU_TANH:
+        return launch_gated_pair_t<false, ACT_GELU_TANH>(ta, tw, to, tg, tu, p, grid, s);
+    case 3 + ACT_SILU:
+        return launch_gated_pair_t<true, ACT_SILU>(ta, tw, to, tg, tu, p, grid, s);
+    case 3 + ACT_GELU:
+        return launch_gated_pair_t<true, ACT_GELU>(ta, tw, to, tg, tu, p, grid, s);
+    case 3 + ACT_GELU_TANH:
+        return launch_gated_pair_t<true, ACT_GELU_TANH>(ta, tw, to, tg, tu, p, grid, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_gated_bwd(int act, const void *dout, const void *gu, void *dgu, int64_t M, int64_t F, int num_sms,
+                             cudaStream_t s)
+{
+    (void)num_sms;
+    const int64_t bx = (F / 8 + 255) / 256;
+    const dim3 grid(static_cast<unsigned>(bx < 1024 ? bx : 1024), static_cast<unsigned>(M < 65535 ? M : 65535));
+    const __nv_bfloat16 *d = static_cast<const __nv_bfloat16 *>(dout), *g = static_cast<const __nv_bfloat16 *>(gu);
+    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(dgu);
+    if (act == ACT_SILU)
+        k_gated_bwd<ACT_SILU><<<grid, 256, 0, s>>>(d, g, o, M, F);
+    else if (act == ACT_GELU)
+        k_gated_bwd<ACT_GELU><<<grid, 256, 0, s>>>(d, g, o, M, F);
+    else
+        k_gated_bwd<ACT_GELU_TANH><<<grid, 256, 0, s>>>(d, g, o, M, F);
+    return cudaGetLastError();
+}
+
+}  // namespace lf

@@ -61,6 +61,47 @@ cudaError_t launch_rope_cos_sin(const void *inv_freq, const int64_t *pos, void *
                                 int64_t S, int num_sms, cudaStream_t s);
 cudaError_t launch_fp8_cast_dual(const void *x, const float *scale, void *out, void *out_t, int64_t M, int64_t K,
                                  int num_sms, cudaStream_t s);
+// Residual addition + RMS norm (rms_norm.cu).  dtype / wdtype as lf_dtype;
+// wdtype is dtype or fp32.  ldx, ldr: row pitches in elements; h and y are [M,D].
+struct NormParams {
+    const void *x, *residual, *weight;  // residual may be null: then h is x and is not written
+    void *h, *y;
+    float *scale;  // [M], the e4m3 form only
+    int64_t M, D, ldx, ldr;
+    float eps;
+};
+cudaError_t launch_rms_norm(const NormParams &p, int dtype, int wdtype, bool fp8, int num_sms, cudaStream_t s);
+
+// Its gradient.  partial: fp32 [rms_norm_bwd_blocks(M)][D], or null with
+// dweight null; dweight has the weight's type.  dh may be null.
+struct NormBwdParams {
+    const void *dy, *h, *weight, *dh;
+    void *dx;
+    float *partial;
+    int64_t M, D;
+    float eps;
+};
+constexpr int RMS_BWD_BLOCKS = 304;  // two blocks for each of 152 SMs
+int rms_norm_bwd_blocks(int64_t M);
+cudaError_t launch_rms_norm_bwd(const NormBwdParams &p, void *dweight, int dtype, int wdtype, cudaStream_t s);
+
+// Gated projections on CTA pairs (gated_ffn.cu): out = act(x Wg^T) * (x Wu^T).
+// g: M, N = F, K, block counts (256-row M blocks, 128-column N blocks, 128-byte
+// K blocks), num_tiles, band_m, err, timeout_ns, inject.
+struct GatedParams {
+    GemmParams g;
+    const float *x_scale, *w_scale;  // e4m3 operands: [M] and [2F]
+    int save;                        // also store gate and up (tg, tu)
+};
+// ta: x, boxes of 128 rows; tw: w [2F, K], boxes of 128 rows (both 128-byte
+// rows, 128-byte swizzle); to: out; tg, tu: the two halves of gu (32 x 32 boxes).
+cudaError_t launch_gated_pair(bool e4m3, int act, const CUtensorMap &ta, const CUtensorMap &tw, const CUtensorMap &to,
+                              const CUtensorMap &tg, const CUtensorMap &tu, const GatedParams &p, int grid,
+                              cudaStream_t s);
+// dgu = [dout u act'(g), dout act(g)] from gu = [g, u]; F % 8 == 0, 16-byte aligned.
+cudaError_t launch_gated_bwd(int act, const void *dout, const void *gu, void *dgu, int64_t M, int64_t F, int num_sms,
+                             cudaStream_t s);
+
 // Test hook: `ctas` CTAs, each holding 200 KiB of shared memory (one per SM),
 // that wait `ns` nanoseconds on the global timer and exit.
 cudaError_t launch_occupy_sms(int ctas, unsigned long long ns, cudaStream_t s);
