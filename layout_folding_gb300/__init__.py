@@ -383,228 +383,6 @@ def bmm(a, b, out=None, stream=None):
     return out3[0] if a.dim() == 2 and b.dim() == 2 and out.dim() == 3 else out
 
 
-LF_BF16, LF_FP16, LF_FP32, LF_E4M3 = 0, 1, 2, 3
-ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
-
-
-def _lf_dtype(t, name):
-    import torch
-    code = {torch.bfloat16: LF_BF16, torch.float16: LF_FP16, torch.float32: LF_FP32}.get(t.dtype)
-    if code is None:
-        raise TypeError("%s must be bf16, fp16 or fp32, got %s" % (name, t.dtype))
-    return code
-
-
-def _activation(act):
-    if act not in ACTIVATIONS:
-        raise ValueError("act must be one of %s, got %r" % (", ".join(sorted(ACTIVATIONS)), act))
-    return ACTIVATIONS[act]
-
-
-def _rows(t, dtype, name):
-    """(M, D, row pitch) of a CUDA tensor [..., D] of equal rows: contiguous, or
-    2-D with unit column stride (a slice of wider rows)."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError("%s must be a CUDA tensor" % name)
-    if t.dtype != dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.dim() == 0:
-        raise ValueError("%s must have at least one dimension" % name)
-    D = t.shape[-1]
-    M = t.numel() // D if D else 0
-    if t.is_contiguous():
-        return M, D, D
-    if t.dim() != 2 or (t.stride(1) != 1 and D > 1) or (t.stride(0) < D and M > 1):
-        raise ValueError("%s must be contiguous, or 2-D with unit column stride and rows that do not overlap" % name)
-    return M, D, t.stride(0) if M > 1 else D
-
-
-def _like(t, ref, dtype, shape, name):
-    """`t`, checked, or a new contiguous tensor on ref's device."""
-    import torch
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=ref.device)
-    _require(t, dtype, name)
-    if tuple(t.shape) != tuple(shape) or t.device != ref.device:
-        raise ValueError("%s must be %s on %s" % (name, tuple(shape), ref.device))
-    return t
-
-
-def _zeroed(t, stream):
-    """t filled with zeros: the weight gradient of no rows."""
-    import torch
-    if t is not None:
-        with torch.cuda.stream(stream):
-            t.zero_()
-    return t
-
-
-def _same_device(ref, **others):
-    for name, t in others.items():
-        if t is not None and t.device != ref.device:
-            raise ValueError("%s is on %s, expected %s" % (name, t.device, ref.device))
-
-
-def add_rms_norm(x, weight, residual=None, eps=1e-6, fp8=False, h=None, y=None, scale=None, stream=None):
-    """Residual addition and root-mean-square norm over the last dimension.
-
-    h = x + residual (rounded to x's type; x itself when residual is None),
-    f = h / sqrt(mean(h^2) + eps) * weight.  Returns (y, h, scale): y = f in x's
-    type with scale None, or with fp8 y = float8_e4m3fn(f / scale) and scale fp32
-    of x's leading shape (one per row: max|f| / 448, 1 for a row of zeros).  No
-    rows at all give empty outputs (and zero weight gradients) here and below.
-    x, residual: bf16, fp16 or fp32 [..., D], contiguous or 2-D slices of wider
-    rows; weight [D] in x's type or fp32.  h may be passed as residual (or x)
-    itself, to update a contiguous stream in place."""
-    import torch
-    M, D, ldx = _rows(x, getattr(x, "dtype", None), "x")
-    dt = _lf_dtype(x, "x")
-    wd = _lf_dtype(weight, "weight") if isinstance(weight, torch.Tensor) else -1
-    if wd not in (dt, LF_FP32):
-        raise TypeError("weight must be a %s or float32 tensor" % x.dtype)
-    _require(weight, weight.dtype, "weight")
-    if weight.numel() != D:
-        raise ValueError("weight must hold D = %d elements" % D)
-    ldr = 0
-    if residual is not None:
-        _, _, ldr = _rows(residual, x.dtype, "residual")
-        if residual.shape != x.shape:
-            raise ValueError("residual must have x's shape")
-        h = _like(h, x, x.dtype, x.shape, "h")
-    elif h is not None:
-        raise ValueError("h is written only where a residual is added")
-    if scale is not None and not fp8:
-        raise ValueError("scale is written only with fp8")
-    y = _like(y, x, torch.float8_e4m3fn if fp8 else x.dtype, x.shape, "y")
-    if fp8:
-        scale = _like(scale, x, torch.float32, x.shape[:-1], "scale")
-    _same_device(x, weight=weight, residual=residual)
-    if M == 0 and D > 0:  # no rows, no work
-        return y, (x if residual is None else h), scale
-    _check(lib().add_rms_norm(x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr,
-                              weight.data_ptr(), None if residual is None else h.data_ptr(), y.data_ptr(),
-                              scale.data_ptr() if fp8 else None, dt, wd, LF_E4M3 if fp8 else dt, eps, M, D,
-                              _stream(stream)), "add_rms_norm")
-    return y, (x if residual is None else h), scale
-
-
-def add_rms_norm_backward(dy, h, weight, dh=None, eps=1e-6, want_dweight=True, dx=None, dweight=None, stream=None):
-    """Gradient of add_rms_norm.  dy, h (add_rms_norm's) and dh (the gradient
-    arriving at h by other ways, or None) contiguous [..., D] of one type.
-    Returns (dx, dweight): dx in h's type is the gradient of x and of residual,
-    dweight has weight's type (None when not wanted)."""
-    import torch
-    dt = _lf_dtype(h, "h") if isinstance(h, torch.Tensor) else -1
-    _require(h, getattr(h, "dtype", None), "h")
-    _require(dy, h.dtype, "dy")
-    if h.dim() == 0 or dy.shape != h.shape:
-        raise ValueError("dy must have h's shape [..., D]")
-    D = h.shape[-1]
-    M = h.numel() // D if D else 0
-    wd = _lf_dtype(weight, "weight") if isinstance(weight, torch.Tensor) else -1
-    if wd not in (dt, LF_FP32):
-        raise TypeError("weight must be a %s or float32 tensor" % h.dtype)
-    _require(weight, weight.dtype, "weight")
-    if weight.numel() != D:
-        raise ValueError("weight must hold D = %d elements" % D)
-    if dh is not None:
-        _require(dh, h.dtype, "dh")
-        if dh.shape != h.shape:
-            raise ValueError("dh must have h's shape")
-    dx = _like(dx, h, h.dtype, h.shape, "dx")
-    scratch = None
-    if want_dweight or dweight is not None:
-        dweight = _like(dweight, h, weight.dtype, weight.shape, "dweight")
-        scratch = torch.empty(lib().add_rms_norm_backward_scratch(M, D), dtype=torch.uint8, device=h.device)
-    _same_device(h, dy=dy, weight=weight, dh=dh)
-    if M == 0 and D > 0:
-        return dx, _zeroed(dweight, stream)
-    if stream is not None and scratch is not None:
-        scratch.record_stream(stream)
-    _check(lib().add_rms_norm_backward(dy.data_ptr(), h.data_ptr(), weight.data_ptr(),
-                                       None if dh is None else dh.data_ptr(), dx.data_ptr(),
-                                       None if dweight is None else dweight.data_ptr(),
-                                       None if scratch is None else scratch.data_ptr(), dt, wd, eps, M, D,
-                                       _stream(stream)), "add_rms_norm_backward")
-    return dx, dweight
-
-
-def _gated_dims(x, w, dtype):
-    _require(x, dtype, "x")
-    _require(w, dtype, "w")
-    if w.dim() != 2 or x.dim() == 0 or w.shape[1] != x.shape[-1] or w.shape[0] % 2:
-        raise ValueError("w must be [2F, K] with K = x.shape[-1]: the gate's rows, then the up projection's")
-    K, F = x.shape[-1], w.shape[0] // 2
-    return x.numel() // K if K else 0, F, K
-
-
-def gated_ffn(x, w, act="silu", x_scale=None, w_scale=None, want_gu=False, out=None, gu=None, stream=None):
-    """The gated projections: out = act(x @ Wg.T) * (x @ Wu.T), w [2F, K] holding
-    Wg's rows and then Wu's; act "silu", "gelu" or "gelu_tanh".
-
-    x [..., K] and w in bf16, or both float8_e4m3fn with fp32 scales for each
-    token (x_scale, x's leading shape) and each row of w (w_scale [2F]).
-    Returns (out bf16 [..., F], gu): gu is bf16 [..., 2F], the two projections
-    that gated_ffn_backward takes, when want_gu (bf16 operands only), else None."""
-    import torch
-    code = _activation(act)
-    scaled = x_scale is not None or w_scale is not None
-    M, F, K = _gated_dims(x, w, torch.float8_e4m3fn if scaled else torch.bfloat16)
-    out = _like(out, x, torch.bfloat16, (*x.shape[:-1], F), "out")
-    if scaled:
-        if x_scale is None or w_scale is None or want_gu or gu is not None:
-            raise ValueError("e4m3 operands take both x_scale and w_scale, and keep no gu")
-        _require(x_scale, torch.float32, "x_scale")
-        _require(w_scale, torch.float32, "w_scale")
-        if x_scale.numel() != M or w_scale.numel() != 2 * F:
-            raise ValueError("x_scale must hold one scale per row of x and w_scale one per row of w")
-        _same_device(x, w=w, x_scale=x_scale, w_scale=w_scale)
-        if M == 0 and F > 0 and K > 0:
-            return out, None
-        _check(lib().gated_ffn_e4m3(x.data_ptr(), x_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), code,
-                                    out.data_ptr(), M, F, K, _stream(stream)), "gated_ffn_e4m3")
-        return out, None
-    if want_gu or gu is not None:
-        gu = _like(gu, x, torch.bfloat16, (*x.shape[:-1], 2 * F), "gu")
-    _same_device(x, w=w)
-    if M == 0 and F > 0 and K > 0:
-        return out, gu
-    _check(lib().gated_ffn(x.data_ptr(), w.data_ptr(), code, out.data_ptr(), None if gu is None else gu.data_ptr(),
-                           M, F, K, _stream(stream)), "gated_ffn")
-    return out, gu
-
-
-def gated_ffn_backward(dout, x, w, gu, act="silu", want_dx=True, want_dw=True, dx=None, dw=None, dgu=None,
-                       stream=None):
-    """Gradient of gated_ffn (bf16): dout [..., F], gu [..., 2F] as gated_ffn
-    returned it.  Returns (dx [..., K], dw [2F, K]), None where not wanted.
-    dgu [..., 2F] receives the gradient of the two projections (pass gu itself
-    to reuse its memory; a new tensor by default)."""
-    import torch
-    code = _activation(act)
-    M, F, K = _gated_dims(x, w, torch.bfloat16)
-    _require(dout, torch.bfloat16, "dout")
-    _require(gu, torch.bfloat16, "gu")
-    if dout.numel() != M * F or dout.shape[-1] != F or gu.numel() != 2 * M * F or gu.shape[-1] != 2 * F:
-        raise ValueError("dout must be [..., F] and gu [..., 2F] for x's rows")
-    _same_device(x, w=w, dout=dout, gu=gu)
-    own_dgu = dgu is None
-    dgu = _like(dgu, x, torch.bfloat16, gu.shape, "dgu")
-    if own_dgu and stream is not None:
-        dgu.record_stream(stream)
-    if want_dx or dx is not None:
-        dx = _like(dx, x, torch.bfloat16, x.shape, "dx")
-    if want_dw or dw is not None:
-        dw = _like(dw, x, torch.bfloat16, w.shape, "dw")
-    if M == 0 and F > 0 and K > 0:
-        return dx, _zeroed(dw, stream)
-    _check(lib().gated_ffn_backward(dout.data_ptr(), x.data_ptr(), w.data_ptr(), gu.data_ptr(), code, dgu.data_ptr(),
-                                    None if dx is None else dx.data_ptr(), None if dw is None else dw.data_ptr(),
-                                    M, F, K, _stream(stream)), "gated_ffn_backward")
-    return dx, dw
-
-
 # which device-side wait gave up (lf_last_device_wait_code)
 WAIT_CODES = {0x101: "operand ring slot never freed", 0x102: "operand stage never landed",
               0x103: "accumulator never released", 0x104: "accumulator never completed",
@@ -693,3 +471,7 @@ def occupy_sms(ctas: int, duration_ns: int, stream=None):
     """Test hook: hold `ctas` SMs (200 KiB of shared memory each) for
     duration_ns on `stream`, standing in for another application's kernels."""
     _check(lib().lf_test_occupy_sms(int(ctas), int(duration_ns), _stream(stream)), "lf_test_occupy_sms")
+
+
+from .ffn import (ACTIVATIONS, LF_BF16, LF_E4M3, LF_FP16, LF_FP32, add_rms_norm,  # noqa: E402,F401
+                  add_rms_norm_backward, gated_ffn, gated_ffn_backward)

@@ -1009,7 +1009,8 @@ static lf_status add_rms_norm_call(const void *x, int64_t ldx, const void *resid
     lf_status st = current_device(&d);
     if (st != LF_OK)
         return st;
-    const lf::NormParams p = {x, residual, weight, h, y, scale, M, D, ldx, ldr, eps};
+    const lf::NormParams p = {x, residual, weight, h, y, scale, M, D, ldx, ldr, eps,
+                              {d->err_word, g_timeout_ns.load(), g_inject.load()}};
     return launched(lf::launch_rms_norm(p, dtype, wdtype, ydtype == LF_E4M3, d->num_sms, stream), 1);
 }
 
@@ -1029,8 +1030,9 @@ static lf_status add_rms_norm_backward_call(const void *dy, const void *h, const
     lf_status st = current_device(&d);
     if (st != LF_OK)
         return st;
-    const lf::NormBwdParams p = {dy, h, weight, dh, dx, dweight ? static_cast<float *>(scratch) : nullptr, M, D, eps};
-    return launched(lf::launch_rms_norm_bwd(p, dweight, dtype, wdtype, stream), dweight ? 2 : 1);
+    const lf::NormBwdParams p = {dy, h, weight, dh, dx, dweight ? static_cast<float *>(scratch) : nullptr, M, D, eps,
+                                 {d->err_word, g_timeout_ns.load(), g_inject.load()}};
+    return launched(lf::launch_rms_norm_bwd(p, dweight, dtype, wdtype, d->num_sms, stream), dweight ? 2 : 1);
 }
 
 static bool act_ok(int act) { return act >= LF_ACT_SILU && act <= LF_ACT_GELU_TANH; }

@@ -61,6 +61,13 @@ cudaError_t launch_rope_cos_sin(const void *inv_freq, const int64_t *pos, void *
                                 int64_t S, int num_sms, cudaStream_t s);
 cudaError_t launch_fp8_cast_dual(const void *x, const float *scale, void *out, void *out_t, int64_t M, int64_t K,
                                  int num_sms, cudaStream_t s);
+// Where a kernel's bounded waits report, and their limit.
+struct WaitLimit {
+    int *err;
+    unsigned long long timeout_ns;
+    int inject;  // test hook: 1 = the first wait is never satisfied
+};
+
 // Residual addition + RMS norm (rms_norm.cu).  dtype / wdtype as lf_dtype;
 // wdtype is dtype or fp32.  ldx, ldr: row pitches in elements; h and y are [M,D].
 struct NormParams {
@@ -69,6 +76,7 @@ struct NormParams {
     float *scale;  // [M], the e4m3 form only
     int64_t M, D, ldx, ldr;
     float eps;
+    WaitLimit limit;
 };
 cudaError_t launch_rms_norm(const NormParams &p, int dtype, int wdtype, bool fp8, int num_sms, cudaStream_t s);
 
@@ -80,10 +88,12 @@ struct NormBwdParams {
     float *partial;
     int64_t M, D;
     float eps;
+    WaitLimit limit;
 };
 constexpr int RMS_BWD_BLOCKS = 304;  // two blocks for each of 152 SMs
 int rms_norm_bwd_blocks(int64_t M);
-cudaError_t launch_rms_norm_bwd(const NormBwdParams &p, void *dweight, int dtype, int wdtype, cudaStream_t s);
+cudaError_t launch_rms_norm_bwd(const NormBwdParams &p, void *dweight, int dtype, int wdtype, int num_sms,
+                                cudaStream_t s);
 
 // Gated projections on CTA pairs (gated_ffn.cu): out = act(x Wg^T) * (x Wu^T).
 // g: M, N = F, K, block counts (256-row M blocks, 128-column N blocks, 128-byte

@@ -13,12 +13,15 @@
 // Both passes are bound by memory: every element of the row is read once and
 // held in registers between the reduction and the output (rows too long for
 // that take the *_long kernels, which read the row again from L2).
+#include <atomic>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <type_traits>
 
 #include "lf_internal.h"
+#include "lf_ptx.cuh"
 
 namespace lf {
 namespace {
@@ -26,66 +29,123 @@ namespace {
 constexpr float E4M3_MAX = 448.f;
 constexpr int MAX_WARPS = 32;
 
+// VEC consecutive elements as they lie in memory: 32-bit words moved 16 bytes at
+// a time, or (VEC = 1) one element with no alignment beyond its own.  get() and
+// set() convert to and from fp32 a pair at a time.
+template <class T, int VEC>
+struct Pack {
+    static constexpr int WORDS = VEC * static_cast<int>(sizeof(T)) / 4;
+    uint32_t u[WORDS];
+    __device__ __forceinline__ void load(const T *p)
+    {
+#pragma unroll
+        for (int i = 0; i < WORDS / 4; ++i) {
+            const uint4 v = reinterpret_cast<const uint4 *>(p)[i];
+            u[4 * i] = v.x;
+            u[4 * i + 1] = v.y;
+            u[4 * i + 2] = v.z;
+            u[4 * i + 3] = v.w;
+        }
+    }
+    __device__ __forceinline__ void store(T *p) const
+    {
+#pragma unroll
+        for (int i = 0; i < WORDS / 4; ++i)
+            reinterpret_cast<uint4 *>(p)[i] = make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+    }
+    __device__ __forceinline__ void get(float (&f)[VEC]) const
+    {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                f[i] = __uint_as_float(u[i]);
+            } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+                f[2 * i] = __uint_as_float(u[i] << 16);
+                f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+            } else {
+                const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&u[i]));
+                f[2 * i] = v.x;
+                f[2 * i + 1] = v.y;
+            }
+        }
+    }
+    __device__ __forceinline__ void set(const float (&f)[VEC])
+    {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                u[i] = __float_as_uint(f[i]);
+            } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+                const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+                u[i] = *reinterpret_cast<const uint32_t *>(&v);
+            } else {
+                const __half2 v = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+                u[i] = *reinterpret_cast<const uint32_t *>(&v);
+            }
+        }
+    }
+    // this += o, each sum rounded once to T.  (For the 16-bit types that is also
+    // what an fp32 addition rounded to T gives: fp32 has more than twice their
+    // digits, so its own rounding cannot move a sum across one of theirs.)
+    __device__ __forceinline__ void add(const Pack &o)
+    {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                u[i] = __float_as_uint(__uint_as_float(u[i]) + __uint_as_float(o.u[i]));
+            } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+                const __nv_bfloat162 v = __hadd2_rn(*reinterpret_cast<const __nv_bfloat162 *>(&u[i]),
+                                                    *reinterpret_cast<const __nv_bfloat162 *>(&o.u[i]));
+                u[i] = *reinterpret_cast<const uint32_t *>(&v);
+            } else {
+                const __half2 v = __hadd2_rn(*reinterpret_cast<const __half2 *>(&u[i]),
+                                             *reinterpret_cast<const __half2 *>(&o.u[i]));
+                u[i] = *reinterpret_cast<const uint32_t *>(&v);
+            }
+        }
+    }
+};
+
 __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
 __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
 template <class T>
-__device__ __forceinline__ T from_f(float v);
-template <>
-__device__ __forceinline__ float from_f<float>(float v)
+__device__ __forceinline__ T from_f(float v)
 {
-    return v;
-}
-template <>
-__device__ __forceinline__ __half from_f<__half>(float v)
-{
-    return __float2half_rn(v);
-}
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v)
-{
-    return __float2bfloat16_rn(v);
+    if constexpr (std::is_same<T, float>::value)
+        return v;
+    else if constexpr (std::is_same<T, __half>::value)
+        return __float2half_rn(v);
+    else
+        return __float2bfloat16_rn(v);
 }
 
-// VEC consecutive elements, moved 16 bytes (VEC * sizeof(T) if that is less) at
-// a time; VEC = 1 has no alignment beyond the element's.
-template <class T, int VEC>
-struct Pack {
-    static constexpr int BYTES = VEC * static_cast<int>(sizeof(T));
-    static constexpr int ALIGN = BYTES >= 16 ? 16 : BYTES;
-    alignas(ALIGN) T v[VEC];
+template <class T>
+struct Pack<T, 1> {
+    T v;
+    __device__ __forceinline__ void load(const T *p) { v = *p; }
+    __device__ __forceinline__ void store(T *p) const { *p = v; }
+    __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = to_f(v); }
+    __device__ __forceinline__ void set(const float (&f)[1]) { v = from_f<T>(f[0]); }
+    __device__ __forceinline__ void add(const Pack &o) { v = from_f<T>(to_f(v) + to_f(o.v)); }
 };
 
 template <class T, int VEC>
 __device__ __forceinline__ Pack<T, VEC> load_pack(const T *p)
 {
     Pack<T, VEC> r;
-    if constexpr (Pack<T, VEC>::BYTES >= 16) {
-#pragma unroll
-        for (int i = 0; i < Pack<T, VEC>::BYTES / 16; ++i)
-            reinterpret_cast<uint4 *>(r.v)[i] = reinterpret_cast<const uint4 *>(p)[i];
-    } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i)
-            r.v[i] = p[i];
-    }
+    r.load(p);
     return r;
 }
 
-template <class T, int VEC>
-__device__ __forceinline__ void store_pack(T *p, const Pack<T, VEC> &r)
+// max(|m|, |a|), a NaN kept: the running maximum of magnitudes (its sign is not
+// meaningful until mag() clears it).
+__device__ __forceinline__ float max_mag(float m, float a)
 {
-    if constexpr (Pack<T, VEC>::BYTES >= 16) {
-#pragma unroll
-        for (int i = 0; i < Pack<T, VEC>::BYTES / 16; ++i)
-            reinterpret_cast<uint4 *>(p)[i] = reinterpret_cast<const uint4 *>(r.v)[i];
-    } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i)
-            p[i] = r.v[i];
-    }
+    float r;
+    asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(a));
+    return r;
 }
-
 // |v| as an unsigned integer: ordered like the magnitudes, infinity above
 // every number and a NaN above infinity, so an integer maximum keeps a NaN.
 __device__ __forceinline__ uint32_t mag_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
@@ -126,19 +186,35 @@ __device__ __forceinline__ float2 block_reduce(float a, uint32_t b, float2 *sh)
     return make_float2(a, __uint_as_float(b));
 }
 
-// The e4m3 scale of a row whose largest |f| is amax, and how to divide by it:
-// a product with the reciprocal, or a division where the reciprocal of a tiny
-// scale could overflow.
+// The e4m3 scale of a row and the factor that takes h weight to its code: f is
+// h weight r, and its largest magnitude r times mx = max |h weight|, so
+// f / scale = h weight (448 / mx).  Rows that are not ordinary: all zeros (scale
+// 1), NaN, and magnitudes so small that 448 / mx could overflow (`tiny`: the
+// codes then come from a division by the scale).
 struct RowScale {
-    float scale, inv;
-    bool divide;
-    __device__ __forceinline__ explicit RowScale(float amax)
+    float scale, factor;
+    bool tiny;
+    __device__ __forceinline__ RowScale(float mx, float r)
     {
+        const float amax = mx * r;
         scale = amax == 0.f ? 1.f : amax / E4M3_MAX;
-        divide = scale < 0x1p-100f;
-        inv = 1.f / scale;
+        tiny = mx < 0x1p-100f || scale < 0x1p-120f;
+        factor = amax == 0.f ? r : amax != amax ? amax : E4M3_MAX / mx;
     }
-    __device__ __forceinline__ float operator()(float f) const { return divide ? f / scale : f * inv; }
+    // f: h weight, N of them, to what is converted to e4m3
+    template <int N>
+    __device__ __forceinline__ void apply(float (&f)[N], float r) const
+    {
+        if (tiny) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                f[i] = f[i] * r / scale;
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                f[i] *= factor;
+        }
+    }
 };
 
 __device__ __forceinline__ uint32_t e4m3_pair(float a, float b)
@@ -177,7 +253,7 @@ __global__ void __launch_bounds__(NV <= 2 ? 512 : 1024) k_rms_norm(const NormPar
     for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x, buf ^= 1) {
         Pack<T, VEC> h[NV];
         float ss = 0.f;
-        uint32_t mx = 0u;
+        float mx = 0.f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = threadIdx.x + j * blockDim.x;
@@ -189,11 +265,8 @@ __global__ void __launch_bounds__(NV <= 2 ? 512 : 1024) k_rms_norm(const NormPar
             for (int j = 0; j < NV; ++j) {
                 const int c = threadIdx.x + j * blockDim.x;
                 if (c < packs) {
-                    const Pack<T, VEC> r = load_pack<T, VEC>(res + row * p.ldr + static_cast<int64_t>(c) * VEC);
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i)
-                        h[j].v[i] = from_f<T>(to_f(h[j].v[i]) + to_f(r.v[i]));
-                    store_pack<T, VEC>(static_cast<T *>(p.h) + row * p.D + static_cast<int64_t>(c) * VEC, h[j]);
+                    h[j].add(load_pack<T, VEC>(res + row * p.ldr + static_cast<int64_t>(c) * VEC));
+                    h[j].store(static_cast<T *>(p.h) + row * p.D + static_cast<int64_t>(c) * VEC);
                 }
             }
         }
@@ -201,45 +274,46 @@ __global__ void __launch_bounds__(NV <= 2 ? 512 : 1024) k_rms_norm(const NormPar
         for (int j = 0; j < NV; ++j) {
             const int c = threadIdx.x + j * blockDim.x;
             if (c < packs) {
+float v[VEC];
+                h[j].get(v);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    const float v = to_f(h[j].v[i]);
-                    ss = fmaf(v, v, ss);
-                }
+                for (int i = 0; i < VEC; ++i)
+                    ss = fmaf(v[i], v[i], ss);
                 if (FP8) {
-                    const Pack<W, VEC> wv = load_pack<W, VEC>(w + static_cast<int64_t>(c) * VEC);
+                    float wv[VEC];
+                    load_pack<W, VEC>(w + static_cast<int64_t>(c) * VEC).get(wv);
 #pragma unroll
                     for (int i = 0; i < VEC; ++i)
-                        mx = max(mx, mag_bits(to_f(h[j].v[i]) * to_f(wv.v[i])));
+                        mx = max_mag(mx, v[i] * wv[i]);
                 }
             }
         }
-        const float2 sums = block_reduce<true>(ss, mx, sh[buf]);
+        const float2 sums = block_reduce<true>(ss, mag_bits(mx), sh[buf]);
         const float r = rsqrtf(sums.x / static_cast<float>(p.D) + p.eps);
-        const RowScale rs(sums.y * r);
+        const RowScale rs(sums.y, r);
         if (FP8 && threadIdx.x == 0)
             p.scale[row] = rs.scale;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = threadIdx.x + j * blockDim.x;
             if (c < packs) {
-                const Pack<W, VEC> wv = load_pack<W, VEC>(w + static_cast<int64_t>(c) * VEC);
                 const int64_t o = row * p.D + static_cast<int64_t>(c) * VEC;
-                float f[VEC];
-#pragma unroll
-                for (int i = 0; i < VEC; ++i)
-                    f[i] = to_f(h[j].v[i]) * r * to_f(wv.v[i]);
+                float f[VEC], wv[VEC];
+                h[j].get(f);
+                load_pack<W, VEC>(w + static_cast<int64_t>(c) * VEC).get(wv);
                 if (FP8) {
 #pragma unroll
                     for (int i = 0; i < VEC; ++i)
-                        f[i] = rs(f[i]);
+                        f[i] *= wv[i];
+                    rs.apply(f, r);
                     store_e4m3<VEC>(static_cast<uint8_t *>(p.y) + o, f);
                 } else {
-                    Pack<T, VEC> yv;
 #pragma unroll
                     for (int i = 0; i < VEC; ++i)
-                        yv.v[i] = from_f<T>(f[i]);
-                    store_pack<T, VEC>(static_cast<T *>(p.y) + o, yv);
+                        f[i] *= r * wv[i];
+                    Pack<T, VEC> yv;
+                    yv.set(f);
+                    yv.store(static_cast<T *>(p.y) + o);
                 }
             }
         }
@@ -259,7 +333,7 @@ __global__ void __launch_bounds__(1024) k_rms_norm_long(const NormParams p)
         const T *x = static_cast<const T *>(p.x) + row * p.ldx;
         T *h = res ? static_cast<T *>(p.h) + row * p.D : nullptr;
         float ss = 0.f;
-        uint32_t mx = 0u;
+        float mx = 0.f;
         for (int64_t c = threadIdx.x; c < p.D; c += blockDim.x) {
             T t = x[c];
             if (res) {
@@ -269,20 +343,21 @@ __global__ void __launch_bounds__(1024) k_rms_norm_long(const NormParams p)
             const float v = to_f(t);
             ss = fmaf(v, v, ss);
             if (FP8)
-                mx = max(mx, mag_bits(v * to_f(w[c])));
+                mx = max_mag(mx, v * to_f(w[c]));
         }
-        const float2 sums = block_reduce<true>(ss, mx, sh[buf]);
+        const float2 sums = block_reduce<true>(ss, mag_bits(mx), sh[buf]);
         const float r = rsqrtf(sums.x / static_cast<float>(p.D) + p.eps);
-        const RowScale rs(sums.y * r);
+        const RowScale rs(sums.y, r);
         if (FP8 && threadIdx.x == 0)
             p.scale[row] = rs.scale;
         for (int64_t c = threadIdx.x; c < p.D; c += blockDim.x) {
-            const float f[1] = {to_f(res ? h[c] : x[c]) * r * to_f(w[c])};
+            const float v = to_f(res ? h[c] : x[c]);
             if (FP8) {
-                const float q[1] = {rs(f[0])};
-                store_e4m3<1>(static_cast<uint8_t *>(p.y) + row * p.D + c, q);
+                float f[1] = {v * to_f(w[c])};
+                rs.apply(f, r);
+                store_e4m3<1>(static_cast<uint8_t *>(p.y) + row * p.D + c, f);
             } else {
-                static_cast<T *>(p.y)[row * p.D + c] = from_f<T>(f[0]);
+                static_cast<T *>(p.y)[row * p.D + c] = from_f<T>(v * (r * to_f(w[c])));
             }
         }
     }
@@ -322,12 +397,14 @@ __global__ void __launch_bounds__(VEC * NV <= 8 ? 512 : 1024) k_rms_norm_bwd(con
         for (int j = 0; j < NV; ++j) {
             const int c = threadIdx.x + j * blockDim.x;
             if (c < packs) {
-                const Pack<W, VEC> wv = load_pack<W, VEC>(w + static_cast<int64_t>(c) * VEC);
+                float v[VEC], d[VEC], wv[VEC];
+                h[j].get(v);
+                dy[j].get(d);
+                load_pack<W, VEC>(w + static_cast<int64_t>(c) * VEC).get(wv);
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
-                    const float v = to_f(h[j].v[i]);
-                    ss = fmaf(v, v, ss);
-                    gh = fmaf(to_f(dy[j].v[i]) * to_f(wv.v[i]), v, gh);
+                    ss = fmaf(v[i], v[i], ss);
+                    gh = fmaf(d[i] * wv[i], v[i], gh);
                 }
             }
         }
@@ -339,18 +416,25 @@ __global__ void __launch_bounds__(VEC * NV <= 8 ? 512 : 1024) k_rms_norm_bwd(con
             const int c = threadIdx.x + j * blockDim.x;
             if (c < packs) {
                 const int64_t oc = o + static_cast<int64_t>(c) * VEC;
-                const Pack<W, VEC> wv = load_pack<W, VEC>(w + static_cast<int64_t>(c) * VEC);
-                Pack<T, VEC> dh, dx;
-                if (p.dh)
-                    dh = load_pack<T, VEC>(static_cast<const T *>(p.dh) + oc);
+                float v[VEC], d[VEC], wv[VEC], o2[VEC];
+                h[j].get(v);
+                dy[j].get(d);
+                load_pack<W, VEC>(w + static_cast<int64_t>(c) * VEC).get(wv);
+                if (p.dh) {
+                    load_pack<T, VEC>(static_cast<const T *>(p.dh) + oc).get(o2);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i)
+                        o2[i] = 0.f;
+                }
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
-                    const float v = to_f(h[j].v[i]), d = to_f(dy[j].v[i]);
-                    acc[j][i] = fmaf(d, v * r, acc[j][i]);
-                    const float g = r * (d * to_f(wv.v[i]) - v * k);
-                    dx.v[i] = from_f<T>(p.dh ? g + to_f(dh.v[i]) : g);
+                    acc[j][i] = fmaf(d[i], v[i] * r, acc[j][i]);
+                    o2[i] = fmaf(r, fmaf(d[i], wv[i], -v[i] * k), o2[i]);
                 }
-                store_pack<T, VEC>(static_cast<T *>(p.dx) + oc, dx);
+                Pack<T, VEC> dx;
+                dx.set(o2);
+                dx.store(static_cast<T *>(p.dx) + oc);
             }
         }
     }
@@ -361,10 +445,8 @@ __global__ void __launch_bounds__(VEC * NV <= 8 ? 512 : 1024) k_rms_norm_bwd(con
             const int c = threadIdx.x + j * blockDim.x;
             if (c < packs) {
                 Pack<float, VEC> a;
-#pragma unroll
-                for (int i = 0; i < VEC; ++i)
-                    a.v[i] = acc[j][i];
-                store_pack<float, VEC>(out + static_cast<int64_t>(c) * VEC, a);
+                a.set(acc[j]);
+                a.store(out + static_cast<int64_t>(c) * VEC);
             }
         }
     }
@@ -405,19 +487,27 @@ __global__ void __launch_bounds__(1024) k_rms_norm_bwd_long(const NormBwdParams 
     }
 }
 
-// dweight[c] = sum over blocks of partial[b][c]: 32 columns per block, 16 rows of
-// threads that each sum every 16th block's row; the 16 sums are added in order.
-constexpr int DW_ROWS = 16;
+// dweight[c] = sum over blocks of partial[b][c]: 32 columns per block, 32 rows of
+// threads that each sum every 32nd block's row (at most 10, all in flight at
+// once); the 32 sums are added in order.
+constexpr int DW_ROWS = 32;
+constexpr int DW_STEPS = (RMS_BWD_BLOCKS + DW_ROWS - 1) / DW_ROWS;
 template <class W>
 __global__ void __launch_bounds__(32 * DW_ROWS)
     k_rms_norm_dweight(const float *partial, W *dweight, int64_t D, int blocks)
 {
     __shared__ float sh[DW_ROWS][32];
     const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x;
+    float v[DW_STEPS];
+#pragma unroll
+    for (int i = 0; i < DW_STEPS; ++i) {
+        const int b = threadIdx.y + i * DW_ROWS;
+        v[i] = c < D && b < blocks ? partial[b * D + c] : 0.f;
+    }
     float s = 0.f;
-    if (c < D)
-        for (int b = threadIdx.y; b < blocks; b += DW_ROWS)
-            s += partial[b * D + c];
+#pragma unroll
+    for (int i = 0; i < DW_STEPS; ++i)
+        s += v[i];
     sh[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
     if (threadIdx.y == 0 && c < D) {
@@ -427,6 +517,415 @@ __global__ void __launch_bounds__(32 * DW_ROWS)
             s += sh[i][threadIdx.x];
         dweight[c] = from_f<W>(s);
     }
+}
+
+// ---------------------------------------------------------------- many rows
+// With many rows the kernels are bound by HBM, which wants some 70 KB in flight
+// on every SM at all times.  So one persistent block per SM splits into groups of
+// warps, each with its own ring of row slots in shared memory that bulk copies
+// (cp.async.bulk, one per input row) fill: group g of the grid takes rows g,
+// g + groups, ...  A group moves a landed row into registers, reduces it over its
+// own warps -- a named barrier, after which every thread has read the slot, so
+// one thread refills it with the row `slots` steps ahead -- and writes its
+// outputs while the copies run.  Registers hold one row only; the latency is
+// covered by the rings.
+constexpr int RING_NV = 4;            // packs per thread: a group has ceil(packs / 128) warps
+constexpr int RING_MAX_GROUPS = 15;   // named barriers 1..15
+constexpr int RING_MAX_SLOTS = 8;
+constexpr int64_t RING_MIN_ROWS = 608;   // fewer rows: one block per row
+constexpr int RING_BUDGET = 220 * 1024;
+constexpr uint64_t RING_SETTLE_NS = 100000;  // after an abort: let copies in flight land
+
+// Shared-memory layout of a ring kernel, computed on the host.
+struct RingPlan {
+    int group_threads, groups, slots;
+    uint32_t row_bytes;                // one input row
+    uint32_t w_off, slot_off, slot_bytes;  // weights; slots ([group][slot][input][row])
+    uint32_t bytes;                    // dynamic shared memory
+};
+
+struct RingSync {
+    float2 sums[2][MAX_WARPS];
+    int failed[2][MAX_WARPS];
+    alignas(8) unsigned long long full[RING_MAX_GROUPS * RING_MAX_SLOTS];
+};
+
+__device__ __forceinline__ void group_barrier(int id, int threads)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// Bounded wait for a slot; on a timeout the code goes to the device error word.
+__device__ __forceinline__ bool ring_wait(uint32_t bar, uint32_t parity, const WaitLimit &lim)
+{
+    if (mbar_try_wait(bar, parity))
+        return true;
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        if (global_timer_ns() - t0 > lim.timeout_ns) {
+            atomicCAS(lim.err, 0, 0x102);
+            return false;
+        }
+    }
+    return true;
+}
+
+// block_reduce over one group.  `ok` (false in a thread whose wait gave up) is
+// combined as well, so that the whole group leaves its loop together.
+template <bool MAXB>
+__device__ __forceinline__ float2 group_reduce(float a, uint32_t b, bool &ok, RingSync &sy, int buf, int first_warp,
+                                               int warps, int id)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+        const uint32_t c = __shfl_xor_sync(0xffffffffu, b, o);
+        b = MAXB ? max(b, c) : __float_as_uint(__uint_as_float(b) + __uint_as_float(c));
+    }
+    ok = __all_sync(0xffffffffu, ok);
+    if (warps == 1) {
+        __syncwarp();  // orders the warp's reads of the slot before its refill
+        return make_float2(a, __uint_as_float(b));
+    }
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (lane == 0) {
+        sy.sums[buf][warp] = make_float2(a, __uint_as_float(b));
+        sy.failed[buf][warp] = ok ? 0 : 1;
+    }
+    group_barrier(id, warps * 32);
+    a = 0.f;
+    b = 0u;
+    int failed = 0;
+    if (lane < warps) {
+        const float2 t = sy.sums[buf][first_warp + lane];
+        a = t.x;
+        b = __float_as_uint(t.y);
+        failed = sy.failed[buf][first_warp + lane];
+    }
+    ok = !__any_sync(0xffffffffu, failed);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+        const uint32_t c = __shfl_xor_sync(0xffffffffu, b, o);
+        b = MAXB ? max(b, c) : __float_as_uint(__uint_as_float(b) + __uint_as_float(c));
+    }
+    return make_float2(a, __uint_as_float(b));
+}
+
+// One group's ring: `inputs` rows (bulk copies) per slot.
+struct Ring {
+    uint32_t slots_s, full_s;  // shared addresses: the group's slots, its barriers
+    const uint8_t *slots;
+    int n, slot = 0;
+    uint32_t phase = 0;
+    uint32_t row_bytes, slot_bytes;
+    __device__ Ring(const RingPlan &r, uint8_t *smem, RingSync &sy, int group)
+        : n(r.slots), row_bytes(r.row_bytes), slot_bytes(r.slot_bytes)
+    {
+        slots = smem + r.slot_off + static_cast<size_t>(group) * r.slots * r.slot_bytes;
+        slots_s = smem_u32(slots);
+        full_s = smem_u32(&sy.full[group * RING_MAX_SLOTS]);
+    }
+    // One thread of the group, before its first fill.
+    __device__ void init() const
+    {
+        for (int s = 0; s < n; ++s)
+            mbar_init(full_s + 8u * s, 1);
+        fence_mbar_init();
+    }
+    __device__ void fill(int s, const void *a, const void *b, const void *c) const
+    {
+        const uint32_t bar = full_s + 8u * s, dst = slots_s + s * slot_bytes;
+        mbar_arrive_expect_tx(bar, slot_bytes);
+        bulk_load_g2s(dst, a, row_bytes, bar);
+        if (b)
+            bulk_load_g2s(dst + row_bytes, b, row_bytes, bar);
+        if (c)
+            bulk_load_g2s(dst + 2 * row_bytes, c, row_bytes, bar);
+    }
+    __device__ const uint8_t *input(int i) const { return slots + slot * slot_bytes + i * row_bytes; }
+    __device__ void advance()
+    {
+        if (++slot == n) {
+            slot = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
+// Copies the weights to shared memory; after it every thread sees them and the
+// groups' barriers.
+template <class W>
+__device__ __forceinline__ W *ring_weights(uint8_t *smem, const RingPlan &r, const W *w, int64_t D)
+{
+    W *ws = reinterpret_cast<W *>(smem + r.w_off);
+    for (int i = threadIdx.x; i < static_cast<int>(D * sizeof(W) / 16); i += blockDim.x)
+        reinterpret_cast<uint4 *>(ws)[i] = reinterpret_cast<const uint4 *>(w)[i];
+    __syncthreads();
+    return ws;
+}
+
+template <class T, class W, bool FP8>
+__global__ void __launch_bounds__(1024) k_rms_norm_ring(const NormParams p, const RingPlan r)
+{
+    constexpr int VEC = 16 / static_cast<int>(sizeof(T));
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ RingSync sy;
+    const int group = threadIdx.x / r.group_threads, t = threadIdx.x % r.group_threads;
+    const int warps = r.group_threads >> 5, first_warp = group * warps;
+    const int packs = static_cast<int>(p.D / VEC);
+    const T *x = static_cast<const T *>(p.x);
+    const T *res = static_cast<const T *>(p.residual);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * r.groups;
+    // neighbouring rows go to neighbouring SMs
+    const int64_t row0 = static_cast<int64_t>(group) * gridDim.x + blockIdx.x;
+    Ring ring(r, smem, sy, group);
+    const auto fill = [&](int slot, int64_t row) {
+        ring.fill(slot, x + row * p.ldx, res ? res + row * p.ldr : nullptr, nullptr);
+    };
+    if (t == 0) {
+        ring.init();
+        // (test hook: the first block's first group never loads its first row)
+        for (int i = p.limit.inject && blockIdx.x == 0 && group == 0 ? 1 : 0; i < r.slots && row0 + i * step < p.M; ++i)
+            fill(i, row0 + i * step);
+    }
+    const W *w = ring_weights<W>(smem, r, static_cast<const W *>(p.weight), p.D);
+    bool ok = true;
+    int buf = 0;
+    for (int64_t row = row0; row < p.M; row += step, buf ^= 1) {
+        ok = ring_wait(ring.full_s + 8u * ring.slot, ring.phase, p.limit);
+        Pack<T, VEC> h[RING_NV];
+        float ss = 0.f;
+        float mx = 0.f;
+#pragma unroll
+        for (int j = 0; j < RING_NV; ++j) {
+            const int c = t + j * r.group_threads;
+            if (c < packs) {
+                h[j] = load_pack<T, VEC>(reinterpret_cast<const T *>(ring.input(0)) + c * VEC);
+                if (res) {
+                    h[j].add(load_pack<T, VEC>(reinterpret_cast<const T *>(ring.input(1)) + c * VEC));
+                    h[j].store(static_cast<T *>(p.h) + row * p.D + static_cast<int64_t>(c) * VEC);
+                }
+float v[VEC];
+                h[j].get(v);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i)
+                    ss = fmaf(v[i], v[i], ss);
+                if (FP8) {
+                    float wv[VEC];
+                    load_pack<W, VEC>(w + c * VEC).get(wv);
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i)
+                        mx = max_mag(mx, v[i] * wv[i]);
+                }
+            }
+        }
+        const float2 sums = group_reduce<true>(ss, mag_bits(mx), ok, sy, buf, first_warp, warps, 1 + group);
+        if (!ok)
+            break;
+        if (t == 0 && row + r.slots * step < p.M)
+            fill(ring.slot, row + r.slots * step);  // every thread of the group has read the slot
+        ring.advance();
+        const float rr = rsqrtf(sums.x / static_cast<float>(p.D) + p.eps);
+        const RowScale rs(sums.y, rr);
+        if (FP8 && t == 0)
+            p.scale[row] = rs.scale;
+#pragma unroll
+        for (int j = 0; j < RING_NV; ++j) {
+            const int c = t + j * r.group_threads;
+            if (c < packs) {
+                const int64_t o = row * p.D + static_cast<int64_t>(c) * VEC;
+                float f[VEC], wv[VEC];
+                h[j].get(f);
+                load_pack<W, VEC>(w + c * VEC).get(wv);
+                if (FP8) {
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i)
+                        f[i] *= wv[i];
+                    rs.apply(f, rr);
+                    store_e4m3<VEC>(static_cast<uint8_t *>(p.y) + o, f);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i)
+                        f[i] *= rr * wv[i];
+                    Pack<T, VEC> yv;
+                    yv.set(f);
+                    yv.store(static_cast<T *>(p.y) + o);
+                }
+            }
+        }
+    }
+    if (!ok) {  // copies of this group may still be in flight: give them time to land
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < RING_SETTLE_NS) {
+        }
+    }
+}
+
+// Backward: as above with the rows of h, dy (and dh); each thread keeps the
+// weight gradient of its columns in registers over its group's rows, the block's
+// groups are added in order through shared memory, and the block writes one row
+// of `partial`.
+template <class T, class W, bool DH>
+__global__ void __launch_bounds__(512) k_rms_norm_bwd_ring(const NormBwdParams p, const RingPlan r)
+{
+    constexpr int VEC = 16 / static_cast<int>(sizeof(T));
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ RingSync sy;
+    const int group = threadIdx.x / r.group_threads, t = threadIdx.x % r.group_threads;
+    const int warps = r.group_threads >> 5, first_warp = group * warps;
+    const int packs = static_cast<int>(p.D / VEC);
+    const T *hg = static_cast<const T *>(p.h), *yg = static_cast<const T *>(p.dy), *dg = static_cast<const T *>(p.dh);
+    const float inv_d = 1.f / static_cast<float>(p.D);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * r.groups;
+    const int64_t row0 = static_cast<int64_t>(group) * gridDim.x + blockIdx.x;
+    Ring ring(r, smem, sy, group);
+    const auto fill = [&](int slot, int64_t row) {
+        ring.fill(slot, hg + row * p.D, yg + row * p.D, DH ? dg + row * p.D : nullptr);
+    };
+    if (t == 0) {
+        ring.init();
+        // (test hook: the first block's first group never loads its first row)
+        for (int i = p.limit.inject && blockIdx.x == 0 && group == 0 ? 1 : 0; i < r.slots && row0 + i * step < p.M; ++i)
+            fill(i, row0 + i * step);
+    }
+    const W *w = ring_weights<W>(smem, r, static_cast<const W *>(p.weight), p.D);
+    float acc[RING_NV][VEC];
+#pragma unroll
+    for (int j = 0; j < RING_NV; ++j)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            acc[j][i] = 0.f;
+    bool ok = true;
+    int buf = 0;
+    for (int64_t row = row0; row < p.M; row += step, buf ^= 1) {
+        ok = ring_wait(ring.full_s + 8u * ring.slot, ring.phase, p.limit);
+        Pack<T, VEC> h[RING_NV], dy[RING_NV], dh[DH ? RING_NV : 1];
+        float ss = 0.f, gh = 0.f;
+#pragma unroll
+        for (int j = 0; j < RING_NV; ++j) {
+            const int c = t + j * r.group_threads;
+            if (c < packs) {
+                h[j] = load_pack<T, VEC>(reinterpret_cast<const T *>(ring.input(0)) + c * VEC);
+                dy[j] = load_pack<T, VEC>(reinterpret_cast<const T *>(ring.input(1)) + c * VEC);
+                if (DH)
+                    dh[DH ? j : 0] = load_pack<T, VEC>(reinterpret_cast<const T *>(ring.input(2)) + c * VEC);
+                float v[VEC], d[VEC], wv[VEC];
+                h[j].get(v);
+                dy[j].get(d);
+                load_pack<W, VEC>(w + c * VEC).get(wv);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    ss = fmaf(v[i], v[i], ss);
+                    gh = fmaf(d[i] * wv[i], v[i], gh);
+                }
+            }
+        }
+        const float2 sums = group_reduce<false>(ss, __float_as_uint(gh), ok, sy, buf, first_warp, warps, 1 + group);
+        if (!ok)
+            break;
+        if (t == 0 && row + r.slots * step < p.M)
+            fill(ring.slot, row + r.slots * step);
+        ring.advance();
+        const float rr = rsqrtf(sums.x * inv_d + p.eps);
+        const float k = (sums.y * inv_d) * rr * rr;  // dx = r (g - h k) + dh
+#pragma unroll
+        for (int j = 0; j < RING_NV; ++j) {
+            const int c = t + j * r.group_threads;
+            if (c < packs) {
+                float v[VEC], d[VEC], wv[VEC], o[VEC];
+                h[j].get(v);
+                dy[j].get(d);
+                load_pack<W, VEC>(w + c * VEC).get(wv);
+                if (DH) {
+                    dh[DH ? j : 0].get(o);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i)
+                        o[i] = 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    acc[j][i] = fmaf(d[i], v[i] * rr, acc[j][i]);
+                    o[i] = fmaf(rr, fmaf(d[i], wv[i], -v[i] * k), o[i]);
+                }
+                Pack<T, VEC> dx;
+                dx.set(o);
+                dx.store(static_cast<T *>(p.dx) + row * p.D + static_cast<int64_t>(c) * VEC);
+            }
+        }
+    }
+    if (!ok) {
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < RING_SETTLE_NS) {
+        }
+    }
+    if (!p.partial)
+        return;
+    // the rings are idle: the first group stores its sums there, the others add
+    // theirs in turn, the last one writes the block's row
+    __syncthreads();
+    float *dw = reinterpret_cast<float *>(smem + r.slot_off);
+    for (int g = 0; g < r.groups; ++g) {
+        if (group == g) {
+#pragma unroll
+            for (int j = 0; j < RING_NV; ++j) {
+                const int c = t + j * r.group_threads;
+                if (c < packs) {
+                    Pack<float, VEC> a;
+                    a.set(acc[j]);
+                    if (g > 0)
+                        a.add(load_pack<float, VEC>(dw + c * VEC));
+                    if (g + 1 < r.groups)
+                        a.store(dw + c * VEC);
+                    else
+                        a.store(p.partial + static_cast<int64_t>(blockIdx.x) * p.D + c * VEC);
+                }
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// A ring of `inputs` rows of D elements per slot, or false where a row is too
+// long for two slots.  At least two slots per group, then as many groups as the
+// threads and the shared memory allow, then more slots.
+bool plan_ring(RingPlan *r, int64_t D, int elem, int welem, int inputs, int max_threads)
+{
+    const int64_t packs = D * elem / 16;
+    const int64_t row_bytes = D * elem, slot = row_bytes * inputs;
+    const int64_t wbytes = (D * welem + 127) / 128 * 128;
+    const int64_t gt = (packs + 32 * RING_NV - 1) / (32 * RING_NV) * 32;
+    if (gt > max_threads || wbytes + 2 * slot > RING_BUDGET)
+        return false;
+    int64_t groups = max_threads / gt;
+    groups = groups < RING_MAX_GROUPS ? groups : RING_MAX_GROUPS;
+    const int64_t fit = (RING_BUDGET - wbytes) / (2 * slot);
+    groups = groups < fit ? groups : fit;
+    int64_t slots = (RING_BUDGET - wbytes) / (slot * groups);
+    slots = slots < RING_MAX_SLOTS ? slots : RING_MAX_SLOTS;
+    r->group_threads = static_cast<int>(gt);
+    r->groups = static_cast<int>(groups);
+    r->slots = static_cast<int>(slots);
+    r->row_bytes = static_cast<uint32_t>(row_bytes);
+    r->w_off = 0;
+    r->slot_off = static_cast<uint32_t>(wbytes);
+    r->slot_bytes = static_cast<uint32_t>(slot);
+    r->bytes = static_cast<uint32_t>(wbytes + groups * slots * slot);
+    return true;
+}
+
+template <class K>
+cudaError_t ring_opt_in(K kernel, std::atomic<unsigned long long> &done)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (done.load() & (1ull << (dev & 63))))
+        return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RING_BUDGET);
+    if (e == cudaSuccess)
+        done.fetch_or(1ull << (dev & 63));
+    return e;
 }
 
 // Threads per block for a row of `packs` packs, NV per thread.
@@ -460,6 +959,15 @@ template <class T, class W, bool FP8>
 cudaError_t launch_norm_t(const NormParams &p, bool vec, int num_sms, cudaStream_t s)
 {
     constexpr int V = 16 / static_cast<int>(sizeof(T));
+    RingPlan r;
+    if (vec && p.M >= RING_MIN_ROWS && plan_ring(&r, p.D, sizeof(T), sizeof(W), p.residual ? 2 : 1, 1024)) {
+        static std::atomic<unsigned long long> opted{0};
+        const cudaError_t e = ring_opt_in(k_rms_norm_ring<T, W, FP8>, opted);
+        if (e != cudaSuccess)
+            return e;
+        k_rms_norm_ring<T, W, FP8><<<num_sms, r.groups * r.group_threads, r.bytes, s>>>(p, r);
+        return cudaGetLastError();
+    }
     const bool done = vec ? launch_norm_regs<T, W, V, FP8>(p, num_sms, s) : launch_norm_regs<T, W, 1, FP8>(p, num_sms, s);
     if (!done)
         k_rms_norm_long<T, W, FP8><<<static_cast<unsigned>(p.M < 0x7fffffff ? p.M : 0x7fffffff), 1024, 0, s>>>(p);
@@ -491,10 +999,24 @@ bool launch_bwd_regs(const NormBwdParams &p, int grid, cudaStream_t s)
 }
 
 template <class T, class W>
-cudaError_t launch_bwd_tw(const NormBwdParams &p, bool vec, void *dweight, int blocks, cudaStream_t s)
+cudaError_t launch_bwd_tw(const NormBwdParams &p, bool vec, void *dweight, int blocks, int num_sms, cudaStream_t s)
 {
     constexpr int V = 16 / static_cast<int>(sizeof(T));
-    if (!(vec ? launch_bwd_regs<T, W, V>(p, blocks, s) : launch_bwd_regs<T, W, 1>(p, blocks, s)))
+    RingPlan r;
+    if (vec && p.M >= RING_MIN_ROWS && num_sms <= blocks &&
+        plan_ring(&r, p.D, sizeof(T), sizeof(W), p.dh ? 3 : 2, 512)) {
+        static std::atomic<unsigned long long> opted[2];
+        cudaError_t e = ring_opt_in(k_rms_norm_bwd_ring<T, W, true>, opted[0]);
+        if (e == cudaSuccess)
+            e = ring_opt_in(k_rms_norm_bwd_ring<T, W, false>, opted[1]);
+        if (e != cudaSuccess)
+            return e;
+        blocks = num_sms;
+        if (p.dh)
+            k_rms_norm_bwd_ring<T, W, true><<<blocks, r.groups * r.group_threads, r.bytes, s>>>(p, r);
+        else
+            k_rms_norm_bwd_ring<T, W, false><<<blocks, r.groups * r.group_threads, r.bytes, s>>>(p, r);
+    } else if (!(vec ? launch_bwd_regs<T, W, V>(p, blocks, s) : launch_bwd_regs<T, W, 1>(p, blocks, s)))
         k_rms_norm_bwd_long<T, W><<<blocks, 1024, 0, s>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !dweight)
@@ -525,19 +1047,20 @@ cudaError_t launch_rms_norm(const NormParams &p, int dtype, int wdtype, bool fp8
 
 int rms_norm_bwd_blocks(int64_t M) { return static_cast<int>(M < RMS_BWD_BLOCKS ? M : RMS_BWD_BLOCKS); }
 
-cudaError_t launch_rms_norm_bwd(const NormBwdParams &p, void *dweight, int dtype, int wdtype, cudaStream_t s)
+cudaError_t launch_rms_norm_bwd(const NormBwdParams &p, void *dweight, int dtype, int wdtype, int num_sms,
+                                cudaStream_t s)
 {
     const int64_t v = dtype == 2 ? 4 : 8;
     const bool vec = p.D % v == 0 && al16(p.dy) && al16(p.h) && al16(p.weight) && al16(p.dx) &&
                      (!p.dh || al16(p.dh)) && (!p.partial || al16(p.partial));
     const int blocks = rms_norm_bwd_blocks(p.M);
     if (dtype == 0)
-        return wdtype == 0 ? launch_bwd_tw<__nv_bfloat16, __nv_bfloat16>(p, vec, dweight, blocks, s)
-                           : launch_bwd_tw<__nv_bfloat16, float>(p, vec, dweight, blocks, s);
+        return wdtype == 0 ? launch_bwd_tw<__nv_bfloat16, __nv_bfloat16>(p, vec, dweight, blocks, num_sms, s)
+                           : launch_bwd_tw<__nv_bfloat16, float>(p, vec, dweight, blocks, num_sms, s);
     if (dtype == 1)
-        return wdtype == 1 ? launch_bwd_tw<__half, __half>(p, vec, dweight, blocks, s)
-                           : launch_bwd_tw<__half, float>(p, vec, dweight, blocks, s);
-    return launch_bwd_tw<float, float>(p, vec, dweight, blocks, s);
+        return wdtype == 1 ? launch_bwd_tw<__half, __half>(p, vec, dweight, blocks, num_sms, s)
+                           : launch_bwd_tw<__half, float>(p, vec, dweight, blocks, num_sms, s);
+    return launch_bwd_tw<float, float>(p, vec, dweight, blocks, num_sms, s);
 }
 
 }  // namespace lf

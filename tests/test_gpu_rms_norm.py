@@ -104,6 +104,55 @@ def test_many_rows_and_leading_dimensions():
     check_forward(x, w, res, False, forward(x, w, res, False))
 
 
+# enough rows for the persistent kernels: one warp per row and many groups of them,
+# several warps, rows that leave room for one group only, rows too long for it
+MANY = [(609, 8), (1000, 136), (2500, 264), (700, 1032), (1300, 2056), (640, 5120), (613, 12296), (610, 20000)]
+
+
+@pytest.mark.parametrize("M,D", MANY)
+@pytest.mark.parametrize("dtype,wdtype", TYPES, ids=IDS)
+def test_many_rows(M, D, dtype, wdtype):
+    x, w = normal((M, D), M + D, 1.0, dtype), 1 + normal((D,), D, 0.2, wdtype)
+    res = normal((M, D), 77 + D, 2.0, dtype)
+    check_forward(x, w, None, True, forward(x, w, None, True))
+    check_forward(x, w, res, True, forward(x, w, res, True))
+    check_forward(x, w, res, False, forward(x, w, res, False))
+    check_backward(x, res, w, None, backward(x, res, w))
+    check_backward(x, res, w, x, backward(x, res, w, x))
+    lf.check_device_error()
+
+
+def test_many_rows_of_wider_tensors_in_place_and_with_nan():
+    M, D = 900, 1024
+    wide, w = normal((M, 1040), 4), 1 + normal((D,), 6, 0.2)
+    wide[17, 100] = float("nan")
+    res = normal((M, D), 5, 2.0)
+    rd = res.to(DEV)
+    y, h, _ = lf.add_rms_norm(wide.to(DEV)[:, 8:8 + D], w.to(DEV), residual=rd, eps=EPS, h=rd)
+    fine = [i for i in range(M) if i != 17]
+    x = wide[:, 8:8 + D].contiguous()
+    check_forward(x[fine], w, res[fine], False, (y[fine], h[fine], None))
+    assert torch.isnan(y[17]).all()
+
+
+def test_stalled_wait_times_out_and_context_survives():
+    M, D = 1000, 1024
+    x, w, res = normal((M, D), 1), 1 + normal((D,), 2, 0.2), normal((M, D), 3, 2.0)
+    for call, check in ((lambda: forward(x, w, res), lambda out: check_forward(x, w, res, False, out)),
+                        (lambda: backward(x, res, w), lambda out: check_backward(x, res, w, None, out))):
+        lf.check_device_error()
+        lf.set_test_hooks(True, 100_000_000)   # the first group's first row never lands; 100 ms per wait
+        try:
+            call()
+            with pytest.raises(lf.LayoutFoldError) as info:
+                lf.check_device_error()
+            assert info.value.status == 6 and lf.last_device_wait_code() in lf.WAIT_CODES
+        finally:
+            lf.set_test_hooks(False, 0)
+        check(call())
+        lf.check_device_error()
+
+
 @pytest.mark.parametrize("pitch,off", [(1032, 8), (1031, 3), (1030, 2)])
 def test_rows_of_wider_tensors(pitch, off):
     wide, wide_r = normal((6, pitch), 4).to(DEV), normal((6, pitch), 5, 2.0).to(DEV)
