@@ -529,6 +529,13 @@ __global__ void __launch_bounds__(32 * DW_ROWS)
 // one thread refills it with the row `slots` steps ahead -- and writes its
 // outputs while the copies run.  Registers hold one row only; the latency is
 // covered by the rings.
+//
+// Rows whose length is not a multiple of 16 bytes (PH, "phased") are moved in
+// 16-byte granules all the same: contiguous rows lie one after another, so the
+// granules that cover row r start `phase` = r D mod VEC elements before it.  The
+// grid is a multiple of VEC, so every row of a block has the phase of its first,
+// and a thread's columns, the shifted weights in shared memory and the places
+// of the row's two ragged granules stay the same for the whole block.
 constexpr int RING_NV = 4;            // packs per thread: a group has ceil(packs / 128) warps
 constexpr int RING_MAX_GROUPS = 15;   // named barriers 1..15
 constexpr int RING_MAX_SLOTS = 8;
@@ -612,6 +619,79 @@ __device__ __forceinline__ float2 group_reduce(float a, uint32_t b, bool &ok, Ri
     return make_float2(a, __uint_as_float(b));
 }
 
+// Where a block's rows lie in their granules.
+template <class T, bool PH>
+struct RowSpan {
+    static constexpr int VEC = 16 / static_cast<int>(sizeof(T));
+    int phase, packs;
+    int64_t D, total;  // elements of a row, of all rows
+    __device__ RowSpan(int64_t M, int64_t d)
+        : phase(PH ? static_cast<int>((blockIdx.x % VEC) * (d % VEC) % VEC) : 0),
+          packs(static_cast<int>((phase + d + VEC - 1) / VEC)), D(d), total(M * d)
+    {
+    }
+    __device__ bool ragged(int c) const { return PH && (c == 0 || c == packs - 1); }
+    __device__ bool inside(int c, int i) const
+    {
+        const int k = c * VEC + i - phase;
+        return k >= 0 && k < D;
+    }
+    // Element 0 of the row's first granule, relative to the row's base address.
+    __device__ int64_t first(int64_t row) const { return row * D - phase; }
+    // Zero the granule's elements that belong to other rows.
+    __device__ void mask(Pack<T, VEC> &v, int c) const
+    {
+        if (ragged(c)) {
+            float f[VEC];
+            v.get(f);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                f[i] = inside(c, i) ? f[i] : 0.f;
+            v.set(f);
+        }
+    }
+    __device__ void store(T *rows, int64_t row, int c, const Pack<T, VEC> &v) const
+    {
+        T *o = rows + first(row) + static_cast<int64_t>(c) * VEC;
+        if (!ragged(c)) {
+            v.store(o);
+            return;
+        }
+        float f[VEC];
+        v.get(f);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            if (inside(c, i))
+                o[i] = from_f<T>(f[i]);
+    }
+    __device__ void store_codes(uint8_t *rows, int64_t row, int c, const float (&f)[VEC]) const
+    {
+        uint8_t *o = rows + first(row) + static_cast<int64_t>(c) * VEC;
+        if (!ragged(c)) {
+            store_e4m3<VEC>(o, f);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            if (inside(c, i))
+                o[i] = static_cast<uint8_t>(e4m3_pair(f[i], 0.f) & 0xffu);
+    }
+    // Fill a ring slot's input `k` from `rows` (the bytes are counted by the
+    // caller).  Granules that reach past the last row's end are not read there:
+    // their elements are copied one by one, before the slot's barrier is armed.
+    __device__ uint32_t bytes(int64_t row) const
+    {
+        const int64_t avail = total - first(row);
+        return 16u * static_cast<uint32_t>(PH && static_cast<int64_t>(packs) * VEC > avail ? packs - 1 : packs);
+    }
+    __device__ void copy_tail(T *slot, const T *rows, int64_t row) const
+    {
+        if (PH)
+            for (int64_t e = first(row) + bytes(row) / sizeof(T); e < total && e < first(row) + packs * VEC; ++e)
+                slot[e - first(row)] = rows[e];
+    }
+};
+
 // One group's ring: `inputs` rows (bulk copies) per slot.
 struct Ring {
     uint32_t slots_s, full_s;  // shared addresses: the group's slots, its barriers
@@ -633,15 +713,30 @@ struct Ring {
             mbar_init(full_s + 8u * s, 1);
         fence_mbar_init();
     }
-    __device__ void fill(int s, const void *a, const void *b, const void *c) const
+    // One thread: arm slot s and start the copies of row `row` (with a PH span,
+    // pitches are D).
+    template <class T, bool PH>
+    __device__ void fill(const RowSpan<T, PH> &span, int s, int64_t row, const T *a, int64_t lda, const T *b,
+                         int64_t ldb, const T *c, int64_t ldc) const
     {
-        const uint32_t bar = full_s + 8u * s, dst = slots_s + s * slot_bytes;
-        mbar_arrive_expect_tx(bar, slot_bytes);
-        bulk_load_g2s(dst, a, row_bytes, bar);
+        const uint32_t bar = full_s + 8u * s, dst = slots_s + s * slot_bytes, n = span.bytes(row);
+        if (PH) {
+            T *slot_p = reinterpret_cast<T *>(const_cast<uint8_t *>(slots) + s * slot_bytes);
+            const int gap = static_cast<int>(row_bytes / sizeof(T));
+            span.copy_tail(slot_p, a, row);
+            if (b)
+                span.copy_tail(slot_p + gap, b, row);
+            if (c)
+                span.copy_tail(slot_p + 2 * gap, c, row);
+        }
+        mbar_arrive_expect_tx(bar, n * (1u + (b ? 1u : 0u) + (c ? 1u : 0u)));
+        if (n == 0)
+            return;
+        bulk_load_g2s(dst, a + (PH ? span.first(row) : row * lda), n, bar);
         if (b)
-            bulk_load_g2s(dst + row_bytes, b, row_bytes, bar);
+            bulk_load_g2s(dst + row_bytes, b + (PH ? span.first(row) : row * ldb), n, bar);
         if (c)
-            bulk_load_g2s(dst + 2 * row_bytes, c, row_bytes, bar);
+            bulk_load_g2s(dst + 2 * row_bytes, c + (PH ? span.first(row) : row * ldc), n, bar);
     }
     __device__ const uint8_t *input(int i) const { return slots + slot * slot_bytes + i * row_bytes; }
     __device__ void advance()
@@ -653,19 +748,24 @@ struct Ring {
     }
 };
 
-// Copies the weights to shared memory; after it every thread sees them and the
-// groups' barriers.
-template <class W>
-__device__ __forceinline__ W *ring_weights(uint8_t *smem, const RingPlan &r, const W *w, int64_t D)
+// Copies the weights to shared memory, shifted by the block's phase (zeros
+// around them); after it every thread sees them and the groups' barriers.
+template <class W, bool PH, class Span>
+__device__ __forceinline__ W *ring_weights(uint8_t *smem, const RingPlan &r, const W *w, const Span &span)
 {
     W *ws = reinterpret_cast<W *>(smem + r.w_off);
-    for (int i = threadIdx.x; i < static_cast<int>(D * sizeof(W) / 16); i += blockDim.x)
-        reinterpret_cast<uint4 *>(ws)[i] = reinterpret_cast<const uint4 *>(w)[i];
+    if (PH) {
+        for (int k = threadIdx.x; k < span.packs * Span::VEC; k += blockDim.x)
+            ws[k] = k >= span.phase && k < span.phase + span.D ? w[k - span.phase] : from_f<W>(0.f);
+    } else {
+        for (int i = threadIdx.x; i < static_cast<int>(span.D * sizeof(W) / 16); i += blockDim.x)
+            reinterpret_cast<uint4 *>(ws)[i] = reinterpret_cast<const uint4 *>(w)[i];
+    }
     __syncthreads();
     return ws;
 }
 
-template <class T, class W, bool FP8>
+template <class T, class W, bool FP8, bool PH>
 __global__ void __launch_bounds__(1024) k_rms_norm_ring(const NormParams p, const RingPlan r)
 {
     constexpr int VEC = 16 / static_cast<int>(sizeof(T));
@@ -673,7 +773,8 @@ __global__ void __launch_bounds__(1024) k_rms_norm_ring(const NormParams p, cons
     __shared__ RingSync sy;
     const int group = threadIdx.x / r.group_threads, t = threadIdx.x % r.group_threads;
     const int warps = r.group_threads >> 5, first_warp = group * warps;
-    const int packs = static_cast<int>(p.D / VEC);
+    const RowSpan<T, PH> span(p.M, p.D);
+    const int packs = span.packs;
     const T *x = static_cast<const T *>(p.x);
     const T *res = static_cast<const T *>(p.residual);
     const int64_t step = static_cast<int64_t>(gridDim.x) * r.groups;
@@ -681,7 +782,7 @@ __global__ void __launch_bounds__(1024) k_rms_norm_ring(const NormParams p, cons
     const int64_t row0 = static_cast<int64_t>(group) * gridDim.x + blockIdx.x;
     Ring ring(r, smem, sy, group);
     const auto fill = [&](int slot, int64_t row) {
-        ring.fill(slot, x + row * p.ldx, res ? res + row * p.ldr : nullptr, nullptr);
+        ring.fill(span, slot, row, x, p.ldx, res, p.ldr, static_cast<const T *>(nullptr), 0);
     };
     if (t == 0) {
         ring.init();
@@ -689,7 +790,7 @@ __global__ void __launch_bounds__(1024) k_rms_norm_ring(const NormParams p, cons
         for (int i = p.limit.inject && blockIdx.x == 0 && group == 0 ? 1 : 0; i < r.slots && row0 + i * step < p.M; ++i)
             fill(i, row0 + i * step);
     }
-    const W *w = ring_weights<W>(smem, r, static_cast<const W *>(p.weight), p.D);
+    const W *w = ring_weights<W, PH>(smem, r, static_cast<const W *>(p.weight), span);
     bool ok = true;
     int buf = 0;
     for (int64_t row = row0; row < p.M; row += step, buf ^= 1) {
@@ -704,8 +805,9 @@ __global__ void __launch_bounds__(1024) k_rms_norm_ring(const NormParams p, cons
                 h[j] = load_pack<T, VEC>(reinterpret_cast<const T *>(ring.input(0)) + c * VEC);
                 if (res) {
                     h[j].add(load_pack<T, VEC>(reinterpret_cast<const T *>(ring.input(1)) + c * VEC));
-                    h[j].store(static_cast<T *>(p.h) + row * p.D + static_cast<int64_t>(c) * VEC);
+                    span.store(static_cast<T *>(p.h), row, c, h[j]);
                 }
+                span.mask(h[j], c);
 float v[VEC];
                 h[j].get(v);
 #pragma unroll
@@ -734,7 +836,6 @@ float v[VEC];
         for (int j = 0; j < RING_NV; ++j) {
             const int c = t + j * r.group_threads;
             if (c < packs) {
-                const int64_t o = row * p.D + static_cast<int64_t>(c) * VEC;
                 float f[VEC], wv[VEC];
                 h[j].get(f);
                 load_pack<W, VEC>(w + c * VEC).get(wv);
@@ -743,14 +844,14 @@ float v[VEC];
                     for (int i = 0; i < VEC; ++i)
                         f[i] *= wv[i];
                     rs.apply(f, rr);
-                    store_e4m3<VEC>(static_cast<uint8_t *>(p.y) + o, f);
+                    span.store_codes(static_cast<uint8_t *>(p.y), row, c, f);
                 } else {
 #pragma unroll
                     for (int i = 0; i < VEC; ++i)
                         f[i] *= rr * wv[i];
                     Pack<T, VEC> yv;
                     yv.set(f);
-                    yv.store(static_cast<T *>(p.y) + o);
+                    span.store(static_cast<T *>(p.y), row, c, yv);
                 }
             }
         }
@@ -766,7 +867,7 @@ float v[VEC];
 // weight gradient of its columns in registers over its group's rows, the block's
 // groups are added in order through shared memory, and the block writes one row
 // of `partial`.
-template <class T, class W, bool DH>
+template <class T, class W, bool DH, bool PH>
 __global__ void __launch_bounds__(512) k_rms_norm_bwd_ring(const NormBwdParams p, const RingPlan r)
 {
     constexpr int VEC = 16 / static_cast<int>(sizeof(T));
@@ -774,14 +875,15 @@ __global__ void __launch_bounds__(512) k_rms_norm_bwd_ring(const NormBwdParams p
     __shared__ RingSync sy;
     const int group = threadIdx.x / r.group_threads, t = threadIdx.x % r.group_threads;
     const int warps = r.group_threads >> 5, first_warp = group * warps;
-    const int packs = static_cast<int>(p.D / VEC);
+    const RowSpan<T, PH> span(p.M, p.D);
+    const int packs = span.packs;
     const T *hg = static_cast<const T *>(p.h), *yg = static_cast<const T *>(p.dy), *dg = static_cast<const T *>(p.dh);
     const float inv_d = 1.f / static_cast<float>(p.D);
     const int64_t step = static_cast<int64_t>(gridDim.x) * r.groups;
     const int64_t row0 = static_cast<int64_t>(group) * gridDim.x + blockIdx.x;
     Ring ring(r, smem, sy, group);
     const auto fill = [&](int slot, int64_t row) {
-        ring.fill(slot, hg + row * p.D, yg + row * p.D, DH ? dg + row * p.D : nullptr);
+        ring.fill(span, slot, row, hg, p.D, yg, p.D, DH ? dg : static_cast<const T *>(nullptr), p.D);
     };
     if (t == 0) {
         ring.init();
@@ -789,7 +891,7 @@ __global__ void __launch_bounds__(512) k_rms_norm_bwd_ring(const NormBwdParams p
         for (int i = p.limit.inject && blockIdx.x == 0 && group == 0 ? 1 : 0; i < r.slots && row0 + i * step < p.M; ++i)
             fill(i, row0 + i * step);
     }
-    const W *w = ring_weights<W>(smem, r, static_cast<const W *>(p.weight), p.D);
+    const W *w = ring_weights<W, PH>(smem, r, static_cast<const W *>(p.weight), span);
     float acc[RING_NV][VEC];
 #pragma unroll
     for (int j = 0; j < RING_NV; ++j)
@@ -808,6 +910,8 @@ __global__ void __launch_bounds__(512) k_rms_norm_bwd_ring(const NormBwdParams p
             if (c < packs) {
                 h[j] = load_pack<T, VEC>(reinterpret_cast<const T *>(ring.input(0)) + c * VEC);
                 dy[j] = load_pack<T, VEC>(reinterpret_cast<const T *>(ring.input(1)) + c * VEC);
+                span.mask(h[j], c);
+                span.mask(dy[j], c);
                 if (DH)
                     dh[DH ? j : 0] = load_pack<T, VEC>(reinterpret_cast<const T *>(ring.input(2)) + c * VEC);
                 float v[VEC], d[VEC], wv[VEC];
@@ -851,7 +955,7 @@ __global__ void __launch_bounds__(512) k_rms_norm_bwd_ring(const NormBwdParams p
                 }
                 Pack<T, VEC> dx;
                 dx.set(o);
-                dx.store(static_cast<T *>(p.dx) + row * p.D + static_cast<int64_t>(c) * VEC);
+                span.store(static_cast<T *>(p.dx), row, c, dx);
             }
         }
     }
@@ -876,7 +980,7 @@ __global__ void __launch_bounds__(512) k_rms_norm_bwd_ring(const NormBwdParams p
                     a.set(acc[j]);
                     if (g > 0)
                         a.add(load_pack<float, VEC>(dw + c * VEC));
-                    if (g + 1 < r.groups)
+                    if (PH || g + 1 < r.groups)
                         a.store(dw + c * VEC);
                     else
                         a.store(p.partial + static_cast<int64_t>(blockIdx.x) * p.D + c * VEC);
@@ -885,16 +989,20 @@ __global__ void __launch_bounds__(512) k_rms_norm_bwd_ring(const NormBwdParams p
         }
         __syncthreads();
     }
+    if (PH)
+        for (int c = threadIdx.x; c < p.D; c += blockDim.x)
+            p.partial[static_cast<int64_t>(blockIdx.x) * p.D + c] = dw[span.phase + c];
 }
 
 // A ring of `inputs` rows of D elements per slot, or false where a row is too
 // long for two slots.  At least two slots per group, then as many groups as the
 // threads and the shared memory allow, then more slots.
-bool plan_ring(RingPlan *r, int64_t D, int elem, int welem, int inputs, int max_threads)
+bool plan_ring(RingPlan *r, bool phased, int64_t D, int elem, int welem, int inputs, int max_threads)
 {
-    const int64_t packs = D * elem / 16;
-    const int64_t row_bytes = D * elem, slot = row_bytes * inputs;
-    const int64_t wbytes = (D * welem + 127) / 128 * 128;
+    const int64_t vec = 16 / elem;
+    const int64_t packs = phased ? (D + 2 * vec - 2) / vec : D / vec;  // at most
+    const int64_t row_bytes = packs * 16, slot = row_bytes * inputs;
+    const int64_t wbytes = (packs * vec * welem + 127) / 128 * 128;
     const int64_t gt = (packs + 32 * RING_NV - 1) / (32 * RING_NV) * 32;
     if (gt > max_threads || wbytes + 2 * slot > RING_BUDGET)
         return false;
@@ -928,6 +1036,11 @@ cudaError_t ring_opt_in(K kernel, std::atomic<unsigned long long> &done)
     return e;
 }
 
+// How a call's rows may be moved: 16-byte packs that start with every row; 16-byte
+// granules of contiguous rows of any length; or element by element.
+enum Rows { ROWS_VEC, ROWS_PHASED, ROWS_ANY };
+constexpr int64_t PHASED_MIN_D = 32;  // a row covers whole granules besides its two ragged ones
+
 // Threads per block for a row of `packs` packs, NV per thread.
 int threads_for(int64_t packs, int nv)
 {
@@ -936,10 +1049,9 @@ int threads_for(int64_t packs, int nv)
 }
 
 template <class T, class W, int VEC, bool FP8>
-bool launch_norm_regs(const NormParams &p, int num_sms, cudaStream_t s)
+bool launch_norm_regs(const NormParams &p, cudaStream_t s)
 {
     const int64_t packs = p.D / VEC;
-    (void)num_sms;
     const unsigned grid = static_cast<unsigned>(p.M < 0x7fffffff ? p.M : 0x7fffffff);
     int t;
     if ((t = threads_for(packs, 1)) && t <= 512)
@@ -955,29 +1067,36 @@ bool launch_norm_regs(const NormParams &p, int num_sms, cudaStream_t s)
     return true;
 }
 
+template <class T, class W, bool FP8, bool PH>
+cudaError_t launch_norm_ring(const NormParams &p, const RingPlan &r, int num_sms, cudaStream_t s)
+{
+    static std::atomic<unsigned long long> opted{0};
+    const cudaError_t e = ring_opt_in(k_rms_norm_ring<T, W, FP8, PH>, opted);
+    if (e != cudaSuccess)
+        return e;
+    k_rms_norm_ring<T, W, FP8, PH><<<num_sms / 8 * 8, r.groups * r.group_threads, r.bytes, s>>>(p, r);
+    return cudaGetLastError();
+}
+
 template <class T, class W, bool FP8>
-cudaError_t launch_norm_t(const NormParams &p, bool vec, int num_sms, cudaStream_t s)
+cudaError_t launch_norm_t(const NormParams &p, Rows rows, int num_sms, cudaStream_t s)
 {
     constexpr int V = 16 / static_cast<int>(sizeof(T));
     RingPlan r;
-    if (vec && p.M >= RING_MIN_ROWS && plan_ring(&r, p.D, sizeof(T), sizeof(W), p.residual ? 2 : 1, 1024)) {
-        static std::atomic<unsigned long long> opted{0};
-        const cudaError_t e = ring_opt_in(k_rms_norm_ring<T, W, FP8>, opted);
-        if (e != cudaSuccess)
-            return e;
-        k_rms_norm_ring<T, W, FP8><<<num_sms, r.groups * r.group_threads, r.bytes, s>>>(p, r);
-        return cudaGetLastError();
-    }
-    const bool done = vec ? launch_norm_regs<T, W, V, FP8>(p, num_sms, s) : launch_norm_regs<T, W, 1, FP8>(p, num_sms, s);
+    if (rows != ROWS_ANY && p.M >= RING_MIN_ROWS && num_sms >= 8 &&
+        plan_ring(&r, rows == ROWS_PHASED, p.D, sizeof(T), sizeof(W), p.residual ? 2 : 1, 1024))
+        return rows == ROWS_PHASED ? launch_norm_ring<T, W, FP8, true>(p, r, num_sms, s)
+                                   : launch_norm_ring<T, W, FP8, false>(p, r, num_sms, s);
+    const bool done = rows == ROWS_VEC ? launch_norm_regs<T, W, V, FP8>(p, s) : launch_norm_regs<T, W, 1, FP8>(p, s);
     if (!done)
         k_rms_norm_long<T, W, FP8><<<static_cast<unsigned>(p.M < 0x7fffffff ? p.M : 0x7fffffff), 1024, 0, s>>>(p);
     return cudaGetLastError();
 }
 
 template <class T, class W>
-cudaError_t launch_norm_tw(const NormParams &p, bool vec, bool fp8, int num_sms, cudaStream_t s)
+cudaError_t launch_norm_tw(const NormParams &p, Rows rows, bool fp8, int num_sms, cudaStream_t s)
 {
-    return fp8 ? launch_norm_t<T, W, true>(p, vec, num_sms, s) : launch_norm_t<T, W, false>(p, vec, num_sms, s);
+    return fp8 ? launch_norm_t<T, W, true>(p, rows, num_sms, s) : launch_norm_t<T, W, false>(p, rows, num_sms, s);
 }
 
 template <class T, class W, int VEC>
@@ -998,27 +1117,38 @@ bool launch_bwd_regs(const NormBwdParams &p, int grid, cudaStream_t s)
     return false;
 }
 
+template <class T, class W, bool DH, bool PH>
+cudaError_t launch_bwd_ring(const NormBwdParams &p, const RingPlan &r, int blocks, cudaStream_t s)
+{
+    static std::atomic<unsigned long long> opted{0};
+    const cudaError_t e = ring_opt_in(k_rms_norm_bwd_ring<T, W, DH, PH>, opted);
+    if (e != cudaSuccess)
+        return e;
+    k_rms_norm_bwd_ring<T, W, DH, PH><<<blocks, r.groups * r.group_threads, r.bytes, s>>>(p, r);
+    return cudaGetLastError();
+}
+
 template <class T, class W>
-cudaError_t launch_bwd_tw(const NormBwdParams &p, bool vec, void *dweight, int blocks, int num_sms, cudaStream_t s)
+cudaError_t launch_bwd_tw(const NormBwdParams &p, Rows rows, void *dweight, int num_sms, cudaStream_t s)
 {
     constexpr int V = 16 / static_cast<int>(sizeof(T));
+    int blocks = rms_norm_bwd_blocks(p.M);
+    cudaError_t e = cudaSuccess;
     RingPlan r;
-    if (vec && p.M >= RING_MIN_ROWS && num_sms <= blocks &&
-        plan_ring(&r, p.D, sizeof(T), sizeof(W), p.dh ? 3 : 2, 512)) {
-        static std::atomic<unsigned long long> opted[2];
-        cudaError_t e = ring_opt_in(k_rms_norm_bwd_ring<T, W, true>, opted[0]);
-        if (e == cudaSuccess)
-            e = ring_opt_in(k_rms_norm_bwd_ring<T, W, false>, opted[1]);
-        if (e != cudaSuccess)
-            return e;
-        blocks = num_sms;
-        if (p.dh)
-            k_rms_norm_bwd_ring<T, W, true><<<blocks, r.groups * r.group_threads, r.bytes, s>>>(p, r);
+    if (rows != ROWS_ANY && p.M >= RING_MIN_ROWS && num_sms >= 8 && num_sms <= blocks &&
+        plan_ring(&r, rows == ROWS_PHASED, p.D, sizeof(T), sizeof(W), p.dh ? 3 : 2, 512)) {
+        blocks = num_sms / 8 * 8;
+        if (rows == ROWS_PHASED)
+            e = p.dh ? launch_bwd_ring<T, W, true, true>(p, r, blocks, s)
+                     : launch_bwd_ring<T, W, false, true>(p, r, blocks, s);
         else
-            k_rms_norm_bwd_ring<T, W, false><<<blocks, r.groups * r.group_threads, r.bytes, s>>>(p, r);
-    } else if (!(vec ? launch_bwd_regs<T, W, V>(p, blocks, s) : launch_bwd_regs<T, W, 1>(p, blocks, s)))
-        k_rms_norm_bwd_long<T, W><<<blocks, 1024, 0, s>>>(p);
-    cudaError_t e = cudaGetLastError();
+            e = p.dh ? launch_bwd_ring<T, W, true, false>(p, r, blocks, s)
+                     : launch_bwd_ring<T, W, false, false>(p, r, blocks, s);
+    } else {
+        if (!(rows == ROWS_VEC ? launch_bwd_regs<T, W, V>(p, blocks, s) : launch_bwd_regs<T, W, 1>(p, blocks, s)))
+            k_rms_norm_bwd_long<T, W><<<blocks, 1024, 0, s>>>(p);
+        e = cudaGetLastError();
+    }
     if (e != cudaSuccess || !dweight)
         return e;
     k_rms_norm_dweight<W><<<static_cast<unsigned>((p.D + 31) / 32), dim3(32, DW_ROWS), 0, s>>>(
@@ -1034,15 +1164,17 @@ bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 cudaError_t launch_rms_norm(const NormParams &p, int dtype, int wdtype, bool fp8, int num_sms, cudaStream_t s)
 {
     const int64_t v = dtype == 2 ? 4 : 8;
-    const bool vec = p.D % v == 0 && p.ldx % v == 0 && al16(p.x) && al16(p.y) && al16(p.weight) &&
-                     (!p.residual || (p.ldr % v == 0 && al16(p.residual) && al16(p.h)));
+    const bool based = al16(p.x) && al16(p.y) && al16(p.weight) && (!p.residual || (al16(p.residual) && al16(p.h)));
+    const bool packed = p.D % v == 0 && p.ldx % v == 0 && (!p.residual || p.ldr % v == 0);
+    const bool contiguous = p.ldx == p.D && (!p.residual || p.ldr == p.D);
+    const Rows rows = !based ? ROWS_ANY : packed ? ROWS_VEC : contiguous && p.D >= PHASED_MIN_D ? ROWS_PHASED : ROWS_ANY;
     if (dtype == 0)
-        return wdtype == 0 ? launch_norm_tw<__nv_bfloat16, __nv_bfloat16>(p, vec, fp8, num_sms, s)
-                           : launch_norm_tw<__nv_bfloat16, float>(p, vec, fp8, num_sms, s);
+        return wdtype == 0 ? launch_norm_tw<__nv_bfloat16, __nv_bfloat16>(p, rows, fp8, num_sms, s)
+                           : launch_norm_tw<__nv_bfloat16, float>(p, rows, fp8, num_sms, s);
     if (dtype == 1)
-        return wdtype == 1 ? launch_norm_tw<__half, __half>(p, vec, fp8, num_sms, s)
-                           : launch_norm_tw<__half, float>(p, vec, fp8, num_sms, s);
-    return launch_norm_tw<float, float>(p, vec, fp8, num_sms, s);
+        return wdtype == 1 ? launch_norm_tw<__half, __half>(p, rows, fp8, num_sms, s)
+                           : launch_norm_tw<__half, float>(p, rows, fp8, num_sms, s);
+    return launch_norm_tw<float, float>(p, rows, fp8, num_sms, s);
 }
 
 int rms_norm_bwd_blocks(int64_t M) { return static_cast<int>(M < RMS_BWD_BLOCKS ? M : RMS_BWD_BLOCKS); }
@@ -1051,16 +1183,16 @@ cudaError_t launch_rms_norm_bwd(const NormBwdParams &p, void *dweight, int dtype
                                 cudaStream_t s)
 {
     const int64_t v = dtype == 2 ? 4 : 8;
-    const bool vec = p.D % v == 0 && al16(p.dy) && al16(p.h) && al16(p.weight) && al16(p.dx) &&
-                     (!p.dh || al16(p.dh)) && (!p.partial || al16(p.partial));
-    const int blocks = rms_norm_bwd_blocks(p.M);
+    const bool based = al16(p.dy) && al16(p.h) && al16(p.weight) && al16(p.dx) && (!p.dh || al16(p.dh)) &&
+                       (!p.partial || al16(p.partial));
+    const Rows rows = !based ? ROWS_ANY : p.D % v == 0 ? ROWS_VEC : p.D >= PHASED_MIN_D ? ROWS_PHASED : ROWS_ANY;
     if (dtype == 0)
-        return wdtype == 0 ? launch_bwd_tw<__nv_bfloat16, __nv_bfloat16>(p, vec, dweight, blocks, num_sms, s)
-                           : launch_bwd_tw<__nv_bfloat16, float>(p, vec, dweight, blocks, num_sms, s);
+        return wdtype == 0 ? launch_bwd_tw<__nv_bfloat16, __nv_bfloat16>(p, rows, dweight, num_sms, s)
+                           : launch_bwd_tw<__nv_bfloat16, float>(p, rows, dweight, num_sms, s);
     if (dtype == 1)
-        return wdtype == 1 ? launch_bwd_tw<__half, __half>(p, vec, dweight, blocks, num_sms, s)
-                           : launch_bwd_tw<__half, float>(p, vec, dweight, blocks, num_sms, s);
-    return launch_bwd_tw<float, float>(p, vec, dweight, blocks, num_sms, s);
+        return wdtype == 1 ? launch_bwd_tw<__half, __half>(p, rows, dweight, num_sms, s)
+                           : launch_bwd_tw<__half, float>(p, rows, dweight, num_sms, s);
+    return launch_bwd_tw<float, float>(p, rows, dweight, num_sms, s);
 }
 
 }  // namespace lf

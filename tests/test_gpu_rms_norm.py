@@ -106,7 +106,9 @@ def test_many_rows_and_leading_dimensions():
 
 # enough rows for the persistent kernels: one warp per row and many groups of them,
 # several warps, rows that leave room for one group only, rows too long for it
-MANY = [(609, 8), (1000, 136), (2500, 264), (700, 1032), (1300, 2056), (640, 5120), (613, 12296), (610, 20000)]
+MANY = [(609, 8), (1000, 136), (2500, 264), (700, 1032), (1300, 2056), (640, 5120), (613, 12296), (610, 20000),
+        # rows that are not a multiple of 16 bytes
+        (700, 33), (611, 37), (900, 250), (1333, 1027), (777, 1530), (650, 5121), (609, 9999), (608, 12301)]
 
 
 @pytest.mark.parametrize("M,D", MANY)
@@ -346,14 +348,14 @@ def test_no_rows():
 def test_outputs_stay_inside_their_buffers():
     """Every output lies between guard bands that must not change."""
     G = 4096
-    for M, D, dtype in ((3, 1027, BF16), (5, 264, FP16), (2, 1530, FP32), (1, 70000, BF16)):
+    for M, D, dtype in ((3, 1027, BF16), (5, 264, FP16), (2, 1530, FP32), (1, 70000, BF16), (700, 1027, BF16),
+                        (613, 53, FP16), (801, 131, FP32), (608, 264, BF16)):
         x, w, res = normal((M, D), 71, 1.0, dtype), 1 + normal((D,), 72, 0.2, dtype), normal((M, D), 73, 1.0, dtype)
         n = M * D
-        # offsets that keep the element's alignment but not always the vector's
         bufs = {k: torch.full((n + 2 * G,), 7.0, dtype=dtype, device=DEV) for k in ("h", "y", "dx")}
         view = {k: b[G:G + n].view(M, D) for k, b in bufs.items()}
         y, h, _ = lf.add_rms_norm(x.to(DEV), w.to(DEV), residual=res.to(DEV), eps=EPS, h=view["h"], y=view["y"])
-        dwb = torch.full((D + 2 * G,), 7.0, dtype=dtype, device=DEV)
+        dwb = torch.full((D + 2 * G,), 7.0, dtype=dtype, device=DEV)  # (G elements keep 16-byte alignment)
         lf.add_rms_norm_backward(res.to(DEV), h, w.to(DEV), eps=EPS, dx=view["dx"], dweight=dwb[G:G + D])
         torch.cuda.synchronize()
         for b, size in [(b, n) for b in bufs.values()] + [(dwb, D)]:
