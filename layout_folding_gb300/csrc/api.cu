@@ -1057,11 +1057,33 @@ static lf_status gated_launch(const void *x, const float *x_scale, const void *w
     const bool e4m3 = x_scale != nullptr;
     lf::GatedParams gp;
     std::memset(&gp, 0, sizeof gp);
-    CUtensorMap ta, tw, to, tg, tu;
-    const bool ok = (e4m3 ? make_tmap_e4m3(&ta, x, M, K, lf::BM) && make_tmap_e4m3(&tw, w, 2 * F, K, lf::BN / 2)
-                          : make_tmap(&ta, x, M, K, lf::BM) && make_tmap(&tw, w, 2 * F, K, lf::BN / 2)) &&
-                    make_tmap_out(&to, out, M, F, F, 1, M * F, false);
-    if (!ok)
+    lf::GemmParams &p = gp.g;
+    const int64_t kblock = e4m3 ? 128 : 64;
+    p.M = static_cast<int>(M);
+    p.N = static_cast<int>(F);
+    p.K = static_cast<int>(K);
+    p.out = out;
+    p.num_k_blocks = static_cast<int>((K + kblock - 1) / kblock);
+    p.num_n_blocks = static_cast<int>((F + lf::BN / 2 - 1) / (lf::BN / 2));
+    p.err = d->err_word;
+    p.timeout_ns = g_timeout_ns.load();
+    p.inject = g_inject.load();
+    gp.x_scale = x_scale;
+    gp.w_scale = w_scale;
+    gp.save = gu ? 1 : 0;
+    CUtensorMap ta, tw;
+    const auto operands = [&](uint32_t x_rows) {
+        return e4m3 ? make_tmap_e4m3(&ta, x, M, K, x_rows) && make_tmap_e4m3(&tw, w, 2 * F, K, lf::BN / 2)
+                    : make_tmap(&ta, x, M, K, x_rows) && make_tmap(&tw, w, 2 * F, K, lf::BN / 2);
+    };
+    if (M <= lf::BM) {
+        const lf::GatedSkinny plan = lf::plan_gated_skinny(M, F, p.num_k_blocks, d->num_sms);
+        if (!operands(static_cast<uint32_t>(plan.n)))
+            return LF_ERR_LAUNCH;
+        return launched(lf::launch_gated_skinny(e4m3, act, ta, tw, gp, plan, gu, stream), 1);
+    }
+    CUtensorMap to, tg, tu;
+    if (!operands(lf::BM) || !make_tmap_out(&to, out, M, F, F, 1, M * F, false))
         return LF_ERR_LAUNCH;
     tg = tu = to;
     if (gu) {
@@ -1070,18 +1092,8 @@ static lf_status gated_launch(const void *x, const float *x_scale, const void *w
             !make_tmap_out(&tu, static_cast<char *>(gu) + 2 * F, M, F, 2 * F, 1, 2 * M * F, false))
             return LF_ERR_LAUNCH;
     }
-    lf::GemmParams &p = gp.g;
-    const int64_t kblock = e4m3 ? 128 : 64;
-    p.M = static_cast<int>(M);
-    p.N = static_cast<int>(F);
-    p.K = static_cast<int>(K);
     p.num_m_blocks = static_cast<int>((M + 2 * lf::BM - 1) / (2 * lf::BM));
-    p.num_n_blocks = static_cast<int>((F + lf::BN / 2 - 1) / (lf::BN / 2));
-    p.num_k_blocks = static_cast<int>((K + kblock - 1) / kblock);
     p.num_tiles = p.num_m_blocks * p.num_n_blocks;
-    p.err = d->err_word;
-    p.timeout_ns = g_timeout_ns.load();
-    p.inject = g_inject.load();
     // bands of M blocks whose X rows stay in L2, as plan_gemm
     const double x_bytes = 2.0 * lf::BM * static_cast<double>(K) * (e4m3 ? 1.0 : 2.0);
     int band = static_cast<int>(BAND_X_BYTES / x_bytes);
@@ -1090,9 +1102,6 @@ static lf_status gated_launch(const void *x, const float *x_scale, const void *w
         const int nbands = (p.num_m_blocks + band - 1) / band;
         p.band_m = (p.num_m_blocks + nbands - 1) / nbands;
     }
-    gp.x_scale = x_scale;
-    gp.w_scale = w_scale;
-    gp.save = gu ? 1 : 0;
     const int grid = 2 * (p.num_tiles < d->pair_clusters ? p.num_tiles : d->pair_clusters);
     return launched(lf::launch_gated_pair(e4m3, act, ta, tw, to, tg, tu, gp, grid, stream), 1);
 }

@@ -404,6 +404,246 @@ cudaError_t launch_gated_pair_t(const CUtensorMap &ta, const CUtensorMap &tw, co
     return cudaLaunchKernelEx(&cfg, k_gated_pair<E4M3, ACT>, ta, tw, to, tg, tu, p);
 }
 
+// ---------------------------------------------------------------- few tokens
+// M <= 128 tokens: the weights' bytes bound the call, so the operands are
+// swapped -- 128 gate rows and 128 up rows of w are the A operands of two
+// 128 x n MMAs whose B operand is the tokens (n: M rounded up to 16) -- and a CTA
+// only streams its share of w through a ring of 32 KiB stages (plus the tokens'
+// slice).  With few tiles of 128 output columns the K blocks of a tile are split
+// over a cluster of 2, 4 or 8 CTAs: each leaves its fp32 sums in its own shared
+// memory, and after a cluster barrier every CTA adds, in rank order, its part of
+// the tokens from all of them.
+constexpr int S_THREADS = 192;     // producer, MMA, 4 epilogue warps
+constexpr int S_MAX_STAGES = 8;
+constexpr int S_W_BYTES = 2 * BM * G_ROW;
+constexpr int S_MISC = 1024 + (2 * S_MAX_STAGES + 1) * 8 + 32;  // alignment, barriers, TMEM address, abort flag
+constexpr int S_SMEM_ONE = 220 * 1024, S_SMEM_TWO = 113 * 1024;  // dynamic shared memory with one / two CTAs per SM
+
+template <bool E4M3, int ACT>
+__device__ __forceinline__ void s_finish(const GatedParams &gp, __nv_bfloat16 *gu, float g, float u, float wg, float wu,
+                                         int m, int f)
+{
+    const size_t F = static_cast<size_t>(gp.g.N);
+    if (E4M3) {
+        const float sx = gp.x_scale[m];
+        g *= sx * wg;
+        u *= sx * wu;
+    }
+    static_cast<__nv_bfloat16 *>(gp.g.out)[m * F + f] = __float2bfloat16_rn(g * act_phi<ACT>(g) * u);
+    if (!E4M3 && gu) {
+        gu[m * 2 * F + f] = __float2bfloat16_rn(g);
+        gu[m * 2 * F + F + f] = __float2bfloat16_rn(u);
+    }
+}
+
+template <bool E4M3, int ACT>
+__global__ void __launch_bounds__(S_THREADS, 2)
+    k_gated_skinny(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
+                   const __grid_constant__ GatedParams gp, const GatedSkinny plan, __nv_bfloat16 *gu)
+{
+    const GemmParams &p = gp.g;
+    constexpr int KELEMS = E4M3 ? 128 : 64;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *gbase = smem_raw + (base - raw);
+    const uint32_t x_bytes = static_cast<uint32_t>(plan.n) * G_ROW;
+    const uint32_t stage_bytes = S_W_BYTES + x_bytes;
+    const uint32_t bar0 = base + static_cast<uint32_t>(plan.stages) * stage_bytes;
+    const uint32_t done_bar = bar0 + 8u * (2 * S_MAX_STAGES);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + (done_bar + 8u - base));
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+#define FULL_BAR(s) (bar0 + 8u * (s))
+#define EMPTY_BAR(s) (bar0 + 8u * (S_MAX_STAGES + (s)))
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int split = plan.split;
+    const int rank = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int f0 = static_cast<int>(blockIdx.x) / split * G_F;
+    const int kb0 = static_cast<int>(static_cast<int64_t>(p.num_k_blocks) * rank / split);
+    const int kb1 = static_cast<int>(static_cast<int64_t>(p.num_k_blocks) * (rank + 1) / split);
+    uint32_t cols = 32;
+    while (cols < 2u * static_cast<uint32_t>(plan.n))
+        cols *= 2;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < plan.stages; ++s) {
+            mbar_init(FULL_BAR(s), 1);
+            mbar_init(EMPTY_BAR(s), 1);
+        }
+        mbar_init(done_bar, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), cols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!wait_bar(EMPTY_BAR(stage), phase ^ 1u, abort_flag, p, ERR_PRODUCER))
+                    break;
+                if (!(kb == kb0 && p.inject == 1 && blockIdx.x == 0)) {  // (test hook)
+                    const uint32_t dst = base + stage * stage_bytes;
+                    mbar_arrive_expect_tx(FULL_BAR(stage), stage_bytes);
+                    tma_load_2d(dst, &tmW, kb * KELEMS, f0, FULL_BAR(stage));
+                    tma_load_2d(dst + BM * G_ROW, &tmW, kb * KELEMS, p.N + f0, FULL_BAR(stage));
+                    tma_load_2d(dst + S_W_BYTES, &tmA, kb * KELEMS, 0, FULL_BAR(stage));
+                }
+                if (++stage == plan.stages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (*abort_flag) {  // let the copies in flight land
+                const uint64_t t0 = global_timer_ns();
+                while (global_timer_ns() - t0 < G_ABORT_SETTLE_NS) {
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            const uint32_t n = static_cast<uint32_t>(plan.n);
+            const uint32_t idesc = E4M3 ? idesc_e4m3_f32(BM, n) : idesc_bf16_f32(BM, n);
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!wait_bar(FULL_BAR(stage), phase, abort_flag, p, ERR_MMA_FULL))
+                    break;
+                tc_fence_after();
+                const uint32_t wg = base + stage * stage_bytes, wu = wg + BM * G_ROW, xs = wg + S_W_BYTES;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint64_t db = smem_desc_k128(xs + k * 32);
+                    const uint32_t accumulate = (kb != kb0 || k != 0) ? 1u : 0u;
+                    if (E4M3) {
+                        umma_f8(tmem_base, smem_desc_k128(wg + k * 32), db, idesc, accumulate);
+                        umma_f8(tmem_base + n, smem_desc_k128(wu + k * 32), db, idesc, accumulate);
+                    } else {
+                        umma_f16(tmem_base, smem_desc_k128(wg + k * 32), db, idesc, accumulate);
+                        umma_f16(tmem_base + n, smem_desc_k128(wu + k * 32), db, idesc, accumulate);
+                    }
+                }
+                umma_commit(EMPTY_BAR(stage));
+                if (++stage == plan.stages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            umma_commit(done_bar);  // also after an abort: what was issued drains
+            wait_bar_drain(done_bar, 0u, abort_flag, p);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------ epilogue: one output column per thread
+        const int q = warp & 3;
+        const int fl = q * 32 + lane, f = f0 + fl;
+        const bool ok = __all_sync(0xffffffffu, wait_bar(done_bar, 0u, abort_flag, p, ERR_EPI));
+        tc_fence_after();
+        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+        float wg = 1.f, wu = 1.f;
+        if (E4M3 && f < p.N) {
+            wg = gp.w_scale[f];
+            wu = gp.w_scale[p.N + f];
+        }
+        float *part = reinterpret_cast<float *>(gbase);  // the ring is idle: [2 M][128] sums
+        for (int c = 0; ok && c < p.M; c += 16) {
+            uint32_t g[16], u[16];
+            tmem_ld_32x32b_x16(taddr + static_cast<uint32_t>(c), g);
+            tmem_ld_32x32b_x16(taddr + static_cast<uint32_t>(plan.n + c), u);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                if (c + i < p.M) {
+                    if (split > 1) {
+                        part[(2 * (c + i)) * BM + fl] = __uint_as_float(g[i]);
+                        part[(2 * (c + i) + 1) * BM + fl] = __uint_as_float(u[i]);
+                    } else if (f < p.N) {
+                        s_finish<E4M3, ACT>(gp, gu, __uint_as_float(g[i]), __uint_as_float(u[i]), wg, wu, c + i, f);
+                    }
+                }
+            }
+        }
+        tc_fence_before();
+        __syncwarp();
+    }
+    if (split > 1) {
+        cluster_sync();  // every CTA's sums are in place
+        if (warp >= 2) {
+            const int fl = (warp & 3) * 32 + lane, f = f0 + fl;
+            float wg = 1.f, wu = 1.f;
+            if (E4M3 && f < p.N) {
+                wg = gp.w_scale[f];
+                wu = gp.w_scale[p.N + f];
+            }
+            const int m1 = p.M * (rank + 1) / split;
+            for (int m = p.M * rank / split; m < m1; ++m) {
+                float g = 0.f, u = 0.f;
+                for (int r = 0; r < split; ++r) {
+                    const uint32_t a = mapa_shared(base + static_cast<uint32_t>((2 * m * BM + fl) * 4), r);
+                    g += ld_cluster_f32(a);
+                    u += ld_cluster_f32(a + BM * 4);
+                }
+                if (f < p.N)
+                    s_finish<E4M3, ACT>(gp, gu, g, u, wg, wu, m, f);
+            }
+            __syncwarp();
+        }
+        cluster_sync();  // no CTA leaves while a peer reads its sums
+    } else {
+        __syncthreads();
+    }
+#undef FULL_BAR
+#undef EMPTY_BAR
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, cols);
+    }
+}
+
+template <bool E4M3, int ACT>
+cudaError_t launch_gated_skinny_t(const CUtensorMap &ta, const CUtensorMap &tw, const GatedParams &p,
+                                  const GatedSkinny &plan, void *gu, cudaStream_t s)
+{
+    static std::atomic<unsigned long long> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(done.load() & bit)) {
+        e = cudaFuncSetAttribute(k_gated_skinny<E4M3, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S_SMEM_ONE);
+        if (e != cudaSuccess)
+            return e;
+        done.fetch_or(bit);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.g.num_n_blocks * plan.split), 1, 1);
+    cfg.blockDim = dim3(S_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(plan.smem);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(plan.split);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = plan.split > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, k_gated_skinny<E4M3, ACT>, ta, tw, p, plan, static_cast<__nv_bfloat16 *>(gu));
+}
+
 // ---------------------------------------------------------------- gradient
 // dgu = [dout u act'(g), dout act(g)] from the kept pre-activations gu = [g, u]:
 // 8 columns per thread and step, 6 bytes read and 4 written per column.
@@ -455,6 +695,44 @@ cudaError_t launch_gated_pair(bool e4m3, int act, const CUtensorMap &ta, const C
         return launch_gated_pair_t<true, ACT_GELU>(ta, tw, to, tg, tu, p, grid, s);
     case 3 + ACT_GELU_TANH:
         return launch_gated_pair_t<true, ACT_GELU_TANH>(ta, tw, to, tg, tu, p, grid, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+GatedSkinny plan_gated_skinny(int64_t M, int64_t F, int num_k_blocks, int num_sms)
+{
+    GatedSkinny g;
+    g.n = static_cast<int>((M + 15) / 16 * 16);
+    const int64_t tiles = (F + G_F - 1) / G_F;
+    // two CTAs per SM while the split's sums (2 M x 128 fp32) fit half an SM
+    const bool two = g.n <= 64;
+    const int64_t room = static_cast<int64_t>(num_sms) * (two ? 2 : 1);
+    g.split = 1;
+    while (g.split < 8 && tiles * g.split * 2 <= room && num_k_blocks / (g.split * 2) >= 4)
+        g.split *= 2;
+    const int stage = S_W_BYTES + g.n * G_ROW;
+    const int fit = ((two ? S_SMEM_TWO : S_SMEM_ONE) - S_MISC) / stage;
+    g.stages = fit < S_MAX_STAGES ? fit : S_MAX_STAGES;
+    g.smem = S_MISC + g.stages * stage;
+    return g;
+}
+
+cudaError_t launch_gated_skinny(bool e4m3, int act, const CUtensorMap &ta, const CUtensorMap &tw, const GatedParams &p,
+                                const GatedSkinny &plan, void *gu, cudaStream_t s)
+{
+    switch (act + (e4m3 ? 3 : 0)) {
+    case ACT_SILU:
+        return launch_gated_skinny_t<false, ACT_SILU>(ta, tw, p, plan, gu, s);
+    case ACT_GELU:
+        return launch_gated_skinny_t<false, ACT_GELU>(ta, tw, p, plan, gu, s);
+    case ACT_GELU_TANH:
+        return launch_gated_skinny_t<false, ACT_GELU_TANH>(ta, tw, p, plan, gu, s);
+    case 3 + ACT_SILU:
+        return launch_gated_skinny_t<true, ACT_SILU>(ta, tw, p, plan, gu, s);
+    case 3 + ACT_GELU:
+        return launch_gated_skinny_t<true, ACT_GELU>(ta, tw, p, plan, gu, s);
+    case 3 + ACT_GELU_TANH:
+        return launch_gated_skinny_t<true, ACT_GELU_TANH>(ta, tw, p, plan, gu, s);
     }
     return cudaErrorInvalidValue;
 }

@@ -108,6 +108,18 @@ struct GatedParams {
 cudaError_t launch_gated_pair(bool e4m3, int act, const CUtensorMap &ta, const CUtensorMap &tw, const CUtensorMap &to,
                               const CUtensorMap &tg, const CUtensorMap &tu, const GatedParams &p, int grid,
                               cudaStream_t s);
+// The same for M <= 128 tokens (operands swapped, the K loop split over clusters).
+struct GatedSkinny {
+    int n;       // the MMA's N: M rounded up to 16
+    int split;   // CTAs per cluster, each with its share of the K blocks: 1, 2, 4 or 8
+    int stages;  // ring stages
+    int smem;    // dynamic shared memory per CTA
+};
+// How a call with M tokens (1..128) runs; num_k_blocks counts 128-byte K blocks.
+GatedSkinny plan_gated_skinny(int64_t M, int64_t F, int num_k_blocks, int num_sms);
+// ta: x, boxes of plan.n rows; tw as above.  gu may be null.
+cudaError_t launch_gated_skinny(bool e4m3, int act, const CUtensorMap &ta, const CUtensorMap &tw, const GatedParams &p,
+                                const GatedSkinny &plan, void *gu, cudaStream_t s);
 // dgu = [dout u act'(g), dout act(g)] from gu = [g, u]; F % 8 == 0, 16-byte aligned.
 cudaError_t launch_gated_bwd(int act, const void *dout, const void *gu, void *dgu, int64_t M, int64_t F, int num_sms,
                              cudaStream_t s);

@@ -84,7 +84,9 @@ def check_backward(dout, x, w, gu, name, dx, dw):
 
 SHAPES = [(1, 8, 8), (1, 1416, 520), (2, 128, 64), (3, 136, 72), (17, 264, 1032), (64, 520, 2048), (127, 8, 256),
           (128, 128, 128), (129, 392, 136), (200, 1416, 520), (256, 256, 64), (257, 248, 1000), (520, 1000, 264),
-          (1030, 136, 192)]
+          (1030, 136, 192),
+          # few tokens: whole K loops and K loops split over 2, 4 and 8 CTAs, one and two CTAs per SM
+          (5, 40000, 256), (33, 9000, 520), (16, 4104, 1024), (65, 2056, 2048), (100, 20000, 136), (113, 520, 2048)]
 
 
 @pytest.mark.parametrize("M,F,K", SHAPES)
@@ -105,7 +107,8 @@ def quantised(t):
 
 
 @pytest.mark.parametrize("M,F,K", [(1, 8, 16), (1, 1416, 528), (3, 136, 80), (48, 520, 2048), (128, 128, 128),
-                                   (129, 392, 144), (300, 1000, 272), (1030, 136, 192)])
+                                   (129, 392, 144), (300, 1000, 272), (1030, 136, 192), (5, 20000, 256),
+                                   (33, 4104, 1040), (65, 2056, 4096), (113, 520, 4096)])
 def test_forward_e4m3(M, F, K):
     x, xs = quantised(normal((M, K), 5) * torch.exp(normal((M, 1), 6)))
     w, ws = quantised(normal((2 * F, K), 7, 1 / math.sqrt(K)))
