@@ -419,20 +419,24 @@ constexpr int S_W_BYTES = 2 * BM * G_ROW;
 constexpr int S_MISC = 1024 + (2 * S_MAX_STAGES + 1) * 8 + 32;  // alignment, barriers, TMEM address, abort flag
 constexpr int S_SMEM_ONE = 220 * 1024, S_SMEM_TWO = 113 * 1024;  // dynamic shared memory with one / two CTAs per SM
 
+// Output columns f .. f + 3 of token m from its sums g and u.
 template <bool E4M3, int ACT>
-__device__ __forceinline__ void s_finish(const GatedParams &gp, __nv_bfloat16 *gu, float g, float u, float wg, float wu,
-                                         int m, int f)
+__device__ __forceinline__ void s_finish(const GatedParams &gp, __nv_bfloat16 *gu, float4 g, float4 u, int m, int f)
 {
     const size_t F = static_cast<size_t>(gp.g.N);
     if (E4M3) {
         const float sx = gp.x_scale[m];
-        g *= sx * wg;
-        u *= sx * wu;
+        const float4 wg = *reinterpret_cast<const float4 *>(gp.w_scale + f);
+        const float4 wu = *reinterpret_cast<const float4 *>(gp.w_scale + F + f);
+        g = make_float4(g.x * (sx * wg.x), g.y * (sx * wg.y), g.z * (sx * wg.z), g.w * (sx * wg.w));
+        u = make_float4(u.x * (sx * wu.x), u.y * (sx * wu.y), u.z * (sx * wu.z), u.w * (sx * wu.w));
     }
-    static_cast<__nv_bfloat16 *>(gp.g.out)[m * F + f] = __float2bfloat16_rn(g * act_phi<ACT>(g) * u);
+    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(gp.g.out) + m * F + f) =
+        make_uint2(pack_bf16(g.x * act_phi<ACT>(g.x) * u.x, g.y * act_phi<ACT>(g.y) * u.y),
+                   pack_bf16(g.z * act_phi<ACT>(g.z) * u.z, g.w * act_phi<ACT>(g.w) * u.w));
     if (!E4M3 && gu) {
-        gu[m * 2 * F + f] = __float2bfloat16_rn(g);
-        gu[m * 2 * F + F + f] = __float2bfloat16_rn(u);
+        *reinterpret_cast<uint2 *>(gu + m * 2 * F + f) = make_uint2(pack_bf16(g.x, g.y), pack_bf16(g.z, g.w));
+        *reinterpret_cast<uint2 *>(gu + m * 2 * F + F + f) = make_uint2(pack_bf16(u.x, u.y), pack_bf16(u.z, u.w));
     }
 }
 
@@ -547,18 +551,12 @@ __global__ void __launch_bounds__(S_THREADS, 2)
         }
         __syncwarp();
     } else {
-        // ------------------------------------------------ epilogue: one output column per thread
+        // ------------------------------------------------ sums to shared memory, one output column per thread
         const int q = warp & 3;
-        const int fl = q * 32 + lane, f = f0 + fl;
         const bool ok = __all_sync(0xffffffffu, wait_bar(done_bar, 0u, abort_flag, p, ERR_EPI));
         tc_fence_after();
         const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
-        float wg = 1.f, wu = 1.f;
-        if (E4M3 && f < p.N) {
-            wg = gp.w_scale[f];
-            wu = gp.w_scale[p.N + f];
-        }
-        float *part = reinterpret_cast<float *>(gbase);  // the ring is idle: [2 M][128] sums
+        float *part = reinterpret_cast<float *>(gbase) + q * 32 + lane;  // the ring is idle: [2 M][128] sums
         for (int c = 0; ok && c < p.M; c += 16) {
             uint32_t g[16], u[16];
             tmem_ld_32x32b_x16(taddr + static_cast<uint32_t>(c), g);
@@ -567,44 +565,41 @@ __global__ void __launch_bounds__(S_THREADS, 2)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 if (c + i < p.M) {
-                    if (split > 1) {
-                        part[(2 * (c + i)) * BM + fl] = __uint_as_float(g[i]);
-                        part[(2 * (c + i) + 1) * BM + fl] = __uint_as_float(u[i]);
-                    } else if (f < p.N) {
-                        s_finish<E4M3, ACT>(gp, gu, __uint_as_float(g[i]), __uint_as_float(u[i]), wg, wu, c + i, f);
-                    }
+                    part[(2 * (c + i)) * BM] = __uint_as_float(g[i]);
+                    part[(2 * (c + i) + 1) * BM] = __uint_as_float(u[i]);
                 }
             }
         }
         tc_fence_before();
         __syncwarp();
     }
-    if (split > 1) {
-        cluster_sync();  // every CTA's sums are in place
-        if (warp >= 2) {
-            const int fl = (warp & 3) * 32 + lane, f = f0 + fl;
-            float wg = 1.f, wu = 1.f;
-            if (E4M3 && f < p.N) {
-                wg = gp.w_scale[f];
-                wu = gp.w_scale[p.N + f];
-            }
-            const int m1 = p.M * (rank + 1) / split;
-            for (int m = p.M * rank / split; m < m1; ++m) {
-                float g = 0.f, u = 0.f;
-                for (int r = 0; r < split; ++r) {
-                    const uint32_t a = mapa_shared(base + static_cast<uint32_t>((2 * m * BM + fl) * 4), r);
-                    g += ld_cluster_f32(a);
-                    u += ld_cluster_f32(a + BM * 4);
-                }
-                if (f < p.N)
-                    s_finish<E4M3, ACT>(gp, gu, g, u, wg, wu, m, f);
-            }
-            __syncwarp();
-        }
-        cluster_sync();  // no CTA leaves while a peer reads its sums
-    } else {
+    // Every CTA's sums are in place: this one finishes its share of the tokens,
+    // one token per warp at a time, four output columns per lane.
+    if (split > 1)
+        cluster_sync();
+    else
         __syncthreads();
+    {
+        const int f = f0 + 4 * lane;
+        const int m1 = p.M * (rank + 1) / split;
+#pragma unroll 2
+        for (int m = p.M * rank / split + warp; m < m1; m += S_THREADS / 32) {
+            const uint32_t a = base + static_cast<uint32_t>((2 * m * BM + 4 * lane) * 4);
+            float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
+#pragma unroll 4
+            for (int r = 0; r < split; ++r) {
+                const uint32_t ar = split > 1 ? mapa_shared(a, static_cast<uint32_t>(r)) : a;
+                const float4 dg = ld_cluster_f32x4(ar), du = ld_cluster_f32x4(ar + BM * 4);
+                g = make_float4(g.x + dg.x, g.y + dg.y, g.z + dg.z, g.w + dg.w);
+                u = make_float4(u.x + du.x, u.y + du.y, u.z + du.z, u.w + du.w);
+            }
+            if (f < p.N)  // N % 8 == 0
+                s_finish<E4M3, ACT>(gp, gu, g, u, m, f);
+        }
+        __syncwarp();
     }
+    if (split > 1)
+        cluster_sync();  // no CTA leaves while a peer reads its sums
 #undef FULL_BAR
 #undef EMPTY_BAR
     if (warp == 1) {
@@ -704,11 +699,14 @@ GatedSkinny plan_gated_skinny(int64_t M, int64_t F, int num_k_blocks, int num_sm
     GatedSkinny g;
     g.n = static_cast<int>((M + 15) / 16 * 16);
     const int64_t tiles = (F + G_F - 1) / G_F;
-    // two CTAs per SM while the split's sums (2 M x 128 fp32) fit half an SM
-    const bool two = g.n <= 64;
-    const int64_t room = static_cast<int64_t>(num_sms) * (two ? 2 : 1);
+    // One CTA per SM with a deep ring, and the largest split that keeps it so
+    // (5120 x 13824, 48 tokens, 108 tiles: 48.6 us unsplit, 50.6 us split in two
+    // with two CTAs per SM; 2048 x 5632, 64 tokens, 44 tiles: 14.8 us split in
+    // two, 16.7 us in four with two CTAs per SM).  More tiles than SMs: two CTAs
+    // per SM while the sums of 64 tokens fit half an SM's ring.
+    const bool two = g.n <= 64 && tiles > num_sms;
     g.split = 1;
-    while (g.split < 8 && tiles * g.split * 2 <= room && num_k_blocks / (g.split * 2) >= 4)
+    while (g.split < 8 && tiles * g.split * 2 <= num_sms && num_k_blocks / (g.split * 2) >= 4)
         g.split *= 2;
     const int stage = S_W_BYTES + g.n * G_ROW;
     const int fit = ((two ? S_SMEM_TWO : S_SMEM_ONE) - S_MISC) / stage;
