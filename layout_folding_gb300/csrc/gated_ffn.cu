@@ -21,11 +21,15 @@ namespace {
 
 constexpr int G_M = 2 * BM;                // 256 rows of x per pair tile
 constexpr int G_F = BN / 2;                // 128 output columns per pair tile
-constexpr int G_STAGES = 6;                // ring slots of one K block (128 bytes of K)
+// The ring: G_SLOTS slots of one K block (128 bytes of K), G_KSUB consecutive
+// slots per stage -- one wait, one commit and one barrier arm per two K blocks.
+constexpr int G_SLOTS = 6;
+constexpr int G_KSUB = 2;
+constexpr int G_STAGES = G_SLOTS / G_KSUB;
 constexpr int G_ROW = 128;                 // bytes of K per row and block
 constexpr int G_A_BYTES = BM * G_ROW;      // this CTA's 128 rows of x
 constexpr int G_B_BYTES = G_F * G_ROW;     // this CTA's 128 rows of w (gate in the leader, up in its peer)
-constexpr int G_STAGE_BYTES = G_A_BYTES + G_B_BYTES;
+constexpr int G_SLOT_BYTES = G_A_BYTES + G_B_BYTES;
 constexpr int G_ACC_BUFS = 2;
 constexpr int G_TMEM_COLS = G_ACC_BUFS * BN;
 constexpr int G_NUM_BARS = 2 * G_STAGES + 2 * G_ACC_BUFS + 1;
@@ -33,7 +37,7 @@ constexpr int G_EPI_WARPS = 8;
 constexpr int G_THREADS = 64 + 32 * G_EPI_WARPS;
 constexpr int G_STG_SLOT = 32 * 64;        // 32 rows x 32 bf16 columns
 constexpr int G_STG_WARP = 2 * G_STG_SLOT;
-constexpr int G_STG_OFF = ((G_STAGES * G_STAGE_BYTES + G_NUM_BARS * 8 + 16 + 1023) / 1024) * 1024;
+constexpr int G_STG_OFF = ((G_SLOTS * G_SLOT_BYTES + G_NUM_BARS * 8 + 16 + 1023) / 1024) * 1024;
 constexpr int G_SMEM = 1024 + G_STG_OFF + G_EPI_WARPS * G_STG_WARP;
 static_assert(G_SMEM <= 232448, "shared memory per CTA");
 constexpr uint64_t G_ABORT_SETTLE_NS = 100000;
@@ -182,10 +186,10 @@ __global__ void __launch_bounds__(G_THREADS, 1)
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *gbase = smem_raw + (base - raw);
     const uint32_t sA = base;
-    const uint32_t sB = base + G_STAGES * G_A_BYTES;
-    const uint32_t bar0 = base + G_STAGES * G_STAGE_BYTES;
+    const uint32_t sB = base + G_SLOTS * G_A_BYTES;
+    const uint32_t bar0 = base + G_SLOTS * G_SLOT_BYTES;
     const uint32_t drain_bar = bar0 + 8u * (2 * G_STAGES + 2 * G_ACC_BUFS);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + G_STAGES * G_STAGE_BYTES + G_NUM_BARS * 8);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + G_SLOTS * G_SLOT_BYTES + G_NUM_BARS * 8);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 #define FULL_BAR(s) (bar0 + 8u * (s))
 #define EMPTY_BAR(s) (bar0 + 8u * (G_STAGES + (s)))
@@ -244,7 +248,8 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                 const int arow = mb * G_M + static_cast<int>(rank) * BM;
                 // gate rows in the leader, up rows in its peer
                 const int brow = static_cast<int>(rank) * p.N + nb * G_F;
-                for (int kb = 0; kb < p.num_k_blocks; ++kb) {
+                for (int kb = 0; kb < p.num_k_blocks; kb += G_KSUB) {
+                    const int nsub = min(G_KSUB, p.num_k_blocks - kb);
                     if (!wait_bar(EMPTY_BAR(stage), phase ^ 1u, abort_flag, p, ERR_PRODUCER, peer_abort)) {
                         ok = false;
                         break;
@@ -254,11 +259,17 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                     first = false;
                     if (!skip) {
                         if (leader) {
-                            mbar_arrive_expect_tx(FULL_BAR(stage), 2u * G_STAGE_BYTES);
+                            mbar_arrive_expect_tx(FULL_BAR(stage), 2u * G_SLOT_BYTES * static_cast<uint32_t>(nsub));
                             ++armed[stage];
                         }
-                        tma_load_2d_pair(sA + stage * G_A_BYTES, &tmA, kb * KELEMS, arow, full_leader);
-                        tma_load_2d_pair(sB + stage * G_B_BYTES, &tmW, kb * KELEMS, brow, full_leader);
+#pragma unroll
+                        for (int j = 0; j < G_KSUB; ++j) {
+                            if (j >= nsub)
+                                break;
+                            const uint32_t slot = static_cast<uint32_t>(stage * G_KSUB + j);
+                            tma_load_2d_pair(sA + slot * G_A_BYTES, &tmA, (kb + j) * KELEMS, arow, full_leader);
+                            tma_load_2d_pair(sB + slot * G_B_BYTES, &tmW, (kb + j) * KELEMS, brow, full_leader);
+                        }
                     }
                     if (++stage == G_STAGES) {
                         stage = 0;
@@ -284,22 +295,28 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                     break;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
-                for (int kb = 0; kb < p.num_k_blocks; ++kb) {
+                for (int kb = 0; kb < p.num_k_blocks; kb += G_KSUB) {
+                    const int nsub = min(G_KSUB, p.num_k_blocks - kb);
                     if (!wait_bar(FULL_BAR(stage), phase, abort_flag, p, ERR_MMA_FULL, peer_abort)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t a0 = sA + stage * G_A_BYTES;
-                    const uint32_t b0 = sB + stage * G_B_BYTES;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {  // 32 bytes of K per MMA
-                        const uint64_t da = smem_desc_k128(a0 + k * 32), db = smem_desc_k128(b0 + k * 32);
-                        const uint32_t accumulate = (kb | k) != 0 ? 1u : 0u;
-                        if (E4M3)
-                            umma_f8_pair(d_tmem, da, db, idesc, accumulate);
-                        else
-                            umma_f16_pair(d_tmem, da, db, idesc, accumulate);
+                    for (int j = 0; j < G_KSUB; ++j) {
+                        if (j >= nsub)
+                            break;
+                        const uint32_t a0 = sA + (stage * G_KSUB + j) * G_A_BYTES;
+                        const uint32_t b0 = sB + (stage * G_KSUB + j) * G_B_BYTES;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {  // 32 bytes of K per MMA
+                            const uint64_t da = smem_desc_k128(a0 + k * 32), db = smem_desc_k128(b0 + k * 32);
+                            const uint32_t accumulate = (kb | j | k) != 0 ? 1u : 0u;
+                            if (E4M3)
+                                umma_f8_pair(d_tmem, da, db, idesc, accumulate);
+                            else
+                                umma_f16_pair(d_tmem, da, db, idesc, accumulate);
+                        }
                     }
                     umma_commit_pair_mc(EMPTY_BAR(stage), 0x3);
                     if (++stage == G_STAGES) {
