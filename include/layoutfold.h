@@ -463,13 +463,20 @@ lf_status gated_ffn_e4m3(const void *x, const float *x_scale, const void *w, con
  *   dgu  : bf16 [M,2F], written (the products read it, so it is rounded to bf16
  *          once); may be the same buffer as gu.
  *   dx_or_null : bf16 [M,K] or NULL;  dw_or_null : bf16 [2F,K] or NULL.
+ *   scratch : gated_ffn_backward_scratch(M, F, K) bytes, 16-byte aligned, device,
+ *          owned by the caller, contents arbitrary; NULL is allowed when that is 0.
  * Sizes and alignment as gated_ffn; outputs otherwise overlap nothing.  One
- * launch for dgu and one for each of dx and dw, which may use the stream-K
- * split and its workspace, ordered across streams as gemm_nt's.
+ * launch for dgu and one for both products, whose tiles share the CTA pairs; a
+ * product with few tiles has its sum split, the parts kept in scratch in fp32 and
+ * added in a fixed order by a third launch.  Two calls on the same inputs give the
+ * same bits, and one product is the same with and without the other.
  */
 lf_status gated_ffn_backward(const void *dout, const void *x, const void *w, const void *gu, int act, void *dgu,
-                             void *dx_or_null, void *dw_or_null, int64_t M, int64_t F, int64_t K,
+                             void *dx_or_null, void *dw_or_null, void *scratch, int64_t M, int64_t F, int64_t K,
                              cudaStream_t stream);
+
+/* Bytes of scratch that gated_ffn_backward may need (0: none, or sizes out of range). */
+int64_t gated_ffn_backward_scratch(int64_t M, int64_t F, int64_t K);
 
 /* Human-readable name of a status code (static storage, never NULL). */
 const char *lf_status_string(lf_status status);

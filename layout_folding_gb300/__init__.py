@@ -113,7 +113,9 @@ def lib():
         L.gated_ffn.restype = I32
         L.gated_ffn_e4m3.argtypes = [P, P, P, P, I32, P, I64, I64, I64, P]
         L.gated_ffn_e4m3.restype = I32
-        L.gated_ffn_backward.argtypes = [P, P, P, P, I32, P, P, P, I64, I64, I64, P]
+        L.gated_ffn_backward.argtypes = [P, P, P, P, I32, P, P, P, P, I64, I64, I64, P]
+        L.gated_ffn_backward_scratch.argtypes = [I64, I64, I64]
+        L.gated_ffn_backward_scratch.restype = I64
         L.gated_ffn_backward.restype = I32
         _lib = L
         return L

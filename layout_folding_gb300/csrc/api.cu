@@ -1133,8 +1133,24 @@ static lf_status gated_ffn_e4m3_call(const void *x, const float *x_scale, const 
     return gated_launch(x, x_scale, w, w_scale, act, out, nullptr, M, F, K, stream);
 }
 
+// `split` fp32 matrices [M, N] one after another (N % 4 == 0), as a TMA map: 32 x
+// 32 x 1 boxes with the 128-byte swizzle.
+static bool make_tmap_parts(CUtensorMap *m, float *ptr, int64_t M, int64_t N, int64_t split)
+{
+    EncodeTiledFn enc = encode_fn();
+    if (!enc)
+        return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(M), static_cast<cuuint64_t>(split)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(N) * 4, static_cast<cuuint64_t>(M * N) * 4};
+    const cuuint32_t box[3] = {32, 32, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, ptr, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 static lf_status gated_ffn_backward_call(const void *dout, const void *x, const void *w, const void *gu, int act,
-                                         void *dgu, void *dx, void *dw, int64_t M, int64_t F, int64_t K,
+                                         void *dgu, void *dx, void *dw, void *scratch, int64_t M, int64_t F, int64_t K,
                                          cudaStream_t stream)
 {
     if (!dout || !x || !w || !gu || !dgu)
@@ -1142,21 +1158,53 @@ static lf_status gated_ffn_backward_call(const void *dout, const void *x, const 
     lf_status st = check_gated_shape(M, F, K, act);
     if (st == LF_OK)
         st = check_gemm_shape(2 * F, K, M);
+    if (st == LF_OK)
+        st = check_gemm_shape(M, K, 2 * F);
     if (st != LF_OK)
         return st;
     if (!aligned16(dout) || !aligned16(x) || !aligned16(w) || !aligned16(gu) || !aligned16(dgu) ||
-        (dx && !aligned16(dx)) || (dw && !aligned16(dw)) || F % 8 != 0 || K % 8 != 0)
+        (dx && !aligned16(dx)) || (dw && !aligned16(dw)) || !aligned16(scratch) || F % 8 != 0 || K % 8 != 0)
         return LF_ERR_ALIGN;
+    lf::GradsParams p;
+    std::memset(&p, 0, sizeof p);
+    lf::plan_gated_grads(&p, dx != nullptr, dw != nullptr, M, F, K, lf::GRAD_PLAN_PAIRS);
+    if (p.part_floats > 0 && !scratch)
+        return LF_ERR_NULL;
     DeviceState *d = nullptr;
     if ((st = current_device(&d)) != LF_OK)
         return st;
-    if ((st = launched(lf::launch_gated_bwd(act, dout, gu, dgu, M, F, d->num_sms, stream), 1)) != LF_OK)
+    if (d->pair_clusters <= 0)
+        return LF_ERR_LAUNCH;
+    float *parts = static_cast<float *>(scratch);
+    p.wait.err = d->err_word;
+    p.wait.timeout_ns = g_timeout_ns.load();
+    p.wait.inject = g_inject.load();
+    lf::GradMaps maps;
+    std::memset(&maps, 0, sizeof maps);
+    const auto mn_map = [](CUtensorMap *m, int *three_d, const void *ptr, int64_t rows, int64_t k) {
+        *three_d = make_tmap_mn3(m, ptr, rows, k) ? 1 : 0;
+        return *three_d || make_tmap_mn(m, ptr, rows, k);
+    };
+    const auto out_map = [&](int s, void *out) {
+        const lf::GradSide &g = p.side[s];
+        return g.split > 1 ? make_tmap_parts(&maps.o[s], parts + g.parts, g.M, g.N, g.split)
+                           : make_tmap_out(&maps.o[s], out, g.M, g.N, g.N, 1, static_cast<int64_t>(g.M) * g.N, false);
+    };
+    if (dx && (!make_tmap(&maps.a[0], dgu, M, 2 * F, lf::BM) || !mn_map(&maps.b[0], &p.side[0].b_3d, w, K, 2 * F) ||
+               !out_map(0, dx)))
+        return LF_ERR_LAUNCH;
+    if (dw && (!mn_map(&maps.a[1], &p.side[1].a_3d, dgu, 2 * F, M) || !mn_map(&maps.b[1], &p.side[1].b_3d, x, K, M) ||
+               !out_map(1, dw)))
+        return LF_ERR_LAUNCH;
+    if ((st = launched(lf::launch_gated_bwd(act, dout, gu, dgu, M, F, stream), 1)) != LF_OK)
         return st;
-    if (dx && (st = gemm_layout_call(dgu, LF_K_MAJOR, w, LF_MN_MAJOR, dx, M, K, 2 * F, stream)) != LF_OK)
+    if (!dx && !dw)
+        return LF_OK;
+    if ((st = launched(lf::launch_gated_grads(maps, p, d->pair_clusters, stream), 1)) != LF_OK)
         return st;
-    if (dw && (st = gemm_layout_call(dgu, LF_MN_MAJOR, x, LF_MN_MAJOR, dw, 2 * F, K, M, stream)) != LF_OK)
-        return st;
-    return LF_OK;
+    if (!(dx && p.side[0].split > 1) && !(dw && p.side[1].split > 1))
+        return LF_OK;
+    return launched(lf::launch_add_parts(p, parts, dx, dw, d->num_sms, stream), 1);
 }
 
 const char *lf_status_string(lf_status s)
@@ -1373,11 +1421,24 @@ lf_status gated_ffn_e4m3(const void *x, const float *x_scale, const void *w, con
     return debug_sync(gated_ffn_e4m3_call(x, x_scale, w, w_scale, act, out, M, F, K, stream), stream);
 }
 
+int64_t gated_ffn_backward_scratch(int64_t M, int64_t F, int64_t K)
+{
+    if (check_gated_shape(M, F, K, LF_ACT_SILU) != LF_OK || check_gemm_shape(2 * F, K, M) != LF_OK ||
+        check_gemm_shape(M, K, 2 * F) != LF_OK)
+        return 0;
+    lf::GradsParams p;
+    std::memset(&p, 0, sizeof p);
+    lf::plan_gated_grads(&p, true, true, M, F, K, lf::GRAD_PLAN_PAIRS);
+    return p.part_floats * static_cast<int64_t>(sizeof(float));
+}
+
 lf_status gated_ffn_backward(const void *dout, const void *x, const void *w, const void *gu, int act, void *dgu,
-                             void *dx_or_null, void *dw_or_null, int64_t M, int64_t F, int64_t K, cudaStream_t stream)
+                             void *dx_or_null, void *dw_or_null, void *scratch, int64_t M, int64_t F, int64_t K,
+                             cudaStream_t stream)
 {
     const lf::CallRange range("gated_ffn_backward");
-    return debug_sync(gated_ffn_backward_call(dout, x, w, gu, act, dgu, dx_or_null, dw_or_null, M, F, K, stream),
+    return debug_sync(gated_ffn_backward_call(dout, x, w, gu, act, dgu, dx_or_null, dw_or_null, scratch, M, F, K,
+                                              stream),
                       stream);
 }
 

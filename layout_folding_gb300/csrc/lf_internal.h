@@ -120,9 +120,37 @@ GatedSkinny plan_gated_skinny(int64_t M, int64_t F, int num_k_blocks, int num_sm
 // ta: x, boxes of plan.n rows; tw as above.  gu may be null.
 cudaError_t launch_gated_skinny(bool e4m3, int act, const CUtensorMap &ta, const CUtensorMap &tw, const GatedParams &p,
                                 const GatedSkinny &plan, void *gu, cudaStream_t s);
-// dgu = [dout u act'(g), dout act(g)] from gu = [g, u]; F % 8 == 0, 16-byte aligned.
-cudaError_t launch_gated_bwd(int act, const void *dout, const void *gu, void *dgu, int64_t M, int64_t F, int num_sms,
+// dgu = [dout u act'(g), dout act(g)] from gu = [g, u]; F % 8 == 0, 16-byte
+// aligned.
+cudaError_t launch_gated_bwd(int act, const void *dout, const void *gu, void *dgu, int64_t M, int64_t F,
                              cudaStream_t s);
+
+// The products of the gradient (gated_grads.cu).  Side 0: dx[M, K] = dgu . w;
+// side 1: dw[2F, K] = dgu^T . x.
+struct GradSide {
+    int M, N;                                    // the output's rows and columns
+    int m_blocks, n_blocks, k_blocks, band;      // 256-row, 256-column and 64-wide K blocks; M blocks per band
+    int tiles, split, items;                     // K parts per tile; items = tiles * split (0: not wanted)
+    int64_t parts;                               // where its parts start, in floats: [split][M][N] (split > 1)
+    int a_3d, b_3d;                              // the MN-major operands' maps are 3-D views
+};
+struct GradsParams {
+    GemmParams wait;  // err, timeout_ns, inject
+    GradSide side[2];
+    int first, rounds;    // the schedule (GradIter)
+    int64_t part_floats;  // of all parts
+};
+// o: the output (bf16, 32 x 32 boxes) or, where the side is split, its parts
+// (fp32, 3-D: N, M, split; 32 x 32 x 1 boxes, 128-byte swizzle).
+struct GradMaps {
+    CUtensorMap a[2], b[2], o[2];
+};
+// Pairs that the splits (and so the scratch) are planned for, whatever the device has.
+constexpr int GRAD_PLAN_PAIRS = 76;
+void plan_gated_grads(GradsParams *p, bool want_dx, bool want_dw, int64_t M, int64_t F, int64_t K, int pairs);
+cudaError_t launch_gated_grads(const GradMaps &maps, const GradsParams &p, int pairs, cudaStream_t s);
+// The wanted split sides' parts added up.
+cudaError_t launch_add_parts(const GradsParams &p, const float *parts, void *dx, void *dw, int num_sms, cudaStream_t s);
 
 // Test hook: `ctas` CTAs, each holding 200 KiB of shared memory (one per SM),
 // that wait `ns` nanoseconds on the global timer and exit.

@@ -247,8 +247,13 @@ def gated_ffn_backward(dout, x, w, gu, act="silu", want_dx=True, want_dw=True, d
         dw = torch.empty_like(w) if dw is None else _output(dw, _BF16, w.shape, dev, "dw")
     if M == 0 and F > 0 and K > 0:
         return dx, _zeroed(dw, stream)
-    _lf._check(_lf.lib().gated_ffn_backward(dout.data_ptr(), x.data_ptr(), w.data_ptr(), gu.data_ptr(), code,
-                                            dgu.data_ptr(), None if dx is None else dx.data_ptr(),
-                                            None if dw is None else dw.data_ptr(), M, F, K, _handle(stream, dev)),
+    L = _lf.lib()
+    nbytes = L.gated_ffn_backward_scratch(M, F, K)
+    scratch = x.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
+    if scratch is not None and stream is not None:
+        scratch.record_stream(stream)
+    _lf._check(L.gated_ffn_backward(dout.data_ptr(), x.data_ptr(), w.data_ptr(), gu.data_ptr(), code, dgu.data_ptr(),
+                                    None if dx is None else dx.data_ptr(), None if dw is None else dw.data_ptr(),
+                                    None if scratch is None else scratch.data_ptr(), M, F, K, _handle(stream, dev)),
                "gated_ffn_backward")
     return dx, dw

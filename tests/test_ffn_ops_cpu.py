@@ -110,15 +110,24 @@ def test_gated_ffn_e4m3_rejects_on_host(L, kw, want):
 
 @pytest.mark.parametrize("kw,want", [
     (dict(dout=None), NULL), (dict(x=None), NULL), (dict(w=None), NULL), (dict(gu=None), NULL), (dict(dgu=None), NULL),
+    (dict(scratch=None, M=64, F=8192), NULL), (dict(scratch=A + 8), ALIGN),
     (dict(act=3), SHAPE), (dict(M=0), SHAPE), (dict(F=1 << 30), SHAPE),
     (dict(dout=A + 8), ALIGN), (dict(gu=A + 8), ALIGN), (dict(dgu=A + 8), ALIGN), (dict(dx=A + 8), ALIGN),
     (dict(dw=A + 8), ALIGN), (dict(F=12), ALIGN), (dict(K=12), ALIGN),
 ])
 def test_gated_ffn_backward_rejects_on_host(L, kw, want):
-    a = dict(dout=A, x=A, w=A, gu=A, act=0, dgu=A, dx=A, dw=A, M=4, F=64, K=64)
+    a = dict(dout=A, x=A, w=A, gu=A, act=0, dgu=A, dx=A, dw=A, scratch=A, M=4, F=64, K=64)
     a.update(kw)
-    assert L.gated_ffn_backward(*[a[k] for k in ("dout", "x", "w", "gu", "act", "dgu", "dx", "dw", "M", "F", "K")],
+    assert L.gated_ffn_backward(*[a[k] for k in ("dout", "x", "w", "gu", "act", "dgu", "dx", "dw", "scratch", "M", "F", "K")],
                                 None) == want
+
+
+def test_gated_ffn_backward_scratch_size(L):
+    size = L.gated_ffn_backward_scratch
+    assert size(0, 64, 64) == size(64, 0, 64) == size(64, 64, -1) == size(64, 1 << 30, 64) == 0
+    assert size(4096, 13824, 5120) == 0          # tiles enough: no sum is split
+    for M, F, K in ((1, 13824, 5120), (333, 5632, 2048), (64, 8192, 64), (100000, 64, 64)):
+        assert 0 < size(M, F, K) < 200 << 20     # a few parts of 256 x 256 floats for each pair of SMs
 
 
 def test_binding_refuses_cpu_tensors_and_unknown_activations():
