@@ -615,6 +615,7 @@ template <int ACT>
 __global__ void __launch_bounds__(256)
     k_gated_bwd(const __nv_bfloat16 *dout, const __nv_bfloat16 *gu, __nv_bfloat16 *dgu, int64_t M, int64_t F)
 {
+    let_next_kernel_start();
     const int64_t packs = F / 8;
     for (int64_t row = blockIdx.y; row < M; row += gridDim.y) {
         for (int64_t c = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; c < packs;

@@ -276,6 +276,9 @@ __global__ void __launch_bounds__(G_THREADS, 1)
     __syncthreads();
     cluster_sync();  // both CTAs' barriers exist before any cross-CTA signal
     tc_fence_after();
+    // everything above touches no global memory and overlaps the kernel before
+    wait_previous_kernel();
+    let_next_kernel_start();
     const uint32_t tmem_base = *tmem_slot;
     const uint32_t peer_abort = mapa_shared(smem_u32(const_cast<int *>(abort_flag)), rank ^ 1u);
 
@@ -340,10 +343,9 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         // warp w reads TMEM lanes 32 (w % 4) ..; warps 2..5 take the tile's first
         // 128 columns, warps 6..9 the rest
         const int q = warp & 3;
-        const int rloc = q * 32 + lane;
         const int c0 = ((warp - 2) >> 2) * (BN / 2), c1 = c0 + BN / 2;
         int acc = 0;
-        uint32_t acc_phase = 0, part_phase = 0;
+        uint32_t acc_phase = 0;
         uint8_t *stg = gbase + GR_STG_OFF + (warp - 2) * G_STG_WARP;
         const uint32_t stg_s = base + static_cast<uint32_t>(GR_STG_OFF + (warp - 2) * G_STG_WARP);
         GradIter iter(gp, pair, num_pairs);
@@ -415,6 +417,7 @@ __global__ void __launch_bounds__(256)
     k_add_parts(const float *parts0, __nv_bfloat16 *out0, int split0, int64_t n0, const float *parts1,
                 __nv_bfloat16 *out1, int split1, int64_t n1)
 {
+    wait_previous_kernel();
     const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x * 8;
     for (int64_t i = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) * 8; i < n0 + n1; i += step) {
         const bool second = i >= n0;
@@ -508,13 +511,15 @@ cudaError_t launch_gated_grads(const GradMaps &maps, const GradsParams &p, int p
     cfg.blockDim = dim3(G_THREADS, 1, 1);
     cfg.dynamicSmemBytes = GR_SMEM;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, k_gated_grads, maps, p);
 }
 
@@ -524,10 +529,17 @@ cudaError_t launch_add_parts(const GradsParams &p, const float *parts, void *dx,
     const int64_t n0 = a.items && a.split > 1 ? static_cast<int64_t>(a.M) * a.N : 0;
     const int64_t n1 = b.items && b.split > 1 ? static_cast<int64_t>(b.M) * b.N : 0;
     const int64_t blocks = ((n0 + n1) / 8 + 255) / 256, most = static_cast<int64_t>(num_sms) * 8;
-    k_add_parts<<<static_cast<unsigned>(blocks < most ? blocks : most), 256, 0, s>>>(
-        parts + a.parts, static_cast<__nv_bfloat16 *>(dx), a.split, n0, parts + b.parts,
-        static_cast<__nv_bfloat16 *>(dw), b.split, n1);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks < most ? blocks : most), 1, 1);
+    cfg.blockDim = dim3(256, 1, 1);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_add_parts, parts + a.parts, static_cast<__nv_bfloat16 *>(dx), a.split, n0,
+                              parts + b.parts, static_cast<__nv_bfloat16 *>(dw), b.split, n1);
 }
 
 }  // namespace lf

@@ -156,6 +156,15 @@ __device__ __forceinline__ void st_release_gpu(unsigned *p, uint32_t v)
     asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
+// ---------------------------------------------------------------- dependent launches
+// A kernel launched with programmatic stream serialisation may start while the
+// kernel before it in the stream still runs: before its first access to global
+// memory it waits until that kernel is complete and its writes are visible.
+__device__ __forceinline__ void wait_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets such a successor's CTAs be scheduled once every CTA of this kernel has
+// started (they still wait for its completion).
+__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---------------------------------------------------------------- TMA
 __device__ __forceinline__ void prefetch_tmap(const CUtensorMap *m)
 {
