@@ -370,6 +370,7 @@ __global__ void __launch_bounds__(1024) k_rms_norm_long(const NormParams p)
 template <class T, class W, int VEC, int NV>
 __global__ void __launch_bounds__(VEC * NV <= 8 ? 512 : 1024) k_rms_norm_bwd(const NormBwdParams p)
 {
+    let_next_kernel_start();
     __shared__ float2 sh[2][MAX_WARPS];
     const int packs = static_cast<int>(p.D / VEC);
     const W *w = static_cast<const W *>(p.weight);
@@ -458,6 +459,7 @@ __global__ void __launch_bounds__(VEC * NV <= 8 ? 512 : 1024) k_rms_norm_bwd(con
 template <class T, class W>
 __global__ void __launch_bounds__(1024) k_rms_norm_bwd_long(const NormBwdParams p)
 {
+    let_next_kernel_start();
     __shared__ float2 sh[2][MAX_WARPS];
     const W *w = static_cast<const W *>(p.weight);
     const float inv_d = 1.f / static_cast<float>(p.D);
@@ -496,6 +498,7 @@ template <class W>
 __global__ void __launch_bounds__(32 * DW_ROWS)
     k_rms_norm_dweight(const float *partial, W *dweight, int64_t D, int blocks)
 {
+    wait_previous_kernel();  // launched early, behind the kernel that writes `partial`
     __shared__ float sh[DW_ROWS][32];
     const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x;
     float v[DW_STEPS];
@@ -870,6 +873,7 @@ float v[VEC];
 template <class T, class W, bool DH, bool PH>
 __global__ void __launch_bounds__(512) k_rms_norm_bwd_ring(const NormBwdParams p, const RingPlan r)
 {
+    let_next_kernel_start();
     constexpr int VEC = 16 / static_cast<int>(sizeof(T));
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ RingSync sy;
@@ -1151,9 +1155,17 @@ cudaError_t launch_bwd_tw(const NormBwdParams &p, Rows rows, void *dweight, int 
     }
     if (e != cudaSuccess || !dweight)
         return e;
-    k_rms_norm_dweight<W><<<static_cast<unsigned>((p.D + 31) / 32), dim3(32, DW_ROWS), 0, s>>>(
-        p.partial, static_cast<W *>(dweight), p.D, blocks);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((p.D + 31) / 32), 1, 1);
+    cfg.blockDim = dim3(32, DW_ROWS, 1);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_rms_norm_dweight<W>, static_cast<const float *>(p.partial),
+                              static_cast<W *>(dweight), p.D, blocks);
 }
 
 bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
