@@ -1,9 +1,10 @@
 """The feed-forward operators of the binding: add_rms_norm, gated_ffn and their
 gradients (include/layoutfold.h is the contract, as for the rest).
 
-One token's norm runs for about 3 us on the GPU, so the checks here are kept to
-attribute reads and the whole call to a few microseconds: outputs come from
-empty_like / new_empty, and the stream is read as a raw handle.
+One token's norm runs for about 3 us on the GPU, so the host's share is kept
+small: checks are attribute reads, the stream is read as a raw handle, and
+outputs come from torch.empty (between launches Tensor.new_empty costs 4 us, torch.empty
+2 us; one buffer cut into views costs more than three tensors).
 """
 from __future__ import annotations
 
@@ -20,6 +21,17 @@ _CODES = {torch.bfloat16: LF_BF16, torch.float16: LF_FP16, torch.float32: LF_FP3
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+_empty = torch.empty
+_L = None
+
+
+def _lib():
+    global _L
+    if _L is None:
+        _L = _lf.lib()
+    return _L
+
+
 def _handle(stream, device):
     if stream is not None:
         return stream.cuda_stream
@@ -28,20 +40,24 @@ def _handle(stream, device):
     return torch.cuda.current_stream().cuda_stream
 
 
+_Tensor = torch.Tensor
+
+
 def _cuda(t, name):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, _Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % name)
 
 
 def _require(t, dtype, device, name):
     """t: a contiguous CUDA tensor of `dtype` on `device`."""
+    if isinstance(t, _Tensor) and t.dtype == dtype and t.get_device() == device and t.is_contiguous():
+        return
     _cuda(t, name)
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    if t.get_device() != device:
-        raise ValueError("%s must be on cuda:%d" % (name, device))
+    raise ValueError("%s must be on cuda:%d" % (name, device))
 
 
 def _output(t, dtype, shape, device, name):
@@ -112,7 +128,8 @@ def add_rms_norm(x, weight, residual=None, eps=1e-6, fp8=False, h=None, y=None, 
     dtype, shape = x.dtype, x.shape
     D = shape[-1]
     M = x.numel() // D if D else 0
-    ldx, ldr, r_ptr, h_ptr = _pitch(x, "x"), 0, None, None
+    ldx = D if x.is_contiguous() else _pitch(x, "x")
+    ldr, r_ptr, h_ptr = 0, None, None
     wcode = _weight_type(weight, code, dtype, D, dev)
     if residual is not None:
         _cuda(residual, "residual")
@@ -120,22 +137,26 @@ def add_rms_norm(x, weight, residual=None, eps=1e-6, fp8=False, h=None, y=None, 
             raise TypeError("residual must be %s, got %s" % (dtype, residual.dtype))
         if residual.shape != shape or residual.get_device() != dev:
             raise ValueError("residual must have x's shape and device")
-        ldr, r_ptr = _pitch(residual, "residual"), residual.data_ptr()
-        h = x.new_empty(shape) if h is None else _output(h, dtype, shape, dev, "h")
+        ldr = D if residual.is_contiguous() else _pitch(residual, "residual")
+        r_ptr = residual.data_ptr()
+        h = _empty(shape, dtype=dtype, device=x.device) if h is None else _output(h, dtype, shape, dev, "h")
         h_ptr = h.data_ptr()
     elif h is not None:
         raise ValueError("h is written only where a residual is added")
     if fp8:
-        y = x.new_empty(shape, dtype=_FP8) if y is None else _output(y, _FP8, shape, dev, "y")
-        scale = x.new_empty(shape[:-1], dtype=_F32) if scale is None else _output(scale, _F32, shape[:-1], dev, "scale")
+        y = _empty(shape, dtype=_FP8, device=x.device) if y is None else _output(y, _FP8, shape, dev, "y")
+        scale = (_empty(shape[:-1], dtype=_F32, device=x.device) if scale is None
+                 else _output(scale, _F32, shape[:-1], dev, "scale"))
     else:
         if scale is not None:
             raise ValueError("scale is written only with fp8")
-        y = x.new_empty(shape) if y is None else _output(y, dtype, shape, dev, "y")
+        y = _empty(shape, dtype=dtype, device=x.device) if y is None else _output(y, dtype, shape, dev, "y")
     if M > 0 or D == 0:
-        _lf._check(_lf.lib().add_rms_norm(x.data_ptr(), ldx, r_ptr, ldr, weight.data_ptr(), h_ptr, y.data_ptr(),
-                                          scale.data_ptr() if fp8 else None, code, wcode, LF_E4M3 if fp8 else code,
-                                          eps, M, D, _handle(stream, dev)), "add_rms_norm")
+        st = _lib().add_rms_norm(x.data_ptr(), ldx, r_ptr, ldr, weight.data_ptr(), h_ptr, y.data_ptr(),
+                                 scale.data_ptr() if fp8 else None, code, wcode, LF_E4M3 if fp8 else code, eps, M, D,
+                                 _handle(stream, dev))
+        if st:
+            _lf._check(st, "add_rms_norm")
     return y, (x if residual is None else h), scale
 
 
@@ -157,17 +178,17 @@ def add_rms_norm_backward(dy, h, weight, dh=None, eps=1e-6, want_dweight=True, d
         _require(dh, dtype, dev, "dh")
         if dh.shape != shape:
             raise ValueError("dh must have h's shape")
-    dx = h.new_empty(shape) if dx is None else _output(dx, dtype, shape, dev, "dx")
+    dx = _empty(shape, dtype=dtype, device=h.device) if dx is None else _output(dx, dtype, shape, dev, "dx")
     want = want_dweight or dweight is not None
     if want:
-        dweight = weight.new_empty(weight.shape) if dweight is None else _output(dweight, weight.dtype, weight.shape,
-                                                                                 dev, "dweight")
+        dweight = (_empty(weight.shape, dtype=weight.dtype, device=h.device) if dweight is None
+                   else _output(dweight, weight.dtype, weight.shape, dev, "dweight"))
     if M == 0 and D > 0:
         return dx, _zeroed(dweight, stream)
-    L = _lf.lib()
+    L = _lib()
     scratch = None
     if want:
-        scratch = h.new_empty(L.add_rms_norm_backward_scratch(M, D), dtype=torch.uint8)
+        scratch = _empty(L.add_rms_norm_backward_scratch(M, D), dtype=torch.uint8, device=h.device)
         if stream is not None:
             scratch.record_stream(stream)
     _lf._check(L.add_rms_norm_backward(dy.data_ptr(), h.data_ptr(), weight.data_ptr(),
@@ -200,7 +221,8 @@ def gated_ffn(x, w, act="silu", x_scale=None, w_scale=None, want_gu=False, out=N
     scaled = x_scale is not None or w_scale is not None
     M, F, K, dev = _gated_dims(x, w, _FP8 if scaled else _BF16)
     lead = x.shape[:-1]
-    out = x.new_empty((*lead, F), dtype=_BF16) if out is None else _output(out, _BF16, (*lead, F), dev, "out")
+    out = (_empty((*lead, F), dtype=_BF16, device=x.device) if out is None
+           else _output(out, _BF16, (*lead, F), dev, "out"))
     if scaled:
         if x_scale is None or w_scale is None or want_gu or gu is not None:
             raise ValueError("e4m3 operands take both x_scale and w_scale, and keep no gu")
@@ -209,14 +231,15 @@ def gated_ffn(x, w, act="silu", x_scale=None, w_scale=None, want_gu=False, out=N
         if x_scale.numel() != M or w_scale.numel() != 2 * F:
             raise ValueError("x_scale must hold one scale per row of x and w_scale one per row of w")
     elif want_gu or gu is not None:
-        gu = x.new_empty((*lead, 2 * F)) if gu is None else _output(gu, _BF16, (*lead, 2 * F), dev, "gu")
+        gu = (_empty((*lead, 2 * F), dtype=_BF16, device=x.device) if gu is None
+              else _output(gu, _BF16, (*lead, 2 * F), dev, "gu"))
     if M == 0 and F > 0 and K > 0:
         return out, gu
     if scaled:
-        _lf._check(_lf.lib().gated_ffn_e4m3(x.data_ptr(), x_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), code,
+        _lf._check(_lib().gated_ffn_e4m3(x.data_ptr(), x_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), code,
                                             out.data_ptr(), M, F, K, _handle(stream, dev)), "gated_ffn_e4m3")
     else:
-        _lf._check(_lf.lib().gated_ffn(x.data_ptr(), w.data_ptr(), code, out.data_ptr(),
+        _lf._check(_lib().gated_ffn(x.data_ptr(), w.data_ptr(), code, out.data_ptr(),
                                        None if gu is None else gu.data_ptr(), M, F, K, _handle(stream, dev)),
                    "gated_ffn")
     return out, gu
@@ -236,20 +259,20 @@ def gated_ffn_backward(dout, x, w, gu, act="silu", want_dx=True, want_dw=True, d
     if tuple(dout.shape) != (*lead, F) or tuple(gu.shape) != (*lead, 2 * F):
         raise ValueError("dout must be [..., F] and gu [..., 2F] for x's rows")
     if dgu is None:
-        dgu = torch.empty_like(gu)
+        dgu = _empty(gu.shape, dtype=_BF16, device=x.device)
         if stream is not None:
             dgu.record_stream(stream)
     else:
         _output(dgu, _BF16, gu.shape, dev, "dgu")
     if want_dx or dx is not None:
-        dx = torch.empty_like(x) if dx is None else _output(dx, _BF16, x.shape, dev, "dx")
+        dx = _empty(x.shape, dtype=_BF16, device=x.device) if dx is None else _output(dx, _BF16, x.shape, dev, "dx")
     if want_dw or dw is not None:
-        dw = torch.empty_like(w) if dw is None else _output(dw, _BF16, w.shape, dev, "dw")
+        dw = _empty(w.shape, dtype=_BF16, device=x.device) if dw is None else _output(dw, _BF16, w.shape, dev, "dw")
     if M == 0 and F > 0 and K > 0:
         return dx, _zeroed(dw, stream)
-    L = _lf.lib()
+    L = _lib()
     nbytes = L.gated_ffn_backward_scratch(M, F, K)
-    scratch = x.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
+    scratch = _empty(nbytes, dtype=torch.uint8, device=x.device) if nbytes else None
     if scratch is not None and stream is not None:
         scratch.record_stream(stream)
     _lf._check(L.gated_ffn_backward(dout.data_ptr(), x.data_ptr(), w.data_ptr(), gu.data_ptr(), code, dgu.data_ptr(),
