@@ -181,6 +181,8 @@ __global__ void __launch_bounds__(G_THREADS, 1)
     __syncthreads();
     cluster_sync();  // both CTAs' barriers exist before any cross-CTA signal
     tc_fence_after();
+    wait_previous_kernel();
+    let_next_kernel_start();
     const uint32_t tmem_base = *tmem_slot;
     const uint32_t peer_abort = mapa_shared(smem_u32(const_cast<int *>(abort_flag)), rank ^ 1u);
 
@@ -358,19 +360,8 @@ cudaError_t launch_gated_pair_t(const CUtensorMap &ta, const CUtensorMap &tw, co
             return e;
         done.fetch_or(bit);
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-    cfg.blockDim = dim3(G_THREADS, 1, 1);
-    cfg.dynamicSmemBytes = G_SMEM;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_gated_pair<E4M3, ACT>, ta, tw, to, tg, tu, p);
+    return launch_overlapped(k_gated_pair<E4M3, ACT>, dim3(static_cast<unsigned>(grid)), dim3(G_THREADS), G_SMEM, 2, s,
+                             ta, tw, to, tg, tu, p);
 }
 
 // ---------------------------------------------------------------- few tokens
@@ -456,6 +447,8 @@ __global__ void __launch_bounds__(S_THREADS, 2)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    wait_previous_kernel();
+    let_next_kernel_start();
     const uint32_t tmem_base = *tmem_slot;
 
     if (warp == 0) {
@@ -593,19 +586,9 @@ cudaError_t launch_gated_skinny_t(const CUtensorMap &ta, const CUtensorMap &tw, 
             return e;
         done.fetch_or(bit);
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.g.num_n_blocks * plan.split), 1, 1);
-    cfg.blockDim = dim3(S_THREADS, 1, 1);
-    cfg.dynamicSmemBytes = static_cast<size_t>(plan.smem);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(plan.split);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = plan.split > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, k_gated_skinny<E4M3, ACT>, ta, tw, p, plan, static_cast<__nv_bfloat16 *>(gu));
+    return launch_overlapped(k_gated_skinny<E4M3, ACT>, dim3(static_cast<unsigned>(p.g.num_n_blocks * plan.split)),
+                             dim3(S_THREADS), static_cast<size_t>(plan.smem), plan.split, s, ta, tw, p, plan,
+                             static_cast<__nv_bfloat16 *>(gu));
 }
 
 // ---------------------------------------------------------------- gradient
@@ -615,6 +598,7 @@ template <int ACT>
 __global__ void __launch_bounds__(256)
     k_gated_bwd(const __nv_bfloat16 *dout, const __nv_bfloat16 *gu, __nv_bfloat16 *dgu, int64_t M, int64_t F)
 {
+    wait_previous_kernel();
     let_next_kernel_start();
     const int64_t packs = F / 8;
     for (int64_t row = blockIdx.y; row < M; row += gridDim.y) {
@@ -712,13 +696,10 @@ cudaError_t launch_gated_bwd(int act, const void *dout, const void *gu, void *dg
     const dim3 grid(static_cast<unsigned>(bx < 1024 ? bx : 1024), static_cast<unsigned>(M < 65535 ? M : 65535));
     const __nv_bfloat16 *d = static_cast<const __nv_bfloat16 *>(dout), *g = static_cast<const __nv_bfloat16 *>(gu);
     __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(dgu);
-    if (act == ACT_SILU)
-        k_gated_bwd<ACT_SILU><<<grid, 256, 0, s>>>(d, g, o, M, F);
-    else if (act == ACT_GELU)
-        k_gated_bwd<ACT_GELU><<<grid, 256, 0, s>>>(d, g, o, M, F);
-    else
-        k_gated_bwd<ACT_GELU_TANH><<<grid, 256, 0, s>>>(d, g, o, M, F);
-    return cudaGetLastError();
+    const auto kernel = act == ACT_SILU   ? k_gated_bwd<ACT_SILU>
+                        : act == ACT_GELU ? k_gated_bwd<ACT_GELU>
+                                          : k_gated_bwd<ACT_GELU_TANH>;
+    return launch_overlapped(kernel, grid, dim3(256), 0, 1, s, d, g, o, M, F);
 }
 
 }  // namespace lf

@@ -506,21 +506,8 @@ cudaError_t launch_gated_grads(const GradMaps &maps, const GradsParams &p, int p
         done.fetch_or(bit);
     }
     const int64_t items = static_cast<int64_t>(p.side[0].items) + p.side[1].items;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * (items < pairs ? items : pairs)), 1, 1);
-    cfg.blockDim = dim3(G_THREADS, 1, 1);
-    cfg.dynamicSmemBytes = GR_SMEM;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, k_gated_grads, maps, p);
+    return launch_overlapped(k_gated_grads, dim3(static_cast<unsigned>(2 * (items < pairs ? items : pairs))),
+                             dim3(G_THREADS), GR_SMEM, 2, s, maps, p);
 }
 
 cudaError_t launch_add_parts(const GradsParams &p, const float *parts, void *dx, void *dw, int num_sms, cudaStream_t s)
@@ -529,17 +516,9 @@ cudaError_t launch_add_parts(const GradsParams &p, const float *parts, void *dx,
     const int64_t n0 = a.items && a.split > 1 ? static_cast<int64_t>(a.M) * a.N : 0;
     const int64_t n1 = b.items && b.split > 1 ? static_cast<int64_t>(b.M) * b.N : 0;
     const int64_t blocks = ((n0 + n1) / 8 + 255) / 256, most = static_cast<int64_t>(num_sms) * 8;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(blocks < most ? blocks : most), 1, 1);
-    cfg.blockDim = dim3(256, 1, 1);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_add_parts, parts + a.parts, static_cast<__nv_bfloat16 *>(dx), a.split, n0,
-                              parts + b.parts, static_cast<__nv_bfloat16 *>(dw), b.split, n1);
+    return launch_overlapped(k_add_parts, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(256), 0, 1, s,
+                             parts + a.parts, static_cast<__nv_bfloat16 *>(dx), a.split, n0, parts + b.parts,
+                             static_cast<__nv_bfloat16 *>(dw), b.split, n1);
 }
 
 }  // namespace lf

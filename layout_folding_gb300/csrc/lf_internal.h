@@ -61,6 +61,30 @@ cudaError_t launch_rope_cos_sin(const void *inv_freq, const int64_t *pos, void *
                                 int64_t S, int num_sms, cudaStream_t s);
 cudaError_t launch_fp8_cast_dual(const void *x, const float *scale, void *out, void *out_t, int64_t M, int64_t K,
                                  int num_sms, cudaStream_t s);
+// Launch with programmatic stream serialisation (and clusters of `cluster` CTAs):
+// the kernel may be set up while its predecessor in the stream ends, so it has to
+// call wait_previous_kernel (lf_ptx.cuh) before it touches global memory.
+template <class... P, class... A>
+cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, int cluster, cudaStream_t s,
+                              A &&...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<A &&>(args)...);
+}
+
 // Where a kernel's bounded waits report, and their limit.
 struct WaitLimit {
     int *err;

@@ -244,6 +244,8 @@ __device__ __forceinline__ void store_e4m3(uint8_t *p, const float (&f)[VEC])
 template <class T, class W, int VEC, int NV, bool FP8>
 __global__ void __launch_bounds__(NV <= 2 ? 512 : 1024) k_rms_norm(const NormParams p)
 {
+    wait_previous_kernel();
+    let_next_kernel_start();
     __shared__ float2 sh[2][MAX_WARPS];
     const int packs = static_cast<int>(p.D / VEC);
     const T *x = static_cast<const T *>(p.x);
@@ -325,6 +327,8 @@ float v[VEC];
 template <class T, class W, bool FP8>
 __global__ void __launch_bounds__(1024) k_rms_norm_long(const NormParams p)
 {
+    wait_previous_kernel();
+    let_next_kernel_start();
     __shared__ float2 sh[2][MAX_WARPS];
     const T *res = static_cast<const T *>(p.residual);
     const W *w = static_cast<const W *>(p.weight);
@@ -370,6 +374,7 @@ __global__ void __launch_bounds__(1024) k_rms_norm_long(const NormParams p)
 template <class T, class W, int VEC, int NV>
 __global__ void __launch_bounds__(VEC * NV <= 8 ? 512 : 1024) k_rms_norm_bwd(const NormBwdParams p)
 {
+    wait_previous_kernel();
     let_next_kernel_start();
     __shared__ float2 sh[2][MAX_WARPS];
     const int packs = static_cast<int>(p.D / VEC);
@@ -459,6 +464,7 @@ __global__ void __launch_bounds__(VEC * NV <= 8 ? 512 : 1024) k_rms_norm_bwd(con
 template <class T, class W>
 __global__ void __launch_bounds__(1024) k_rms_norm_bwd_long(const NormBwdParams p)
 {
+    wait_previous_kernel();
     let_next_kernel_start();
     __shared__ float2 sh[2][MAX_WARPS];
     const W *w = static_cast<const W *>(p.weight);
@@ -498,7 +504,7 @@ template <class W>
 __global__ void __launch_bounds__(32 * DW_ROWS)
     k_rms_norm_dweight(const float *partial, W *dweight, int64_t D, int blocks)
 {
-    wait_previous_kernel();  // launched early, behind the kernel that writes `partial`
+    wait_previous_kernel();
     __shared__ float sh[DW_ROWS][32];
     const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x;
     float v[DW_STEPS];
@@ -787,8 +793,11 @@ __global__ void __launch_bounds__(1024) k_rms_norm_ring(const NormParams p, cons
     const auto fill = [&](int slot, int64_t row) {
         ring.fill(span, slot, row, x, p.ldx, res, p.ldr, static_cast<const T *>(nullptr), 0);
     };
-    if (t == 0) {
+    if (t == 0)
         ring.init();
+    wait_previous_kernel();
+    let_next_kernel_start();
+    if (t == 0) {
         // (test hook: the first block's first group never loads its first row)
         for (int i = p.limit.inject && blockIdx.x == 0 && group == 0 ? 1 : 0; i < r.slots && row0 + i * step < p.M; ++i)
             fill(i, row0 + i * step);
@@ -873,7 +882,6 @@ float v[VEC];
 template <class T, class W, bool DH, bool PH>
 __global__ void __launch_bounds__(512) k_rms_norm_bwd_ring(const NormBwdParams p, const RingPlan r)
 {
-    let_next_kernel_start();
     constexpr int VEC = 16 / static_cast<int>(sizeof(T));
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ RingSync sy;
@@ -889,8 +897,11 @@ __global__ void __launch_bounds__(512) k_rms_norm_bwd_ring(const NormBwdParams p
     const auto fill = [&](int slot, int64_t row) {
         ring.fill(span, slot, row, hg, p.D, yg, p.D, DH ? dg : static_cast<const T *>(nullptr), p.D);
     };
-    if (t == 0) {
+    if (t == 0)
         ring.init();
+    wait_previous_kernel();
+    let_next_kernel_start();
+    if (t == 0) {
         // (test hook: the first block's first group never loads its first row)
         for (int i = p.limit.inject && blockIdx.x == 0 && group == 0 ? 1 : 0; i < r.slots && row0 + i * step < p.M; ++i)
             fill(i, row0 + i * step);
@@ -1053,19 +1064,19 @@ int threads_for(int64_t packs, int nv)
 }
 
 template <class T, class W, int VEC, bool FP8>
-bool launch_norm_regs(const NormParams &p, cudaStream_t s)
+bool launch_norm_regs(const NormParams &p, cudaStream_t s, cudaError_t *e)
 {
     const int64_t packs = p.D / VEC;
-    const unsigned grid = static_cast<unsigned>(p.M < 0x7fffffff ? p.M : 0x7fffffff);
+    const unsigned grid = static_cast<unsigned>(p.M);  // < 2^31
     int t;
     if ((t = threads_for(packs, 1)) && t <= 512)
-        k_rms_norm<T, W, VEC, 1, FP8><<<grid, t, 0, s>>>(p);
+        *e = launch_overlapped(k_rms_norm<T, W, VEC, 1, FP8>, dim3(grid), dim3(t), 0, 1, s, p);
     else if ((t = threads_for(packs, 2)) && t <= 512)
-        k_rms_norm<T, W, VEC, 2, FP8><<<grid, t, 0, s>>>(p);
+        *e = launch_overlapped(k_rms_norm<T, W, VEC, 2, FP8>, dim3(grid), dim3(t), 0, 1, s, p);
     else if ((t = threads_for(packs, 4)))
-        k_rms_norm<T, W, VEC, 4, FP8><<<grid, t, 0, s>>>(p);
+        *e = launch_overlapped(k_rms_norm<T, W, VEC, 4, FP8>, dim3(grid), dim3(t), 0, 1, s, p);
     else if ((t = threads_for(packs, 8)))
-        k_rms_norm<T, W, VEC, 8, FP8><<<grid, t, 0, s>>>(p);
+        *e = launch_overlapped(k_rms_norm<T, W, VEC, 8, FP8>, dim3(grid), dim3(t), 0, 1, s, p);
     else
         return false;
     return true;
@@ -1078,8 +1089,8 @@ cudaError_t launch_norm_ring(const NormParams &p, const RingPlan &r, int num_sms
     const cudaError_t e = ring_opt_in(k_rms_norm_ring<T, W, FP8, PH>, opted);
     if (e != cudaSuccess)
         return e;
-    k_rms_norm_ring<T, W, FP8, PH><<<num_sms / 8 * 8, r.groups * r.group_threads, r.bytes, s>>>(p, r);
-    return cudaGetLastError();
+    return launch_overlapped(k_rms_norm_ring<T, W, FP8, PH>, dim3(num_sms / 8 * 8), dim3(r.groups * r.group_threads),
+                             r.bytes, 1, s, p, r);
 }
 
 template <class T, class W, bool FP8>
@@ -1091,10 +1102,10 @@ cudaError_t launch_norm_t(const NormParams &p, Rows rows, int num_sms, cudaStrea
         plan_ring(&r, rows == ROWS_PHASED, p.D, sizeof(T), sizeof(W), p.residual ? 2 : 1, 1024))
         return rows == ROWS_PHASED ? launch_norm_ring<T, W, FP8, true>(p, r, num_sms, s)
                                    : launch_norm_ring<T, W, FP8, false>(p, r, num_sms, s);
-    const bool done = rows == ROWS_VEC ? launch_norm_regs<T, W, V, FP8>(p, s) : launch_norm_regs<T, W, 1, FP8>(p, s);
-    if (!done)
-        k_rms_norm_long<T, W, FP8><<<static_cast<unsigned>(p.M < 0x7fffffff ? p.M : 0x7fffffff), 1024, 0, s>>>(p);
-    return cudaGetLastError();
+    cudaError_t e = cudaSuccess;
+    if (rows == ROWS_VEC ? launch_norm_regs<T, W, V, FP8>(p, s, &e) : launch_norm_regs<T, W, 1, FP8>(p, s, &e))
+        return e;
+    return launch_overlapped(k_rms_norm_long<T, W, FP8>, dim3(static_cast<unsigned>(p.M)), dim3(1024), 0, 1, s, p);
 }
 
 template <class T, class W>
@@ -1104,18 +1115,18 @@ cudaError_t launch_norm_tw(const NormParams &p, Rows rows, bool fp8, int num_sms
 }
 
 template <class T, class W, int VEC>
-bool launch_bwd_regs(const NormBwdParams &p, int grid, cudaStream_t s)
+bool launch_bwd_regs(const NormBwdParams &p, int grid, cudaStream_t s, cudaError_t *e)
 {
     constexpr int PER = 16 / VEC;  // at most 16 columns per thread
     const int64_t packs = p.D / VEC;
     int t;
     if constexpr (PER >= 2)
         if ((t = threads_for(packs, PER / 2)) && t <= 512) {
-            k_rms_norm_bwd<T, W, VEC, PER / 2><<<grid, t, 0, s>>>(p);
+            *e = launch_overlapped(k_rms_norm_bwd<T, W, VEC, PER / 2>, dim3(grid), dim3(t), 0, 1, s, p);
             return true;
         }
     if ((t = threads_for(packs, PER))) {
-        k_rms_norm_bwd<T, W, VEC, PER><<<grid, t, 0, s>>>(p);
+        *e = launch_overlapped(k_rms_norm_bwd<T, W, VEC, PER>, dim3(grid), dim3(t), 0, 1, s, p);
         return true;
     }
     return false;
@@ -1128,8 +1139,8 @@ cudaError_t launch_bwd_ring(const NormBwdParams &p, const RingPlan &r, int block
     const cudaError_t e = ring_opt_in(k_rms_norm_bwd_ring<T, W, DH, PH>, opted);
     if (e != cudaSuccess)
         return e;
-    k_rms_norm_bwd_ring<T, W, DH, PH><<<blocks, r.groups * r.group_threads, r.bytes, s>>>(p, r);
-    return cudaGetLastError();
+    return launch_overlapped(k_rms_norm_bwd_ring<T, W, DH, PH>, dim3(blocks), dim3(r.groups * r.group_threads), r.bytes, 1,
+                             s, p, r);
 }
 
 template <class T, class W>
@@ -1149,23 +1160,13 @@ cudaError_t launch_bwd_tw(const NormBwdParams &p, Rows rows, void *dweight, int 
             e = p.dh ? launch_bwd_ring<T, W, true, false>(p, r, blocks, s)
                      : launch_bwd_ring<T, W, false, false>(p, r, blocks, s);
     } else {
-        if (!(rows == ROWS_VEC ? launch_bwd_regs<T, W, V>(p, blocks, s) : launch_bwd_regs<T, W, 1>(p, blocks, s)))
-            k_rms_norm_bwd_long<T, W><<<blocks, 1024, 0, s>>>(p);
-        e = cudaGetLastError();
+        if (!(rows == ROWS_VEC ? launch_bwd_regs<T, W, V>(p, blocks, s, &e) : launch_bwd_regs<T, W, 1>(p, blocks, s, &e)))
+            e = launch_overlapped(k_rms_norm_bwd_long<T, W>, dim3(blocks), dim3(1024), 0, 1, s, p);
     }
     if (e != cudaSuccess || !dweight)
         return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((p.D + 31) / 32), 1, 1);
-    cfg.blockDim = dim3(32, DW_ROWS, 1);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_rms_norm_dweight<W>, static_cast<const float *>(p.partial),
-                              static_cast<W *>(dweight), p.D, blocks);
+    return launch_overlapped(k_rms_norm_dweight<W>, dim3(static_cast<unsigned>((p.D + 31) / 32)), dim3(32, DW_ROWS), 0, 1,
+                             s, static_cast<const float *>(p.partial), static_cast<W *>(dweight), p.D, blocks);
 }
 
 bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
