@@ -3,8 +3,10 @@ gradients (include/layoutfold.h is the contract, as for the rest).
 
 One token's norm runs for about 3 us on the GPU, so the host's share is kept
 small: checks are attribute reads, the stream is read as a raw handle, and
-outputs come from torch.empty (between launches Tensor.new_empty costs 4 us, torch.empty
-2 us; one buffer cut into views costs more than three tensors).
+outputs come from _new (between launches an output costs 4 us from
+Tensor.new_empty, 2 us from torch.empty, 1 us from the allocation call that
+torch's compiled programs use; one buffer cut into views costs more than three
+tensors).
 """
 from __future__ import annotations
 
@@ -21,8 +23,23 @@ _CODES = {torch.bfloat16: LF_BF16, torch.float16: LF_FP16, torch.float32: LF_FP3
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-_empty = torch.empty
 _L = None
+try:
+    # contiguous tensors on the current device, without the general argument parser
+    from torch._C._dynamo.guards import _empty_strided_cuda as _strided
+    _current_device = torch._C._cuda_getDevice
+except (ImportError, AttributeError):  # pragma: no cover
+    _strided = _current_device = None
+
+
+def _new(shape, dtype, ref, device):
+    """A contiguous tensor of `shape` on ref's device (index `device`)."""
+    n = len(shape)
+    if _strided is None or n > 2 or _current_device() != device:
+        return torch.empty(shape, dtype=dtype, device=ref.device)
+    if n == 2:
+        return _strided(tuple(shape), (shape[1] or 1, 1), dtype)
+    return _strided(tuple(shape), (1,) if n else (), dtype)
 
 
 def _lib():
@@ -139,18 +156,18 @@ def add_rms_norm(x, weight, residual=None, eps=1e-6, fp8=False, h=None, y=None, 
             raise ValueError("residual must have x's shape and device")
         ldr = D if residual.is_contiguous() else _pitch(residual, "residual")
         r_ptr = residual.data_ptr()
-        h = _empty(shape, dtype=dtype, device=x.device) if h is None else _output(h, dtype, shape, dev, "h")
+        h = _new(shape, dtype, x, dev) if h is None else _output(h, dtype, shape, dev, "h")
         h_ptr = h.data_ptr()
     elif h is not None:
         raise ValueError("h is written only where a residual is added")
     if fp8:
-        y = _empty(shape, dtype=_FP8, device=x.device) if y is None else _output(y, _FP8, shape, dev, "y")
-        scale = (_empty(shape[:-1], dtype=_F32, device=x.device) if scale is None
+        y = _new(shape, _FP8, x, dev) if y is None else _output(y, _FP8, shape, dev, "y")
+        scale = (_new(shape[:-1], _F32, x, dev) if scale is None
                  else _output(scale, _F32, shape[:-1], dev, "scale"))
     else:
         if scale is not None:
             raise ValueError("scale is written only with fp8")
-        y = _empty(shape, dtype=dtype, device=x.device) if y is None else _output(y, dtype, shape, dev, "y")
+        y = _new(shape, dtype, x, dev) if y is None else _output(y, dtype, shape, dev, "y")
     if M > 0 or D == 0:
         st = _lib().add_rms_norm(x.data_ptr(), ldx, r_ptr, ldr, weight.data_ptr(), h_ptr, y.data_ptr(),
                                  scale.data_ptr() if fp8 else None, code, wcode, LF_E4M3 if fp8 else code, eps, M, D,
@@ -178,17 +195,17 @@ def add_rms_norm_backward(dy, h, weight, dh=None, eps=1e-6, want_dweight=True, d
         _require(dh, dtype, dev, "dh")
         if dh.shape != shape:
             raise ValueError("dh must have h's shape")
-    dx = _empty(shape, dtype=dtype, device=h.device) if dx is None else _output(dx, dtype, shape, dev, "dx")
+    dx = _new(shape, dtype, h, dev) if dx is None else _output(dx, dtype, shape, dev, "dx")
     want = want_dweight or dweight is not None
     if want:
-        dweight = (_empty(weight.shape, dtype=weight.dtype, device=h.device) if dweight is None
+        dweight = (_new(weight.shape, weight.dtype, h, dev) if dweight is None
                    else _output(dweight, weight.dtype, weight.shape, dev, "dweight"))
     if M == 0 and D > 0:
         return dx, _zeroed(dweight, stream)
     L = _lib()
     scratch = None
     if want:
-        scratch = _empty(L.add_rms_norm_backward_scratch(M, D), dtype=torch.uint8, device=h.device)
+        scratch = _new((L.add_rms_norm_backward_scratch(M, D),), torch.uint8, h, dev)
         if stream is not None:
             scratch.record_stream(stream)
     _lf._check(L.add_rms_norm_backward(dy.data_ptr(), h.data_ptr(), weight.data_ptr(),
@@ -221,7 +238,7 @@ def gated_ffn(x, w, act="silu", x_scale=None, w_scale=None, want_gu=False, out=N
     scaled = x_scale is not None or w_scale is not None
     M, F, K, dev = _gated_dims(x, w, _FP8 if scaled else _BF16)
     lead = x.shape[:-1]
-    out = (_empty((*lead, F), dtype=_BF16, device=x.device) if out is None
+    out = (_new((*lead, F), _BF16, x, dev) if out is None
            else _output(out, _BF16, (*lead, F), dev, "out"))
     if scaled:
         if x_scale is None or w_scale is None or want_gu or gu is not None:
@@ -231,7 +248,7 @@ def gated_ffn(x, w, act="silu", x_scale=None, w_scale=None, want_gu=False, out=N
         if x_scale.numel() != M or w_scale.numel() != 2 * F:
             raise ValueError("x_scale must hold one scale per row of x and w_scale one per row of w")
     elif want_gu or gu is not None:
-        gu = (_empty((*lead, 2 * F), dtype=_BF16, device=x.device) if gu is None
+        gu = (_new((*lead, 2 * F), _BF16, x, dev) if gu is None
               else _output(gu, _BF16, (*lead, 2 * F), dev, "gu"))
     if M == 0 and F > 0 and K > 0:
         return out, gu
@@ -259,20 +276,20 @@ def gated_ffn_backward(dout, x, w, gu, act="silu", want_dx=True, want_dw=True, d
     if tuple(dout.shape) != (*lead, F) or tuple(gu.shape) != (*lead, 2 * F):
         raise ValueError("dout must be [..., F] and gu [..., 2F] for x's rows")
     if dgu is None:
-        dgu = _empty(gu.shape, dtype=_BF16, device=x.device)
+        dgu = _new(gu.shape, _BF16, x, dev)
         if stream is not None:
             dgu.record_stream(stream)
     else:
         _output(dgu, _BF16, gu.shape, dev, "dgu")
     if want_dx or dx is not None:
-        dx = _empty(x.shape, dtype=_BF16, device=x.device) if dx is None else _output(dx, _BF16, x.shape, dev, "dx")
+        dx = _new(x.shape, _BF16, x, dev) if dx is None else _output(dx, _BF16, x.shape, dev, "dx")
     if want_dw or dw is not None:
-        dw = _empty(w.shape, dtype=_BF16, device=x.device) if dw is None else _output(dw, _BF16, w.shape, dev, "dw")
+        dw = _new(w.shape, _BF16, x, dev) if dw is None else _output(dw, _BF16, w.shape, dev, "dw")
     if M == 0 and F > 0 and K > 0:
         return dx, _zeroed(dw, stream)
     L = _lib()
     nbytes = L.gated_ffn_backward_scratch(M, F, K)
-    scratch = _empty(nbytes, dtype=torch.uint8, device=x.device) if nbytes else None
+    scratch = _new((nbytes,), torch.uint8, x, dev) if nbytes else None
     if scratch is not None and stream is not None:
         scratch.record_stream(stream)
     _lf._check(L.gated_ffn_backward(dout.data_ptr(), x.data_ptr(), w.data_ptr(), gu.data_ptr(), code, dgu.data_ptr(),
