@@ -27,6 +27,28 @@ constexpr float GELU_A = 0.044715f;
 // infinity and the quotient to 0).
 __device__ __forceinline__ float sigmoid_f(float v) { return __fdividef(1.f, 1.f + ex2_approx(-v * LOG2E)); }
 
+// The standard normal distribution function, Phi(v) = erfc(-v / sqrt 2) / 2, by the
+// Chebyshev fit of erfc in Press, Teukolsky, Vetterling and Flannery, Numerical
+// Recipes, 6.2 (erfcc: t exp(-z^2 + P(t)), t = 1 / (1 + z / 2), relative error
+// below 1.2e-7 for every z >= 0).  One polynomial, one exponential and one
+// reciprocal: with normcdff the epilogue of a tile took 10 us.
+__device__ __forceinline__ float normal_cdf(float v)
+{
+    const float z = fabsf(v) * 0.70710678f;
+    const float t = __fdividef(1.f, fmaf(0.5f, z, 1.f));
+    float q = fmaf(t, 0.17087277f, -0.82215223f);
+    q = fmaf(t, q, 1.48851587f);
+    q = fmaf(t, q, -1.13520398f);
+    q = fmaf(t, q, 0.27886807f);
+    q = fmaf(t, q, -0.18628806f);
+    q = fmaf(t, q, 0.09678418f);
+    q = fmaf(t, q, 0.37409196f);
+    q = fmaf(t, q, 1.00002368f);
+    q = fmaf(t, q, -1.26551223f);
+    const float e = 0.5f * t * ex2_approx(fmaf(-z, z, q) * LOG2E);
+    return v < 0.f ? e : 1.f - e;
+}
+
 // act(v) = v * phi(v)
 template <int ACT>
 __device__ __forceinline__ float act_phi(float v)
@@ -34,7 +56,7 @@ __device__ __forceinline__ float act_phi(float v)
     if (ACT == ACT_SILU)
         return sigmoid_f(v);
     if (ACT == ACT_GELU)
-        return normcdff(v);
+        return normal_cdf(v);
     return sigmoid_f(GELU_C2 * fmaf(GELU_A * v * v, v, v));
 }
 
