@@ -383,6 +383,22 @@ bool make_tmap_out(CUtensorMap *m, void *ptr, int64_t M, int64_t N, int64_t ld, 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The output of the gated kernels: bf16 [M, N] with a row pitch of ld elements;
+// 64 x 32 boxes with the 128-byte swizzle of their staging buffers.
+bool make_tmap_out64(CUtensorMap *m, void *ptr, int64_t M, int64_t N, int64_t ld)
+{
+    EncodeTiledFn enc = encode_fn();
+    if (!enc)
+        return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(M)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+    const cuuint32_t box[2] = {64, 32};
+    const cuuint32_t estr[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, ptr, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // A batch of strided views (gemm_batched): row pitches and batch strides in
 // elements; sw == 0 means one W for every batch.
 struct BatchSpec {
@@ -1083,13 +1099,13 @@ static lf_status gated_launch(const void *x, const float *x_scale, const void *w
         return launched(lf::launch_gated_skinny(e4m3, act, ta, tw, gp, plan, gu, stream), 1);
     }
     CUtensorMap to, tg, tu;
-    if (!operands(lf::BM) || !make_tmap_out(&to, out, M, F, F, 1, M * F, false))
+    if (!operands(lf::BM) || !make_tmap_out64(&to, out, M, F, F))
         return LF_ERR_LAUNCH;
     tg = tu = to;
     if (gu) {
         // two views of gu, so that a box past column F is clipped there
-        if (!make_tmap_out(&tg, gu, M, F, 2 * F, 1, 2 * M * F, false) ||
-            !make_tmap_out(&tu, static_cast<char *>(gu) + 2 * F, M, F, 2 * F, 1, 2 * M * F, false))
+        if (!make_tmap_out64(&tg, gu, M, F, 2 * F) ||
+            !make_tmap_out64(&tu, static_cast<char *>(gu) + 2 * F, M, F, 2 * F))
             return LF_ERR_LAUNCH;
     }
     p.num_m_blocks = static_cast<int>((M + 2 * lf::BM - 1) / (2 * lf::BM));
@@ -1188,7 +1204,7 @@ static lf_status gated_ffn_backward_call(const void *dout, const void *x, const 
     const auto out_map = [&](int s, void *out) {
         const lf::GradSide &g = p.side[s];
         return g.split > 1 ? make_tmap_parts(&maps.o[s], parts + g.parts, g.M, g.N, g.split)
-                           : make_tmap_out(&maps.o[s], out, g.M, g.N, g.N, 1, static_cast<int64_t>(g.M) * g.N, false);
+                           : make_tmap_out64(&maps.o[s], out, g.M, g.N, g.N);
     };
     if (dx && (!make_tmap(&maps.a[0], dgu, M, 2 * F, lf::BM) || !mn_map(&maps.b[0], &p.side[0].b_3d, w, K, 2 * F) ||
                !out_map(0, dx)))

@@ -23,35 +23,62 @@ constexpr int G_TMEM_COLS = G_ACC_BUFS * BN;
 constexpr int G_NUM_BARS = 2 * G_STAGES + 2 * G_ACC_BUFS + 1;
 constexpr int G_EPI_WARPS = 8;
 constexpr int G_THREADS = 64 + 32 * G_EPI_WARPS;
-constexpr int G_STG_SLOT = 32 * 64;        // 32 rows x 32 bf16 columns
-constexpr int G_STG_WARP = 2 * G_STG_SLOT;
+constexpr int G_STG_WARP = 32 * 128;       // a warp's staging: 32 rows x 64 bf16 (or 32 fp32) columns
 constexpr int G_STG_OFF = ((G_SLOTS * G_SLOT_BYTES + G_NUM_BARS * 8 + 16 + 1023) / 1024) * 1024;
 constexpr int G_SMEM = 1024 + G_STG_OFF + G_EPI_WARPS * G_STG_WARP;
 static_assert(G_SMEM <= 232448, "shared memory per CTA");
 constexpr uint64_t G_ABORT_SETTLE_NS = 100000;
 
-// One 32 x 32 chunk of output (this thread's row as 16 packed pairs) through
-// staging slot k & 1 and a TMA store, as tma_store_chunk of gemm_nt_pair.cu.
-__device__ __forceinline__ void g_store_chunk(const CUtensorMap *tm, uint8_t *stg, uint32_t stg_s, int k,
-                                              const uint32_t (&pk)[16], int col, int row0, int M)
+// Stores of a finished tile go through a warp's staging buffer, 32 rows of 128
+// bytes whose 16-byte pieces are XOR-swizzled by row (the 128-byte swizzle of the
+// output's tensor map), and leave as one box.  (64-byte rows -- 32 bf16 columns a
+// store -- made the tensor-copy unit the bottleneck of tiles with short K loops.)
+//
+// Before the buffer is written again: the store issued from it has read it.
+__device__ __forceinline__ void stage_begin()
+{
+    if ((threadIdx.x & 31) == 0)
+        bulk_wait_group_read<0>();
+    __syncwarp();
+}
+// 16-byte piece j (0..7) of this thread's row.
+__device__ __forceinline__ void stage_piece(uint8_t *stg, int j, uint4 v)
 {
     const int lane = threadIdx.x & 31;
-    const int slot = k & 1;
-    if (k >= 2) {
-        if (lane == 0)
-            bulk_wait_group_read<1>();
-        __syncwarp();
-    }
-    uint8_t *buf = stg + slot * G_STG_SLOT;
+    *reinterpret_cast<uint4 *>(stg + lane * 128 + ((j ^ (lane & 7)) << 4)) = v;
+}
+// 32 values of this thread's row as bf16: half 0 or 1 of its 64 columns.
+__device__ __forceinline__ void stage_half(uint8_t *stg, int half, const float (&f)[32])
+{
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<uint4 *>(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
-            make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+        stage_piece(stg, 4 * half + j,
+                    make_uint4(pack_bf16(f[8 * j], f[8 * j + 1]), pack_bf16(f[8 * j + 2], f[8 * j + 3]),
+                               pack_bf16(f[8 * j + 4], f[8 * j + 5]), pack_bf16(f[8 * j + 6], f[8 * j + 7])));
+}
+// The buffer is full: lane 0 stores it at (col, row0); rows and columns outside
+// the map are left out.
+__device__ __forceinline__ void stage_end(const CUtensorMap *tm, uint32_t stg_s, int col, int row0, int M)
+{
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0 && row0 < M) {
-        tma_store_2d(tm, stg_s + static_cast<uint32_t>(slot * G_STG_SLOT), col, row0);
+    if ((threadIdx.x & 31) == 0 && row0 < M) {
+        tma_store_2d(tm, stg_s, col, row0);
         bulk_commit_group();
+    }
+}
+
+// Two runs of 32 accumulator columns of this thread's row.
+__device__ __forceinline__ void load_acc2(uint32_t t0, uint32_t t1, float (&f)[32], float (&g)[32])
+{
+    uint32_t v[32], w[32];
+    tmem_ld_32x32b_x32(t0, v);
+    tmem_ld_32x32b_x32(t1, w);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        f[i] = __uint_as_float(v[i]);
+        g[i] = __uint_as_float(w[i]);
     }
 }
 

@@ -84,67 +84,69 @@ __device__ __forceinline__ void g_tile_coords(const GemmParams &p, int tile, int
     nb = local / rows;
 }
 
-// The warp's 32 rows x columns [c0, c1) of a finished tile.  The gate of output
-// column c is accumulator column c, its up projection accumulator column 128 + c.
+// 32 columns of one projection as they stand for: f times the token's scale and
+// the output channels' (e4m3 operands), or f itself.
+template <bool E4M3>
+__device__ __forceinline__ void g_scale(float (&f)[32], float sx, const float *w_scale, int valid)
+{
+    if (E4M3) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+            if (i < valid) {  // N % 8 == 0
+                const float4 w = *reinterpret_cast<const float4 *>(w_scale + i);
+                f[i] *= sx * w.x;
+                f[i + 1] *= sx * w.y;
+                f[i + 2] *= sx * w.z;
+                f[i + 3] *= sx * w.w;
+            }
+        }
+    }
+}
+
+// The warp's 32 rows x 64 columns (from c0) of a finished tile.  The gate of
+// output column c is accumulator column c, its up projection accumulator column
+// 128 + c.  Returns once the accumulator has been read.
 template <bool E4M3, int ACT>
 __device__ __forceinline__ void g_epilogue(const GatedParams &gp, const CUtensorMap *tmO, const CUtensorMap *tmG,
-                                           const CUtensorMap *tmU, uint32_t taddr, int row0, int nb, int c0, int c1,
+                                           const CUtensorMap *tmU, uint32_t taddr, int row0, int nb, int c0,
                                            uint8_t *stg, uint32_t stg_s)
 {
     const GemmParams &p = gp.g;
     const int lane = threadIdx.x & 31;
+    const int col = nb * G_F + c0;
+    if (col >= p.N)
+        return;  // warp-uniform
     float sx = 1.f;
     if (E4M3)
         sx = row0 + lane < p.M ? gp.x_scale[row0 + lane] : 0.f;
-    int k = 0;
+    // (the accumulator is read before the wait for the staging buffer: the two overlap)
+    if (!E4M3 && gp.save) {
 #pragma unroll 1
-    for (int c = c0; c < c1; c += 32) {
-        const int col = nb * G_F + c;
-        if (col >= p.N)
-            break;  // warp-uniform
-        uint32_t g[32], u[32];
-        tmem_ld_32x32b_x32(taddr + static_cast<uint32_t>(c), g);
-        tmem_ld_32x32b_x32(taddr + static_cast<uint32_t>(G_F + c), u);
-        tmem_wait_ld();
-        if (E4M3) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-                if (col + i < p.N) {  // N % 8 == 0
-                    const float4 wg = *reinterpret_cast<const float4 *>(gp.w_scale + col + i);
-                    const float4 wu = *reinterpret_cast<const float4 *>(gp.w_scale + p.N + col + i);
-                    g[i] = __float_as_uint(__uint_as_float(g[i]) * (sx * wg.x));
-                    g[i + 1] = __float_as_uint(__uint_as_float(g[i + 1]) * (sx * wg.y));
-                    g[i + 2] = __float_as_uint(__uint_as_float(g[i + 2]) * (sx * wg.z));
-                    g[i + 3] = __float_as_uint(__uint_as_float(g[i + 3]) * (sx * wg.w));
-                    u[i] = __float_as_uint(__uint_as_float(u[i]) * (sx * wu.x));
-                    u[i + 1] = __float_as_uint(__uint_as_float(u[i + 1]) * (sx * wu.y));
-                    u[i + 2] = __float_as_uint(__uint_as_float(u[i + 2]) * (sx * wu.z));
-                    u[i + 3] = __float_as_uint(__uint_as_float(u[i + 3]) * (sx * wu.w));
-                }
-            }
+        for (int side = 0; side < 2; ++side) {
+            const uint32_t t = taddr + static_cast<uint32_t>(side * G_F + c0);
+            float f[32], h[32];
+            load_acc2(t, t + 32, f, h);
+            stage_begin();
+            stage_half(stg, 0, f);
+            stage_half(stg, 1, h);
+            stage_end(side ? tmU : tmG, stg_s, col, row0, p.M);
         }
-        uint32_t pk[16];
-        if (gp.save) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                pk[i] = pack_bf16(__uint_as_float(g[2 * i]), __uint_as_float(g[2 * i + 1]));
-            g_store_chunk(tmG, stg, stg_s, k++, pk, col, row0, p.M);
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                pk[i] = pack_bf16(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
-            g_store_chunk(tmU, stg, stg_s, k++, pk, col, row0, p.M);
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float g0 = __uint_as_float(g[2 * i]), g1 = __uint_as_float(g[2 * i + 1]);
-            pk[i] = pack_bf16(g0 * act_phi<ACT>(g0) * __uint_as_float(u[2 * i]),
-                              g1 * act_phi<ACT>(g1) * __uint_as_float(u[2 * i + 1]));
-        }
-        g_store_chunk(tmO, stg, stg_s, k++, pk, col, row0, p.M);
     }
-    if (lane == 0)
-        bulk_wait_group_read<0>();  // the staging slots are free for the next tile
-    __syncwarp();
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const uint32_t t = taddr + static_cast<uint32_t>(c0 + 32 * half);
+        float g[32], u[32];
+        load_acc2(t, t + G_F, g, u);
+        g_scale<E4M3>(g, sx, gp.w_scale + col + 32 * half, p.N - col - 32 * half);
+        g_scale<E4M3>(u, sx, gp.w_scale + p.N + col + 32 * half, p.N - col - 32 * half);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            g[i] = g[i] * act_phi<ACT>(g[i]) * u[i];
+        if (half == 0)
+            stage_begin();
+        stage_half(stg, half, g);
+    }
+    stage_end(tmO, stg_s, col, row0, p.M);
 }
 
 template <bool E4M3, int ACT>
@@ -331,7 +333,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             tc_fence_after();
             g_epilogue<E4M3, ACT>(gp, &tmO, &tmG, &tmU,
                                   tmem_base + static_cast<uint32_t>(acc * BN) + (static_cast<uint32_t>(q * 32) << 16),
-                                  mb * G_M + static_cast<int>(rank) * BM + q * 32, nb, c0, c0 + G_F / 2, stg, stg_s);
+                                  mb * G_M + static_cast<int>(rank) * BM + q * 32, nb, c0, stg, stg_s);
             tc_fence_before();
             __syncwarp();
             if (lane == 0)

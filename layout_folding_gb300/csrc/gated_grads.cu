@@ -110,30 +110,6 @@ __device__ __forceinline__ void load_mn(uint32_t dst, const CUtensorMap *m, bool
     }
 }
 
-// One 32 x 32 chunk of a part's fp32 sums (this thread's row) into the part's
-// matrix (`part`: the map's third coordinate), through the warp's whole 4 KiB of
-// staging: 128-byte rows, 16-byte pieces XOR-swizzled by row.
-__device__ __forceinline__ void store_part(const CUtensorMap *tm, uint8_t *stg, uint32_t stg_s, int k,
-                                           const uint32_t (&v)[32], int col, int row0, int part, int M)
-{
-    const int lane = threadIdx.x & 31;
-    if (k > 0) {
-        if (lane == 0)
-            bulk_wait_group_read<0>();
-        __syncwarp();
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        *reinterpret_cast<uint4 *>(stg + lane * 128 + ((j ^ (lane & 7)) << 4)) =
-            make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0 && row0 < M) {
-        tma_store_3d(tm, stg_s, col, row0, part);
-        bulk_commit_group();
-    }
-}
-
 // What the producer and the MMA issuer keep across items.
 struct RingPos {
     int stage = 0;
@@ -357,27 +333,39 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             if (!__all_sync(0xffffffffu, ok))
                 break;
             tc_fence_after();
-            int k = 0;
+            // 64 columns at a time, read before the wait for the staging buffer (the two overlap)
 #pragma unroll 1
-            for (int c = c0; c < c1; c += 32, ++k) {
+            for (int c = c0; c < c1; c += 64) {
                 const int col = it.nb * BN + c;
                 if (col >= g.N)
                     break;  // warp-uniform
-                uint32_t v[32];
-                tmem_ld_32x32b_x32(taddr + static_cast<uint32_t>(c), v);
-                tmem_wait_ld();
-                if (g.split > 1) {
-                    store_part(&maps.o[it.side], stg, stg_s, k, v, col, row0, it.part, g.M);
-                } else {
-                    uint32_t pk[16];
+                float f[2][32];
+                load_acc2(taddr + static_cast<uint32_t>(c), taddr + static_cast<uint32_t>(c + 32), f[0], f[1]);
+                stage_begin();
+                if (g.split == 1) {
+                    stage_half(stg, 0, f[0]);
+                    stage_half(stg, 1, f[1]);
+                    stage_end(&maps.o[it.side], stg_s, col, row0, g.M);
+                    continue;
+                }
+                // fp32 into the part's matrix (the map's third coordinate), 32 columns a store
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        pk[i] = pack_bf16(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-                    g_store_chunk(&maps.o[it.side], stg, stg_s, k, pk, col, row0, g.M);
+                for (int half = 0; half < 2; ++half) {
+                    if (half)
+                        stage_begin();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        stage_piece(stg, j,
+                                    make_uint4(__float_as_uint(f[half][4 * j]), __float_as_uint(f[half][4 * j + 1]),
+                                               __float_as_uint(f[half][4 * j + 2]), __float_as_uint(f[half][4 * j + 3])));
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && row0 < g.M && col + 32 * half < g.N) {
+                        tma_store_3d(&maps.o[it.side], stg_s, col + 32 * half, row0, it.part);
+                        bulk_commit_group();
+                    }
                 }
             }
-            if (lane == 0)
-                bulk_wait_group_read<0>();
             tc_fence_before();
             __syncwarp();
             if (lane == 0)

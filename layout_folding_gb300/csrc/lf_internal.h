@@ -128,7 +128,8 @@ struct GatedParams {
     int save;                        // also store gate and up (tg, tu)
 };
 // ta: x, boxes of 128 rows; tw: w [2F, K], boxes of 128 rows (both 128-byte
-// rows, 128-byte swizzle); to: out; tg, tu: the two halves of gu (32 x 32 boxes).
+// rows, 128-byte swizzle); to: out; tg, tu: the two halves of gu (64 x 32
+// boxes, 128-byte swizzle).
 cudaError_t launch_gated_pair(bool e4m3, int act, const CUtensorMap &ta, const CUtensorMap &tw, const CUtensorMap &to,
                               const CUtensorMap &tg, const CUtensorMap &tu, const GatedParams &p, int grid,
                               cudaStream_t s);
@@ -164,7 +165,7 @@ struct GradsParams {
     int first, rounds;    // the schedule (GradIter)
     int64_t part_floats;  // of all parts
 };
-// o: the output (bf16, 32 x 32 boxes) or, where the side is split, its parts
+// o: the output (bf16, 64 x 32 boxes, 128-byte swizzle) or, where the side is split, its parts
 // (fp32, 3-D: N, M, split; 32 x 32 x 1 boxes, 128-byte swizzle).
 struct GradMaps {
     CUtensorMap a[2], b[2], o[2];
