@@ -343,3 +343,60 @@ def test_block_training_and_generation():
     if D % 16 == 0:
         qw, sw = quantised(w.float())
         lf.gated_ffn(q, qw.to(DEV), x_scale=s, w_scale=sw.to(DEV))
+
+
+@pytest.mark.parametrize("M,F,K", [(300, 264, 520), (33, 2056, 264)])
+def test_stalled_wait_in_the_gradient_times_out(M, F, K):
+    x, w = inputs(M, F, K)
+    gu = ref.gated(x.double(), w.double(), "silu")[1].to(BF16)
+    dout = normal((M, F), 9).to(BF16)
+    dev = [t.to(DEV) for t in (dout, x, w, gu)]
+    lf.check_device_error()
+    lf.set_test_hooks(True, 200_000_000)
+    try:
+        lf.gated_ffn_backward(*dev)
+        with pytest.raises(lf.LayoutFoldError) as info:
+            lf.check_device_error()
+        assert info.value.status == 6 and lf.last_device_wait_code() in lf.WAIT_CODES
+    finally:
+        lf.set_test_hooks(False, 0)
+    dx, dw = lf.gated_ffn_backward(*dev)
+    lf.check_device_error()
+    check_backward(dout, x, w, gu, "silu", dx, dw)
+
+
+def test_tokens_and_sums_of_every_size():
+    """Sizes around the tile, split and stage borders of every kernel, forward and
+    backward, norm-wise (the element bounds are test_forward's and test_backward's):
+    at most HALF for an output rounded once, 1.1 HALF where the gradient of the
+    projections was rounded as well."""
+    for M in (1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 191, 255, 256, 257, 511, 513):
+        for F, K in ((8, 16), (120, 64), (128, 136), (136, 1040), (1000, 128)):
+            x, w = inputs(M, F, K, M + F + K)
+            xd, wd = x.to(DEV), w.to(DEV)
+            out, gu = lf.gated_ffn(xd, wd, want_gu=True)
+            want, p = ref.gated(x.double(), w.double(), "silu")
+            for a, b in ((out, want), (gu, p)):
+                assert float((a.double().cpu() - b).norm()) <= HALF * float(b.norm()), (M, F, K)
+            dout = normal((M, F), M).to(BF16)
+            dx, dw = lf.gated_ffn_backward(dout.to(DEV), xd, wd, gu)
+            g64 = gu.double().cpu().requires_grad_()
+            (dgu,) = ref.grads(ref.gated_from_gu(g64, "silu"), (g64,), dout.double())
+            for a, b in ((dx, dgu @ w.double()), (dw, dgu.t() @ x.double())):
+                assert float((a.double().cpu() - b).norm()) <= 1.1 * HALF * float(b.norm()), (M, F, K)
+    lf.check_device_error()
+
+
+def test_example_block_learns():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "ffn_block.py")
+    spec = importlib.util.spec_from_file_location("ffn_block", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    losses, off = mod.main(["--tokens", "200", "--hidden", "256", "--ffn", "520", "--steps", "12"])
+    assert losses[-1] < 0.7 * losses[0]
+    # e4m3 activations and weights: each product is off by two roundings of at most
+    # 2^-4, of random sign, so the block's output by well under sqrt(3) 2^-4 (gate, up and
+    # their product)
+    assert off < 3 ** 0.5 * 2 ** -4
