@@ -138,6 +138,55 @@ __device__ __forceinline__ Pack<T, VEC> load_pack(const T *p)
     return r;
 }
 
+// Two fp32 operations per instruction (each half rounded as the scalar one).
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+// max(|a|, |b|, |c|), a NaN kept
+__device__ __forceinline__ float max_mag3(float a, float b, float c)
+{
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// The values of a pack, two at a time.
+template <class T, int VEC>
+__device__ __forceinline__ void get2(const Pack<T, VEC> &p, float2 (&f)[VEC / 2])
+{
+    float v[VEC];
+    p.get(v);
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i)
+        f[i] = make_float2(v[2 * i], v[2 * i + 1]);
+}
+template <class T, int VEC>
+__device__ __forceinline__ void set2(Pack<T, VEC> &p, const float2 (&f)[VEC / 2])
+{
+    float v[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) {
+        v[2 * i] = f[i].x;
+        v[2 * i + 1] = f[i].y;
+    }
+    p.set(v);
+}
+
 // max(|m|, |a|), a NaN kept: the running maximum of magnitudes (its sign is not
 // meaningful until mag() clears it).
 __device__ __forceinline__ float max_mag(float m, float a)
@@ -209,6 +258,13 @@ struct RowScale {
 #pragma unroll
             for (int i = 0; i < N; ++i)
                 f[i] = f[i] * r / scale;
+        } else if constexpr (N % 2 == 0) {
+#pragma unroll
+            for (int i = 0; i < N; i += 2) {
+                const float2 v = mul2(make_float2(f[i], f[i + 1]), both(factor));
+                f[i] = v.x;
+                f[i + 1] = v.y;
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < N; ++i)
@@ -276,7 +332,7 @@ __global__ void __launch_bounds__(NV <= 2 ? 512 : 1024) k_rms_norm(const NormPar
         for (int j = 0; j < NV; ++j) {
             const int c = threadIdx.x + j * blockDim.x;
             if (c < packs) {
-float v[VEC];
+                float v[VEC];
                 h[j].get(v);
 #pragma unroll
                 for (int i = 0; i < VEC; ++i)
@@ -774,8 +830,12 @@ __device__ __forceinline__ W *ring_weights(uint8_t *smem, const RingPlan &r, con
     return ws;
 }
 
+// Threads of a forward block: the e4m3 form keeps the row's products in fp32 and
+// gets 72 registers for it instead of 64.
+__host__ __device__ constexpr int ring_threads(bool fp8) { return fp8 ? 896 : 1024; }
+
 template <class T, class W, bool FP8, bool PH>
-__global__ void __launch_bounds__(1024) k_rms_norm_ring(const NormParams p, const RingPlan r)
+__global__ void __launch_bounds__(ring_threads(FP8)) k_rms_norm_ring(const NormParams p, const RingPlan r)
 {
     constexpr int VEC = 16 / static_cast<int>(sizeof(T));
     extern __shared__ __align__(128) uint8_t smem[];
@@ -807,34 +867,42 @@ __global__ void __launch_bounds__(1024) k_rms_norm_ring(const NormParams p, cons
     int buf = 0;
     for (int64_t row = row0; row < p.M; row += step, buf ^= 1) {
         ok = ring_wait(ring.full_s + 8u * ring.slot, ring.phase, p.limit);
-        Pack<T, VEC> h[RING_NV];
-        float ss = 0.f;
+        // what the second half needs of the row: h, or for e4m3 its products with the weights
+        Pack<T, VEC> h[FP8 ? 1 : RING_NV];
+        float2 hw[FP8 ? RING_NV : 1][VEC / 2];
+        float2 ss2 = both(0.f);
         float mx = 0.f;
 #pragma unroll
         for (int j = 0; j < RING_NV; ++j) {
             const int c = t + j * r.group_threads;
             if (c < packs) {
-                h[j] = load_pack<T, VEC>(reinterpret_cast<const T *>(ring.input(0)) + c * VEC);
+                Pack<T, VEC> v = load_pack<T, VEC>(reinterpret_cast<const T *>(ring.input(0)) + c * VEC);
                 if (res) {
-                    h[j].add(load_pack<T, VEC>(reinterpret_cast<const T *>(ring.input(1)) + c * VEC));
-                    span.store(static_cast<T *>(p.h), row, c, h[j]);
+                    v.add(load_pack<T, VEC>(reinterpret_cast<const T *>(ring.input(1)) + c * VEC));
+                    span.store(static_cast<T *>(p.h), row, c, v);
                 }
-                span.mask(h[j], c);
-float v[VEC];
-                h[j].get(v);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i)
-                    ss = fmaf(v[i], v[i], ss);
+                span.mask(v, c);
+                float2 f[VEC / 2];
+                get2<T, VEC>(v, f);
                 if (FP8) {
-                    float wv[VEC];
-                    load_pack<W, VEC>(w + c * VEC).get(wv);
+                    float2 wv[VEC / 2];
+                    get2<W, VEC>(load_pack<W, VEC>(w + c * VEC), wv);
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i)
-                        mx = max_mag(mx, v[i] * wv[i]);
+                    for (int i = 0; i < VEC / 2; ++i) {
+                        ss2 = fma2(f[i], f[i], ss2);
+                        const float2 m = mul2(f[i], wv[i]);
+                        hw[FP8 ? j : 0][i] = m;
+                        mx = max_mag3(mx, m.x, m.y);
+                    }
+                } else {
+                    h[FP8 ? 0 : j] = v;
+#pragma unroll
+                    for (int i = 0; i < VEC / 2; ++i)
+                        ss2 = fma2(f[i], f[i], ss2);
                 }
             }
         }
-        const float2 sums = group_reduce<true>(ss, mag_bits(mx), ok, sy, buf, first_warp, warps, 1 + group);
+        const float2 sums = group_reduce<true>(ss2.x + ss2.y, mag_bits(mx), ok, sy, buf, first_warp, warps, 1 + group);
         if (!ok)
             break;
         if (t == 0 && row + r.slots * step < p.M)
@@ -848,21 +916,24 @@ float v[VEC];
         for (int j = 0; j < RING_NV; ++j) {
             const int c = t + j * r.group_threads;
             if (c < packs) {
-                float f[VEC], wv[VEC];
-                h[j].get(f);
-                load_pack<W, VEC>(w + c * VEC).get(wv);
                 if (FP8) {
+                    float f[VEC];
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i)
-                        f[i] *= wv[i];
+                    for (int i = 0; i < VEC / 2; ++i) {
+                        f[2 * i] = hw[FP8 ? j : 0][i].x;
+                        f[2 * i + 1] = hw[FP8 ? j : 0][i].y;
+                    }
                     rs.apply(f, rr);
                     span.store_codes(static_cast<uint8_t *>(p.y), row, c, f);
                 } else {
+                    float2 f[VEC / 2], wv[VEC / 2];
+                    get2<T, VEC>(h[FP8 ? 0 : j], f);
+                    get2<W, VEC>(load_pack<W, VEC>(w + c * VEC), wv);
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i)
-                        f[i] *= rr * wv[i];
+                    for (int i = 0; i < VEC / 2; ++i)
+                        f[i] = mul2(f[i], mul2(both(rr), wv[i]));
                     Pack<T, VEC> yv;
-                    yv.set(f);
+                    set2<T, VEC>(yv, f);
                     span.store(static_cast<T *>(p.y), row, c, yv);
                 }
             }
@@ -907,18 +978,18 @@ __global__ void __launch_bounds__(512) k_rms_norm_bwd_ring(const NormBwdParams p
             fill(i, row0 + i * step);
     }
     const W *w = ring_weights<W, PH>(smem, r, static_cast<const W *>(p.weight), span);
-    float acc[RING_NV][VEC];
+    float2 acc[RING_NV][VEC / 2];
 #pragma unroll
     for (int j = 0; j < RING_NV; ++j)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i)
-            acc[j][i] = 0.f;
+        for (int i = 0; i < VEC / 2; ++i)
+            acc[j][i] = both(0.f);
     bool ok = true;
     int buf = 0;
     for (int64_t row = row0; row < p.M; row += step, buf ^= 1) {
         ok = ring_wait(ring.full_s + 8u * ring.slot, ring.phase, p.limit);
         Pack<T, VEC> h[RING_NV], dy[RING_NV], dh[DH ? RING_NV : 1];
-        float ss = 0.f, gh = 0.f;
+        float2 ss = both(0.f), gh = both(0.f);
 #pragma unroll
         for (int j = 0; j < RING_NV; ++j) {
             const int c = t + j * r.group_threads;
@@ -929,18 +1000,19 @@ __global__ void __launch_bounds__(512) k_rms_norm_bwd_ring(const NormBwdParams p
                 span.mask(dy[j], c);
                 if (DH)
                     dh[DH ? j : 0] = load_pack<T, VEC>(reinterpret_cast<const T *>(ring.input(2)) + c * VEC);
-                float v[VEC], d[VEC], wv[VEC];
-                h[j].get(v);
-                dy[j].get(d);
-                load_pack<W, VEC>(w + c * VEC).get(wv);
+                float2 v[VEC / 2], d[VEC / 2], wv[VEC / 2];
+                get2<T, VEC>(h[j], v);
+                get2<T, VEC>(dy[j], d);
+                get2<W, VEC>(load_pack<W, VEC>(w + c * VEC), wv);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    ss = fmaf(v[i], v[i], ss);
-                    gh = fmaf(d[i] * wv[i], v[i], gh);
+                for (int i = 0; i < VEC / 2; ++i) {
+                    ss = fma2(v[i], v[i], ss);
+                    gh = fma2(mul2(d[i], wv[i]), v[i], gh);
                 }
             }
         }
-        const float2 sums = group_reduce<false>(ss, __float_as_uint(gh), ok, sy, buf, first_warp, warps, 1 + group);
+        const float2 sums = group_reduce<false>(ss.x + ss.y, __float_as_uint(gh.x + gh.y), ok, sy, buf, first_warp, warps,
+                                                1 + group);
         if (!ok)
             break;
         if (t == 0 && row + r.slots * step < p.M)
@@ -952,24 +1024,20 @@ __global__ void __launch_bounds__(512) k_rms_norm_bwd_ring(const NormBwdParams p
         for (int j = 0; j < RING_NV; ++j) {
             const int c = t + j * r.group_threads;
             if (c < packs) {
-                float v[VEC], d[VEC], wv[VEC], o[VEC];
-                h[j].get(v);
-                dy[j].get(d);
-                load_pack<W, VEC>(w + c * VEC).get(wv);
-                if (DH) {
-                    dh[DH ? j : 0].get(o);
-                } else {
+                float2 v[VEC / 2], d[VEC / 2], wv[VEC / 2], o[VEC / 2];
+                get2<T, VEC>(h[j], v);
+                get2<T, VEC>(dy[j], d);
+                get2<W, VEC>(load_pack<W, VEC>(w + c * VEC), wv);
+                if (DH)
+                    get2<T, VEC>(dh[DH ? j : 0], o);
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i)
-                        o[i] = 0.f;
-                }
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    acc[j][i] = fmaf(d[i], v[i] * rr, acc[j][i]);
-                    o[i] = fmaf(rr, fmaf(d[i], wv[i], -v[i] * k), o[i]);
+                for (int i = 0; i < VEC / 2; ++i) {
+                    acc[j][i] = fma2(d[i], mul2(v[i], both(rr)), acc[j][i]);
+                    const float2 g = fma2(d[i], wv[i], mul2(v[i], both(-k)));
+                    o[i] = DH ? fma2(both(rr), g, o[i]) : mul2(both(rr), g);
                 }
                 Pack<T, VEC> dx;
-                dx.set(o);
+                set2<T, VEC>(dx, o);
                 span.store(static_cast<T *>(p.dx), row, c, dx);
             }
         }
@@ -992,7 +1060,7 @@ __global__ void __launch_bounds__(512) k_rms_norm_bwd_ring(const NormBwdParams p
                 const int c = t + j * r.group_threads;
                 if (c < packs) {
                     Pack<float, VEC> a;
-                    a.set(acc[j]);
+                    set2<float, VEC>(a, acc[j]);
                     if (g > 0)
                         a.add(load_pack<float, VEC>(dw + c * VEC));
                     if (PH || g + 1 < r.groups)
@@ -1099,7 +1167,7 @@ cudaError_t launch_norm_t(const NormParams &p, Rows rows, int num_sms, cudaStrea
     constexpr int V = 16 / static_cast<int>(sizeof(T));
     RingPlan r;
     if (rows != ROWS_ANY && p.M >= RING_MIN_ROWS && num_sms >= 8 &&
-        plan_ring(&r, rows == ROWS_PHASED, p.D, sizeof(T), sizeof(W), p.residual ? 2 : 1, 1024))
+        plan_ring(&r, rows == ROWS_PHASED, p.D, sizeof(T), sizeof(W), p.residual ? 2 : 1, ring_threads(FP8)))
         return rows == ROWS_PHASED ? launch_norm_ring<T, W, FP8, true>(p, r, num_sms, s)
                                    : launch_norm_ring<T, W, FP8, false>(p, r, num_sms, s);
     cudaError_t e = cudaSuccess;
