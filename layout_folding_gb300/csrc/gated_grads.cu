@@ -9,10 +9,11 @@
 // most of all, whose tiles are few and long (4096 x 5120 x 13824: 320 tiles of 432
 // K blocks are 4.2 waves of 76 pairs, so a fifth wave for a fifth of the pairs).
 // Here the pairs without a tile of that last wave start on the other product, whose
-// tiles are short, and all of them end within one short tile of each other:
-// 1343 us for the two launches, see k_gated_grads' figures below.  The schedule
-// is fixed (GradIter), so no pair waits for another, replays of a captured call
-// are the same, and every output is summed in the same order every time.
+// tiles are short, and all of them end within one short tile of each other: 1280 us
+// in a burst (1.81 PFLOP/s) where two launches took 685 + 636.  The schedule is
+// fixed (GradIter), so no pair waits for another, replays of a captured call are
+// the same, and every output is summed in the same order every time.  What
+// bounds it: the tensor cores, and over many calls the power limit.
 //
 // A product with too few tiles to go round has its K blocks split: each part
 // leaves its sums in fp32 in the caller's scratch, and a last, elementwise kernel
@@ -123,9 +124,11 @@ struct RingPos {
     }
 };
 
+// Two K blocks per ring stage: 1381 us for the whole call against 1392 with one.
 // After a wait that gave up (`alive` false) the producer and the MMA issuer walk
 // through their remaining steps without doing any: loops that never leave early
-// keep their indexes, and so the MMA descriptors, warp-uniform.
+// keep their indexes, and so the MMA descriptors, warp-uniform (with early exits
+// the call took 1525 us).
 // One item's copies (one thread of each CTA).  A_MN: side 1, whose A operand is MN-major.
 template <bool A_MN>
 __device__ __forceinline__ void produce_item(const GemmParams &p, const GradItem &it, const CUtensorMap *tA,
