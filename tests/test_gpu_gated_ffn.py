@@ -400,3 +400,26 @@ def test_example_block_learns():
     # 2^-4, of random sign, so the block's output by well under sqrt(3) 2^-4 (gate, up and
     # their product)
     assert off < 3 ** 0.5 * 2 ** -4
+
+
+def test_offsets_past_32_bits():
+    """gu and dgu of more than 2^31 elements (M 2F): rows at both ends and at the border,
+    and the weight gradient of a block of columns."""
+    M, F, K = 300_000, 4096, 64
+    w = inputs(1, F, K)[1]
+    g = torch.Generator(device=DEV).manual_seed(1)
+    xd = torch.empty(M, K, dtype=BF16, device=DEV).normal_(generator=g)
+    wd = w.to(DEV)
+    border = 2 ** 31 // (2 * F)
+    rows = torch.tensor([0, 255, border - 1, border, border + 1, M - 1], device=DEV)
+    out, gu = lf.gated_ffn(xd, wd, want_gu=True)
+    x = xd[rows].cpu()
+    gus = gu[rows].cpu()
+    check_forward(x.double(), w.double(), "silu", out[rows], gus)
+    dx, dw = lf.gated_ffn_backward(out, xd, wd, gu, dgu=gu)
+    outs = out[rows].cpu()
+    check_backward(outs, x, w, gus, "silu", dx[rows], None)
+    # dgu now lies in gu: the weight gradient of its last 64 columns
+    want = gu[:, -64:].double().t() @ xd.double()
+    assert float((dw[-64:].double() - want).norm()) <= HALF * float(want.norm())
+    lf.check_device_error()

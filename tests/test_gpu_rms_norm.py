@@ -399,3 +399,22 @@ def test_on_a_side_stream_and_captured():
         torch.cuda.synchronize()
         check_forward(x.cpu(), w.cpu(), res.cpu(), True, q)
         check_backward(res.cpu(), q[1].cpu(), w.cpu(), x.cpu(), grad)
+
+
+@pytest.mark.parametrize("M,D", [(525_000, 4104), (300_001, 7171)])
+def test_offsets_past_32_bits(M, D):
+    """More than 2^31 elements: rows at both ends and around the border."""
+    w = 1 + normal((D,), 3, 0.2)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.empty(M, D, dtype=BF16, device=DEV).normal_(generator=g)
+    res = torch.empty(M, D, dtype=BF16, device=DEV).normal_(generator=g)
+    border = 2 ** 31 // D
+    rows = torch.tensor([0, 1, border - 1, border, border + 1, M - 2, M - 1], device=DEV)
+    xs, rs = x[rows].cpu(), res[rows].cpu()
+    q, h, s = lf.add_rms_norm(x, w.to(DEV), residual=res, eps=EPS, fp8=True)
+    hs = h[rows]
+    check_forward(xs, w, rs, True, (q.view(torch.uint8)[rows].view(E4M3), hs, s[rows]))
+    del q, s
+    dx, _ = lf.add_rms_norm_backward(x, h, w.to(DEV), dh=res, eps=EPS, dx=res)
+    check_backward(xs, hs.cpu(), w, rs, (dx[rows], None))
+    lf.check_device_error()
