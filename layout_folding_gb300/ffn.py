@@ -10,6 +10,8 @@ tensors).
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
 import layout_folding_gb300 as _lf
@@ -47,6 +49,16 @@ def _lib():
     if _L is None:
         _L = _lf.lib()
     return _L
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_scratch(M, D):
+    return _lib().add_rms_norm_backward_scratch(M, D)
+
+
+@functools.lru_cache(maxsize=1024)
+def _gated_scratch(M, F, K):
+    return _lib().gated_ffn_backward_scratch(M, F, K)
 
 
 def _handle(stream, device):
@@ -96,10 +108,11 @@ def _stream_type(t, name):
 
 
 def _weight_type(weight, code, dtype, D, device):
-    wcode = _CODES.get(weight.dtype, -1) if isinstance(weight, torch.Tensor) else -1
+    wcode = _CODES.get(weight.dtype, -1) if isinstance(weight, _Tensor) else -1
     if wcode != code and wcode != LF_FP32:
         raise TypeError("weight must be a %s or float32 tensor" % dtype)
-    _require(weight, weight.dtype, device, "weight")
+    if weight.get_device() != device or not weight.is_contiguous():
+        _require(weight, weight.dtype, device, "weight")
     if weight.numel() != D:
         raise ValueError("weight must hold D = %d elements" % D)
     return wcode
@@ -141,19 +154,24 @@ def add_rms_norm(x, weight, residual=None, eps=1e-6, fp8=False, h=None, y=None, 
     x, residual: bf16, fp16 or fp32 [..., D], contiguous or 2-D slices of wider
     rows; weight [D] in x's type or fp32.  h may be passed as residual (or x)
     itself, to update a contiguous stream in place."""
-    code, dev = _stream_type(x, "x")
-    dtype, shape = x.dtype, x.shape
+    dtype = getattr(x, "dtype", None)
+    code = _CODES.get(dtype, -1)
+    dev = x.get_device() if code >= 0 else -1
+    shape = x.shape if dev >= 0 else ()
+    if not shape:
+        _stream_type(x, "x")  # raises
     D = shape[-1]
     M = x.numel() // D if D else 0
     ldx = D if x.is_contiguous() else _pitch(x, "x")
-    ldr, r_ptr, h_ptr = 0, None, None
     wcode = _weight_type(weight, code, dtype, D, dev)
+    ldr = 0
+    r_ptr = h_ptr = s_ptr = None
     if residual is not None:
-        _cuda(residual, "residual")
-        if residual.dtype != dtype:
-            raise TypeError("residual must be %s, got %s" % (dtype, residual.dtype))
-        if residual.shape != shape or residual.get_device() != dev:
-            raise ValueError("residual must have x's shape and device")
+        if not isinstance(residual, _Tensor) or residual.dtype != dtype or residual.get_device() != dev:
+            _cuda(residual, "residual")
+            raise TypeError("residual must be %s on cuda:%d" % (dtype, dev))
+        if residual.shape != shape:
+            raise ValueError("residual must have x's shape")
         ldr = D if residual.is_contiguous() else _pitch(residual, "residual")
         r_ptr = residual.data_ptr()
         h = _new(shape, dtype, x, dev) if h is None else _output(h, dtype, shape, dev, "h")
@@ -162,16 +180,15 @@ def add_rms_norm(x, weight, residual=None, eps=1e-6, fp8=False, h=None, y=None, 
         raise ValueError("h is written only where a residual is added")
     if fp8:
         y = _new(shape, _FP8, x, dev) if y is None else _output(y, _FP8, shape, dev, "y")
-        scale = (_new(shape[:-1], _F32, x, dev) if scale is None
-                 else _output(scale, _F32, shape[:-1], dev, "scale"))
+        scale = _new(shape[:-1], _F32, x, dev) if scale is None else _output(scale, _F32, shape[:-1], dev, "scale")
+        s_ptr = scale.data_ptr()
     else:
         if scale is not None:
             raise ValueError("scale is written only with fp8")
         y = _new(shape, dtype, x, dev) if y is None else _output(y, dtype, shape, dev, "y")
     if M > 0 or D == 0:
-        st = _lib().add_rms_norm(x.data_ptr(), ldx, r_ptr, ldr, weight.data_ptr(), h_ptr, y.data_ptr(),
-                                 scale.data_ptr() if fp8 else None, code, wcode, LF_E4M3 if fp8 else code, eps, M, D,
-                                 _handle(stream, dev))
+        st = _lib().add_rms_norm(x.data_ptr(), ldx, r_ptr, ldr, weight.data_ptr(), h_ptr, y.data_ptr(), s_ptr, code,
+                                 wcode, LF_E4M3 if fp8 else code, eps, M, D, _handle(stream, dev))
         if st:
             _lf._check(st, "add_rms_norm")
     return y, (x if residual is None else h), scale
@@ -182,8 +199,12 @@ def add_rms_norm_backward(dy, h, weight, dh=None, eps=1e-6, want_dweight=True, d
     arriving at h by other ways, or None) contiguous [..., D] of one type.
     Returns (dx, dweight): dx in h's type is the gradient of x and of residual,
     dweight has weight's type (None when not wanted)."""
-    code, dev = _stream_type(h, "h")
-    dtype, shape = h.dtype, h.shape
+    dtype = getattr(h, "dtype", None)
+    code = _CODES.get(dtype, -1)
+    dev = h.get_device() if code >= 0 else -1
+    shape = h.shape if dev >= 0 else ()
+    if not shape:
+        _stream_type(h, "h")  # raises
     _require(h, dtype, dev, "h")
     _require(dy, dtype, dev, "dy")
     if dy.shape != shape:
@@ -191,27 +212,27 @@ def add_rms_norm_backward(dy, h, weight, dh=None, eps=1e-6, want_dweight=True, d
     D = shape[-1]
     M = h.numel() // D if D else 0
     wcode = _weight_type(weight, code, dtype, D, dev)
+    dh_ptr = dw_ptr = scratch = scratch_ptr = None
     if dh is not None:
         _require(dh, dtype, dev, "dh")
         if dh.shape != shape:
             raise ValueError("dh must have h's shape")
+        dh_ptr = dh.data_ptr()
     dx = _new(shape, dtype, h, dev) if dx is None else _output(dx, dtype, shape, dev, "dx")
-    want = want_dweight or dweight is not None
-    if want:
+    if want_dweight or dweight is not None:
         dweight = (_new(weight.shape, weight.dtype, h, dev) if dweight is None
                    else _output(dweight, weight.dtype, weight.shape, dev, "dweight"))
+        if M > 0:
+            scratch = _new((_norm_scratch(M, D),), torch.uint8, h, dev)
+            if stream is not None:
+                scratch.record_stream(stream)
+            dw_ptr, scratch_ptr = dweight.data_ptr(), scratch.data_ptr()
     if M == 0 and D > 0:
         return dx, _zeroed(dweight, stream)
-    L = _lib()
-    scratch = None
-    if want:
-        scratch = _new((L.add_rms_norm_backward_scratch(M, D),), torch.uint8, h, dev)
-        if stream is not None:
-            scratch.record_stream(stream)
-    _lf._check(L.add_rms_norm_backward(dy.data_ptr(), h.data_ptr(), weight.data_ptr(),
-                                       None if dh is None else dh.data_ptr(), dx.data_ptr(),
-                                       dweight.data_ptr() if want else None, scratch.data_ptr() if want else None,
-                                       code, wcode, eps, M, D, _handle(stream, dev)), "add_rms_norm_backward")
+    st = _lib().add_rms_norm_backward(dy.data_ptr(), h.data_ptr(), weight.data_ptr(), dh_ptr, dx.data_ptr(), dw_ptr,
+                                      scratch_ptr, code, wcode, eps, M, D, _handle(stream, dev))
+    if st:
+        _lf._check(st, "add_rms_norm_backward")
     return dx, dweight
 
 
@@ -288,7 +309,7 @@ def gated_ffn_backward(dout, x, w, gu, act="silu", want_dx=True, want_dw=True, d
     if M == 0 and F > 0 and K > 0:
         return dx, _zeroed(dw, stream)
     L = _lib()
-    nbytes = L.gated_ffn_backward_scratch(M, F, K)
+    nbytes = _gated_scratch(M, F, K)
     scratch = _new((nbytes,), torch.uint8, x, dev) if nbytes else None
     if scratch is not None and stream is not None:
         scratch.record_stream(stream)
