@@ -1092,8 +1092,8 @@ static lf_status gated_launch(const void *x, const float *x_scale, const void *w
         return e4m3 ? make_tmap_e4m3(&ta, x, M, K, x_rows) && make_tmap_e4m3(&tw, w, 2 * F, K, lf::BN / 2)
                     : make_tmap(&ta, x, M, K, x_rows) && make_tmap(&tw, w, 2 * F, K, lf::BN / 2);
     };
-    if (M <= lf::BM) {
-        const lf::GatedSkinny plan = lf::plan_gated_skinny(M, F, p.num_k_blocks, d->num_sms);
+    const lf::GatedSkinny plan = lf::plan_gated_skinny(M, F, p.num_k_blocks, d->num_sms);
+    if (plan.preferred) {
         if (!operands(static_cast<uint32_t>(plan.n)))
             return LF_ERR_LAUNCH;
         return launched(lf::launch_gated_skinny(e4m3, act, ta, tw, gp, plan, gu, stream), 1);

@@ -392,7 +392,8 @@ cudaError_t launch_gated_pair_t(const CUtensorMap &ta, const CUtensorMap &tw, co
 }
 
 // ---------------------------------------------------------------- few tokens
-// M <= 128 tokens: the weights' bytes bound the call, so the operands are
+// Up to 128 tokens (and groups of 128 where tiles are few, plan_gated_skinny): the
+// weights' bytes bound the call, so the operands are
 // swapped -- 128 gate rows and 128 up rows of w are the A operands of two
 // 128 x n MMAs whose B operand is the tokens (n: M rounded up to 16) -- and a CTA
 // only streams its share of w through a ring of 32 KiB stages (plus the tokens'
@@ -454,6 +455,8 @@ __global__ void __launch_bounds__(S_THREADS, 2)
     const int split = plan.split;
     const int rank = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int f0 = static_cast<int>(blockIdx.x) / split * G_F;
+    const int m0 = static_cast<int>(blockIdx.y) * plan.tokens;  // this CTA's tokens: m0 .. m0 + M - 1
+    const int M = min(plan.tokens, p.M - m0);
     const int kb0 = static_cast<int>(static_cast<int64_t>(p.num_k_blocks) * rank / split);
     const int kb1 = static_cast<int>(static_cast<int64_t>(p.num_k_blocks) * (rank + 1) / split);
     uint32_t cols = 32;
@@ -488,12 +491,12 @@ __global__ void __launch_bounds__(S_THREADS, 2)
             for (int kb = kb0; kb < kb1; ++kb) {
                 if (!wait_bar(EMPTY_BAR(stage), phase ^ 1u, abort_flag, p, ERR_PRODUCER))
                     break;
-                if (!(kb == kb0 && p.inject == 1 && blockIdx.x == 0)) {  // (test hook)
+                if (!(kb == kb0 && p.inject == 1 && blockIdx.x == 0 && blockIdx.y == 0)) {  // (test hook)
                     const uint32_t dst = base + stage * stage_bytes;
                     mbar_arrive_expect_tx(FULL_BAR(stage), stage_bytes);
                     tma_load_2d(dst, &tmW, kb * KELEMS, f0, FULL_BAR(stage));
                     tma_load_2d(dst + BM * G_ROW, &tmW, kb * KELEMS, p.N + f0, FULL_BAR(stage));
-                    tma_load_2d(dst + S_W_BYTES, &tmA, kb * KELEMS, 0, FULL_BAR(stage));
+                    tma_load_2d(dst + S_W_BYTES, &tmA, kb * KELEMS, m0, FULL_BAR(stage));
                 }
                 if (++stage == plan.stages) {
                     stage = 0;
@@ -548,14 +551,14 @@ __global__ void __launch_bounds__(S_THREADS, 2)
         tc_fence_after();
         const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
         float *part = reinterpret_cast<float *>(gbase) + q * 32 + lane;  // the ring is idle: [2 M][128] sums
-        for (int c = 0; ok && c < p.M; c += 16) {
+        for (int c = 0; ok && c < M; c += 16) {
             uint32_t g[16], u[16];
             tmem_ld_32x32b_x16(taddr + static_cast<uint32_t>(c), g);
             tmem_ld_32x32b_x16(taddr + static_cast<uint32_t>(plan.n + c), u);
             tmem_wait_ld();
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                if (c + i < p.M) {
+                if (c + i < M) {
                     part[(2 * (c + i)) * BM] = __uint_as_float(g[i]);
                     part[(2 * (c + i) + 1) * BM] = __uint_as_float(u[i]);
                 }
@@ -572,9 +575,9 @@ __global__ void __launch_bounds__(S_THREADS, 2)
         __syncthreads();
     {
         const int f = f0 + 4 * lane;
-        const int m1 = p.M * (rank + 1) / split;
+        const int m1 = M * (rank + 1) / split;
 #pragma unroll 2
-        for (int m = p.M * rank / split + warp; m < m1; m += S_THREADS / 32) {
+        for (int m = M * rank / split + warp; m < m1; m += S_THREADS / 32) {
             const uint32_t a = base + static_cast<uint32_t>((2 * m * BM + 4 * lane) * 4);
             float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
 #pragma unroll 4
@@ -585,7 +588,7 @@ __global__ void __launch_bounds__(S_THREADS, 2)
                 u = make_float4(u.x + du.x, u.y + du.y, u.z + du.z, u.w + du.w);
             }
             if (f < p.N)  // N % 8 == 0
-                s_finish<E4M3, ACT>(gp, gu, g, u, m, f);
+                s_finish<E4M3, ACT>(gp, gu, g, u, m0 + m, f);
         }
         __syncwarp();
     }
@@ -615,7 +618,8 @@ cudaError_t launch_gated_skinny_t(const CUtensorMap &ta, const CUtensorMap &tw, 
             return e;
         done.fetch_or(bit);
     }
-    return launch_overlapped(k_gated_skinny<E4M3, ACT>, dim3(static_cast<unsigned>(p.g.num_n_blocks * plan.split)),
+    return launch_overlapped(k_gated_skinny<E4M3, ACT>, dim3(static_cast<unsigned>(p.g.num_n_blocks * plan.split),
+                                  static_cast<unsigned>((p.g.M + plan.tokens - 1) / plan.tokens)),
                              dim3(S_THREADS), static_cast<size_t>(plan.smem), plan.split, s, ta, tw, p, plan,
                              static_cast<__nv_bfloat16 *>(gu));
 }
@@ -678,24 +682,69 @@ cudaError_t launch_gated_pair(bool e4m3, int act, const CUtensorMap &ta, const C
     return cudaErrorInvalidValue;
 }
 
+// Clusters of `split` few-token CTAs (one per SM) that the device holds at once:
+// clusters stay within a group of SMs, so 152 SMs hold 76, 36 and 15 of two,
+// four and eight, and a sixteenth cluster of eight would wait for a second wave.
+static int skinny_clusters(int split, int num_sms)
+{
+    static std::atomic<int> known[4][64];
+    int dev = 0;
+    if (split == 1 || cudaGetDevice(&dev) != cudaSuccess)
+        return num_sms;
+    const int i = split == 2 ? 1 : split == 4 ? 2 : 3;
+    std::atomic<int> &k = known[i][dev & 63];
+    int n = k.load();
+    if (n == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(split), 1, 1);
+        cfg.blockDim = dim3(S_THREADS, 1, 1);
+        cfg.dynamicSmemBytes = S_SMEM_ONE;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(split);
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaFuncSetAttribute(k_gated_skinny<false, ACT_SILU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 S_SMEM_ONE) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, k_gated_skinny<false, ACT_SILU>, &cfg) != cudaSuccess || n < 1) {
+            cudaGetLastError();
+            n = 1;
+        }
+        k.store(n);
+    }
+    return n;
+}
+
 GatedSkinny plan_gated_skinny(int64_t M, int64_t F, int num_k_blocks, int num_sms)
 {
     GatedSkinny g;
-    g.n = static_cast<int>((M + 15) / 16 * 16);
-    const int64_t tiles = (F + G_F - 1) / G_F;
-    // One CTA per SM with a deep ring, and the largest split that keeps it so
-    // (5120 x 13824, 48 tokens, 108 tiles: 48.6 us unsplit, 50.6 us split in two
-    // with two CTAs per SM; 2048 x 5632, 64 tokens, 44 tiles: 14.8 us split in
-    // two, 16.7 us in four with two CTAs per SM).  More tiles than SMs: two CTAs
-    // per SM while the sums of 64 tokens fit half an SM's ring.
+    const int64_t groups = (M + BM - 1) / BM;
+    g.tokens = groups == 1 ? static_cast<int>(M) : static_cast<int>(((M + groups - 1) / groups + 15) / 16 * 16);
+    g.n = (g.tokens + 15) / 16 * 16;
+    const int64_t tiles = (F + G_F - 1) / G_F * groups;
+    // One CTA per SM with a deep ring, and the largest split that keeps all of them in
+    // one wave (5120 x 13824, 48 tokens, 108 tiles: 48.6 us unsplit, 50.6 us split
+    // in two with two CTAs per SM; 2048 x 5632, 64 tokens, 44 tiles: 14.8 us split in
+    // two, 16.7 us in four with two CTAs per SM; 4096 x 2048, one token, 16 tiles: 11.0 us
+    // split in four, 15.5 us in eight, whose sixteen clusters are two waves).
+    // More tiles than SMs: two CTAs per SM while the sums of 64 tokens fit half an
+    // SM's ring.
     const bool two = g.n <= 64 && tiles > num_sms;
     g.split = 1;
-    while (g.split < 8 && tiles * g.split * 2 <= num_sms && num_k_blocks / (g.split * 2) >= 4)
+    while (g.split < 8 && num_k_blocks / (g.split * 2) >= 4 && tiles <= skinny_clusters(g.split * 2, num_sms))
         g.split *= 2;
     const int stage = S_W_BYTES + g.n * G_ROW;
     const int fit = ((two ? S_SMEM_TWO : S_SMEM_ONE) - S_MISC) / stage;
     g.stages = fit < S_MAX_STAGES ? fit : S_MAX_STAGES;
     g.smem = S_MISC + g.stages * stage;
+    // More than 128 tokens run here in groups only where the pair kernel's tiles
+    // are few and their K loops long enough for the split to pay (us, pair kernel
+    // against this one: 200 x 2048 x 1408 13.6 / 10.2, split in four, but 200 x 512 x
+    // 1408 7.0 / 8.7; 200 x 5120 x 4096 31.1 / 26.2, split in two, but 256 x 2048 x
+    // 4096 15.7 / 16.1; unsplit 333 x 5120 x 4096 31.5 / 40.5).
+    g.preferred = groups == 1 || (g.split >= 4 && num_k_blocks >= 16) || (g.split == 2 && num_k_blocks >= 64);
     return g;
 }
 

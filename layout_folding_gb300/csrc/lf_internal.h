@@ -133,14 +133,17 @@ struct GatedParams {
 cudaError_t launch_gated_pair(bool e4m3, int act, const CUtensorMap &ta, const CUtensorMap &tw, const CUtensorMap &to,
                               const CUtensorMap &tg, const CUtensorMap &tu, const GatedParams &p, int grid,
                               cudaStream_t s);
-// The same for M <= 128 tokens (operands swapped, the K loop split over clusters).
+// The same for few tokens (operands swapped, the K loop split over clusters).
 struct GatedSkinny {
-    int n;       // the MMA's N: M rounded up to 16
+    bool preferred;  // to the pair kernel
+
+    int tokens;  // of one CTA (at most 128)
+    int n;       // the MMA's N: tokens rounded up to 16
     int split;   // CTAs per cluster, each with its share of the K blocks: 1, 2, 4 or 8
     int stages;  // ring stages
     int smem;    // dynamic shared memory per CTA
 };
-// How a call with M tokens (1..128) runs; num_k_blocks counts 128-byte K blocks.
+// How a call with M tokens would run (in groups of at most 128); num_k_blocks counts 128-byte K blocks.
 GatedSkinny plan_gated_skinny(int64_t M, int64_t F, int num_k_blocks, int num_sms);
 // ta: x, boxes of plan.n rows; tw as above.  gu may be null.
 cudaError_t launch_gated_skinny(bool e4m3, int act, const CUtensorMap &ta, const CUtensorMap &tw, const GatedParams &p,

@@ -86,7 +86,9 @@ SHAPES = [(1, 8, 8), (1, 1416, 520), (2, 128, 64), (3, 136, 72), (17, 264, 1032)
           (128, 128, 128), (129, 392, 136), (200, 1416, 520), (256, 256, 64), (257, 248, 1000), (520, 1000, 264),
           (1030, 136, 192),
           # few tokens: whole K loops and K loops split over 2, 4 and 8 CTAs, one and two CTAs per SM
-          (5, 40000, 256), (33, 9000, 520), (16, 4104, 1024), (65, 2056, 2048), (100, 20000, 136), (113, 520, 2048)]
+          (5, 40000, 256), (33, 9000, 520), (16, 4104, 1024), (65, 2056, 2048), (100, 20000, 136), (113, 520, 2048),
+          # more tokens in groups: split in eight, four and two, ragged groups; and just not
+          (130, 264, 1032), (333, 1408, 1040), (200, 4104, 4096), (1000, 520, 2048), (512, 512, 1024), (700, 2056, 512)]
 
 
 @pytest.mark.parametrize("M,F,K", SHAPES)
@@ -108,7 +110,8 @@ def quantised(t):
 
 @pytest.mark.parametrize("M,F,K", [(1, 8, 16), (1, 1416, 528), (3, 136, 80), (48, 520, 2048), (128, 128, 128),
                                    (129, 392, 144), (300, 1000, 272), (1030, 136, 192), (5, 20000, 256),
-                                   (33, 4104, 1040), (65, 2056, 4096), (113, 520, 4096)])
+                                   (33, 4104, 1040), (65, 2056, 4096), (113, 520, 4096),
+                                   (130, 264, 2064), (333, 1408, 2064), (150, 4104, 8208), (1000, 520, 4096)])
 def test_forward_e4m3(M, F, K):
     x, xs = quantised(normal((M, K), 5) * torch.exp(normal((M, 1), 6)))
     w, ws = quantised(normal((2 * F, K), 7, 1 / math.sqrt(K)))
