@@ -266,55 +266,60 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer (leader only)
-        if (leader && lane == 0) {
+        // (the whole warp, converged, with one thread issuing: see lf_ptx.cuh; after a
+        // wait that gave up the loops run on without doing anything)
+        if (leader) {
+            const uint32_t one = elect_one();
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
-            bool ok = true;
+            bool alive = true;
             const uint32_t idesc = E4M3 ? idesc_e4m3_f32(G_M, BN) : idesc_bf16_f32(G_M, BN);
-            for (int tile = pair; ok && tile < p.num_tiles; tile += num_pairs) {
-                if (!wait_bar(TEMPTY_BAR(acc), acc_phase ^ 1u, abort_flag, p, ERR_MMA_ACC, peer_abort))
-                    break;
+            for (int tile = pair; tile < p.num_tiles; tile += num_pairs) {
+                if (alive)
+                    alive = __all_sync(0xffffffffu, wait_bar(TEMPTY_BAR(acc), acc_phase ^ 1u, abort_flag, p, ERR_MMA_ACC,
+                                                             peer_abort));
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
                 for (int kb = 0; kb < p.num_k_blocks; kb += G_KSUB) {
                     const int nsub = min(G_KSUB, p.num_k_blocks - kb);
-                    if (!wait_bar(FULL_BAR(stage), phase, abort_flag, p, ERR_MMA_FULL, peer_abort)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
+                    if (alive)
+                        alive = __all_sync(0xffffffffu, wait_bar(FULL_BAR(stage), phase, abort_flag, p, ERR_MMA_FULL,
+                                                                 peer_abort));
+                    if (alive) {
+                        tc_fence_after();
 #pragma unroll
-                    for (int j = 0; j < G_KSUB; ++j) {
-                        if (j >= nsub)
-                            break;
-                        const uint32_t a0 = sA + (stage * G_KSUB + j) * G_A_BYTES;
-                        const uint32_t b0 = sB + (stage * G_KSUB + j) * G_B_BYTES;
+                        for (int j = 0; j < G_KSUB; ++j) {
+                            if (j >= nsub)
+                                break;
+                            const uint32_t a0 = sA + (stage * G_KSUB + j) * G_A_BYTES;
+                            const uint32_t b0 = sB + (stage * G_KSUB + j) * G_B_BYTES;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {  // 32 bytes of K per MMA
-                            const uint64_t da = smem_desc_k128(a0 + k * 32), db = smem_desc_k128(b0 + k * 32);
-                            const uint32_t accumulate = (kb | j | k) != 0 ? 1u : 0u;
-                            if (E4M3)
-                                umma_f8_pair(d_tmem, da, db, idesc, accumulate);
-                            else
-                                umma_f16_pair(d_tmem, da, db, idesc, accumulate);
+                            for (int k = 0; k < 4; ++k) {  // 32 bytes of K per MMA
+                                const uint64_t da = smem_desc_k128(a0 + k * 32), db = smem_desc_k128(b0 + k * 32);
+                                const uint32_t accumulate = (kb | j | k) != 0 ? 1u : 0u;
+                                if (E4M3)
+                                    umma_f8_pair_one(one, d_tmem, da, db, idesc, accumulate);
+                                else
+                                    umma_f16_pair_one(one, d_tmem, da, db, idesc, accumulate);
+                            }
                         }
+                        umma_commit_pair_mc_one(one, EMPTY_BAR(stage), 0x3);
                     }
-                    umma_commit_pair_mc(EMPTY_BAR(stage), 0x3);
                     if (++stage == G_STAGES) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
-                if (!ok)
-                    break;
-                umma_commit_pair_mc(TFULL_BAR(acc), 0x3);
+                if (alive)
+                    umma_commit_pair_mc_one(one, TFULL_BAR(acc), 0x3);
                 if (++acc == G_ACC_BUFS) {
                     acc = 0;
                     acc_phase ^= 1u;
                 }
             }
-            umma_commit_pair_mc(drain_bar, 0x1);
-            wait_bar_drain(drain_bar, 0u, abort_flag, p, peer_abort);
+            umma_commit_pair_mc_one(one, drain_bar, 0x1);
+            if (lane == 0)
+                wait_bar_drain(drain_bar, 0u, abort_flag, p, peer_abort);
         }
         __syncwarp();
     } else {
