@@ -1110,10 +1110,11 @@ static lf_status gated_launch(const void *x, const float *x_scale, const void *w
     }
     p.num_m_blocks = static_cast<int>((M + 2 * lf::BM - 1) / (2 * lf::BM));
     p.num_tiles = p.num_m_blocks * p.num_n_blocks;
-    // bands of M blocks whose X rows stay in L2, as plan_gemm
+    // bands of M blocks whose X rows stay in L2, and at least eight (see
+    // plan_gated_grads)
     const double x_bytes = 2.0 * lf::BM * static_cast<double>(K) * (e4m3 ? 1.0 : 2.0);
-    int band = static_cast<int>(BAND_X_BYTES / x_bytes);
-    band = band < 1 ? 1 : band;
+    const int fit = static_cast<int>(BAND_X_BYTES / x_bytes);
+    const int band = fit < 8 ? 8 : fit;
     if (band < p.num_m_blocks) {
         const int nbands = (p.num_m_blocks + band - 1) / band;
         p.band_m = (p.num_m_blocks + nbands - 1) / nbands;
