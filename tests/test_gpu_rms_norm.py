@@ -418,3 +418,22 @@ def test_offsets_past_32_bits(M, D):
     dx, _ = lf.add_rms_norm_backward(x, h, w.to(DEV), dh=res, eps=EPS, dx=res)
     check_backward(xs, hs.cpu(), w, rs, (dx[rows], None))
     lf.check_device_error()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("M", [5, 700])
+def test_sums_of_subnormal_and_of_far_apart_numbers(dtype, M):
+    """The packed 16-bit addition against one fp32 addition rounded once, over
+    exponents from the type's subnormals to its largest."""
+    D = 512
+    g = torch.Generator().manual_seed(5)
+    fi = torch.finfo(dtype)
+    lo, hi = np.log2(fi.tiny * fi.eps), np.log2(fi.max) - 2
+
+    def spread():
+        e = torch.rand(M, D, generator=g, dtype=torch.float64) * (hi - lo) + lo
+        return (torch.sign(torch.randn(M, D, generator=g)).double() * 2.0 ** e).to(dtype)
+    x, res = spread(), spread()
+    res[:, ::3] = (-x[:, ::3].float() * (1 + 2.0 ** -7)).to(dtype)      # cancellation
+    y, h, _ = lf.add_rms_norm(x.to(DEV), torch.ones(D, dtype=dtype, device=DEV), residual=res.to(DEV), eps=EPS)
+    assert torch.equal(h.cpu().view(torch.int16), kept(x, res).view(torch.int16))
