@@ -406,23 +406,23 @@ cudaError_t launch_gated_pair_t(const CUtensorMap &ta, const CUtensorMap &tw, co
 // over a cluster of 2, 4 or 8 CTAs: each leaves its fp32 sums in its own shared
 // memory, and after a cluster barrier every CTA adds, in rank order, its part of
 // the tokens from all of them.  5120 x 13824: one token 45-47 us bf16 (90 % of the
-// copy rate), 48 tokens e4m3 28.5 us; 8192 x 28672 97-99 %: what is left is the
+// copy rate), 48 tokens e4m3 27.6 us; 8192 x 28672 97-99 %: what is left is the
 // launch's 4-5 us.
 constexpr int S_THREADS = 192;     // producer, MMA, 4 epilogue warps
+constexpr int S_WARPS = S_THREADS / 32;
 constexpr int S_MAX_STAGES = 8;
 constexpr int S_W_BYTES = 2 * BM * G_ROW;
 constexpr int S_MISC = 1024 + (2 * S_MAX_STAGES + 1) * 8 + 32;  // alignment, barriers, TMEM address, abort flag
 constexpr int S_SMEM_ONE = 220 * 1024, S_SMEM_TWO = 113 * 1024;  // dynamic shared memory with one / two CTAs per SM
 
-// Output columns f .. f + 3 of token m from its sums g and u.
+// Output columns f .. f + 3 of token m from its sums g and u (e4m3 operands: sx the
+// token's scale, wg and wu the columns').
 template <bool E4M3, int ACT>
-__device__ __forceinline__ void s_finish(const GatedParams &gp, __nv_bfloat16 *gu, float4 g, float4 u, int m, int f)
+__device__ __forceinline__ void s_finish(const GatedParams &gp, __nv_bfloat16 *gu, float4 g, float4 u, int m, int f,
+                                         float sx, float4 wg, float4 wu)
 {
     const size_t F = static_cast<size_t>(gp.g.N);
     if (E4M3) {
-        const float sx = gp.x_scale[m];
-        const float4 wg = *reinterpret_cast<const float4 *>(gp.w_scale + f);
-        const float4 wu = *reinterpret_cast<const float4 *>(gp.w_scale + F + f);
         g = make_float4(g.x * (sx * wg.x), g.y * (sx * wg.y), g.z * (sx * wg.z), g.w * (sx * wg.w));
         u = make_float4(u.x * (sx * wu.x), u.y * (sx * wu.y), u.z * (sx * wu.z), u.w * (sx * wu.w));
     }
@@ -487,6 +487,20 @@ __global__ void __launch_bounds__(S_THREADS, 2)
     wait_previous_kernel();
     let_next_kernel_start();
     const uint32_t tmem_base = *tmem_slot;
+    // The scales this thread finishes with, loaded while the weights stream: of its
+    // four output columns, and of the warp's tokens m_first + 6 i (in lane i).
+    const int f = f0 + 4 * lane;
+    const int m_first = M * rank / split + warp, m_end = M * (rank + 1) / split;
+    float4 wg4 = make_float4(1.f, 1.f, 1.f, 1.f), wu4 = wg4;
+    float sx_lane = 1.f;
+    if (E4M3) {
+        if (f < p.N) {  // N % 8 == 0
+            wg4 = *reinterpret_cast<const float4 *>(gp.w_scale + f);
+            wu4 = *reinterpret_cast<const float4 *>(gp.w_scale + p.N + f);
+        }
+        if (m_first + S_WARPS * lane < m_end)
+            sx_lane = gp.x_scale[m0 + m_first + S_WARPS * lane];
+    }
 
     if (warp == 0) {
         // ------------------------------------------------ TMA producer
@@ -578,25 +592,22 @@ __global__ void __launch_bounds__(S_THREADS, 2)
         cluster_sync();
     else
         __syncthreads();
-    {
-        const int f = f0 + 4 * lane;
-        const int m1 = M * (rank + 1) / split;
-#pragma unroll 2
-        for (int m = M * rank / split + warp; m < m1; m += S_THREADS / 32) {
-            const uint32_t a = base + static_cast<uint32_t>((2 * m * BM + 4 * lane) * 4);
-            float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
-#pragma unroll 4
-            for (int r = 0; r < split; ++r) {
-                const uint32_t ar = split > 1 ? mapa_shared(a, static_cast<uint32_t>(r)) : a;
-                const float4 dg = ld_cluster_f32x4(ar), du = ld_cluster_f32x4(ar + BM * 4);
-                g = make_float4(g.x + dg.x, g.y + dg.y, g.z + dg.z, g.w + dg.w);
-                u = make_float4(u.x + du.x, u.y + du.y, u.z + du.z, u.w + du.w);
-            }
-            if (f < p.N)  // N % 8 == 0
-                s_finish<E4M3, ACT>(gp, gu, g, u, m0 + m, f);
+#pragma unroll(E4M3 ? 4 : 2)
+    for (int i = 0; m_first + S_WARPS * i < m_end; ++i) {
+        const int m = m_first + S_WARPS * i;
+        const uint32_t a = base + static_cast<uint32_t>((2 * m * BM + 4 * lane) * 4);
+        float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
+        for (int r = 0; r < split; ++r) {
+            const uint32_t ar = split > 1 ? mapa_shared(a, static_cast<uint32_t>(r)) : a;
+            const float4 dg = ld_cluster_f32x4(ar), du = ld_cluster_f32x4(ar + BM * 4);
+            g = make_float4(g.x + dg.x, g.y + dg.y, g.z + dg.z, g.w + dg.w);
+            u = make_float4(u.x + du.x, u.y + du.y, u.z + du.z, u.w + du.w);
         }
-        __syncwarp();
+        const float sx = E4M3 ? __shfl_sync(0xffffffffu, sx_lane, i) : 1.f;
+        if (f < p.N)
+            s_finish<E4M3, ACT>(gp, gu, g, u, m0 + m, f, sx, wg4, wu4);
     }
+    __syncwarp();
     if (split > 1)
         cluster_sync();  // no CTA leaves while a peer reads its sums
 #undef FULL_BAR
