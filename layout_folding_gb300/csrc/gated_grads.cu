@@ -9,8 +9,8 @@
 // most of all, whose tiles are few and long (4096 x 5120 x 13824: 320 tiles of 432
 // K blocks are 4.2 waves of 76 pairs, so a fifth wave for a fifth of the pairs).
 // Here the pairs without a tile of that last wave start on the other product, whose
-// tiles are short, and all of them end within one short tile of each other: 1280 us
-// in a burst (1.81 PFLOP/s) where two launches took 685 + 636.  The schedule is
+// tiles are short, and all of them end within one short tile of each other: 1240 us
+// in a burst (1.87 PFLOP/s) where two launches took 685 + 636.  The schedule is
 // fixed (GradIter), so no pair waits for another, replays of a captured call are
 // the same, and every output is summed in the same order every time.  What
 // bounds it: the tensor cores, and over many calls the power limit.
