@@ -9,8 +9,8 @@
 // has both in the same TMEM lane: activation and product happen in registers
 // and neither projection is written unless the caller keeps it for the
 // backward pass.  Compute bound from a few hundred rows on (4 M F K FLOP):
-// 4096 x 5120 x 13824 takes 575 us in a burst (2.0 PFLOP/s; 597 with the
-// pre-activations kept), 665 us sustained under the power limit, and 302 us in
+// 4096 x 5120 x 13824 takes 582 us in a burst (2.0 PFLOP/s; 597 with the
+// pre-activations kept), 667 us sustained under the power limit, and 302 us in
 // e4m3 (3.85 PFLOP/s).  Stages of two K blocks: 603 us with one.
 //
 // The roles, barriers and bounded waits are those of gemm_nt_pair.cu (whole

@@ -608,15 +608,17 @@ constexpr int RING_MAX_GROUPS = 15;   // named barriers 1..15
 constexpr int RING_MAX_SLOTS = 8;
 // Fewer rows than four per SM: one block per row.  At the border both take the
 // same (600 x 5120 3.7 us, 608 in rings 3.8 us); 8192 x 5120 into e4m3 takes 68 us by
-// blocks and 50 us in rings.
-constexpr int64_t RING_MIN_ROWS = 608;
-constexpr int RING_BUDGET = 220 * 1024;
+// blocks and 50 us in rings.  Phased rows, which blocks move element by element,
+// from 100 rows on (100 x 5121 4.8 us by blocks, 4.5 in rings; 300 x 5121 8.9 / 4.8).
+constexpr int64_t RING_MIN_ROWS = 608, RING_MIN_ROWS_PHASED = 100;
+constexpr int RING_BUDGET = 225 * 1024;  // dynamic shared memory; RingSync takes 2 KB more
 constexpr uint64_t RING_SETTLE_NS = 100000;  // after an abort: let copies in flight land
 
 // Shared-memory layout of a ring kernel, computed on the host.
 struct RingPlan {
     int group_threads, groups, slots;
     uint32_t row_bytes;                // one input row
+    int w_shared;                          // weights copied to shared memory (else read where they are)
     uint32_t w_off, slot_off, slot_bytes;  // weights; slots ([group][slot][input][row])
     uint32_t bytes;                    // dynamic shared memory
 };
@@ -821,9 +823,13 @@ struct Ring {
 // Copies the weights to shared memory, shifted by the block's phase (zeros
 // around them); after it every thread sees them and the groups' barriers.
 template <class W, bool PH, class Span>
-__device__ __forceinline__ W *ring_weights(uint8_t *smem, const RingPlan &r, const W *w, const Span &span)
+__device__ __forceinline__ const W *ring_weights(uint8_t *smem, const RingPlan &r, const W *w, const Span &span)
 {
     W *ws = reinterpret_cast<W *>(smem + r.w_off);
+    if (!PH && !r.w_shared) {
+        __syncthreads();
+        return w;
+    }
     if (PH) {
         for (int k = threadIdx.x; k < span.packs * Span::VEC; k += blockDim.x)
             ws[k] = k >= span.phase && k < span.phase + span.D ? w[k - span.phase] : from_f<W>(0.f);
@@ -1090,7 +1096,12 @@ bool plan_ring(RingPlan *r, bool phased, int64_t D, int elem, int welem, int inp
     const int64_t vec = 16 / elem;
     const int64_t packs = phased ? (D + 2 * vec - 2) / vec : D / vec;  // at most
     const int64_t row_bytes = packs * 16, slot = row_bytes * inputs;
-    const int64_t wbytes = (packs * vec * welem + 127) / 128 * 128;
+    int64_t wbytes = (packs * vec * welem + 127) / 128 * 128;
+    r->w_shared = 1;
+    if (!phased && wbytes + 2 * slot > RING_BUDGET && 2 * slot <= RING_BUDGET) {
+        wbytes = 0;
+        r->w_shared = 0;
+    }
     const int64_t gt = (packs + 32 * RING_NV - 1) / (32 * RING_NV) * 32;
     if (gt > max_threads || wbytes + 2 * slot > RING_BUDGET)
         return false;
@@ -1127,6 +1138,10 @@ cudaError_t ring_opt_in(K kernel, std::atomic<unsigned long long> &done)
 // How a call's rows may be moved: 16-byte packs that start with every row; 16-byte
 // granules of contiguous rows of any length; or element by element.
 enum Rows { ROWS_VEC, ROWS_PHASED, ROWS_ANY };
+int64_t ring_min_rows(Rows rows)
+{
+    return rows == ROWS_VEC ? RING_MIN_ROWS : rows == ROWS_PHASED ? RING_MIN_ROWS_PHASED : INT64_MAX;
+}
 constexpr int64_t PHASED_MIN_D = 32;  // a row covers whole granules besides its two ragged ones
 
 // Threads per block for a row of `packs` packs, NV per thread.
@@ -1171,7 +1186,7 @@ cudaError_t launch_norm_t(const NormParams &p, Rows rows, int num_sms, cudaStrea
 {
     constexpr int V = 16 / static_cast<int>(sizeof(T));
     RingPlan r;
-    if (rows != ROWS_ANY && p.M >= RING_MIN_ROWS && num_sms >= 8 &&
+    if (p.M >= ring_min_rows(rows) && num_sms >= 8 &&
         plan_ring(&r, rows == ROWS_PHASED, p.D, sizeof(T), sizeof(W), p.residual ? 2 : 1, ring_threads(FP8)))
         return rows == ROWS_PHASED ? launch_norm_ring<T, W, FP8, true>(p, r, num_sms, s)
                                    : launch_norm_ring<T, W, FP8, false>(p, r, num_sms, s);
@@ -1223,7 +1238,7 @@ cudaError_t launch_bwd_tw(const NormBwdParams &p, Rows rows, void *dweight, int 
     int blocks = rms_norm_bwd_blocks(p.M);
     cudaError_t e = cudaSuccess;
     RingPlan r;
-    if (rows != ROWS_ANY && p.M >= RING_MIN_ROWS && num_sms >= 8 && num_sms <= blocks &&
+    if (p.M >= ring_min_rows(rows) && num_sms >= 8 && num_sms <= blocks &&
         plan_ring(&r, rows == ROWS_PHASED, p.D, sizeof(T), sizeof(W), p.dh ? 3 : 2, 512)) {
         blocks = num_sms / 8 * 8;
         if (rows == ROWS_PHASED)

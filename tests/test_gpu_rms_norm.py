@@ -108,7 +108,9 @@ def test_many_rows_and_leading_dimensions():
 # several warps, rows that leave room for one group only, rows too long for it
 MANY = [(609, 8), (1000, 136), (2500, 264), (700, 1032), (1300, 2056), (640, 5120), (613, 12296), (610, 20000),
         # rows that are not a multiple of 16 bytes
-        (700, 33), (611, 37), (900, 250), (1333, 1027), (777, 1530), (650, 5121), (609, 9999), (608, 12301)]
+        (700, 33), (611, 37), (900, 250), (1333, 1027), (777, 1530), (650, 5121), (609, 9999), (608, 12301),
+        # the longest rows that fit, weights in shared memory or not; few phased rows
+        (620, 16384), (609, 16383), (100, 1027), (153, 515), (303, 2050)]
 
 
 @pytest.mark.parametrize("M,D", MANY)
