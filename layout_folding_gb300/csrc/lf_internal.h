@@ -104,7 +104,7 @@ struct NormParams {
 };
 cudaError_t launch_rms_norm(const NormParams &p, int dtype, int wdtype, bool fp8, int num_sms, cudaStream_t s);
 
-// Its gradient.  partial: fp32 [rms_norm_bwd_blocks(M)][D], or null with
+// Its gradient.  partial: fp32 [rms_norm_bwd_blocks(M)][D] at most, or null with
 // dweight null; dweight has the weight's type.  dh may be null.
 struct NormBwdParams {
     const void *dy, *h, *weight, *dh;

@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(1024) k_rms_norm_bwd_long(const NormBwdParams 
 
 // dweight[c] = sum over blocks of partial[b][c]: 32 columns per block, 32 rows of
 // threads that each sum every 32nd block's row (at most 10, all in flight at
-// once); the 32 sums are added in order.
+// once); then warp y adds the 32 sums of column y as a tree.
 constexpr int DW_ROWS = 32;
 constexpr int DW_STEPS = (RMS_BWD_BLOCKS + DW_ROWS - 1) / DW_ROWS;
 template <class W>
@@ -563,7 +563,7 @@ __global__ void __launch_bounds__(32 * DW_ROWS)
     k_rms_norm_dweight(const float *partial, W *dweight, int64_t D, int blocks)
 {
     wait_previous_kernel();
-    __shared__ float sh[DW_ROWS][32];
+    __shared__ float sh[DW_ROWS][33];
     const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x;
     float v[DW_STEPS];
 #pragma unroll
@@ -577,13 +577,13 @@ __global__ void __launch_bounds__(32 * DW_ROWS)
         s += v[i];
     sh[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
-    if (threadIdx.y == 0 && c < D) {
-        s = 0.f;
+    s = sh[threadIdx.x][threadIdx.y];
 #pragma unroll
-        for (int i = 0; i < DW_ROWS; ++i)
-            s += sh[i][threadIdx.x];
-        dweight[c] = from_f<W>(s);
-    }
+    for (int o = 16; o > 0; o >>= 1)
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+    const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.y;
+    if (threadIdx.x == 0 && col < D)
+        dweight[col] = from_f<W>(s);
 }
 
 // ---------------------------------------------------------------- many rows
@@ -609,8 +609,9 @@ constexpr int RING_MAX_SLOTS = 8;
 // Fewer rows than four per SM: one block per row.  At the border both take the
 // same (600 x 5120 3.7 us, 608 in rings 3.8 us); 8192 x 5120 into e4m3 takes 68 us by
 // blocks and 50 us in rings.  Phased rows, which blocks move element by element,
-// from 100 rows on (100 x 5121 4.8 us by blocks, 4.5 in rings; 300 x 5121 8.9 / 4.8).
-constexpr int64_t RING_MIN_ROWS = 608, RING_MIN_ROWS_PHASED = 100;
+// always where they are long, and from 100 rows on (32 x 5121 4.4 us by blocks, 4.0 in
+// rings; 300 x 5121 8.9 / 4.8).
+constexpr int64_t RING_MIN_ROWS = 608, RING_MIN_ROWS_PHASED = 100, RING_LONG_D = 1024;
 constexpr int RING_BUDGET = 225 * 1024;  // dynamic shared memory; RingSync takes 2 KB more
 constexpr uint64_t RING_SETTLE_NS = 100000;  // after an abort: let copies in flight land
 
@@ -831,8 +832,23 @@ __device__ __forceinline__ const W *ring_weights(uint8_t *smem, const RingPlan &
         return w;
     }
     if (PH) {
-        for (int k = threadIdx.x; k < span.packs * Span::VEC; k += blockDim.x)
-            ws[k] = k >= span.phase && k < span.phase + span.D ? w[k - span.phase] : from_f<W>(0.f);
+        // 16 bytes a load, several in flight, each element to its shifted place
+        constexpr int VW = 16 / static_cast<int>(sizeof(W));
+        const int d = static_cast<int>(span.D), whole = d / VW, end = span.phase + d;
+#pragma unroll 4
+        for (int c = threadIdx.x; c < whole; c += blockDim.x) {
+            const uint4 v = reinterpret_cast<const uint4 *>(w)[c];
+            const W *e = reinterpret_cast<const W *>(&v);
+#pragma unroll
+            for (int i = 0; i < VW; ++i)
+                ws[span.phase + c * VW + i] = e[i];
+        }
+        if (threadIdx.x < VW && whole * VW + static_cast<int>(threadIdx.x) < d)
+            ws[span.phase + whole * VW + threadIdx.x] = w[whole * VW + threadIdx.x];
+        if (static_cast<int>(threadIdx.x) < span.phase)
+            ws[threadIdx.x] = from_f<W>(0.f);
+        if (end + static_cast<int>(threadIdx.x) < span.packs * Span::VEC)
+            ws[end + threadIdx.x] = from_f<W>(0.f);
     } else {
         for (int i = threadIdx.x; i < static_cast<int>(span.D * sizeof(W) / 16); i += blockDim.x)
             reinterpret_cast<uint4 *>(ws)[i] = reinterpret_cast<const uint4 *>(w)[i];
@@ -1138,9 +1154,17 @@ cudaError_t ring_opt_in(K kernel, std::atomic<unsigned long long> &done)
 // How a call's rows may be moved: 16-byte packs that start with every row; 16-byte
 // granules of contiguous rows of any length; or element by element.
 enum Rows { ROWS_VEC, ROWS_PHASED, ROWS_ANY };
-int64_t ring_min_rows(Rows rows)
+bool use_ring(Rows rows, int64_t M, int64_t D)
 {
-    return rows == ROWS_VEC ? RING_MIN_ROWS : rows == ROWS_PHASED ? RING_MIN_ROWS_PHASED : INT64_MAX;
+    if (rows == ROWS_PHASED)
+        return D >= RING_LONG_D || M >= RING_MIN_ROWS_PHASED;
+    return rows == ROWS_VEC && M >= RING_MIN_ROWS;
+}
+// Blocks of a ring kernel: a multiple of eight (RowSpan), at most one per SM.
+int ring_blocks(int64_t M, int num_sms)
+{
+    const int64_t most = num_sms / 8 * 8, want = (M + 7) / 8 * 8;
+    return static_cast<int>(want < most ? want : most);
 }
 constexpr int64_t PHASED_MIN_D = 32;  // a row covers whole granules besides its two ragged ones
 
@@ -1177,8 +1201,8 @@ cudaError_t launch_norm_ring(const NormParams &p, const RingPlan &r, int num_sms
     const cudaError_t e = ring_opt_in(k_rms_norm_ring<T, W, FP8, PH>, opted);
     if (e != cudaSuccess)
         return e;
-    return launch_overlapped(k_rms_norm_ring<T, W, FP8, PH>, dim3(num_sms / 8 * 8), dim3(r.groups * r.group_threads),
-                             r.bytes, 1, s, p, r);
+    return launch_overlapped(k_rms_norm_ring<T, W, FP8, PH>, dim3(ring_blocks(p.M, num_sms)),
+                             dim3(r.groups * r.group_threads), r.bytes, 1, s, p, r);
 }
 
 template <class T, class W, bool FP8>
@@ -1186,7 +1210,7 @@ cudaError_t launch_norm_t(const NormParams &p, Rows rows, int num_sms, cudaStrea
 {
     constexpr int V = 16 / static_cast<int>(sizeof(T));
     RingPlan r;
-    if (p.M >= ring_min_rows(rows) && num_sms >= 8 &&
+    if (num_sms >= 8 && use_ring(rows, p.M, p.D) &&
         plan_ring(&r, rows == ROWS_PHASED, p.D, sizeof(T), sizeof(W), p.residual ? 2 : 1, ring_threads(FP8)))
         return rows == ROWS_PHASED ? launch_norm_ring<T, W, FP8, true>(p, r, num_sms, s)
                                    : launch_norm_ring<T, W, FP8, false>(p, r, num_sms, s);
@@ -1235,12 +1259,12 @@ template <class T, class W>
 cudaError_t launch_bwd_tw(const NormBwdParams &p, Rows rows, void *dweight, int num_sms, cudaStream_t s)
 {
     constexpr int V = 16 / static_cast<int>(sizeof(T));
-    int blocks = rms_norm_bwd_blocks(p.M);
+    int blocks = static_cast<int>(p.M < RMS_BWD_BLOCKS ? p.M : RMS_BWD_BLOCKS);
     cudaError_t e = cudaSuccess;
     RingPlan r;
-    if (p.M >= ring_min_rows(rows) && num_sms >= 8 && num_sms <= blocks &&
+    if (num_sms >= 8 && num_sms <= RMS_BWD_BLOCKS && use_ring(rows, p.M, p.D) &&
         plan_ring(&r, rows == ROWS_PHASED, p.D, sizeof(T), sizeof(W), p.dh ? 3 : 2, 512)) {
-        blocks = num_sms / 8 * 8;
+        blocks = ring_blocks(p.M, num_sms);
         if (rows == ROWS_PHASED)
             e = p.dh ? launch_bwd_ring<T, W, true, true>(p, r, blocks, s)
                      : launch_bwd_ring<T, W, false, true>(p, r, blocks, s);
@@ -1278,7 +1302,10 @@ cudaError_t launch_rms_norm(const NormParams &p, int dtype, int wdtype, bool fp8
     return launch_norm_tw<float, float>(p, rows, fp8, num_sms, s);
 }
 
-int rms_norm_bwd_blocks(int64_t M) { return static_cast<int>(M < RMS_BWD_BLOCKS ? M : RMS_BWD_BLOCKS); }
+int rms_norm_bwd_blocks(int64_t M)
+{
+    return static_cast<int>(M < RMS_BWD_BLOCKS ? (M + 7) / 8 * 8 : RMS_BWD_BLOCKS);  // (304 is a multiple of eight)
+}
 
 cudaError_t launch_rms_norm_bwd(const NormBwdParams &p, void *dweight, int dtype, int wdtype, int num_sms,
                                 cudaStream_t s)

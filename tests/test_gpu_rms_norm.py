@@ -110,7 +110,8 @@ MANY = [(609, 8), (1000, 136), (2500, 264), (700, 1032), (1300, 2056), (640, 512
         # rows that are not a multiple of 16 bytes
         (700, 33), (611, 37), (900, 250), (1333, 1027), (777, 1530), (650, 5121), (609, 9999), (608, 12301),
         # the longest rows that fit, weights in shared memory or not; few phased rows
-        (620, 16384), (609, 16383), (100, 1027), (153, 515), (303, 2050)]
+        (620, 16384), (609, 16383), (100, 1027), (153, 515), (303, 2050),
+        (1, 5121), (4, 10303), (7, 1031), (9, 2047), (33, 13611)]
 
 
 @pytest.mark.parametrize("M,D", MANY)
