@@ -468,11 +468,26 @@ void plan_gated_grads(GradsParams *p, bool want_dx, bool want_dw, int64_t M, int
     }
     const double share = 0.75 * total / pairs;
     const double most = share < 8 ? 8 : share;
+    if (p->side[0].tiles + p->side[1].tiles > pairs) {
+        for (int s = 0; s < 2; ++s)
+            while (p->side[s].split < GR_MAX_SPLIT && p->side[s].k_blocks > most * p->side[s].split)
+                ++p->side[s].split;
+    } else {
+        // one item for each pair at most: split the side with the longer items while
+        // that leaves 8 K blocks to an item and no pair with two
+        for (;;) {
+            GradSide &a = p->side[0], &b = p->side[1];
+            const bool first = static_cast<int64_t>(a.k_blocks) * b.split >= static_cast<int64_t>(b.k_blocks) * a.split;
+            GradSide &g = first ? a : b;
+            if (g.split >= GR_MAX_SPLIT || g.k_blocks <= 8 * g.split ||
+                a.tiles * a.split + b.tiles * b.split + g.tiles > pairs)
+                break;
+            ++g.split;
+        }
+    }
     int64_t floats = 0;
     for (int s = 0; s < 2; ++s) {
         GradSide &g = p->side[s];
-        while (g.split < GR_MAX_SPLIT && g.k_blocks > most * g.split)
-            ++g.split;
         g.items = want[s] ? g.tiles * g.split : 0;
         g.parts = floats;
         if (g.split > 1)
