@@ -1080,7 +1080,6 @@ static lf_status gated_launch(const void *x, const float *x_scale, const void *w
     p.K = static_cast<int>(K);
     p.out = out;
     p.num_k_blocks = static_cast<int>((K + kblock - 1) / kblock);
-    p.num_n_blocks = static_cast<int>((F + lf::BN / 2 - 1) / (lf::BN / 2));
     p.err = d->err_word;
     p.timeout_ns = g_timeout_ns.load();
     p.inject = g_inject.load();
@@ -1088,18 +1087,23 @@ static lf_status gated_launch(const void *x, const float *x_scale, const void *w
     gp.w_scale = w_scale;
     gp.save = gu ? 1 : 0;
     CUtensorMap ta, tw;
-    const auto operands = [&](uint32_t x_rows) {
-        return e4m3 ? make_tmap_e4m3(&ta, x, M, K, x_rows) && make_tmap_e4m3(&tw, w, 2 * F, K, lf::BN / 2)
-                    : make_tmap(&ta, x, M, K, x_rows) && make_tmap(&tw, w, 2 * F, K, lf::BN / 2);
+    const auto operands = [&](uint32_t x_rows, uint32_t w_rows) {
+        return e4m3 ? make_tmap_e4m3(&ta, x, M, K, x_rows) && make_tmap_e4m3(&tw, w, 2 * F, K, w_rows)
+                    : make_tmap(&ta, x, M, K, x_rows) && make_tmap(&tw, w, 2 * F, K, w_rows);
     };
     const lf::GatedSkinny plan = lf::plan_gated_skinny(M, F, p.num_k_blocks, d->num_sms);
     if (plan.preferred) {
-        if (!operands(static_cast<uint32_t>(plan.n)))
+        p.num_n_blocks = static_cast<int>((F + lf::BN / 2 - 1) / (lf::BN / 2));
+        if (!operands(static_cast<uint32_t>(plan.n), lf::BM))
             return LF_ERR_LAUNCH;
         return launched(lf::launch_gated_skinny(e4m3, act, ta, tw, gp, plan, gu, stream), 1);
     }
+    p.num_m_blocks = static_cast<int>((M + 2 * lf::BM - 1) / (2 * lf::BM));
+    gp.cols = lf::plan_gated_cols(p.num_m_blocks, F, d->pair_clusters);
+    p.num_n_blocks = static_cast<int>((F + gp.cols - 1) / gp.cols);
+    p.num_tiles = p.num_m_blocks * p.num_n_blocks;
     CUtensorMap to, tg, tu;
-    if (!operands(lf::BM) || !make_tmap_out64(&to, out, M, F, F))
+    if (!operands(lf::BM, static_cast<uint32_t>(gp.cols)) || !make_tmap_out64(&to, out, M, F, F))
         return LF_ERR_LAUNCH;
     tg = tu = to;
     if (gu) {
@@ -1108,8 +1112,6 @@ static lf_status gated_launch(const void *x, const float *x_scale, const void *w
             !make_tmap_out64(&tu, static_cast<char *>(gu) + 2 * F, M, F, 2 * F))
             return LF_ERR_LAUNCH;
     }
-    p.num_m_blocks = static_cast<int>((M + 2 * lf::BM - 1) / (2 * lf::BM));
-    p.num_tiles = p.num_m_blocks * p.num_n_blocks;
     // bands of M blocks whose X rows stay in L2, and at least eight (see
     // plan_gated_grads)
     const double x_bytes = 2.0 * lf::BM * static_cast<double>(K) * (e4m3 ? 1.0 : 2.0);

@@ -8,7 +8,8 @@ namespace lf {
 namespace {
 
 constexpr int G_M = 2 * BM;                // 256 rows of x per pair tile
-constexpr int G_F = BN / 2;                // 128 output columns per pair tile
+constexpr int G_F = BN / 2;                // output columns per pair tile: at most 128,
+constexpr int G_MIN_F = 64;                // and at least what half the epilogue's warps store
 // The ring: G_SLOTS slots of one K block (128 bytes of K), G_KSUB consecutive
 // slots per stage -- one wait, one commit and one barrier arm per two K blocks.
 constexpr int G_SLOTS = 6;

@@ -2,10 +2,11 @@
 //   out = act(x Wg^T) * (x Wu^T),   w = [2F, K]: Wg's rows, then Wu's,
 // in one kernel, and the elementwise part of their gradient.
 //
-// Both projections share x, so one tile computes 128 columns of each: the B
-// operand of the 256 x 256 MMA is 128 rows of Wg and 128 rows of Wu (one half
-// staged by each CTA of the pair), the accumulator's columns 0..127 are the gate
-// and 128..255 the up projection of the same output columns, and the epilogue
+// Both projections share x, so one tile computes c = 128 columns of each (64 to
+// 112 where that fills the pairs better, plan_gated_cols): the B operand of the
+// 256 x 2c MMA is c rows of Wg and c rows of Wu (one half staged by each CTA of the
+// pair), the accumulator's columns 0..c-1 are the gate and c..2c-1 the up
+// projection of the same output columns, and the epilogue
 // has both in the same TMEM lane: activation and product happen in registers
 // and neither projection is written unless the caller keeps it for the
 // backward pass.  Compute bound from a few hundred rows on (4 M F K FLOP):
@@ -108,7 +109,7 @@ __device__ __forceinline__ void g_scale(float (&f)[32], float sx, const float *w
 
 // The warp's 32 rows x 64 columns (from c0) of a finished tile.  The gate of
 // output column c is accumulator column c, its up projection accumulator column
-// 128 + c.  Returns once the accumulator has been read.
+// gp.cols + c.  Returns once the accumulator has been read.
 template <bool E4M3, int ACT>
 __device__ __forceinline__ void g_epilogue(const GatedParams &gp, const CUtensorMap *tmO, const CUtensorMap *tmG,
                                            const CUtensorMap *tmU, uint32_t taddr, int row0, int nb, int c0,
@@ -116,7 +117,7 @@ __device__ __forceinline__ void g_epilogue(const GatedParams &gp, const CUtensor
 {
     const GemmParams &p = gp.g;
     const int lane = threadIdx.x & 31;
-    const int col = nb * G_F + c0;
+    const int col = nb * gp.cols + c0;
     if (col >= p.N)
         return;  // warp-uniform
     float sx = 1.f;
@@ -126,7 +127,7 @@ __device__ __forceinline__ void g_epilogue(const GatedParams &gp, const CUtensor
     if (!E4M3 && gp.save) {
 #pragma unroll 1
         for (int side = 0; side < 2; ++side) {
-            const uint32_t t = taddr + static_cast<uint32_t>(side * G_F + c0);
+            const uint32_t t = taddr + static_cast<uint32_t>(side * gp.cols + c0);
             float f[32], h[32];
             load_acc2(t, t + 32, f, h);
             stage_begin();
@@ -139,7 +140,7 @@ __device__ __forceinline__ void g_epilogue(const GatedParams &gp, const CUtensor
     for (int half = 0; half < 2; ++half) {
         const uint32_t t = taddr + static_cast<uint32_t>(c0 + 32 * half);
         float g[32], u[32];
-        load_acc2(t, t + G_F, g, u);
+        load_acc2(t, t + static_cast<uint32_t>(gp.cols), g, u);
         g_scale<E4M3>(g, sx, gp.w_scale + col + 32 * half, p.N - col - 32 * half);
         g_scale<E4M3>(u, sx, gp.w_scale + p.N + col + 32 * half, p.N - col - 32 * half);
 #pragma unroll
@@ -181,6 +182,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
     const bool leader = rank == 0;
     const int pair = blockIdx.x >> 1;
     const int num_pairs = gridDim.x >> 1;
+    const int cols = gp.cols;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < G_STAGES; ++s) {
@@ -218,6 +220,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         if (lane == 0) {
             int stage = 0;
             uint32_t phase = 0;
+            const uint32_t slot_bytes = 2u * static_cast<uint32_t>(G_A_BYTES + cols * G_ROW);
             uint32_t armed[G_STAGES];
 #pragma unroll
             for (int s = 0; s < G_STAGES; ++s)
@@ -228,7 +231,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                 g_tile_coords(p, tile, mb, nb);
                 const int arow = mb * G_M + static_cast<int>(rank) * BM;
                 // gate rows in the leader, up rows in its peer
-                const int brow = static_cast<int>(rank) * p.N + nb * G_F;
+                const int brow = static_cast<int>(rank) * p.N + nb * cols;
                 for (int kb = 0; kb < p.num_k_blocks; kb += G_KSUB) {
                     const int nsub = min(G_KSUB, p.num_k_blocks - kb);
                     if (!wait_bar(EMPTY_BAR(stage), phase ^ 1u, abort_flag, p, ERR_PRODUCER, peer_abort)) {
@@ -240,7 +243,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                     first = false;
                     if (!skip) {
                         if (leader) {
-                            mbar_arrive_expect_tx(FULL_BAR(stage), 2u * G_SLOT_BYTES * static_cast<uint32_t>(nsub));
+                            mbar_arrive_expect_tx(FULL_BAR(stage), slot_bytes * static_cast<uint32_t>(nsub));
                             ++armed[stage];
                         }
 #pragma unroll
@@ -273,7 +276,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool alive = true;
-            const uint32_t idesc = E4M3 ? idesc_e4m3_f32(G_M, BN) : idesc_bf16_f32(G_M, BN);
+            const uint32_t idesc = E4M3 ? idesc_e4m3_f32(G_M, 2 * cols) : idesc_bf16_f32(G_M, 2 * cols);
             for (int tile = pair; tile < p.num_tiles; tile += num_pairs) {
                 if (alive)
                     alive = __all_sync(0xffffffffu, wait_bar(TEMPTY_BAR(acc), acc_phase ^ 1u, abort_flag, p, ERR_MMA_ACC,
@@ -324,10 +327,12 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         __syncwarp();
     } else {
         // ------------------------------------------------ epilogue (both CTAs)
-        // warp w reads TMEM lanes 32 (w % 4) ..; warps 2..5 take output columns
-        // 0..63 of the tile, warps 6..9 columns 64..127
+        // warp w reads TMEM lanes 32 (w % 4) ..; warps 2..5 take the tile's first 64
+        // output columns, warps 6..9 its last 64 (columns that both cover are
+        // written twice, with the same values; a tile of 64 columns needs one of them)
         const int q = warp & 3;
-        const int c0 = ((warp - 2) >> 2) * (G_F / 2);
+        const bool second = warp >= 2 + G_EPI_WARPS / 2;
+        const int c0 = second ? cols - G_MIN_F : 0;
         int acc = 0;
         uint32_t acc_phase = 0;
         uint8_t *stg = gbase + G_STG_OFF + (warp - 2) * G_STG_WARP;
@@ -339,7 +344,8 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             if (!__all_sync(0xffffffffu, ok))
                 break;
             tc_fence_after();
-            g_epilogue<E4M3, ACT>(gp, &tmO, &tmG, &tmU,
+            if (!second || cols > G_MIN_F)
+                g_epilogue<E4M3, ACT>(gp, &tmO, &tmG, &tmU,
                                   tmem_base + static_cast<uint32_t>(acc * BN) + (static_cast<uint32_t>(q * 32) << 16),
                                   mb * G_M + static_cast<int>(rank) * BM + q * 32, nb, c0, stg, stg_s);
             tc_fence_before();
@@ -733,6 +739,29 @@ static int skinny_clusters(int split, int num_sms)
     return n;
 }
 
+// 128 columns per tile keep the tensor cores fullest, and fewer fill the last wave
+// better.  A K block then costs as much as its operands' way into shared memory, 128
+// rows of x and `cols` rows of w per CTA (200 tokens of 5120 x 4096, one wave: 30.0 us
+// with 128 columns, 28.9 with 112, 27.7 with 96, 26.9 with 80, 25.1 with 64), so
+// waves x (128 + cols) orders the choices: 200 x 5120 x 13824 62.8 -> 57.6 us (96
+// columns, two waves as with 128), 333 x 2048 x 5632 24.6 -> 21.6 (80), 1024 x 4096 x
+// 8192 85.0 -> 82.3 (112), 200 x 520 x 1416 8.0 -> 6.3 (64); 4096 x 5120 x 13824
+// stays at 128 (584 us; 619 with 112).
+int plan_gated_cols(int m_blocks, int64_t F, int pairs)
+{
+    int best = 0;
+    int64_t least = 0;
+    for (int cols = G_F; cols >= G_MIN_F; cols -= 16) {  // the MMA's N is a multiple of 32
+        const int64_t tiles = (F + cols - 1) / cols * m_blocks;
+        const int64_t t = (tiles + pairs - 1) / pairs * (BM + cols);
+        if (best == 0 || t < least) {
+            least = t;
+            best = cols;
+        }
+    }
+    return best;
+}
+
 GatedSkinny plan_gated_skinny(int64_t M, int64_t F, int num_k_blocks, int num_sms)
 {
     GatedSkinny g;
@@ -757,10 +786,10 @@ GatedSkinny plan_gated_skinny(int64_t M, int64_t F, int num_k_blocks, int num_sm
     g.smem = S_MISC + g.stages * stage;
     // More than 128 tokens run here in groups only where the pair kernel's tiles
     // are few and their K loops long enough for the split to pay (us, pair kernel
-    // against this one: 200 x 2048 x 1408 13.6 / 10.2, split in four, but 200 x 512 x
-    // 1408 7.0 / 8.7; 200 x 5120 x 4096 31.1 / 26.2, split in two, but 256 x 2048 x
-    // 4096 15.7 / 16.1; unsplit 333 x 5120 x 4096 31.5 / 40.5).
-    g.preferred = groups == 1 || (g.split >= 4 && num_k_blocks >= 16) || (g.split == 2 && num_k_blocks >= 64);
+    // against this one: split in four 256 x 4096 x 1408 18.7 / 14.8, but 256 x 2048 x
+    // 1408 10.7 / 11.0 and in e4m3 7.3 / 8.9; split in two 144 x 8192 x 4096 37.8 /
+    // 33.0, but 256 x 5120 x 4096 25.3 / 26.5; unsplit 333 x 5120 x 4096 29.6 / 40.5).
+    g.preferred = groups == 1 || (g.split >= 4 && num_k_blocks >= 32) || (g.split == 2 && num_k_blocks >= 96);
     return g;
 }
 

@@ -120,19 +120,22 @@ cudaError_t launch_rms_norm_bwd(const NormBwdParams &p, void *dweight, int dtype
                                 cudaStream_t s);
 
 // Gated projections on CTA pairs (gated_ffn.cu): out = act(x Wg^T) * (x Wu^T).
-// g: M, N = F, K, block counts (256-row M blocks, 128-column N blocks, 128-byte
+// g: M, N = F, K, block counts (256-row M blocks, N blocks of cols, 128-byte
 // K blocks), num_tiles, band_m, err, timeout_ns, inject.
 struct GatedParams {
     GemmParams g;
     const float *x_scale, *w_scale;  // e4m3 operands: [M] and [2F]
     int save;                        // also store gate and up (tg, tu)
+    int cols;                        // output columns of a pair tile (plan_gated_cols)
 };
-// ta: x, boxes of 128 rows; tw: w [2F, K], boxes of 128 rows (both 128-byte
+// ta: x, boxes of 128 rows; tw: w [2F, K], boxes of cols rows (both 128-byte
 // rows, 128-byte swizzle); to: out; tg, tu: the two halves of gu (64 x 32
 // boxes, 128-byte swizzle).
 cudaError_t launch_gated_pair(bool e4m3, int act, const CUtensorMap &ta, const CUtensorMap &tw, const CUtensorMap &to,
                               const CUtensorMap &tg, const CUtensorMap &tu, const GatedParams &p, int grid,
                               cudaStream_t s);
+// The output columns of a pair tile for m_blocks blocks of 256 tokens on `pairs` CTA pairs.
+int plan_gated_cols(int m_blocks, int64_t F, int pairs);
 // The same for few tokens (operands swapped, the K loop split over clusters).
 struct GatedSkinny {
     bool preferred;  // to the pair kernel
@@ -145,7 +148,7 @@ struct GatedSkinny {
 };
 // How a call with M tokens would run (in groups of at most 128); num_k_blocks counts 128-byte K blocks.
 GatedSkinny plan_gated_skinny(int64_t M, int64_t F, int num_k_blocks, int num_sms);
-// ta: x, boxes of plan.n rows; tw as above.  gu may be null.
+// ta: x, boxes of plan.n rows; tw: boxes of 128 rows.  gu may be null.
 cudaError_t launch_gated_skinny(bool e4m3, int act, const CUtensorMap &ta, const CUtensorMap &tw, const GatedParams &p,
                                 const GatedSkinny &plan, void *gu, cudaStream_t s);
 // dgu = [dout u act'(g), dout act(g)] from gu = [g, u]; F % 8 == 0, 16-byte

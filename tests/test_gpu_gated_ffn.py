@@ -122,6 +122,52 @@ def test_forward_e4m3(M, F, K):
         check_forward(x.double() * xs.double()[:, None], w.double() * ws.double()[:, None], name, out)
 
 
+# Pair tiles of 128, 112, 96, 80 and 64 columns (with 76 pairs: the widest of them that gives
+# one wave), two waves of 96 and of 112, full and clipped last tiles
+WIDTHS = [(1000, 2432, 72), (1000, 2120, 72), (1000, 1800, 72), (1000, 1512, 72), (1000, 1208, 72), (1024, 2128, 128),
+          (257, 6912, 136), (520, 5544, 200), (140, 6160, 80), (4096, 1408, 64)]
+
+
+@pytest.mark.parametrize("M,F,K", WIDTHS)
+def test_forward_tile_widths(M, F, K):
+    x, w = inputs(M, F, K, M + F + K)
+    xd, wd = x.to(DEV), w.to(DEV)
+    out, gu = lf.gated_ffn(xd, wd, want_gu=True)
+    only, _ = lf.gated_ffn(xd, wd)
+    assert torch.equal(out, only)
+    check_forward(x.double(), w.double(), "silu", out, gu)
+    x, xs = quantised(normal((M, 2 * K), 5))
+    w, ws = quantised(normal((2 * F, 2 * K), 7, 1 / math.sqrt(K)))
+    out, _ = lf.gated_ffn(x.to(DEV), w.to(DEV), act="gelu", x_scale=xs.to(DEV), w_scale=ws.to(DEV))
+    lf.check_device_error()
+    check_forward(x.double() * xs.double()[:, None], w.double() * ws.double()[:, None], "gelu", out)
+
+
+@pytest.mark.parametrize("M,F,K", [(130, 264, 2056), (333, 1408, 2056), (200, 4104, 6152), (1000, 136, 4096)])
+def test_forward_groups_of_tokens(M, F, K):
+    """More than 128 tokens with long K loops: groups split in eight, four and two."""
+    x, w = inputs(M, F, K, M + F + K)
+    out, gu = lf.gated_ffn(x.to(DEV), w.to(DEV), want_gu=True)
+    check_forward(x.double(), w.double(), "silu", out, gu)
+    x, xs = quantised(normal((M, 2 * K), 5))
+    w, ws = quantised(normal((2 * F, 2 * K), 7, 1 / math.sqrt(K)))
+    out, _ = lf.gated_ffn(x.to(DEV), w.to(DEV), act="gelu_tanh", x_scale=xs.to(DEV), w_scale=ws.to(DEV))
+    lf.check_device_error()
+    check_forward(x.double() * xs.double()[:, None], w.double() * ws.double()[:, None], "gelu_tanh", out)
+
+
+@pytest.mark.parametrize("M,F,K", [(1000, 2120, 72), (1000, 1512, 72)])
+def test_narrow_tiles_stay_inside_their_buffers(M, F, K):
+    """Two epilogue halves that overlap: nothing outside the output, nothing left out."""
+    x, w = inputs(M, F, K)
+    buf = torch.full((M * F + 8192,), 7.0, dtype=BF16, device=DEV)
+    out = buf[4096:4096 + M * F].view(M, F)
+    lf.gated_ffn(x.to(DEV), w.to(DEV), out=out)
+    lf.check_device_error()
+    assert bool((buf[:4096] == 7).all()) and bool((buf[4096 + M * F:] == 7).all())
+    check_forward(x.double(), w.double(), "silu", out)
+
+
 @pytest.mark.parametrize("M,F,K", SHAPES)
 def test_backward(M, F, K):
     x, w = inputs(M, F, K, M + F + K)
