@@ -6,7 +6,9 @@ small: checks are attribute reads, the stream is read as a raw handle, and
 outputs come from _new (between launches an output costs 4 us from
 Tensor.new_empty, 2 us from torch.empty, 1 us from the allocation call that
 torch's compiled programs use; one buffer cut into views costs more than three
-tensors).
+tensors).  With `stream` the call runs there, its new tensors are memory of that
+stream, and ordering it against the current stream is the caller's, as for every
+other operator.
 """
 from __future__ import annotations
 
@@ -34,8 +36,23 @@ except (ImportError, AttributeError):  # pragma: no cover
     _strided = _current_device = None
 
 
-def _new(shape, dtype, ref, device):
+def _new_on(stream, shape, dtype, device):
+    """The same for a call on a stream of its own: memory whose earlier users, if
+    any, ran on that stream (work that the current stream still has to do may
+    read anything else that it freed), and that is not handed out again before
+    the current stream is done with it either."""
+    current = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if current != stream:
+        t.record_stream(current)
+    return t
+
+
+def _new(shape, dtype, ref, device, stream=None):
     """A contiguous tensor of `shape` on ref's device (index `device`)."""
+    if stream is not None:
+        return _new_on(stream, shape, dtype, ref.device)
     n = len(shape)
     if _strided is None or n > 2 or _current_device() != device:
         return torch.empty(shape, dtype=dtype, device=ref.device)
@@ -174,18 +191,19 @@ def add_rms_norm(x, weight, residual=None, eps=1e-6, fp8=False, h=None, y=None, 
             raise ValueError("residual must have x's shape")
         ldr = D if residual.is_contiguous() else _pitch(residual, "residual")
         r_ptr = residual.data_ptr()
-        h = _new(shape, dtype, x, dev) if h is None else _output(h, dtype, shape, dev, "h")
+        h = _new(shape, dtype, x, dev, stream) if h is None else _output(h, dtype, shape, dev, "h")
         h_ptr = h.data_ptr()
     elif h is not None:
         raise ValueError("h is written only where a residual is added")
     if fp8:
-        y = _new(shape, _FP8, x, dev) if y is None else _output(y, _FP8, shape, dev, "y")
-        scale = _new(shape[:-1], _F32, x, dev) if scale is None else _output(scale, _F32, shape[:-1], dev, "scale")
+        y = _new(shape, _FP8, x, dev, stream) if y is None else _output(y, _FP8, shape, dev, "y")
+        scale = (_new(shape[:-1], _F32, x, dev, stream) if scale is None
+                 else _output(scale, _F32, shape[:-1], dev, "scale"))
         s_ptr = scale.data_ptr()
     else:
         if scale is not None:
             raise ValueError("scale is written only with fp8")
-        y = _new(shape, dtype, x, dev) if y is None else _output(y, dtype, shape, dev, "y")
+        y = _new(shape, dtype, x, dev, stream) if y is None else _output(y, dtype, shape, dev, "y")
     if M > 0 or D == 0:
         st = _lib().add_rms_norm(x.data_ptr(), ldx, r_ptr, ldr, weight.data_ptr(), h_ptr, y.data_ptr(), s_ptr, code,
                                  wcode, LF_E4M3 if fp8 else code, eps, M, D, _handle(stream, dev))
@@ -218,14 +236,12 @@ def add_rms_norm_backward(dy, h, weight, dh=None, eps=1e-6, want_dweight=True, d
         if dh.shape != shape:
             raise ValueError("dh must have h's shape")
         dh_ptr = dh.data_ptr()
-    dx = _new(shape, dtype, h, dev) if dx is None else _output(dx, dtype, shape, dev, "dx")
+    dx = _new(shape, dtype, h, dev, stream) if dx is None else _output(dx, dtype, shape, dev, "dx")
     if want_dweight or dweight is not None:
-        dweight = (_new(weight.shape, weight.dtype, h, dev) if dweight is None
+        dweight = (_new(weight.shape, weight.dtype, h, dev, stream) if dweight is None
                    else _output(dweight, weight.dtype, weight.shape, dev, "dweight"))
         if M > 0:
-            scratch = _new((_norm_scratch(M, D),), torch.uint8, h, dev)
-            if stream is not None:
-                scratch.record_stream(stream)
+            scratch = _new((_norm_scratch(M, D),), torch.uint8, h, dev, stream)
             dw_ptr, scratch_ptr = dweight.data_ptr(), scratch.data_ptr()
     if M == 0 and D > 0:
         return dx, _zeroed(dweight, stream)
@@ -259,7 +275,7 @@ def gated_ffn(x, w, act="silu", x_scale=None, w_scale=None, want_gu=False, out=N
     scaled = x_scale is not None or w_scale is not None
     M, F, K, dev = _gated_dims(x, w, _FP8 if scaled else _BF16)
     lead = x.shape[:-1]
-    out = (_new((*lead, F), _BF16, x, dev) if out is None
+    out = (_new((*lead, F), _BF16, x, dev, stream) if out is None
            else _output(out, _BF16, (*lead, F), dev, "out"))
     if scaled:
         if x_scale is None or w_scale is None or want_gu or gu is not None:
@@ -269,7 +285,7 @@ def gated_ffn(x, w, act="silu", x_scale=None, w_scale=None, want_gu=False, out=N
         if x_scale.numel() != M or w_scale.numel() != 2 * F:
             raise ValueError("x_scale must hold one scale per row of x and w_scale one per row of w")
     elif want_gu or gu is not None:
-        gu = (_new((*lead, 2 * F), _BF16, x, dev) if gu is None
+        gu = (_new((*lead, 2 * F), _BF16, x, dev, stream) if gu is None
               else _output(gu, _BF16, (*lead, 2 * F), dev, "gu"))
     if M == 0 and F > 0 and K > 0:
         return out, gu
@@ -297,22 +313,18 @@ def gated_ffn_backward(dout, x, w, gu, act="silu", want_dx=True, want_dw=True, d
     if tuple(dout.shape) != (*lead, F) or tuple(gu.shape) != (*lead, 2 * F):
         raise ValueError("dout must be [..., F] and gu [..., 2F] for x's rows")
     if dgu is None:
-        dgu = _new(gu.shape, _BF16, x, dev)
-        if stream is not None:
-            dgu.record_stream(stream)
+        dgu = _new(gu.shape, _BF16, x, dev, stream)
     else:
         _output(dgu, _BF16, gu.shape, dev, "dgu")
     if want_dx or dx is not None:
-        dx = _new(x.shape, _BF16, x, dev) if dx is None else _output(dx, _BF16, x.shape, dev, "dx")
+        dx = _new(x.shape, _BF16, x, dev, stream) if dx is None else _output(dx, _BF16, x.shape, dev, "dx")
     if want_dw or dw is not None:
-        dw = _new(w.shape, _BF16, x, dev) if dw is None else _output(dw, _BF16, w.shape, dev, "dw")
+        dw = _new(w.shape, _BF16, x, dev, stream) if dw is None else _output(dw, _BF16, w.shape, dev, "dw")
     if M == 0 and F > 0 and K > 0:
         return dx, _zeroed(dw, stream)
     L = _lib()
     nbytes = _gated_scratch(M, F, K)
-    scratch = _new((nbytes,), torch.uint8, x, dev) if nbytes else None
-    if scratch is not None and stream is not None:
-        scratch.record_stream(stream)
+    scratch = _new((nbytes,), torch.uint8, x, dev, stream) if nbytes else None
     _lf._check(L.gated_ffn_backward(dout.data_ptr(), x.data_ptr(), w.data_ptr(), gu.data_ptr(), code, dgu.data_ptr(),
                                     None if dx is None else dx.data_ptr(), None if dw is None else dw.data_ptr(),
                                     None if scratch is None else scratch.data_ptr(), M, F, K, _handle(stream, dev)),

@@ -332,6 +332,25 @@ def test_on_side_streams_and_captured():
         check_backward(dout.cpu(), x, w, gu.cpu(), "silu", dx, dw)
 
 
+def test_new_tensors_of_a_side_stream():
+    """They are not memory that work of the current stream may still read."""
+    M, F, K = 1024, 2048, 1024
+    x, w = (t.to(DEV) for t in inputs(M, F, K))
+    out, gu = lf.gated_ffn(x, w, want_gu=True)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    for call, like in ((lambda: lf.gated_ffn(x, w, stream=side)[0], out),
+                       (lambda: lf.gated_ffn_backward(out, x, w, gu, stream=side)[1], w)):
+        freed = torch.empty_like(like)
+        at = freed.data_ptr()
+        del freed
+        got = call()
+        assert got.data_ptr() != at
+        torch.cuda.synchronize()
+        lf.check_device_error()
+
+
 def test_repeatable():
     x, w = (t.to(DEV) for t in inputs(700, 392, 1032))
     dout = normal((700, 392), 3).to(BF16).to(DEV)

@@ -404,6 +404,30 @@ def test_on_a_side_stream_and_captured():
         check_backward(res.cpu(), q[1].cpu(), w.cpu(), x.cpu(), grad)
 
 
+def test_new_tensors_of_a_side_stream():
+    """They are neither memory that work of the current stream may still read, nor handed
+    out again while the current stream may still read them."""
+    M, D = 512, 4096
+    x, w = normal((M, D), 96).to(DEV), torch.ones(D, device=DEV)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    calls = (lambda: lf.add_rms_norm(x, w, stream=side)[0], lambda: lf.add_rms_norm_backward(x, x, w, stream=side)[0])
+    for call in calls:
+        freed = torch.empty_like(x)
+        at = freed.data_ptr()
+        del freed
+        got = call()
+        assert got.data_ptr() != at
+        at = got.data_ptr()
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda._sleep(50_000_000)  # the current stream is at work, and could be reading got
+        del got
+        again = call()
+        assert again.data_ptr() != at
+        torch.cuda.synchronize()
+
+
 @pytest.mark.parametrize("M,D", [(525_000, 4104), (300_001, 7171)])
 def test_offsets_past_32_bits(M, D):
     """More than 2^31 elements: rows at both ends and around the border."""
