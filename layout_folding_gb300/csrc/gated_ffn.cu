@@ -417,8 +417,8 @@ cudaError_t launch_gated_pair_t(const CUtensorMap &ta, const CUtensorMap &tw, co
 }
 
 // ---------------------------------------------------------------- few tokens
-// Up to 128 tokens (and groups of 128 where tiles are few, plan_gated_skinny): the
-// weights' bytes bound the call, so the operands are
+// Up to 128 tokens (and groups of 128 where tiles are few and K long, see
+// plan_gated_skinny): the weights' bytes bound the call, so the operands are
 // swapped -- 128 gate rows and 128 up rows of w are the A operands of two
 // 128 x n MMAs whose B operand is the tokens (n: M rounded up to 16) -- and a CTA
 // only streams its share of w through a ring of 32 KiB stages (plus the tokens'
@@ -799,12 +799,23 @@ GatedSkinny plan_gated_skinny(int64_t M, int64_t F, int num_k_blocks, int num_sm
     const int fit = ((two ? S_SMEM_TWO : S_SMEM_ONE) - S_MISC) / stage;
     g.stages = fit < S_MAX_STAGES ? fit : S_MAX_STAGES;
     g.smem = S_MISC + g.stages * stage;
-    // More than 128 tokens run here in groups only where the pair kernel's tiles
-    // are few and their K loops long enough for the split to pay (us, pair kernel
-    // against this one: split in four 256 x 4096 x 1408 18.7 / 14.8, but 256 x 2048 x
-    // 1408 10.7 / 11.0 and in e4m3 7.3 / 8.9; split in two 144 x 8192 x 4096 37.8 /
-    // 33.0, but 256 x 5120 x 4096 25.3 / 26.5; unsplit 333 x 5120 x 4096 29.6 / 40.5).
-    g.preferred = groups == 1 || (g.split >= 4 && num_k_blocks >= 32) || (g.split == 2 && num_k_blocks >= 96);
+    // The choice between this kernel and the pair kernel, which has no sums to exchange
+    // (us, pair kernel against this one, K blocks in brackets).  Up to 16 tokens: always
+    // this one (16 x 256 x 4096 e4m3 [2] 5.8 / 3.9).  Up to 128: where the K loop is long
+    // for the tokens (64 x 512 x 1408 [8] 4.9 / 6.7, 64 x 1024 x 1408 [16] 6.3 / 6.2; 128 x
+    // 1024 x 4096 [16] 7.3 / 9.3, 128 x 2048 x 1408 [32] 9.3 / 9.8), or the tiles fill the
+    // device without a split (64 x 512 x 11008 10.0 / 8.4, 96 x 512 x 11008 10.6 / 9.8, but
+    // 128 x 512 x 11008 9.5 / 11.3).
+    // More tokens, in groups: only where the tiles are few, and the K loops long enough
+    // for the split to pay for its sums, which grow with the tokens of a group (split in
+    // four or eight 144 x 2048 x 512 [32] 9.0 / 7.4, 144 x 1024 x 512 [16] 6.3 / 6.5; 256 x
+    // 4096 x 512 [64] 14.4 / 11.2, 256 x 2048 x 512 [32] 9.1 / 9.6; split in two 144 x 5120 x
+    // 4096 [80] 24.9 / 23.5, 256 x 5120 x 4096 [80] 25.3 / 26.5, 256 x 8192 x 4096 [128]
+    // 38.1 / 36.8; unsplit 333 x 5120 x 4096 29.6 / 40.5).
+    if (groups == 1)
+        g.preferred = g.n <= 16 || 4 * num_k_blocks >= g.n || (g.n <= 96 && tiles > num_sms / 2);
+    else
+        g.preferred = (g.split >= 4 && 3 * num_k_blocks >= g.n) || (g.split == 2 && 4 * num_k_blocks >= 3 * g.n);
     return g;
 }
 

@@ -156,6 +156,21 @@ def test_forward_groups_of_tokens(M, F, K):
     check_forward(x.double() * xs.double()[:, None], w.double() * ws.double()[:, None], "gelu_tanh", out)
 
 
+@pytest.mark.parametrize("M,F,K", [(1, 520, 72), (15, 136, 200), (33, 20000, 200), (64, 520, 1016), (64, 520, 1032),
+                                   (90, 12000, 136), (112, 12000, 136), (128, 136, 2056), (128, 1000, 2000),
+                                   (300, 1408, 2760)])
+def test_forward_on_both_sides_of_the_choice(M, F, K):
+    """Few tokens with short and long K loops, few and many tiles."""
+    x, w = inputs(M, F, K, M + F + K)
+    out, gu = lf.gated_ffn(x.to(DEV), w.to(DEV), want_gu=True)
+    check_forward(x.double(), w.double(), "silu", out, gu)
+    x, xs = quantised(normal((M, 2 * K), 5))
+    w, ws = quantised(normal((2 * F, 2 * K), 7, 1 / math.sqrt(K)))
+    out, _ = lf.gated_ffn(x.to(DEV), w.to(DEV), act="gelu_tanh", x_scale=xs.to(DEV), w_scale=ws.to(DEV))
+    lf.check_device_error()
+    check_forward(x.double() * xs.double()[:, None], w.double() * ws.double()[:, None], "gelu_tanh", out)
+
+
 @pytest.mark.parametrize("M,F,K", [(1000, 2120, 72), (1000, 1512, 72)])
 def test_narrow_tiles_stay_inside_their_buffers(M, F, K):
     """Two epilogue halves that overlap: nothing outside the output, nothing left out."""
