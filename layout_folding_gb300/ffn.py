@@ -8,7 +8,7 @@ Tensor.new_empty, 2 us from torch.empty, 1 us from the allocation call that
 torch's compiled programs use; one buffer cut into views costs more than three
 tensors).  With `stream` the call runs there, its new tensors are memory of that
 stream, and ordering it against the current stream is the caller's, as for every
-other operator.
+other operator.  Tensors and stream are of the current device.
 """
 from __future__ import annotations
 
@@ -31,9 +31,20 @@ _L = None
 try:
     # contiguous tensors on the current device, without the general argument parser
     from torch._C._dynamo.guards import _empty_strided_cuda as _strided
-    _current_device = torch._C._cuda_getDevice
-except (ImportError, AttributeError):  # pragma: no cover
-    _strided = _current_device = None
+except ImportError:  # pragma: no cover
+    _strided = None
+# the current device as an integer (the calls have a CUDA tensor in hand, so CUDA is initialised)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _on_current(device, stream):
+    """Kernels are launched on the current device, with its tensor maps, limits and
+    error word: tensors or a stream of another one are refused."""
+    current = _current_device()
+    if device != current:
+        raise ValueError("the tensors are on cuda:%d and the current device is cuda:%d" % (device, current))
+    if stream is not None and stream.device.index != current:
+        raise ValueError("stream is of cuda:%d and the current device is cuda:%d" % (stream.device.index, current))
 
 
 def _new_on(stream, shape, dtype, device):
@@ -49,12 +60,12 @@ def _new_on(stream, shape, dtype, device):
     return t
 
 
-def _new(shape, dtype, ref, device, stream=None):
-    """A contiguous tensor of `shape` on ref's device (index `device`)."""
+def _new(shape, dtype, ref, stream=None):
+    """A contiguous tensor of `shape` on ref's device, the current one."""
     if stream is not None:
         return _new_on(stream, shape, dtype, ref.device)
     n = len(shape)
-    if _strided is None or n > 2 or _current_device() != device:
+    if _strided is None or n > 2:
         return torch.empty(shape, dtype=dtype, device=ref.device)
     if n == 2:
         return _strided(tuple(shape), (shape[1] or 1, 1), dtype)
@@ -83,7 +94,7 @@ def _handle(stream, device):
         return stream.cuda_stream
     if _raw_stream is not None:
         return _raw_stream(device)
-    return torch.cuda.current_stream().cuda_stream
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 _Tensor = torch.Tensor
@@ -177,6 +188,7 @@ def add_rms_norm(x, weight, residual=None, eps=1e-6, fp8=False, h=None, y=None, 
     shape = x.shape if dev >= 0 else ()
     if not shape:
         _stream_type(x, "x")  # raises
+    _on_current(dev, stream)
     D = shape[-1]
     M = x.numel() // D if D else 0
     ldx = D if x.is_contiguous() else _pitch(x, "x")
@@ -191,19 +203,19 @@ def add_rms_norm(x, weight, residual=None, eps=1e-6, fp8=False, h=None, y=None, 
             raise ValueError("residual must have x's shape")
         ldr = D if residual.is_contiguous() else _pitch(residual, "residual")
         r_ptr = residual.data_ptr()
-        h = _new(shape, dtype, x, dev, stream) if h is None else _output(h, dtype, shape, dev, "h")
+        h = _new(shape, dtype, x, stream) if h is None else _output(h, dtype, shape, dev, "h")
         h_ptr = h.data_ptr()
     elif h is not None:
         raise ValueError("h is written only where a residual is added")
     if fp8:
-        y = _new(shape, _FP8, x, dev, stream) if y is None else _output(y, _FP8, shape, dev, "y")
-        scale = (_new(shape[:-1], _F32, x, dev, stream) if scale is None
+        y = _new(shape, _FP8, x, stream) if y is None else _output(y, _FP8, shape, dev, "y")
+        scale = (_new(shape[:-1], _F32, x, stream) if scale is None
                  else _output(scale, _F32, shape[:-1], dev, "scale"))
         s_ptr = scale.data_ptr()
     else:
         if scale is not None:
             raise ValueError("scale is written only with fp8")
-        y = _new(shape, dtype, x, dev, stream) if y is None else _output(y, dtype, shape, dev, "y")
+        y = _new(shape, dtype, x, stream) if y is None else _output(y, dtype, shape, dev, "y")
     if M > 0 or D == 0:
         st = _lib().add_rms_norm(x.data_ptr(), ldx, r_ptr, ldr, weight.data_ptr(), h_ptr, y.data_ptr(), s_ptr, code,
                                  wcode, LF_E4M3 if fp8 else code, eps, M, D, _handle(stream, dev))
@@ -223,6 +235,7 @@ def add_rms_norm_backward(dy, h, weight, dh=None, eps=1e-6, want_dweight=True, d
     shape = h.shape if dev >= 0 else ()
     if not shape:
         _stream_type(h, "h")  # raises
+    _on_current(dev, stream)
     _require(h, dtype, dev, "h")
     _require(dy, dtype, dev, "dy")
     if dy.shape != shape:
@@ -236,12 +249,12 @@ def add_rms_norm_backward(dy, h, weight, dh=None, eps=1e-6, want_dweight=True, d
         if dh.shape != shape:
             raise ValueError("dh must have h's shape")
         dh_ptr = dh.data_ptr()
-    dx = _new(shape, dtype, h, dev, stream) if dx is None else _output(dx, dtype, shape, dev, "dx")
+    dx = _new(shape, dtype, h, stream) if dx is None else _output(dx, dtype, shape, dev, "dx")
     if want_dweight or dweight is not None:
-        dweight = (_new(weight.shape, weight.dtype, h, dev, stream) if dweight is None
+        dweight = (_new(weight.shape, weight.dtype, h, stream) if dweight is None
                    else _output(dweight, weight.dtype, weight.shape, dev, "dweight"))
         if M > 0:
-            scratch = _new((_norm_scratch(M, D),), torch.uint8, h, dev, stream)
+            scratch = _new((_norm_scratch(M, D),), torch.uint8, h, stream)
             dw_ptr, scratch_ptr = dweight.data_ptr(), scratch.data_ptr()
     if M == 0 and D > 0:
         return dx, _zeroed(dweight, stream)
@@ -252,9 +265,10 @@ def add_rms_norm_backward(dy, h, weight, dh=None, eps=1e-6, want_dweight=True, d
     return dx, dweight
 
 
-def _gated_dims(x, w, dtype):
+def _gated_dims(x, w, dtype, stream):
     _cuda(x, "x")
     dev = x.get_device()
+    _on_current(dev, stream)
     _require(x, dtype, dev, "x")
     _require(w, dtype, dev, "w")
     if w.dim() != 2 or x.dim() == 0 or w.shape[1] != x.shape[-1] or w.shape[0] % 2:
@@ -273,9 +287,9 @@ def gated_ffn(x, w, act="silu", x_scale=None, w_scale=None, want_gu=False, out=N
     that gated_ffn_backward takes, when want_gu (bf16 operands only), else None."""
     code = _activation(act)
     scaled = x_scale is not None or w_scale is not None
-    M, F, K, dev = _gated_dims(x, w, _FP8 if scaled else _BF16)
+    M, F, K, dev = _gated_dims(x, w, _FP8 if scaled else _BF16, stream)
     lead = x.shape[:-1]
-    out = (_new((*lead, F), _BF16, x, dev, stream) if out is None
+    out = (_new((*lead, F), _BF16, x, stream) if out is None
            else _output(out, _BF16, (*lead, F), dev, "out"))
     if scaled:
         if x_scale is None or w_scale is None or want_gu or gu is not None:
@@ -285,7 +299,7 @@ def gated_ffn(x, w, act="silu", x_scale=None, w_scale=None, want_gu=False, out=N
         if x_scale.numel() != M or w_scale.numel() != 2 * F:
             raise ValueError("x_scale must hold one scale per row of x and w_scale one per row of w")
     elif want_gu or gu is not None:
-        gu = (_new((*lead, 2 * F), _BF16, x, dev, stream) if gu is None
+        gu = (_new((*lead, 2 * F), _BF16, x, stream) if gu is None
               else _output(gu, _BF16, (*lead, 2 * F), dev, "gu"))
     if M == 0 and F > 0 and K > 0:
         return out, gu
@@ -306,25 +320,25 @@ def gated_ffn_backward(dout, x, w, gu, act="silu", want_dx=True, want_dw=True, d
     dgu [..., 2F] receives the gradient of the two projections (pass gu itself
     to reuse its memory; a new tensor by default)."""
     code = _activation(act)
-    M, F, K, dev = _gated_dims(x, w, _BF16)
+    M, F, K, dev = _gated_dims(x, w, _BF16, stream)
     lead = x.shape[:-1]
     _require(dout, _BF16, dev, "dout")
     _require(gu, _BF16, dev, "gu")
     if tuple(dout.shape) != (*lead, F) or tuple(gu.shape) != (*lead, 2 * F):
         raise ValueError("dout must be [..., F] and gu [..., 2F] for x's rows")
     if dgu is None:
-        dgu = _new(gu.shape, _BF16, x, dev, stream)
+        dgu = _new(gu.shape, _BF16, x, stream)
     else:
         _output(dgu, _BF16, gu.shape, dev, "dgu")
     if want_dx or dx is not None:
-        dx = _new(x.shape, _BF16, x, dev, stream) if dx is None else _output(dx, _BF16, x.shape, dev, "dx")
+        dx = _new(x.shape, _BF16, x, stream) if dx is None else _output(dx, _BF16, x.shape, dev, "dx")
     if want_dw or dw is not None:
-        dw = _new(w.shape, _BF16, x, dev, stream) if dw is None else _output(dw, _BF16, w.shape, dev, "dw")
+        dw = _new(w.shape, _BF16, x, stream) if dw is None else _output(dw, _BF16, w.shape, dev, "dw")
     if M == 0 and F > 0 and K > 0:
         return dx, _zeroed(dw, stream)
     L = _lib()
     nbytes = _gated_scratch(M, F, K)
-    scratch = _new((nbytes,), torch.uint8, x, dev, stream) if nbytes else None
+    scratch = _new((nbytes,), torch.uint8, x, stream) if nbytes else None
     _lf._check(L.gated_ffn_backward(dout.data_ptr(), x.data_ptr(), w.data_ptr(), gu.data_ptr(), code, dgu.data_ptr(),
                                     None if dx is None else dx.data_ptr(), None if dw is None else dw.data_ptr(),
                                     None if scratch is None else scratch.data_ptr(), M, F, K, _handle(stream, dev)),
