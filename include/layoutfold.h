@@ -16,8 +16,8 @@
  *
  * Every compute call requires an sm_103 device (LF_ERR_ARCH otherwise).  There
  * is no CPU fallback.  Calls run on the device that is current when they are
- * made: every pointer and the stream have to be that device's, which the
- * library cannot check.
+ * made: every pointer and the stream have to be that device's.  The library
+ * cannot check that; the Python binding does, and refuses the call.
  *
  * Debugging aids: with LF_DEBUG_SYNC set (to anything but "0") in the
  * environment when the library is first used, every compute call
