@@ -374,7 +374,8 @@ typedef enum {
  *            f[m,d] = h[m,d] r weight[d] (statistics and products in fp32):
  *              y = rn(f), or for LF_E4M3 y = e4m3(f / scale[m])
  *   scale_or_null : fp32 [M], required exactly when ydtype is LF_E4M3:
- *              scale[m] = max_d |f[m,d]| / 448, or 1 where that maximum is 0,
+ *              scale[m] = max_d |f[m,d]| / 448, or 1 where that is 0 in fp32 (a row
+ *              of zeros, or of magnitudes below about 2^-141),
  *            so y[m,d] scale[m] stands for f.  A row with a NaN (or an
  *            infinity, whose norm is undefined) gets a NaN scale and NaN codes.
  *   eps >= 0.  1 <= M, D < 2^31; ldx, ldr >= D (LF_ERR_SHAPE otherwise).

@@ -20,6 +20,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
+#include <math_constants.h>
 #include <type_traits>
 
 #include "lf_internal.h"
@@ -219,28 +220,28 @@ __device__ __forceinline__ float2 block_reduce(float a, uint32_t b, float2 *sh)
 
 // The e4m3 scale of a row and the factor that takes h weight to its code: f is
 // h weight r, and its largest magnitude r times mx = max |h weight|, so
-// f / scale = h weight (448 / mx).  Rows that are not ordinary: all zeros (scale
-// 1), NaN, and magnitudes so small that 448 / mx could overflow (`tiny`: the
-// codes then come from a division by the scale).
+// f / scale = h weight (448 / mx).  A scale that would be 0 is 1; NaN stays NaN.
+// `wide`: a product h weight overflowed, or they are so small that they lose bits or
+// 448 / mx could overflow, although (h r) weight may be an ordinary number: its scale
+// is left as -r for wide_rows, which does the row again.  Rows of zeros stay here: h or
+// the weights are 0, h so small that its squares are, or products below 2^-150 with
+// r <= 2^8, whose f / 448 is 0 as well.
 struct RowScale {
     float scale, factor;
-    bool tiny;
-    __device__ __forceinline__ RowScale(float mx, float r)
+    bool wide;
+    __device__ __forceinline__ RowScale(float mx, float ss, float r)
     {
-        const float amax = mx * r;
-        scale = amax == 0.f ? 1.f : amax / E4M3_MAX;
-        tiny = mx < 0x1p-100f || scale < 0x1p-120f;
-        factor = amax == 0.f ? r : amax != amax ? amax : E4M3_MAX / mx;
+        const float q = mx * r / E4M3_MAX;
+        const bool zeros = mx == 0.f && (ss == 0.f || r <= 256.f);
+        wide = !zeros && (mx < 0x1p-100f || q < 0x1p-120f || mx == CUDART_INF_F);
+        scale = wide ? -r : q == 0.f ? 1.f : q;
+        factor = q == 0.f ? r : q != q ? q : E4M3_MAX / mx;
     }
     // f: h weight, N of them, to what is converted to e4m3
     template <int N>
-    __device__ __forceinline__ void apply(float (&f)[N], float r) const
+    __device__ __forceinline__ void apply(float (&f)[N]) const
     {
-        if (tiny) {
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                f[i] = f[i] * r / scale;
-        } else if constexpr (N % 2 == 0) {
+        if constexpr (N % 2 == 0) {
 #pragma unroll
             for (int i = 0; i < N; i += 2) {
                 const float2 v = mul2(make_float2(f[i], f[i + 1]), both(factor));
@@ -277,19 +278,82 @@ __device__ __forceinline__ void store_e4m3(uint8_t *p, const float (&f)[VEC])
     }
 }
 
+__device__ __forceinline__ void group_barrier(int id, int threads)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// This thread's group's rows (group g of the block's `groups` of group_threads each:
+// rows g gridDim + blockIdx, and so on in steps of all groups) whose scale says wide:
+// f = (h r) weight and f / scale, element by element from their h in memory.  `sh`
+// holds one word per warp of the block.  Done after a kernel's own rows, with nothing
+// kept for it but that there is one: inside their loop it makes the ring kernel keep some
+// fifty bytes of a thread's registers in local memory.
+template <class T, class W>
+__device__ __forceinline__ void wide_rows(const NormParams &p, uint32_t *sh, int group_threads, int groups)
+{
+    const int group = threadIdx.x / group_threads, t = threadIdx.x % group_threads;
+    const int warps = group_threads >> 5, first_warp = group * warps, lane = t & 31;
+    const T *h = static_cast<const T *>(p.residual ? p.h : p.x);
+    const int64_t ld = p.residual ? p.D : p.ldx, D = p.D;
+    const W *w = static_cast<const W *>(p.weight);
+    const auto sync = [&] {
+        if (warps > 1)
+            group_barrier(1 + group, group_threads);
+        else
+            __syncwarp();
+    };
+    const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+#pragma unroll 1
+    for (int64_t row = static_cast<int64_t>(group) * gridDim.x + blockIdx.x; row < p.M; row += step) {
+        sync();  // the row's h, codes and scale are written, the last row's words read
+        const float mark = p.scale[row];
+        if (static_cast<int>(__float_as_uint(mark)) >= 0 || mark != mark)
+            continue;
+        const float r = -mark;
+        const T *hr = h + row * ld;
+        float m = 0.f;
+#pragma unroll 1
+        for (int64_t c = t; c < D; c += group_threads)
+            m = max_mag(m, to_f(hr[c]) * r * to_f(w[c]));
+        uint32_t b = __reduce_max_sync(0xffffffffu, mag_bits(m));
+        if (lane == 0)
+            sh[first_warp + (t >> 5)] = b;
+        sync();
+        b = __reduce_max_sync(0xffffffffu, lane < warps ? sh[first_warp + lane] : 0u);
+        const float q = __uint_as_float(b) / E4M3_MAX, s = q == 0.f ? 1.f : q;
+        if (t == 0)
+            p.scale[row] = s;
+#pragma unroll 1
+        for (int64_t c = t; c < D; c += group_threads)
+            static_cast<uint8_t *>(p.y)[row * D + c] =
+                static_cast<uint8_t>(e4m3_pair(to_f(hr[c]) * r * to_f(w[c]) / s, 0.f) & 0xffu);
+    }
+}
+
+// The same for the ring kernel, out of the way of its code (8192 x 5120 49.4 us, in line
+// 50.4; the kernels of one block per row need eight registers more for a call).
+template <class T, class W>
+__device__ __noinline__ void ring_wide_rows(const NormParams &p, uint32_t *sh, int group_threads, int groups)
+{
+    wide_rows<T, W>(p, sh, group_threads, groups);
+}
+
 // One row per block and step; thread t holds the row's packs t, t + threads, ...
 // (NV of them at most).
 template <class T, class W, int VEC, int NV, bool FP8>
-__global__ void __launch_bounds__(NV <= 2 ? 512 : 1024) k_rms_norm(const NormParams p)
+__global__ void __launch_bounds__(NV <= 2 ? 512 : 1024) k_rms_norm(const __grid_constant__ NormParams p)
 {
     wait_previous_kernel();
     let_next_kernel_start();
     __shared__ float2 sh[2][MAX_WARPS];
+    __shared__ uint32_t wide_sh[MAX_WARPS];
     const int packs = static_cast<int>(p.D / VEC);
     const T *x = static_cast<const T *>(p.x);
     const T *res = static_cast<const T *>(p.residual);
     const W *w = static_cast<const W *>(p.weight);
     int buf = 0;
+    bool wide = false;
     for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x, buf ^= 1) {
         Pack<T, VEC> h[NV];
         float ss = 0.f;
@@ -330,9 +394,10 @@ __global__ void __launch_bounds__(NV <= 2 ? 512 : 1024) k_rms_norm(const NormPar
         }
         const float2 sums = block_reduce<true>(ss, mag_bits(mx), sh[buf]);
         const float r = rsqrtf(sums.x / static_cast<float>(p.D) + p.eps);
-        const RowScale rs(sums.y, r);
+        const RowScale rs(sums.y, sums.x, r);
         if (FP8 && threadIdx.x == 0)
             p.scale[row] = rs.scale;
+        wide |= FP8 && rs.wide;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = threadIdx.x + j * blockDim.x;
@@ -345,7 +410,7 @@ __global__ void __launch_bounds__(NV <= 2 ? 512 : 1024) k_rms_norm(const NormPar
 #pragma unroll
                     for (int i = 0; i < VEC; ++i)
                         f[i] *= wv[i];
-                    rs.apply(f, r);
+                    rs.apply(f);
                     store_e4m3<VEC>(static_cast<uint8_t *>(p.y) + o, f);
                 } else {
 #pragma unroll
@@ -358,19 +423,24 @@ __global__ void __launch_bounds__(NV <= 2 ? 512 : 1024) k_rms_norm(const NormPar
             }
         }
     }
+    if constexpr (FP8)
+        if (wide)  // the same for every thread
+            wide_rows<T, W>(p, wide_sh, blockDim.x, 1);
 }
 
 // Rows that do not fit the registers of a block: the row is read a second time
 // (h, which each thread wrote itself, or x where nothing is added).
 template <class T, class W, bool FP8>
-__global__ void __launch_bounds__(1024) k_rms_norm_long(const NormParams p)
+__global__ void __launch_bounds__(1024) k_rms_norm_long(const __grid_constant__ NormParams p)
 {
     wait_previous_kernel();
     let_next_kernel_start();
     __shared__ float2 sh[2][MAX_WARPS];
+    __shared__ uint32_t wide_sh[MAX_WARPS];
     const T *res = static_cast<const T *>(p.residual);
     const W *w = static_cast<const W *>(p.weight);
     int buf = 0;
+    bool wide = false;
     for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x, buf ^= 1) {
         const T *x = static_cast<const T *>(p.x) + row * p.ldx;
         T *h = res ? static_cast<T *>(p.h) + row * p.D : nullptr;
@@ -389,20 +459,24 @@ __global__ void __launch_bounds__(1024) k_rms_norm_long(const NormParams p)
         }
         const float2 sums = block_reduce<true>(ss, mag_bits(mx), sh[buf]);
         const float r = rsqrtf(sums.x / static_cast<float>(p.D) + p.eps);
-        const RowScale rs(sums.y, r);
+        const RowScale rs(sums.y, sums.x, r);
         if (FP8 && threadIdx.x == 0)
             p.scale[row] = rs.scale;
+        wide |= FP8 && rs.wide;
         for (int64_t c = threadIdx.x; c < p.D; c += blockDim.x) {
             const float v = to_f(res ? h[c] : x[c]);
             if (FP8) {
                 float f[1] = {v * to_f(w[c])};
-                rs.apply(f, r);
+                rs.apply(f);
                 store_e4m3<1>(static_cast<uint8_t *>(p.y) + row * p.D + c, f);
             } else {
                 static_cast<T *>(p.y)[row * p.D + c] = from_f<T>(v * (r * to_f(w[c])));
             }
         }
     }
+    if constexpr (FP8)
+        if (wide)  // the same for every thread
+            wide_rows<T, W>(p, wide_sh, blockDim.x, 1);
 }
 
 // Backward: block b takes rows b, b + blocks, ...; thread t keeps the weight
@@ -607,13 +681,10 @@ struct RingPlan {
 struct RingSync {
     float2 sums[2][MAX_WARPS];
     int failed[2][MAX_WARPS];
+    int wide;                      // the block had a row for wide_rows
+    uint32_t wide_max[MAX_WARPS];  // (its sh)
     alignas(8) unsigned long long full[RING_MAX_GROUPS * RING_MAX_SLOTS];
 };
-
-__device__ __forceinline__ void group_barrier(int id, int threads)
-{
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
 
 // Bounded wait for a slot; on a timeout the code goes to the device error word.
 __device__ __forceinline__ bool ring_wait(uint32_t bar, uint32_t parity, const WaitLimit &lim)
@@ -677,10 +748,10 @@ template <class T, bool PH>
 struct RowSpan {
     static constexpr int VEC = 16 / static_cast<int>(sizeof(T));
     int phase, packs;
-    int64_t D, total;  // elements of a row, of all rows
-    __device__ RowSpan(int64_t M, int64_t d)
+    const int64_t &M, &D;  // the kernel's parameters, which need no registers
+    __device__ RowSpan(const int64_t &m, const int64_t &d)
         : phase(PH ? static_cast<int>((blockIdx.x % VEC) * (d % VEC) % VEC) : 0),
-          packs(static_cast<int>((phase + d + VEC - 1) / VEC)), D(d), total(M * d)
+          packs(static_cast<int>((phase + d + VEC - 1) / VEC)), M(m), D(d)
     {
     }
     __device__ bool ragged(int c) const { return PH && (c == 0 || c == packs - 1); }
@@ -734,13 +805,13 @@ struct RowSpan {
     // their elements are copied one by one, before the slot's barrier is armed.
     __device__ uint32_t bytes(int64_t row) const
     {
-        const int64_t avail = total - first(row);
+        const int64_t avail = M * D - first(row);
         return 16u * static_cast<uint32_t>(PH && static_cast<int64_t>(packs) * VEC > avail ? packs - 1 : packs);
     }
     __device__ void copy_tail(T *slot, const T *rows, int64_t row) const
     {
         if (PH)
-            for (int64_t e = first(row) + bytes(row) / sizeof(T); e < total && e < first(row) + packs * VEC; ++e)
+            for (int64_t e = first(row) + bytes(row) / sizeof(T); e < M * D && e < first(row) + packs * VEC; ++e)
                 slot[e - first(row)] = rows[e];
     }
 };
@@ -842,7 +913,7 @@ __device__ __forceinline__ const W *ring_weights(uint8_t *smem, const RingPlan &
 __host__ __device__ constexpr int ring_threads(bool fp8) { return fp8 ? 896 : 1024; }
 
 template <class T, class W, bool FP8, bool PH>
-__global__ void __launch_bounds__(ring_threads(FP8)) k_rms_norm_ring(const NormParams p, const RingPlan r)
+__global__ void __launch_bounds__(ring_threads(FP8)) k_rms_norm_ring(const __grid_constant__ NormParams p, const RingPlan r)
 {
     constexpr int VEC = 16 / static_cast<int>(sizeof(T));
     extern __shared__ __align__(128) uint8_t smem[];
@@ -862,6 +933,8 @@ __global__ void __launch_bounds__(ring_threads(FP8)) k_rms_norm_ring(const NormP
     };
     if (t == 0)
         ring.init();
+    if (FP8 && threadIdx.x == 0)
+        sy.wide = 0;
     wait_previous_kernel();
     let_next_kernel_start();
     if (t == 0) {
@@ -916,9 +989,11 @@ __global__ void __launch_bounds__(ring_threads(FP8)) k_rms_norm_ring(const NormP
             fill(ring.slot, row + r.slots * step);  // every thread of the group has read the slot
         ring.advance();
         const float rr = rsqrtf(sums.x / static_cast<float>(p.D) + p.eps);
-        const RowScale rs(sums.y, rr);
+        const RowScale rs(sums.y, sums.x, rr);
         if (FP8 && t == 0)
             p.scale[row] = rs.scale;
+        if (FP8 && rs.wide)
+            sy.wide = 1;
 #pragma unroll
         for (int j = 0; j < RING_NV; ++j) {
             const int c = t + j * r.group_threads;
@@ -930,7 +1005,7 @@ __global__ void __launch_bounds__(ring_threads(FP8)) k_rms_norm_ring(const NormP
                         f[2 * i] = hw[FP8 ? j : 0][i].x;
                         f[2 * i + 1] = hw[FP8 ? j : 0][i].y;
                     }
-                    rs.apply(f, rr);
+                    rs.apply(f);
                     span.store_codes(static_cast<uint8_t *>(p.y), row, c, f);
                 } else {
                     float2 f[VEC / 2], wv[VEC / 2];
@@ -950,6 +1025,11 @@ __global__ void __launch_bounds__(ring_threads(FP8)) k_rms_norm_ring(const NormP
         const uint64_t t0 = global_timer_ns();
         while (global_timer_ns() - t0 < RING_SETTLE_NS) {
         }
+    }
+    if constexpr (FP8) {
+        __syncthreads();
+        if (ok && sy.wide)
+            ring_wide_rows<T, W>(p, sy.wide_max, r.group_threads, r.groups);
     }
 }
 

@@ -177,7 +177,7 @@ def add_rms_norm(x, weight, residual=None, eps=1e-6, fp8=False, h=None, y=None, 
     h = x + residual (rounded to x's type; x itself when residual is None),
     f = h / sqrt(mean(h^2) + eps) * weight.  Returns (y, h, scale): y = f in x's
     type with scale None, or with fp8 y = float8_e4m3fn(f / scale) and scale fp32
-    of x's leading shape (one per row: max|f| / 448, 1 for a row of zeros).  No
+    of x's leading shape (one per row: max|f| / 448, 1 where that is 0).  No
     rows at all give empty outputs (and zero weight gradients) here and below.
     x, residual: bf16, fp16 or fp32 [..., D], contiguous or 2-D slices of wider
     rows; weight [D] in x's type or fp32.  h may be passed as residual (or x)
