@@ -5,6 +5,7 @@
 //   h = rn(x + residual)                      the stream, kept in its own type
 //   r = 1 / sqrt(mean_d h^2 + eps),  f = h r weight
 //   y = rn(f),  or  scale = max_d |f| / 448 (1 if that is 0),  y = e4m3(f / scale)
+// (f as (h r) weight: h r is of order one, where r weight may leave fp32's range)
 // Backward, with g = dy weight and the same r (recomputed from the h that the
 // forward pass kept, so nothing but h has to be saved):
 //   dx = r g - h r^3 mean_d(g h) + dh         the gradient of x and of residual
@@ -415,7 +416,7 @@ __global__ void __launch_bounds__(NV <= 2 ? 512 : 1024) k_rms_norm(const __grid_
                 } else {
 #pragma unroll
                     for (int i = 0; i < VEC; ++i)
-                        f[i] *= r * wv[i];
+                        f[i] = f[i] * r * wv[i];
                     Pack<T, VEC> yv;
                     yv.set(f);
                     yv.store(static_cast<T *>(p.y) + o);
@@ -470,7 +471,7 @@ __global__ void __launch_bounds__(1024) k_rms_norm_long(const __grid_constant__ 
                 rs.apply(f);
                 store_e4m3<1>(static_cast<uint8_t *>(p.y) + row * p.D + c, f);
             } else {
-                static_cast<T *>(p.y)[row * p.D + c] = from_f<T>(v * (r * to_f(w[c])));
+                static_cast<T *>(p.y)[row * p.D + c] = from_f<T>(v * r * to_f(w[c]));
             }
         }
     }
@@ -1013,7 +1014,7 @@ __global__ void __launch_bounds__(ring_threads(FP8)) k_rms_norm_ring(const __gri
                     get2<W, VEC>(load_pack<W, VEC>(w + c * VEC), wv);
 #pragma unroll
                     for (int i = 0; i < VEC / 2; ++i)
-                        f[i] = mul2(f[i], mul2(both(rr), wv[i]));
+                        f[i] = mul2(mul2(f[i], both(rr)), wv[i]);
                     Pack<T, VEC> yv;
                     set2<T, VEC>(yv, f);
                     span.store(static_cast<T *>(p.y), row, c, yv);

@@ -102,3 +102,17 @@ def test_zeros_and_nan_among_them(M, D):
     # weights of zero: nothing to scale
     y, _, scale = lf.add_rms_norm(x[fine].to(DEV), torch.zeros(D, device=DEV), fp8=True)
     assert not y.float().any() and bool((scale == 1).all())
+
+
+@pytest.mark.parametrize("M,D", SIZES)
+@pytest.mark.parametrize("hexp,wexp,eps", [(40, -120, 1e-5),    # r weight is 0 in fp32
+                                           (40, -100, 1e-5),    # subnormal
+                                           (-50, 90, 0.0)])     # infinite; h / rms(h) weight is not
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+def test_factors_outside_the_range(M, D, hexp, wexp, eps, dtype):
+    x, w = row(M, D, hexp, 1, dtype), weights(D, wexp, 2)
+    y, _, _ = lf.add_rms_norm(x.to(DEV), w.to(DEV), eps=eps)
+    f = ref.rms_norm(x.double(), w.double(), eps)
+    bad = ~((y.cpu().double() - f).abs() <= (ref.half_step(dtype) + R) * f.abs() + ref.smallest(dtype))
+    assert not bad.any(), (int(bad.sum()), bad.nonzero()[0].tolist())
+    lf.check_device_error()
