@@ -443,7 +443,7 @@ lf_status gated_ffn(const void *x, const void *w, int act, void *out, void *gu_o
 
 /*
  * gated_ffn_e4m3 -- gated_ffn on e4m3 operands with a scale for each token and
- * each output channel (applied to the fp32 accumulators):
+ * each output channel (applied to the fp32 accumulators, x_scale first):
  *   g[m,f] = x_scale[m] w_scale[f]     sum_k x[m,k] w[f,k]
  *   u[m,f] = x_scale[m] w_scale[F + f] sum_k x[m,k] w[F + f,k]
  *

@@ -96,8 +96,9 @@ __device__ __forceinline__ void g_tile_coords(const GemmParams &p, int tile, int
     nb = local / rows;
 }
 
-// 32 columns of one projection as they stand for: f times the token's scale and
-// the output channels' (e4m3 operands), or f itself.
+// 32 columns of one projection as they stand for: f times the token's scale, then
+// the output channels' (e4m3 operands), or f itself.  (f sx is what the token stands
+// for; sx w alone may be a subnormal number that has lost its bits.)
 template <bool E4M3>
 __device__ __forceinline__ void g_scale(float (&f)[32], float sx, const float *w_scale, int valid)
 {
@@ -106,8 +107,8 @@ __device__ __forceinline__ void g_scale(float (&f)[32], float sx, const float *w
         for (int i = 0; i < 32; i += 4) {
             if (i < valid) {  // N % 8 == 0
                 const float4 w = *reinterpret_cast<const float4 *>(w_scale + i);
-                const float2 a = mul2(make_float2(f[i], f[i + 1]), mul2(both(sx), make_float2(w.x, w.y)));
-                const float2 b = mul2(make_float2(f[i + 2], f[i + 3]), mul2(both(sx), make_float2(w.z, w.w)));
+                const float2 a = mul2(mul2(make_float2(f[i], f[i + 1]), both(sx)), make_float2(w.x, w.y));
+                const float2 b = mul2(mul2(make_float2(f[i + 2], f[i + 3]), both(sx)), make_float2(w.z, w.w));
                 f[i] = a.x;
                 f[i + 1] = a.y;
                 f[i + 2] = b.x;
@@ -443,8 +444,8 @@ __device__ __forceinline__ void s_finish(const GatedParams &gp, __nv_bfloat16 *g
 {
     const size_t F = static_cast<size_t>(gp.g.N);
     if (E4M3) {
-        g = make_float4(g.x * (sx * wg.x), g.y * (sx * wg.y), g.z * (sx * wg.z), g.w * (sx * wg.w));
-        u = make_float4(u.x * (sx * wu.x), u.y * (sx * wu.y), u.z * (sx * wu.z), u.w * (sx * wu.w));
+        g = make_float4(g.x * sx * wg.x, g.y * sx * wg.y, g.z * sx * wg.z, g.w * sx * wg.w);
+        u = make_float4(u.x * sx * wu.x, u.y * sx * wu.y, u.z * sx * wu.z, u.w * sx * wu.w);
     }
     const float2 p = act_phi<ACT>(make_float2(g.x, g.y)), q = act_phi<ACT>(make_float2(g.z, g.w));
     *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(gp.g.out) + m * F + f) =
