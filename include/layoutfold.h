@@ -381,7 +381,9 @@ typedef enum {
  *   eps >= 0.  1 <= M, D < 2^31; ldx, ldr >= D (LF_ERR_SHAPE otherwise).
  * Alignment: that of the elements; rows whose bases and pitches are multiples
  * of 16 bytes take the vectorised kernel.  h may be the same buffer as x or
- * residual (row pitch D) and y the same as x; other overlaps are not allowed.
+ * residual, and y in x's type the same as x, where that input's row pitch is D
+ * (LF_ERR_SHAPE for an e4m3 y over x, or another pitch); other overlaps are not
+ * allowed.
  * One launch; nothing is allocated.  A combination of types outside the above
  * is LF_ERR_SHAPE.
  */

@@ -1021,6 +1021,10 @@ static lf_status add_rms_norm_call(const void *x, int64_t ldx, const void *resid
     if (misaligned_for(x, dtype) || misaligned_for(weight, wdtype) || misaligned_for(y, ydtype) ||
         (residual && (misaligned_for(residual, dtype) || misaligned_for(h, dtype))) || (scale && !aligned4(scale)))
         return LF_ERR_ALIGN;
+    // Outputs over inputs go row by row: only where both lie in the same type and pitch.
+    if ((y == x && (ydtype != dtype || (M > 1 && ldx != D))) ||
+        (residual && M > 1 && ((h == x && ldx != D) || (h == residual && ldr != D))))
+        return LF_ERR_SHAPE;
     DeviceState *d = nullptr;
     lf_status st = current_device(&d);
     if (st != LF_OK)
