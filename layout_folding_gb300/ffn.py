@@ -29,10 +29,13 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 _L = None
 try:
-    # contiguous tensors on the current device, without the general argument parser
+    # contiguous tensors on the current device, without the general argument parser -- and
+    # without the dispatcher, so only while no dispatch mode (one that tracks allocations,
+    # say) wants to see them
     from torch._C._dynamo.guards import _empty_strided_cuda as _strided
-except ImportError:  # pragma: no cover
-    _strided = None
+    _dispatch_modes = torch._C._len_torch_dispatch_stack
+except (ImportError, AttributeError):  # pragma: no cover
+    _strided = _dispatch_modes = None
 # the current device as an integer (the calls have a CUDA tensor in hand, so CUDA is initialised)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
@@ -65,7 +68,7 @@ def _new(shape, dtype, ref, stream=None):
     if stream is not None:
         return _new_on(stream, shape, dtype, ref.device)
     n = len(shape)
-    if _strided is None or n > 2:
+    if _strided is None or n > 2 or _dispatch_modes():
         return torch.empty(shape, dtype=dtype, device=ref.device)
     if n == 2:
         return _strided(tuple(shape), (shape[1] or 1, 1), dtype)
