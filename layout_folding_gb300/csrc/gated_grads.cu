@@ -29,12 +29,6 @@ constexpr uint32_t GR_MN_HALF = G_A_BYTES / 2;  // an MN-major operand: two 64 x
 constexpr uint32_t GR_MN_KSTEP = 2 * 1024;      // 16 rows of K in it
 // an MN-major descriptor of the ring's last slot can reach 8 KiB past the ring: barriers and staging follow it
 static_assert(G_EPI_WARPS * G_STG_WARP >= 8192, "room past the ring for MN-major descriptors");
-constexpr int GR_KSUB = 2;                      // K blocks per ring stage
-constexpr int GR_STAGES = G_SLOTS / GR_KSUB;
-constexpr int GR_NUM_BARS = 2 * GR_STAGES + 2 * G_ACC_BUFS + 1;
-constexpr int GR_STG_OFF = ((G_SLOTS * G_SLOT_BYTES + GR_NUM_BARS * 8 + 16 + 1023) / 1024) * 1024;
-constexpr int GR_SMEM = 1024 + GR_STG_OFF + G_EPI_WARPS * G_STG_WARP;
-static_assert(GR_SMEM <= 232448, "shared memory per CTA");
 
 struct GradItem {
     int side, mb, nb, kb0, kb1, part;
@@ -117,7 +111,7 @@ struct RingPos {
     uint32_t phase = 0;
     __device__ __forceinline__ void advance()
     {
-        if (++stage == GR_STAGES) {
+        if (++stage == G_STAGES) {
             stage = 0;
             phase ^= 1u;
         }
@@ -133,15 +127,15 @@ struct RingPos {
 template <bool A_MN>
 __device__ __forceinline__ void produce_item(const GemmParams &p, const GradItem &it, const CUtensorMap *tA,
                                              const CUtensorMap *tB, bool a_3d, bool b_3d, RingPos &pos,
-                                             uint32_t (&armed)[GR_STAGES], bool &alive, bool &skip_next, uint32_t sA, uint32_t sB,
+                                             uint32_t (&armed)[G_STAGES], bool &alive, bool &skip_next, uint32_t sA, uint32_t sB,
                                              uint32_t bar0, uint32_t rank, volatile int *abort_flag, uint32_t peer_abort)
 {
     const int arow = it.mb * G_M + static_cast<int>(rank) * BM;
     const int brow = it.nb * BN + static_cast<int>(rank) * (BN / 2);
-    for (int kb = it.kb0; kb < it.kb1; kb += GR_KSUB) {
-        const int nsub = min(GR_KSUB, it.kb1 - kb);
+    for (int kb = it.kb0; kb < it.kb1; kb += G_KSUB) {
+        const int nsub = min(G_KSUB, it.kb1 - kb);
         if (alive)
-            alive = wait_bar(bar0 + 8u * (GR_STAGES + pos.stage), pos.phase ^ 1u, abort_flag, p, ERR_PRODUCER, peer_abort);
+            alive = wait_bar(bar0 + 8u * (G_STAGES + pos.stage), pos.phase ^ 1u, abort_flag, p, ERR_PRODUCER, peer_abort);
         const uint32_t full = bar0 + 8u * pos.stage;
         const uint32_t full_leader = mapa_shared(full, 0u);
         if (alive && !skip_next) {
@@ -150,10 +144,10 @@ __device__ __forceinline__ void produce_item(const GemmParams &p, const GradItem
                 ++armed[pos.stage];
             }
 #pragma unroll
-            for (int j = 0; j < GR_KSUB; ++j) {
+            for (int j = 0; j < G_KSUB; ++j) {
                 if (j >= nsub)
                     break;
-                const uint32_t slot = static_cast<uint32_t>(pos.stage * GR_KSUB + j);
+                const uint32_t slot = static_cast<uint32_t>(pos.stage * G_KSUB + j);
                 const int k = (kb + j) * BK;
                 if (A_MN)
                     load_mn(sA + slot * G_A_BYTES, tA, a_3d, arow, k, full_leader);
@@ -174,19 +168,19 @@ __device__ __forceinline__ void multiply_item(const GemmParams &p, const GradIte
                                               uint32_t peer_abort)
 {
     constexpr uint32_t idesc = idesc_bf16_f32_major(G_M, BN, A_MN, true);
-    for (int kb = it.kb0; kb < it.kb1; kb += GR_KSUB) {
-        const int nsub = min(GR_KSUB, it.kb1 - kb);
+    for (int kb = it.kb0; kb < it.kb1; kb += G_KSUB) {
+        const int nsub = min(G_KSUB, it.kb1 - kb);
         if (alive)
             alive = __all_sync(0xffffffffu,
                                wait_bar(bar0 + 8u * pos.stage, pos.phase, abort_flag, p, ERR_MMA_FULL, peer_abort));
         if (alive) {
             tc_fence_after();
 #pragma unroll
-            for (int j = 0; j < GR_KSUB; ++j) {
+            for (int j = 0; j < G_KSUB; ++j) {
                 if (j >= nsub)
                     break;
-                const uint32_t a0 = sA + (pos.stage * GR_KSUB + j) * G_A_BYTES;
-                const uint32_t b0 = sB + (pos.stage * GR_KSUB + j) * G_B_BYTES;
+                const uint32_t a0 = sA + (pos.stage * G_KSUB + j) * G_A_BYTES;
+                const uint32_t b0 = sB + (pos.stage * G_KSUB + j) * G_B_BYTES;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const uint64_t da =
@@ -195,7 +189,7 @@ __device__ __forceinline__ void multiply_item(const GemmParams &p, const GradIte
                     umma_f16_pair_one(one, d_tmem, da, db, idesc, (kb != it.kb0 || j != 0 || k != 0) ? 1u : 0u);
                 }
             }
-            umma_commit_pair_mc_one(one, bar0 + 8u * (GR_STAGES + pos.stage), 0x3);
+            umma_commit_pair_mc_one(one, bar0 + 8u * (G_STAGES + pos.stage), 0x3);
         }
         pos.advance();
     }
@@ -212,13 +206,13 @@ __global__ void __launch_bounds__(G_THREADS, 1)
     const uint32_t sA = base;
     const uint32_t sB = base + G_SLOTS * G_A_BYTES;
     const uint32_t bar0 = base + G_SLOTS * G_SLOT_BYTES;
-    const uint32_t drain_bar = bar0 + 8u * (2 * GR_STAGES + 2 * G_ACC_BUFS);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + G_SLOTS * G_SLOT_BYTES + GR_NUM_BARS * 8);
+    const uint32_t drain_bar = bar0 + 8u * (2 * G_STAGES + 2 * G_ACC_BUFS);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + G_SLOTS * G_SLOT_BYTES + G_NUM_BARS * 8);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 #define FULL_BAR(s) (bar0 + 8u * (s))
-#define EMPTY_BAR(s) (bar0 + 8u * (GR_STAGES + (s)))
-#define TFULL_BAR(b) (bar0 + 8u * (2 * GR_STAGES + (b)))
-#define TEMPTY_BAR(b) (bar0 + 8u * (2 * GR_STAGES + G_ACC_BUFS + (b)))
+#define EMPTY_BAR(s) (bar0 + 8u * (G_STAGES + (s)))
+#define TFULL_BAR(b) (bar0 + 8u * (2 * G_STAGES + (b)))
+#define TEMPTY_BAR(b) (bar0 + 8u * (2 * G_STAGES + G_ACC_BUFS + (b)))
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -228,7 +222,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
     const int num_pairs = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < GR_STAGES; ++s) {
+        for (int s = 0; s < G_STAGES; ++s) {
             mbar_init(FULL_BAR(s), 1);   // leader: its arrive.expect_tx + both CTAs' bytes
             mbar_init(EMPTY_BAR(s), 1);  // the leader's multicast commit
         }
@@ -265,9 +259,9 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         // ------------------------------------------------ TMA producer (both CTAs)
         if (lane == 0) {
             RingPos pos;
-            uint32_t armed[GR_STAGES];
+            uint32_t armed[G_STAGES];
 #pragma unroll
-            for (int s = 0; s < GR_STAGES; ++s)
+            for (int s = 0; s < G_STAGES; ++s)
                 armed[s] = 0;
             bool alive = true, skip_next = p.inject == 1 && blockIdx.x == 0;  // test hook
             GradIter iter(gp, pair, num_pairs);
@@ -281,7 +275,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                                        skip_next, sA, sB, bar0, rank, abort_flag, peer_abort);
             }
             if (leader)
-                for (int s = 0; s < GR_STAGES; ++s)
+                for (int s = 0; s < G_STAGES; ++s)
                     if (armed[s])
                         wait_bar_drain(FULL_BAR(s), (armed[s] - 1u) & 1u, abort_flag, p, peer_abort);
         }
@@ -325,8 +319,8 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         const int c0 = ((warp - 2) >> 2) * (BN / 2), c1 = c0 + BN / 2;
         int acc = 0;
         uint32_t acc_phase = 0;
-        uint8_t *stg = gbase + GR_STG_OFF + (warp - 2) * G_STG_WARP;
-        const uint32_t stg_s = base + static_cast<uint32_t>(GR_STG_OFF + (warp - 2) * G_STG_WARP);
+        uint8_t *stg = gbase + G_STG_OFF + (warp - 2) * G_STG_WARP;
+        const uint32_t stg_s = base + static_cast<uint32_t>(G_STG_OFF + (warp - 2) * G_STG_WARP);
         GradIter iter(gp, pair, num_pairs);
         for (GradItem it; iter.next(it);) {
             const GradSide &g = gp.side[it.side];
@@ -512,14 +506,14 @@ cudaError_t launch_gated_grads(const GradMaps &maps, const GradsParams &p, int p
         return e;
     const unsigned long long bit = 1ull << (dev & 63);
     if (!(done.load() & bit)) {
-        e = cudaFuncSetAttribute(k_gated_grads, cudaFuncAttributeMaxDynamicSharedMemorySize, GR_SMEM);
+        e = cudaFuncSetAttribute(k_gated_grads, cudaFuncAttributeMaxDynamicSharedMemorySize, G_SMEM);
         if (e != cudaSuccess)
             return e;
         done.fetch_or(bit);
     }
     const int64_t items = static_cast<int64_t>(p.side[0].items) + p.side[1].items;
     return launch_overlapped(k_gated_grads, dim3(static_cast<unsigned>(2 * (items < pairs ? items : pairs))),
-                             dim3(G_THREADS), GR_SMEM, 2, s, maps, p);
+                             dim3(G_THREADS), G_SMEM, 2, s, maps, p);
 }
 
 cudaError_t launch_add_parts(const GradsParams &p, const float *parts, void *dx, void *dw, int num_sms, cudaStream_t s)
