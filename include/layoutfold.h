@@ -379,8 +379,10 @@ typedef enum {
  *            so y[m,d] scale[m] stands for f.  A row with a NaN (or an
  *            infinity, whose norm is undefined) gets a NaN scale and NaN codes.
  *   eps >= 0.  1 <= M, D < 2^31; ldx, ldr >= D (LF_ERR_SHAPE otherwise).
- * Alignment: that of the elements; rows whose bases and pitches are multiples
- * of 16 bytes take the vectorised kernel.  h may be the same buffer as x or
+ * Alignment: that of the elements.  With bases that are multiples of 16 bytes,
+ * rows whose pitches and length are too, and contiguous rows of any length from
+ * 32 elements, are moved 16 bytes at a time; other rows element by element (five
+ * to seven times slower where rows are many).  h may be the same buffer as x or
  * residual, and y in x's type the same as x, where that input's row pitch is D
  * (LF_ERR_SHAPE for an e4m3 y over x, or another pitch); other overlaps are not
  * allowed.

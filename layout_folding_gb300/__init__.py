@@ -5,6 +5,7 @@ kernels of the library (``include/layoutfold.h`` is the contract).  PyTorch is
 used for device memory and the current stream.  There is no fallback: if the
 library is missing or the device is not sm_103, the calls raise.  Calls run on
 the current device; tensors or a stream of another one are refused (ValueError).
+No call records an autograd graph: its outputs do not require gradients.
 
 Entry points (same names as the C ABI):
   gemm_nt(x, w, out=None)                       -> out = x @ w.T   (bf16)

@@ -1,6 +1,6 @@
 // gated_common.cuh -- what the CTA-pair kernels of the gated projections and of
 // their gradient share: the tile and ring constants, and the store of a finished
-// 32 x 32 chunk.  Roles, barriers and bounded waits are those of gemm_nt_pair.cu.
+// tile by boxes of 32 rows x 128 bytes (64 bf16 or 32 fp32 columns).  Roles, barriers and bounded waits are those of gemm_nt_pair.cu.
 #pragma once
 #include "lf_gemm_common.cuh"
 

@@ -10,9 +10,9 @@
 // has both in the same TMEM lane: activation and product happen in registers
 // and neither projection is written unless the caller keeps it for the
 // backward pass.  Compute bound from a few hundred rows on (4 M F K FLOP):
-// 4096 x 5120 x 13824 takes 582 us in a burst (2.0 PFLOP/s; 597 with the
-// pre-activations kept), 667 us sustained under the power limit, and 302 us in
-// e4m3 (3.85 PFLOP/s).  Stages of two K blocks: 603 us with one.
+// 4096 x 5120 x 13824 takes 583 us in a burst (2.0 PFLOP/s; 599 with the
+// pre-activations kept), 665 us sustained under the power limit, and in e4m3 304 us
+// (3.8 PFLOP/s) and 347.  Stages of two K blocks: 603 us with one.
 //
 // The roles, barriers and bounded waits are those of gemm_nt_pair.cu (whole
 // tiles only: nothing here waits for another pair).
@@ -429,7 +429,7 @@ cudaError_t launch_gated_pair_t(const CUtensorMap &ta, const CUtensorMap &tw, co
 // over a cluster of 2, 4 or 8 CTAs: each leaves its fp32 sums in its own shared
 // memory, and after a cluster barrier every CTA adds, in rank order, its part of
 // the tokens from all of them.  5120 x 13824: one token 45-47 us bf16 (90 % of the
-// copy rate), 48 tokens e4m3 27.6 us; 8192 x 28672 97-99 %: what is left is the
+// copy rate), 48 tokens e4m3 27.0 us; 8192 x 28672 97-99 %: what is left is the
 // launch's 4-5 us.
 constexpr int S_THREADS = 192;     // producer, MMA, 4 epilogue warps
 constexpr int S_WARPS = S_THREADS / 32;
@@ -763,7 +763,7 @@ static int skinny_clusters(int split, int num_sms)
 // with 128 columns, 28.9 with 112, 27.7 with 96, 26.9 with 80, 25.1 with 64), so
 // waves x (128 + cols) orders the choices: 200 x 5120 x 13824 62.8 -> 57.6 us (96
 // columns, two waves as with 128), 333 x 2048 x 5632 24.6 -> 21.6 (80), 1024 x 4096 x
-// 8192 85.0 -> 82.3 (112), 200 x 520 x 1416 8.0 -> 6.3 (64); 4096 x 5120 x 13824
+// 8192 85.0 -> 82.3 (112), 200 x 520 x 1416 silu 8.0 -> 6.3 (64); 4096 x 5120 x 13824
 // stays at 128 (584 us; 619 with 112).
 int plan_gated_cols(int m_blocks, int64_t F, int pairs)
 {
@@ -802,19 +802,24 @@ GatedSkinny plan_gated_skinny(int64_t M, int64_t F, int num_k_blocks, int num_sm
     const int fit = ((two ? S_SMEM_TWO : S_SMEM_ONE) - S_MISC) / stage;
     g.stages = fit < S_MAX_STAGES ? fit : S_MAX_STAGES;
     g.smem = S_MISC + g.stages * stage;
-    // The choice between this kernel and the pair kernel, which has no sums to exchange
-    // (us, pair kernel against this one, K blocks in brackets).  Up to 16 tokens: always
-    // this one (16 x 256 x 4096 e4m3 [2] 5.8 / 3.9).  Up to 128: where the K loop is long
-    // for the tokens (64 x 512 x 1408 [8] 4.9 / 6.7, 64 x 1024 x 1408 [16] 6.3 / 6.2; 128 x
-    // 1024 x 4096 [16] 7.3 / 9.3, 128 x 2048 x 1408 [32] 9.3 / 9.8), or the tiles fill the
-    // device without a split (64 x 512 x 11008 10.0 / 8.4, 96 x 512 x 11008 10.6 / 9.8, but
-    // 128 x 512 x 11008 9.5 / 11.3).
+    // The choice between this kernel and the pair kernel, which has no sums to exchange: one
+    // rule for both types, over K blocks of 128 bytes.  (us, pair kernel / this one, bf16 and
+    // then e4m3, which has twice the K in as many blocks [in brackets].)
+    // Up to 16 tokens: always this one (16 x 256 x 4096 bf16 [4] 5.0 / 4.3, e4m3 [2] 5.7 / 3.7).
+    // Up to 128: where the K loop is long for the tokens
+    //   64 x .. x 1408   [8] 4.9 / 6.7, 6.1 / 6.8    [16] 6.5 / 6.2, 7.5 / 6.4
+    //   128 x .. x 4096  [16] 8.3 / 10.7, 9.2 / 10.8  [32] bf16 12.3 / 13.1
+    //   128 x .. x 1408  [32] 11.5 / 10.9, 12.2 / 10.9
+    // or the tiles fill the device without a split
+    //   .. x 11008 [8]   64 tokens 10.0 / 9.6, 10.8 / 10.0   96 10.2 / 10.8, 11.1 / 11.5   128 9.9 / 12.2, 10.8 / 13.1
+    // so at the border of 96 tokens and at 128 x 2048 x 4096 the other kernel is up to 6 % faster.
     // More tokens, in groups: only where the tiles are few, and the K loops long enough
-    // for the split to pay for its sums, which grow with the tokens of a group (split in
-    // four or eight 144 x 2048 x 512 [32] 9.0 / 7.4, 144 x 1024 x 512 [16] 6.3 / 6.5; 256 x
-    // 4096 x 512 [64] 14.4 / 11.2, 256 x 2048 x 512 [32] 9.1 / 9.6; split in two 144 x 5120 x
-    // 4096 [80] 24.9 / 23.5, 256 x 5120 x 4096 [80] 25.3 / 26.5, 256 x 8192 x 4096 [128]
-    // 38.1 / 36.8; unsplit 333 x 5120 x 4096 29.6 / 40.5).
+    // for the split to pay for its sums, which grow with the tokens of a group
+    //   split in four or eight  144 x .. x 512 [16] 6.2 / 6.5, 7.0 / 6.8  [32] 9.0 / 7.4, 9.7 / 7.6
+    //                           256 x .. x 512 [32] 9.0 / 9.6, 9.7 / 9.6  [64] 18.8 / 11.8, 19.6 / 11.8
+    //   split in two            144 x .. x 4096 [80] 24.8 / 23.5, 26.1 / 23.9
+    //                           256 x .. x 4096 [80] 25.0 / 26.5, 26.3 / 26.9  [128] 38.0 / 37.0, 39.6 / 37.3
+    //   unsplit                 333 x .. x 4096 [80] 29.6 / 39.7, 31.0 / 40.9
     if (groups == 1)
         g.preferred = g.n <= 16 || 4 * num_k_blocks >= g.n || (g.n <= 96 && tiles > num_sms / 2);
     else

@@ -13,9 +13,10 @@
 //
 // Both passes are bound by memory: every element of the row is read once and
 // held in registers between the reduction and the output (rows too long for
-// that take the *_long kernels, which read the row again from L2).  One row takes
-// 2.5 us; 8192 x 4096 bf16 45.4 us (5.9 TB/s, 87 % of the copy rate), 8192 x 5120
-// into e4m3 50.3 us, the gradient of 8192 x 4096 48.7 us with dweight.
+// that take the *_long kernels, which read the row again from L2).  In replays of a
+// captured call one row takes 2.3 us; 8192 x 4096 bf16 44.5 us (6.0 TB/s, 89 % of the
+// copy rate), 8192 x 5120 into e4m3 49.6 us, the gradient of 8192 x 4096 47.4 us with
+// dweight.
 #include <atomic>
 
 #include <cuda_bf16.h>
@@ -661,11 +662,12 @@ __global__ void __launch_bounds__(32 * DW_ROWS)
 constexpr int RING_NV = 4;            // packs per thread: a group has ceil(packs / 128) warps
 constexpr int RING_MAX_GROUPS = 15;   // named barriers 1..15
 constexpr int RING_MAX_SLOTS = 8;
-// Fewer rows than four per SM: one block per row.  At the border both take the
-// same (600 x 5120 3.7 us, 608 in rings 3.8 us); 8192 x 5120 into e4m3 takes 68 us by
-// blocks and 50 us in rings.  Phased rows, which blocks move element by element,
-// always where they are long, and from 100 rows on (32 x 5121 4.4 us by blocks, 4.0 in
-// rings; 300 x 5121 8.9 / 4.8).
+// Fewer rows than four per SM: one block per row.  Around the border both take about
+// the same (us by blocks / in rings: 608 x 5120 bf16 4.7 / 5.0, into e4m3 5.1 / 5.0, 608 x
+// 1024 into e4m3 2.4 / 2.8, 1000 x 5120 bf16 7.4 / 7.4); 8192 x 5120 into e4m3 takes 54.4 /
+// 49.7.  Phased rows, which blocks move element by element, always where they are long,
+// and from 100 rows on (32 x 5121 4.5 / 3.5, 300 x 5121 13.4 / 5.2; a ring's setup shows with
+// short rows, 100 x 517 1.9 / 3.7).
 constexpr int64_t RING_MIN_ROWS = 608, RING_MIN_ROWS_PHASED = 100, RING_LONG_D = 1024;
 constexpr int RING_BUDGET = 225 * 1024;  // dynamic shared memory; RingSync takes 2 KB more
 constexpr uint64_t RING_SETTLE_NS = 100000;  // after an abort: let copies in flight land

@@ -1,5 +1,6 @@
 """The feed-forward operators of the binding: add_rms_norm, gated_ffn and their
-gradients (include/layoutfold.h is the contract, as for the rest).
+gradients (include/layoutfold.h is the contract, as for the rest).  Gradients are
+calls of their own: no autograd graph is recorded through any operator here.
 
 One token's norm runs for about 3 us on the GPU, so the host's share is kept
 small: checks are attribute reads, the stream is read as a raw handle, and
