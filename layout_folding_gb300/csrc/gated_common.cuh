@@ -3,6 +3,7 @@
 // tile by boxes of 32 rows x 128 bytes (64 bf16 or 32 fp32 columns).  Roles, barriers and bounded waits are those of gemm_nt_pair.cu.
 #pragma once
 #include "lf_gemm_common.cuh"
+#include "lf_ptx_ffn.cuh"
 
 namespace lf {
 namespace {

@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer (leader only)
-        // (the whole warp, converged, with one thread issuing: see lf_ptx.cuh; after a
+        // (the whole warp, converged, with one thread issuing: see lf_ptx_ffn.cuh; after a
         // wait that gave up the loops run on without doing anything)
         if (leader) {
             const uint32_t one = elect_one();

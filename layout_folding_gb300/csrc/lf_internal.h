@@ -63,7 +63,7 @@ cudaError_t launch_fp8_cast_dual(const void *x, const float *scale, void *out, v
                                  int num_sms, cudaStream_t s);
 // Launch with programmatic stream serialisation (and clusters of `cluster` CTAs):
 // the kernel may be set up while its predecessor in the stream ends, so it has to
-// call wait_previous_kernel (lf_ptx.cuh) before it touches global memory.
+// call wait_previous_kernel (lf_ptx_ffn.cuh) before it touches global memory.
 template <class... P, class... A>
 cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, int cluster, cudaStream_t s,
                               A &&...args)

@@ -26,7 +26,7 @@
 #include <type_traits>
 
 #include "lf_internal.h"
-#include "lf_ptx.cuh"
+#include "lf_ptx_ffn.cuh"
 
 namespace lf {
 namespace {
