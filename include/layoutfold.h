@@ -349,7 +349,8 @@ typedef enum {
 typedef enum {
     LF_ACT_SILU = 0,      /* v / (1 + exp(-v)) */
     LF_ACT_GELU = 1,      /* v Phi(v), Phi the standard normal distribution function */
-    LF_ACT_GELU_TANH = 2  /* v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) / 2 */
+    LF_ACT_GELU_TANH = 2, /* v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) / 2 */
+    LF_ACT_NONE = 3       /* v; taken by linear, linear_e4m3 and linear_backward only */
 } lf_act;
 
 /*
@@ -484,6 +485,74 @@ lf_status gated_ffn_backward(const void *dout, const void *x, const void *w, con
 
 /* Bytes of scratch that gated_ffn_backward may need (0: none, or sizes out of range). */
 int64_t gated_ffn_backward_scratch(int64_t M, int64_t F, int64_t K);
+
+/*
+ * linear -- a projection with bias, activation and residual in its epilogue:
+ *   z = X . W^T + bias,   out = act(z) + residual
+ * ("Allow reductions in matmul epilogues", NVIDIA/Fuser issue 2213: work on the
+ * matmul's result inside its epilogue; "Strength reduction: fold transpose into a
+ * subsequent GEMM call", lightning-thunder issue 1252: the weight is read as it is
+ * stored).
+ *
+ *   x    : bf16 [M,K], device, row-major.
+ *   w    : bf16 [N,K], device, row-major.
+ *   bias_or_null : [N] of bias_dtype (LF_BF16 or LF_FP32; not read without a bias).
+ *   act  : an lf_act value, LF_ACT_NONE among them.
+ *   residual_or_null : bf16 [M,N].
+ *   out  : bf16 [M,N]; out = bf16_rn(act(z) + residual), z the fp32 accumulator plus
+ *          the bias, nothing rounded in between.  May be the residual's buffer (a
+ *          stream updated in place).
+ *   pre_or_null : NULL, or bf16 [M,N]: bf16_rn(z), which linear_backward takes.
+ *   K % 8 == 0, N % 8 == 0 (16-byte row pitches), 1 <= M, N, K < 2^31; all pointers
+ *   16-byte aligned; outputs otherwise overlap nothing (a pre that is out's or the
+ *   residual's buffer is LF_ERR_SHAPE).  One launch; nothing is allocated.
+ */
+lf_status linear(const void *x, const void *w, const void *bias_or_null, int bias_dtype, int act,
+                 const void *residual_or_null, void *out, void *pre_or_null, int64_t M, int64_t N, int64_t K,
+                 cudaStream_t stream);
+
+/*
+ * linear_e4m3 -- linear on e4m3 operands with a scale for each token and each output
+ * channel (applied to the fp32 accumulators, x_scale first):
+ *   z[m,n] = x_scale[m] w_scale[n] sum_k x[m,k] w[n,k] + bias[n]
+ *
+ *   x : e4m3 [M,K] and x_scale : fp32 [M], as add_rms_norm and block_norm write them.
+ *   w : e4m3 [N,K] and w_scale : fp32 [N].
+ *   bias, act, residual, out as linear.  K % 16 == 0 and N % 8 == 0; x_scale 4-byte
+ *   aligned, all other pointers 16-byte aligned.  One launch.
+ */
+lf_status linear_e4m3(const void *x, const float *x_scale, const void *w, const float *w_scale, const void *bias_or_null,
+                      int bias_dtype, int act, const void *residual_or_null, void *out, int64_t M, int64_t N, int64_t K,
+                      cudaStream_t stream);
+
+/*
+ * linear_backward -- the gradient of linear, given dout and (with an activation) the
+ * kept z (the residual's gradient is dout itself):
+ *   dz = dout act'(pre),  dx = dz . W,  dw = dz^T . X,  dbias = sum_m dz
+ * No operand of either product is transposed in memory.
+ *
+ *   dout : bf16 [M,N]; x : bf16 [M,K]; w : bf16 [N,K].
+ *   pre_or_null : bf16 [M,N], linear's; not read with LF_ACT_NONE.
+ *   dz_or_null  : bf16 [M,N], written (the products read it, so it is rounded to bf16
+ *          once); may be the same buffer as pre or dout.  Not used with LF_ACT_NONE, where
+ *          dz is dout.
+ *   dx_or_null : bf16 [M,K] or NULL;  dw_or_null : bf16 [N,K] or NULL.
+ *   dbias_or_null : [N] of bias_dtype (LF_BF16 or LF_FP32), the sum of the unrounded
+ *          dz in fp32, or NULL.
+ *   scratch : linear_backward_scratch(M, N, K) bytes, 16-byte aligned, device, owned by
+ *          the caller, contents arbitrary; NULL is allowed when that is 0.
+ * Sizes and alignment as linear; outputs otherwise overlap nothing.  One launch for dz
+ * and dbias's sums, one that adds those up where many rows are shared out over blocks,
+ * one for both products and one for their parts where a sum was split (see
+ * gated_ffn_backward).  Two calls on the same inputs give the same bits, and one
+ * output is the same with and without the others.
+ */
+lf_status linear_backward(const void *dout, const void *x, const void *w, const void *pre_or_null, int act,
+                          void *dz_or_null, void *dx_or_null, void *dw_or_null, void *dbias_or_null, int bias_dtype,
+                          void *scratch, int64_t M, int64_t N, int64_t K, cudaStream_t stream);
+
+/* Bytes of scratch that linear_backward may need (0: none, or sizes out of range). */
+int64_t linear_backward_scratch(int64_t M, int64_t N, int64_t K);
 
 /* Human-readable name of a status code (static storage, never NULL). */
 const char *lf_status_string(lf_status status);

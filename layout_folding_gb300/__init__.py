@@ -20,6 +20,8 @@ Entry points (same names as the C ABI):
   add_rms_norm_backward(dy, h, weight, dh)      -> (dx, dweight)
   gated_ffn(x, w, act, x_scale, w_scale)        -> (act(x Wg^T) * (x Wu^T), [g, u] on request); bf16 or e4m3 operands
   gated_ffn_backward(dout, x, w, gu, act)       -> (dx, dw)
+  linear(x, w, bias, act, residual, ...)        -> (act(x w^T + bias) + residual, x w^T + bias on request); bf16 or e4m3
+  linear_backward(dout, x, w, pre, act, bias)   -> (dx, dw, dbias)
 """
 from __future__ import annotations
 
@@ -119,6 +121,14 @@ def lib():
         L.gated_ffn_backward_scratch.argtypes = [I64, I64, I64]
         L.gated_ffn_backward_scratch.restype = I64
         L.gated_ffn_backward.restype = I32
+        L.linear.argtypes = [P, P, P, I32, I32, P, P, P, I64, I64, I64, P]
+        L.linear.restype = I32
+        L.linear_e4m3.argtypes = [P, P, P, P, P, I32, I32, P, P, I64, I64, I64, P]
+        L.linear_e4m3.restype = I32
+        L.linear_backward.argtypes = [P, P, P, P, I32, P, P, P, P, I32, P, I64, I64, I64, P]
+        L.linear_backward.restype = I32
+        L.linear_backward_scratch.argtypes = [I64, I64, I64]
+        L.linear_backward_scratch.restype = I64
         _lib = L
         return L
 
@@ -500,3 +510,4 @@ def occupy_sms(ctas: int, duration_ns: int, stream=None):
 
 from .ffn import (ACTIVATIONS, LF_BF16, LF_E4M3, LF_FP16, LF_FP32, add_rms_norm,  # noqa: E402,F401
                   add_rms_norm_backward, gated_ffn, gated_ffn_backward)
+from .projections import linear, linear_backward  # noqa: E402,F401

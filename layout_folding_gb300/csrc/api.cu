@@ -1064,6 +1064,19 @@ static lf_status check_gated_shape(int64_t M, int64_t F, int64_t K, int act)
     return check_gemm_shape(M, 2 * F, K);
 }
 
+// Bands of M blocks (of 256 rows) whose X rows stay in L2, and at least eight (see
+// plan_gated_grads); 0: one band.
+static int band_of(int m_blocks, int64_t K, bool e4m3)
+{
+    const double x_bytes = 2.0 * lf::BM * static_cast<double>(K) * (e4m3 ? 1.0 : 2.0);
+    const int fit = static_cast<int>(BAND_X_BYTES / x_bytes);
+    const int band = fit < 8 ? 8 : fit;
+    if (band >= m_blocks)
+        return 0;
+    const int nbands = (m_blocks + band - 1) / band;
+    return (m_blocks + nbands - 1) / nbands;
+}
+
 // gated_ffn and gated_ffn_e4m3 (x_scale and w_scale set), arguments checked.
 static lf_status gated_launch(const void *x, const float *x_scale, const void *w, const float *w_scale, int act,
                               void *out, void *gu, int64_t M, int64_t F, int64_t K, cudaStream_t stream)
@@ -1116,15 +1129,7 @@ static lf_status gated_launch(const void *x, const float *x_scale, const void *w
             !make_tmap_out64(&tu, static_cast<char *>(gu) + 2 * F, M, F, 2 * F))
             return LF_ERR_LAUNCH;
     }
-    // bands of M blocks whose X rows stay in L2, and at least eight (see
-    // plan_gated_grads)
-    const double x_bytes = 2.0 * lf::BM * static_cast<double>(K) * (e4m3 ? 1.0 : 2.0);
-    const int fit = static_cast<int>(BAND_X_BYTES / x_bytes);
-    const int band = fit < 8 ? 8 : fit;
-    if (band < p.num_m_blocks) {
-        const int nbands = (p.num_m_blocks + band - 1) / band;
-        p.band_m = (p.num_m_blocks + nbands - 1) / nbands;
-    }
+    p.band_m = band_of(p.num_m_blocks, K, e4m3);
     const int grid = 2 * (p.num_tiles < d->pair_clusters ? p.num_tiles : d->pair_clusters);
     return launched(lf::launch_gated_pair(e4m3, act, ta, tw, to, tg, tu, gp, grid, stream), 1);
 }
@@ -1172,6 +1177,42 @@ static bool make_tmap_parts(CUtensorMap *m, float *ptr, int64_t M, int64_t N, in
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The tensor maps of the gradient's products: grad [M, N], x [M, K], w [N, K].
+static bool grad_maps(lf::GradMaps *maps, lf::GradsParams *p, const void *grad, const void *x, const void *w, void *dx,
+                      void *dw, float *parts, int64_t M, int64_t N, int64_t K)
+{
+    std::memset(maps, 0, sizeof *maps);
+    const auto mn_map = [](CUtensorMap *m, int *three_d, const void *ptr, int64_t rows, int64_t k) {
+        *three_d = make_tmap_mn3(m, ptr, rows, k) ? 1 : 0;
+        return *three_d || make_tmap_mn(m, ptr, rows, k);
+    };
+    const auto out_map = [&](int s, void *out) {
+        const lf::GradSide &g = p->side[s];
+        return g.split > 1 ? make_tmap_parts(&maps->o[s], parts + g.parts, g.M, g.N, g.split)
+                           : make_tmap_out64(&maps->o[s], out, g.M, g.N, g.N);
+    };
+    if (dx && (!make_tmap(&maps->a[0], grad, M, N, lf::BM) || !mn_map(&maps->b[0], &p->side[0].b_3d, w, K, N) ||
+               !out_map(0, dx)))
+        return false;
+    return !dw || (mn_map(&maps->a[1], &p->side[1].a_3d, grad, N, M) && mn_map(&maps->b[1], &p->side[1].b_3d, x, K, M) &&
+                   out_map(1, dw));
+}
+
+// Its launches: both products, and the sum of their parts where there are any.
+static lf_status grad_products(DeviceState *d, const lf::GradMaps &maps, lf::GradsParams *p, const float *parts, void *dx,
+                               void *dw, cudaStream_t stream)
+{
+    if (!dx && !dw)
+        return LF_OK;
+    p->wait.err = d->err_word;
+    p->wait.timeout_ns = g_timeout_ns.load();
+    p->wait.inject = g_inject.load();
+    const lf_status st = launched(lf::launch_gated_grads(maps, *p, d->pair_clusters, stream), 1);
+    if (st != LF_OK || (!(dx && p->side[0].split > 1) && !(dw && p->side[1].split > 1)))
+        return st;
+    return launched(lf::launch_add_parts(*p, parts, dx, dw, d->num_sms, stream), 1);
+}
+
 static lf_status gated_ffn_backward_call(const void *dout, const void *x, const void *w, const void *gu, int act,
                                          void *dgu, void *dx, void *dw, void *scratch, int64_t M, int64_t F, int64_t K,
                                          cudaStream_t stream)
@@ -1190,7 +1231,7 @@ static lf_status gated_ffn_backward_call(const void *dout, const void *x, const 
         return LF_ERR_ALIGN;
     lf::GradsParams p;
     std::memset(&p, 0, sizeof p);
-    lf::plan_gated_grads(&p, dx != nullptr, dw != nullptr, M, F, K, lf::GRAD_PLAN_PAIRS);
+    lf::plan_gated_grads(&p, dx != nullptr, dw != nullptr, M, 2 * F, K, lf::GRAD_PLAN_PAIRS);
     if (p.part_floats > 0 && !scratch)
         return LF_ERR_NULL;
     DeviceState *d = nullptr;
@@ -1199,35 +1240,148 @@ static lf_status gated_ffn_backward_call(const void *dout, const void *x, const 
     if (d->pair_clusters <= 0)
         return LF_ERR_LAUNCH;
     float *parts = static_cast<float *>(scratch);
-    p.wait.err = d->err_word;
-    p.wait.timeout_ns = g_timeout_ns.load();
-    p.wait.inject = g_inject.load();
     lf::GradMaps maps;
-    std::memset(&maps, 0, sizeof maps);
-    const auto mn_map = [](CUtensorMap *m, int *three_d, const void *ptr, int64_t rows, int64_t k) {
-        *three_d = make_tmap_mn3(m, ptr, rows, k) ? 1 : 0;
-        return *three_d || make_tmap_mn(m, ptr, rows, k);
-    };
-    const auto out_map = [&](int s, void *out) {
-        const lf::GradSide &g = p.side[s];
-        return g.split > 1 ? make_tmap_parts(&maps.o[s], parts + g.parts, g.M, g.N, g.split)
-                           : make_tmap_out64(&maps.o[s], out, g.M, g.N, g.N);
-    };
-    if (dx && (!make_tmap(&maps.a[0], dgu, M, 2 * F, lf::BM) || !mn_map(&maps.b[0], &p.side[0].b_3d, w, K, 2 * F) ||
-               !out_map(0, dx)))
-        return LF_ERR_LAUNCH;
-    if (dw && (!mn_map(&maps.a[1], &p.side[1].a_3d, dgu, 2 * F, M) || !mn_map(&maps.b[1], &p.side[1].b_3d, x, K, M) ||
-               !out_map(1, dw)))
+    if (!grad_maps(&maps, &p, dgu, x, w, dx, dw, parts, M, 2 * F, K))
         return LF_ERR_LAUNCH;
     if ((st = launched(lf::launch_gated_bwd(act, dout, gu, dgu, M, F, stream), 1)) != LF_OK)
         return st;
-    if (!dx && !dw)
-        return LF_OK;
-    if ((st = launched(lf::launch_gated_grads(maps, p, d->pair_clusters, stream), 1)) != LF_OK)
+    return grad_products(d, maps, &p, parts, dx, dw, stream);
+}
+
+static lf_status check_linear(const void *bias, int bias_dtype, int act, int64_t M, int64_t N, int64_t K)
+{
+    if ((act != LF_ACT_NONE && !act_ok(act)) || (bias && bias_dtype != LF_BF16 && bias_dtype != LF_FP32))
+        return LF_ERR_SHAPE;
+    return check_gemm_shape(M, N, K);
+}
+
+// linear and linear_e4m3 (x_scale and w_scale set), arguments checked.
+static lf_status linear_launch(const void *x, const float *x_scale, const void *w, const float *w_scale, const void *bias,
+                               int bias_dtype, int act, const void *residual, void *out, void *pre, int64_t M, int64_t N,
+                               int64_t K, cudaStream_t stream)
+{
+    DeviceState *d = nullptr;
+    lf_status st = current_device(&d);
+    if (st != LF_OK)
         return st;
-    if (!(dx && p.side[0].split > 1) && !(dw && p.side[1].split > 1))
-        return LF_OK;
-    return launched(lf::launch_add_parts(p, parts, dx, dw, d->num_sms, stream), 1);
+    if (d->pair_clusters <= 0)
+        return LF_ERR_LAUNCH;
+    const bool e4m3 = x_scale != nullptr;
+    lf::LinearParams lp;
+    std::memset(&lp, 0, sizeof lp);
+    lf::GemmParams &p = lp.g;
+    const int64_t kblock = e4m3 ? 128 : 64;
+    p.M = static_cast<int>(M);
+    p.N = static_cast<int>(N);
+    p.K = static_cast<int>(K);
+    p.out = out;
+    p.num_k_blocks = static_cast<int>((K + kblock - 1) / kblock);
+    p.err = d->err_word;
+    p.timeout_ns = g_timeout_ns.load();
+    p.inject = g_inject.load();
+    lp.x_scale = x_scale;
+    lp.w_scale = w_scale;
+    lp.bias = bias;
+    lp.bias_f32 = bias_dtype == LF_FP32 ? 1 : 0;
+    lp.residual = residual ? 1 : 0;
+    lp.save = pre ? 1 : 0;
+    lf::LinearMaps m;
+    const auto operands = [&](uint32_t x_rows, uint32_t w_rows) {
+        return e4m3 ? make_tmap_e4m3(&m.x, x, M, K, x_rows) && make_tmap_e4m3(&m.w, w, N, K, w_rows)
+                    : make_tmap(&m.x, x, M, K, x_rows) && make_tmap(&m.w, w, N, K, w_rows);
+    };
+    p.num_m_blocks = static_cast<int>((M + 2 * lf::BM - 1) / (2 * lf::BM));
+    lp.cols = lf::plan_linear_cols(p.num_m_blocks, N, d->pair_clusters);
+    p.num_n_blocks = static_cast<int>((N + lp.cols - 1) / lp.cols);
+    p.num_tiles = p.num_m_blocks * p.num_n_blocks;
+    if (!operands(lf::BM, static_cast<uint32_t>(lp.cols / 2)) || !make_tmap_out64(&m.out, out, M, N, N))
+        return LF_ERR_LAUNCH;
+    m.pre = m.residual = m.out;
+    if ((pre && !make_tmap_out64(&m.pre, pre, M, N, N)) ||
+        (residual && !make_tmap_out64(&m.residual, const_cast<void *>(residual), M, N, N)))
+        return LF_ERR_LAUNCH;
+    p.band_m = band_of(p.num_m_blocks, K, e4m3);
+    const int grid = 2 * (p.num_tiles < d->pair_clusters ? p.num_tiles : d->pair_clusters);
+    return launched(lf::launch_linear_pair(e4m3, act, m, lp, grid, stream), 1);
+}
+
+static lf_status linear_call(const void *x, const void *w, const void *bias, int bias_dtype, int act, const void *residual,
+                             void *out, void *pre, int64_t M, int64_t N, int64_t K, cudaStream_t stream)
+{
+    if (!x || !w || !out)
+        return LF_ERR_NULL;
+    const lf_status st = check_linear(bias, bias_dtype, act, M, N, K);
+    if (st != LF_OK)
+        return st;
+    if (!aligned16(x) || !aligned16(w) || !aligned16(out) || !aligned16(bias) || !aligned16(residual) ||
+        !aligned16(pre) || N % 8 != 0 || K % 8 != 0)
+        return LF_ERR_ALIGN;
+    if (pre && (pre == out || pre == residual))
+        return LF_ERR_SHAPE;
+    return linear_launch(x, nullptr, w, nullptr, bias, bias_dtype, act, residual, out, pre, M, N, K, stream);
+}
+
+static lf_status linear_e4m3_call(const void *x, const float *x_scale, const void *w, const float *w_scale,
+                                  const void *bias, int bias_dtype, int act, const void *residual, void *out, int64_t M,
+                                  int64_t N, int64_t K, cudaStream_t stream)
+{
+    if (!x || !x_scale || !w || !w_scale || !out)
+        return LF_ERR_NULL;
+    const lf_status st = check_linear(bias, bias_dtype, act, M, N, K);
+    if (st != LF_OK)
+        return st;
+    if (!aligned16(x) || !aligned16(w) || !aligned16(out) || !aligned16(w_scale) || !aligned4(x_scale) ||
+        !aligned16(bias) || !aligned16(residual) || N % 8 != 0 || K % 16 != 0)
+        return LF_ERR_ALIGN;
+    return linear_launch(x, x_scale, w, w_scale, bias, bias_dtype, act, residual, out, nullptr, M, N, K, stream);
+}
+
+// Floats of linear_backward's scratch: the products' parts, then the bias's partial sums.
+static int64_t linear_bias_floats(int64_t M, int64_t N)
+{
+    const int64_t blocks = lf::linear_dz_blocks(M, N);
+    return blocks > 1 ? blocks * N : 0;
+}
+
+static lf_status linear_backward_call(const void *dout, const void *x, const void *w, const void *pre, int act, void *dz,
+                                      void *dx, void *dw, void *dbias, int bias_dtype, void *scratch, int64_t M, int64_t N,
+                                      int64_t K, cudaStream_t stream)
+{
+    if (!dout || !x || !w || (act != LF_ACT_NONE && (!pre || !dz)))
+        return LF_ERR_NULL;
+    lf_status st = check_linear(dbias, bias_dtype, act, M, N, K);
+    if (st == LF_OK)
+        st = check_gemm_shape(N, K, M);
+    if (st == LF_OK)
+        st = check_gemm_shape(M, K, N);
+    if (st != LF_OK)
+        return st;
+    if (!aligned16(dout) || !aligned16(x) || !aligned16(w) || !aligned16(pre) || !aligned16(dz) || !aligned16(dx) ||
+        !aligned16(dw) || !aligned16(dbias) || !aligned16(scratch) || N % 8 != 0 || K % 8 != 0)
+        return LF_ERR_ALIGN;
+    lf::GradsParams p;
+    std::memset(&p, 0, sizeof p);
+    lf::plan_gated_grads(&p, dx != nullptr, dw != nullptr, M, N, K, lf::GRAD_PLAN_PAIRS);
+    const bool summed = dbias && linear_bias_floats(M, N) > 0;  // by a second kernel
+    if ((p.part_floats > 0 || summed) && !scratch)
+        return LF_ERR_NULL;
+    DeviceState *d = nullptr;
+    if ((st = current_device(&d)) != LF_OK)
+        return st;
+    if (d->pair_clusters <= 0)
+        return LF_ERR_LAUNCH;
+    const void *grad = act == LF_ACT_NONE ? dout : dz;
+    float *parts = static_cast<float *>(scratch), *sums = parts + p.part_floats;
+    lf::GradMaps maps;
+    if (!grad_maps(&maps, &p, grad, x, w, dx, dw, parts, M, N, K))
+        return LF_ERR_LAUNCH;
+    const bool f32 = bias_dtype == LF_FP32;
+    if ((act != LF_ACT_NONE || dbias) &&
+        (st = launched(lf::launch_linear_dz(act, dout, pre, dz, sums, dbias, f32, M, N, stream), 1)) != LF_OK)
+        return st;
+    if (summed && (st = launched(lf::launch_linear_dbias(sums, dbias, f32, M, N, stream), 1)) != LF_OK)
+        return st;
+    return grad_products(d, maps, &p, parts, dx, dw, stream);
 }
 
 const char *lf_status_string(lf_status s)
@@ -1451,7 +1605,7 @@ int64_t gated_ffn_backward_scratch(int64_t M, int64_t F, int64_t K)
         return 0;
     lf::GradsParams p;
     std::memset(&p, 0, sizeof p);
-    lf::plan_gated_grads(&p, true, true, M, F, K, lf::GRAD_PLAN_PAIRS);
+    lf::plan_gated_grads(&p, true, true, M, 2 * F, K, lf::GRAD_PLAN_PAIRS);
     return p.part_floats * static_cast<int64_t>(sizeof(float));
 }
 
@@ -1462,6 +1616,45 @@ lf_status gated_ffn_backward(const void *dout, const void *x, const void *w, con
     const lf::CallRange range("gated_ffn_backward");
     return debug_sync(gated_ffn_backward_call(dout, x, w, gu, act, dgu, dx_or_null, dw_or_null, scratch, M, F, K,
                                               stream),
+                      stream);
+}
+
+lf_status linear(const void *x, const void *w, const void *bias_or_null, int bias_dtype, int act,
+                 const void *residual_or_null, void *out, void *pre_or_null, int64_t M, int64_t N, int64_t K,
+                 cudaStream_t stream)
+{
+    const lf::CallRange range("linear");
+    return debug_sync(linear_call(x, w, bias_or_null, bias_dtype, act, residual_or_null, out, pre_or_null, M, N, K, stream),
+                      stream);
+}
+
+lf_status linear_e4m3(const void *x, const float *x_scale, const void *w, const float *w_scale, const void *bias_or_null,
+                      int bias_dtype, int act, const void *residual_or_null, void *out, int64_t M, int64_t N, int64_t K,
+                      cudaStream_t stream)
+{
+    const lf::CallRange range("linear_e4m3");
+    return debug_sync(linear_e4m3_call(x, x_scale, w, w_scale, bias_or_null, bias_dtype, act, residual_or_null, out, M, N,
+                                       K, stream),
+                      stream);
+}
+
+int64_t linear_backward_scratch(int64_t M, int64_t N, int64_t K)
+{
+    if (check_gemm_shape(M, N, K) != LF_OK || check_gemm_shape(N, K, M) != LF_OK || check_gemm_shape(M, K, N) != LF_OK)
+        return 0;
+    lf::GradsParams p;
+    std::memset(&p, 0, sizeof p);
+    lf::plan_gated_grads(&p, true, true, M, N, K, lf::GRAD_PLAN_PAIRS);
+    return (p.part_floats + linear_bias_floats(M, N)) * static_cast<int64_t>(sizeof(float));
+}
+
+lf_status linear_backward(const void *dout, const void *x, const void *w, const void *pre_or_null, int act,
+                          void *dz_or_null, void *dx_or_null, void *dw_or_null, void *dbias_or_null, int bias_dtype,
+                          void *scratch, int64_t M, int64_t N, int64_t K, cudaStream_t stream)
+{
+    const lf::CallRange range("linear_backward");
+    return debug_sync(linear_backward_call(dout, x, w, pre_or_null, act, dz_or_null, dx_or_null, dw_or_null,
+                                           dbias_or_null, bias_dtype, scratch, M, N, K, stream),
                       stream);
 }
 

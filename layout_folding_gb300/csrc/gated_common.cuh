@@ -84,5 +84,40 @@ __device__ __forceinline__ void load_acc2(uint32_t t0, uint32_t t1, float (&f)[3
     }
 }
 
+// Tile order: bands of band_m M blocks (M block fastest), as gemm_nt_pair.cu.
+__device__ __forceinline__ void g_tile_coords(const GemmParams &p, int tile, int &mb, int &nb)
+{
+    const int MB = p.num_m_blocks;
+    const int bm = p.band_m > 0 && p.band_m < MB ? p.band_m : MB;
+    const int per_band = bm * p.num_n_blocks;
+    const int band = tile / per_band;
+    const int local = tile - band * per_band;
+    const int rows = min(bm, MB - band * bm);
+    mb = band * bm + local % rows;
+    nb = local / rows;
+}
+
+// 32 columns of one projection as they stand for: f times the token's scale, then
+// the output channels' (e4m3 operands), or f itself.  (f sx is what the token stands
+// for; sx w alone may be a subnormal number that has lost its bits.)
+template <bool E4M3>
+__device__ __forceinline__ void g_scale(float (&f)[32], float sx, const float *w_scale, int valid)
+{
+    if (E4M3) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+            if (i < valid) {  // N % 8 == 0
+                const float4 w = *reinterpret_cast<const float4 *>(w_scale + i);
+                const float2 a = mul2(mul2(make_float2(f[i], f[i + 1]), both(sx)), make_float2(w.x, w.y));
+                const float2 b = mul2(mul2(make_float2(f[i + 2], f[i + 3]), both(sx)), make_float2(w.z, w.w));
+                f[i] = a.x;
+                f[i + 1] = a.y;
+                f[i + 2] = b.x;
+                f[i + 3] = b.y;
+            }
+        }
+    }
+}
+
 }  // namespace
 }  // namespace lf

@@ -18,107 +18,11 @@
 // tiles only: nothing here waits for another pair).
 #include <atomic>
 
+#include "activations.cuh"
 #include "gated_common.cuh"
 
 namespace lf {
 namespace {
-
-constexpr int ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2;
-constexpr float GELU_C2 = 1.5957691216057308f;  // 2 sqrt(2 / pi): gelu_tanh(v) = v sigmoid(GELU_C2 (v + a v^3))
-constexpr float GELU_A = 0.044715f;
-
-// 1 / (1 + exp(-v)) in fp32: off by about 2^-21, and for negative v by |v| 2^-24 more,
-// what the rounding of its exponent makes of exp(-v).  Below -87, where 1 + exp(-v)
-// passes 2^126, it is 0.
-__device__ __forceinline__ float sigmoid_f(float v) { return __fdividef(1.f, 1.f + ex2_approx(-v * LOG2E)); }
-
-// Activations, act(v) = v phi(v), two values at a time: the polynomials of gelu and
-// gelu_tanh run in packed operations (2048 x 1024 x 4096 gelu 28.1 -> 25.4 us, 4096 x
-// 2048 x 5632 113.3 -> 105.8, e4m3 64.5 -> 60.3); silu's sigmoid, an exponential and a
-// reciprocal, is faster one value at a time (2621 x 224 x 12368 40.8 against 41.4).
-//
-// The standard normal distribution function, with a = |v| and t = 1 / (1 + 0.3 a):
-//   Phi(-a) = exp(-a^2 / 2) t Q(t),  Phi(a) = 1 - Phi(-a).
-// exp(a^2 / 2) Phi(-a) falls from 1/2 like 1 / a, so divided by t it is smooth over all of
-// 0 < t <= 1, and Q of degree 7 comes within 1.8e-7 of it (relative; least squares on
-// Chebyshev nodes for a up to 14, reweighted until the errors were level, coefficients
-// rounded to fp32; 0.3 was the best of 0.15 to 0.75).  As evaluated here Phi(-a) is off
-// by up to 2^-20 + a^2 2^-24: the rest is the rounding of a^2 in the exponent.  One
-// polynomial, one exponential and one reciprocal: with normcdff the epilogue of a tile
-// took 10 us.
-__device__ __forceinline__ float2 normal_cdf(float2 v)
-{
-    const float2 t = make_float2(__fdividef(1.f, fmaf(0.3f, fabsf(v.x), 1.f)),
-                                 __fdividef(1.f, fmaf(0.3f, fabsf(v.y), 1.f)));
-    float2 q = fma2(t, both(0.03567476f), both(-0.15720302f));
-    q = fma2(t, q, both(0.2063534f));
-    q = fma2(t, q, both(-0.05368354f));
-    q = fma2(t, q, both(0.12856157f));
-    q = fma2(t, q, both(0.09991351f));
-    q = fma2(t, q, both(0.12075395f));
-    q = fma2(t, q, both(0.1196293f));
-    const float2 x = mul2(mul2(v, v), both(-0.5f * LOG2E));
-    const float2 e = mul2(mul2(t, q), make_float2(ex2_approx(x.x), ex2_approx(x.y)));
-    const float2 r = fma2(e, both(-1.f), both(1.f));
-    return make_float2(v.x < 0.f ? e.x : r.x, v.y < 0.f ? e.y : r.y);
-}
-
-// phi(v)
-template <int ACT>
-__device__ __forceinline__ float2 act_phi(float2 v)
-{
-    if (ACT == ACT_GELU)
-        return normal_cdf(v);
-    if (ACT == ACT_GELU_TANH)
-        v = mul2(both(GELU_C2), fma2(mul2(mul2(both(GELU_A), v), v), v, v));
-    return make_float2(sigmoid_f(v.x), sigmoid_f(v.y));
-}
-
-// d phi / d v, given p = phi(v)
-template <int ACT>
-__device__ __forceinline__ float act_dphi(float v, float p)
-{
-    if (ACT == ACT_SILU)
-        return p * (1.f - p);
-    if (ACT == ACT_GELU)
-        return 0.3989422804014327f * ex2_approx(-0.5f * LOG2E * v * v);
-    return p * (1.f - p) * GELU_C2 * fmaf(3.f * GELU_A * v, v, 1.f);
-}
-
-// Tile order: bands of band_m M blocks (M block fastest), as gemm_nt_pair.cu.
-__device__ __forceinline__ void g_tile_coords(const GemmParams &p, int tile, int &mb, int &nb)
-{
-    const int MB = p.num_m_blocks;
-    const int bm = p.band_m > 0 && p.band_m < MB ? p.band_m : MB;
-    const int per_band = bm * p.num_n_blocks;
-    const int band = tile / per_band;
-    const int local = tile - band * per_band;
-    const int rows = min(bm, MB - band * bm);
-    mb = band * bm + local % rows;
-    nb = local / rows;
-}
-
-// 32 columns of one projection as they stand for: f times the token's scale, then
-// the output channels' (e4m3 operands), or f itself.  (f sx is what the token stands
-// for; sx w alone may be a subnormal number that has lost its bits.)
-template <bool E4M3>
-__device__ __forceinline__ void g_scale(float (&f)[32], float sx, const float *w_scale, int valid)
-{
-    if (E4M3) {
-#pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-            if (i < valid) {  // N % 8 == 0
-                const float4 w = *reinterpret_cast<const float4 *>(w_scale + i);
-                const float2 a = mul2(mul2(make_float2(f[i], f[i + 1]), both(sx)), make_float2(w.x, w.y));
-                const float2 b = mul2(mul2(make_float2(f[i + 2], f[i + 3]), both(sx)), make_float2(w.z, w.w));
-                f[i] = a.x;
-                f[i + 1] = a.y;
-                f[i + 2] = b.x;
-                f[i + 3] = b.y;
-            }
-        }
-    }
-}
 
 // The warp's 32 rows x 64 columns (from c0) of a finished tile.  The gate of
 // output column c is accumulator column c, its up projection accumulator column

@@ -1,6 +1,7 @@
 // gated_grads.cu -- the two products of the gated projections' gradient,
 //   dx[M, K] = dgu[M, 2F] . w[2F, K]      and      dw[2F, K] = dgu^T . x[M, K],
-// in one persistent launch on CTA pairs (256 x 256 tiles, cta_group::2).
+// in one persistent launch on CTA pairs (256 x 256 tiles, cta_group::2); and the same
+// two of a plain projection's, with dz[M, N] in the place of dgu.
 //
 // No operand is transposed in memory: dgu is the K-major A operand of dx and the
 // MN-major A operand of dw; w and x are MN-major B operands.
@@ -436,9 +437,9 @@ constexpr int GR_MAX_SPLIT = 16;
 // and 110).  Fewer tiles are split into at most one item for each pair (2323 x 144 x
 // 1000: 80 items by the first rule 21.2 us, 72 by this one 18.1).  Both products are
 // planned, wanted or not, so that one is summed the same way with and without the other.
-void plan_gated_grads(GradsParams *p, bool want_dx, bool want_dw, int64_t M, int64_t F, int64_t K, int pairs)
+void plan_gated_grads(GradsParams *p, bool want_dx, bool want_dw, int64_t M, int64_t N, int64_t K, int pairs)
 {
-    const int64_t rows[2] = {M, 2 * F}, kg[2] = {2 * F, M};
+    const int64_t rows[2] = {M, N}, kg[2] = {N, M};
     const bool want[2] = {want_dx, want_dw};
     double total = 0;
     for (int s = 0; s < 2; ++s) {

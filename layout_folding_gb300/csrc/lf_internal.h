@@ -157,7 +157,7 @@ cudaError_t launch_gated_bwd(int act, const void *dout, const void *gu, void *dg
                              cudaStream_t s);
 
 // The products of the gradient (gated_grads.cu).  Side 0: dx[M, K] = dgu . w;
-// side 1: dw[2F, K] = dgu^T . x.
+// side 1: dw[N, K] = dgu^T . x, dgu [M, N] (N = 2F for the gated projections).
 struct GradSide {
     int M, N;                                    // the output's rows and columns
     int m_blocks, n_blocks, k_blocks, band;      // 256-row, 256-column and 64-wide K blocks; M blocks per band
@@ -178,10 +178,36 @@ struct GradMaps {
 };
 // Pairs that the splits (and so the scratch) are planned for, whatever the device has.
 constexpr int GRAD_PLAN_PAIRS = 76;
-void plan_gated_grads(GradsParams *p, bool want_dx, bool want_dw, int64_t M, int64_t F, int64_t K, int pairs);
+void plan_gated_grads(GradsParams *p, bool want_dx, bool want_dw, int64_t M, int64_t N, int64_t K, int pairs);
 cudaError_t launch_gated_grads(const GradMaps &maps, const GradsParams &p, int pairs, cudaStream_t s);
 // The wanted split sides' parts added up.
 cudaError_t launch_add_parts(const GradsParams &p, const float *parts, void *dx, void *dw, int num_sms, cudaStream_t s);
+
+// A projection with bias, activation and residual in its epilogue, on CTA pairs
+// (linear.cu): out = act(x w^T + bias) + residual.  g: M, N, K, block counts (256-row M
+// blocks, N blocks of cols, 128-byte K blocks), num_tiles, band_m, err, timeout_ns, inject.
+struct LinearParams {
+    GemmParams g;
+    const float *x_scale, *w_scale;  // e4m3 operands: [M] and [N]
+    const void *bias;                // [N] or null
+    int bias_f32;                    // it is fp32 (else bf16)
+    int residual, save;              // add the residual (map residual), store z (map pre)
+    int cols;                        // columns of a pair tile (plan_linear_cols)
+};
+// x: boxes of 128 rows; w: boxes of cols / 2 rows (both 128-byte rows, 128-byte
+// swizzle); out, pre, residual: bf16 [M, N], 64 x 32 boxes, 128-byte swizzle.
+struct LinearMaps {
+    CUtensorMap x, w, out, pre, residual;
+};
+cudaError_t launch_linear_pair(bool e4m3, int act, const LinearMaps &m, const LinearParams &p, int grid, cudaStream_t s);
+int plan_linear_cols(int m_blocks, int64_t N, int pairs);
+// dz = dout act'(pre) (not written without an activation) and its column sums: to
+// dbias, or to `partial` (fp32 [linear_dz_blocks][N]) where that is more than one row,
+// and from there by launch_linear_dbias.  dbias may be null.  N % 8 == 0, 16-byte aligned.
+int linear_dz_blocks(int64_t M, int64_t N);
+cudaError_t launch_linear_dz(int act, const void *dout, const void *pre, void *dz, float *partial, void *dbias,
+                             bool bias_f32, int64_t M, int64_t N, cudaStream_t s);
+cudaError_t launch_linear_dbias(const float *partial, void *dbias, bool bias_f32, int64_t M, int64_t N, cudaStream_t s);
 
 // Test hook: `ctas` CTAs, each holding 200 KiB of shared memory (one per SM),
 // that wait `ns` nanoseconds on the global timer and exit.
