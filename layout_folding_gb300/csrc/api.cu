@@ -1290,8 +1290,15 @@ static lf_status linear_launch(const void *x, const float *x_scale, const void *
         return e4m3 ? make_tmap_e4m3(&m.x, x, M, K, x_rows) && make_tmap_e4m3(&m.w, w, N, K, w_rows)
                     : make_tmap(&m.x, x, M, K, x_rows) && make_tmap(&m.w, w, N, K, w_rows);
     };
+    const lf::LinearSkinny plan = lf::plan_linear_skinny(M, N, p.num_k_blocks, d->num_sms);
+    if (plan.preferred) {
+        p.num_n_blocks = static_cast<int>((N + lf::BM - 1) / lf::BM);
+        if (!operands(static_cast<uint32_t>(plan.n), lf::BM))
+            return LF_ERR_LAUNCH;
+        return launched(lf::launch_linear_skinny(e4m3, act, m, lp, plan, residual, pre, stream), 1);
+    }
     p.num_m_blocks = static_cast<int>((M + 2 * lf::BM - 1) / (2 * lf::BM));
-    lp.cols = lf::plan_linear_cols(p.num_m_blocks, N, d->pair_clusters);
+    lf::plan_linear_pair(p.num_m_blocks, N, p.num_k_blocks, d->pair_clusters, &lp.cols, &lp.split);
     p.num_n_blocks = static_cast<int>((N + lp.cols - 1) / lp.cols);
     p.num_tiles = p.num_m_blocks * p.num_n_blocks;
     if (!operands(lf::BM, static_cast<uint32_t>(lp.cols / 2)) || !make_tmap_out64(&m.out, out, M, N, N))
@@ -1301,7 +1308,8 @@ static lf_status linear_launch(const void *x, const float *x_scale, const void *
         (residual && !make_tmap_out64(&m.residual, const_cast<void *>(residual), M, N, N)))
         return LF_ERR_LAUNCH;
     p.band_m = band_of(p.num_m_blocks, K, e4m3);
-    const int grid = 2 * (p.num_tiles < d->pair_clusters ? p.num_tiles : d->pair_clusters);
+    const int most = lp.split > 1 ? p.num_tiles : d->pair_clusters;
+    const int grid = 2 * lp.split * (p.num_tiles < most ? p.num_tiles : most);
     return launched(lf::launch_linear_pair(e4m3, act, m, lp, grid, stream), 1);
 }
 

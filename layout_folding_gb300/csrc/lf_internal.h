@@ -192,7 +192,7 @@ struct LinearParams {
     const void *bias;                // [N] or null
     int bias_f32;                    // it is fp32 (else bf16)
     int residual, save;              // add the residual (map residual), store z (map pre)
-    int cols;                        // columns of a pair tile (plan_linear_cols)
+    int cols, split;                 // columns of a tile, pairs that share its K blocks (plan_linear_pair)
 };
 // x: boxes of 128 rows; w: boxes of cols / 2 rows (both 128-byte rows, 128-byte
 // swizzle); out, pre, residual: bf16 [M, N], 64 x 32 boxes, 128-byte swizzle.
@@ -200,7 +200,22 @@ struct LinearMaps {
     CUtensorMap x, w, out, pre, residual;
 };
 cudaError_t launch_linear_pair(bool e4m3, int act, const LinearMaps &m, const LinearParams &p, int grid, cudaStream_t s);
-int plan_linear_cols(int m_blocks, int64_t N, int pairs);
+void plan_linear_pair(int m_blocks, int64_t N, int num_k_blocks, int pairs, int *cols, int *split);
+// The same for few tokens (operands swapped, the K loop split over clusters).
+struct LinearSkinny {
+    bool preferred;  // to the pair kernel
+    int tokens;      // of one CTA (at most 128)
+    int n;           // the MMA's N: tokens rounded up to 16
+    int split;       // CTAs per cluster, each with its share of the K blocks: 1 to 8
+    int stages;      // ring stages
+    int smem;        // dynamic shared memory per CTA
+};
+// How a call with M tokens would run (in groups of at most 128); num_k_blocks counts 128-byte K blocks.
+LinearSkinny plan_linear_skinny(int64_t M, int64_t N, int num_k_blocks, int num_sms);
+// m.x: boxes of plan.n rows; m.w: boxes of 128 rows; the other maps are not read.
+// p.g.num_n_blocks counts blocks of 128 columns.  residual and pre: [M, N] or null.
+cudaError_t launch_linear_skinny(bool e4m3, int act, const LinearMaps &m, const LinearParams &p,
+                                 const LinearSkinny &plan, const void *residual, void *pre, cudaStream_t s);
 // dz = dout act'(pre) (not written without an activation) and its column sums: to
 // dbias, or to `partial` (fp32 [linear_dz_blocks][N]) where that is more than one row,
 // and from there by launch_linear_dbias.  dbias may be null.  N % 8 == 0, 16-byte aligned.

@@ -178,6 +178,33 @@ def test_forward_tile_widths(M, N, K):
     check_forward(x.double() * xs.double()[:, None], w.double() * ws.double()[:, None], b, res, None, out)
 
 
+@pytest.mark.parametrize("M,N,K", [(256, 2048, 4096), (520, 1000, 8192), (300, 264, 8200), (140, 4104, 2056),
+                                   (129, 520, 1032), (1000, 1032, 2056), (256, 4096, 1024), (260, 200, 4104)])
+def test_forward_shared_sums(M, N, K):
+    """Few tiles and long K loops: the pairs of a cluster (two to four, tiles of every width)
+    share a tile's K blocks."""
+    x, w, b, res = inputs(M, N, K, M + N + K)
+    xd, wd, bd, rd = dev(x, w, b, res)
+    x64, w64 = x.double(), w.double()
+    for name in ACTS:
+        out, pre = lf.linear(xd, wd, bias=bd, act=name, residual=rd, want_pre=True)
+        only, _ = lf.linear(xd, wd, bias=bd, act=name, residual=rd)
+        assert torch.equal(out, only)
+        check_forward(x64, w64, b, res, name, out, pre)
+    out, _ = lf.linear(xd, wd)
+    check_forward(x64, w64, None, None, None, out)
+    over = rd.clone()
+    lf.linear(xd, wd, bias=bd, act=name, residual=over, out=over)
+    assert torch.equal(over, only)
+    if K % 16 == 0:
+        x, xs = quantised(x)
+        w, ws = quantised(w)
+        xd, sd, wd, td = dev(x, xs, w, ws)
+        out, _ = lf.linear(xd, wd, bias=bd, act="silu", residual=rd, x_scale=sd, w_scale=td)
+        check_forward(x.double() * xs.double()[:, None], w.double() * ws.double()[:, None], b, res, "silu", out)
+    lf.check_device_error()
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 264, 136), (70, 1000, 520), (130, 264, 1032), (1000, 2424, 72), (2000, 5120, 64)])
 def test_residual_updated_in_place(M, N, K):
     """out over the residual, several tiles for each pair among the shapes."""
@@ -427,9 +454,9 @@ def test_repeatable_and_on_two_streams_at_once():
             assert torch.equal(a, c)
 
 
-@pytest.mark.parametrize("M", [4, 300])
-def test_stalled_wait_times_out_and_context_survives(M):
-    x, w, b, res = inputs(M, 264, 520)
+@pytest.mark.parametrize("M,K", [(4, 520), (300, 136), (300, 4104)])
+def test_stalled_wait_times_out_and_context_survives(M, K):
+    x, w, b, res = inputs(M, 264, K)
     xd, wd, bd, rd = dev(x, w, b, res)
     lf.check_device_error()
     for residual in (None, rd):
