@@ -423,6 +423,76 @@ lf_status add_rms_norm_backward(const void *dy, const void *h, const void *weigh
 int64_t add_rms_norm_backward_scratch(int64_t M, int64_t D);
 
 /*
+ * block_norm -- the norm after a block, its gate, the scaled addition to the stream, and
+ * the norm before the next block, in one kernel that reads each row once (sandwich norms,
+ * layer scale, adaptive gates; without pre and gate an output norm, without post the
+ * gated addition before a norm).  The pages have no counterpart: out of the projections'
+ * x (linear) it makes the X that the next projection reads, in e4m3 on request.
+ *
+ *   p = (x r1) post,  r1 = 1 / sqrt(mean_d x[m,d]^2 + eps)     (p = x without post)
+ *   h = rn(residual_scale residual + branch_scale (p gate))    (p without a gate)
+ *   f = (h r2) pre,   r2 = 1 / sqrt(mean_d h[m,d]^2 + eps)
+ *   y = rn(f), or for LF_E4M3 y = e4m3(f / scale[m])           (no y without pre)
+ * Products and statistics in fp32, each row's mean from a sum in a fixed order; the second
+ * norm reads h as it is kept.
+ *
+ *   dtype, wdtype, ydtype : as add_rms_norm (ydtype is not read without pre).
+ *   x, residual : [M,D] with row pitches of ldx and ldr elements, device.
+ *   post_or_null, pre_or_null : [D] of wdtype.
+ *   gate_or_null : [gate_rows, D] contiguous, of gate_dtype (dtype or LF_FP32); row g is for
+ *              the tokens g M / gate_rows .. (g + 1) M / gate_rows - 1.  gate_rows >= 1
+ *              divides M (neither it nor gate_dtype is read without a gate).
+ *   h      : [M,D] contiguous.
+ *   y      : [M,D] contiguous; not read (NULL allowed) without pre.
+ *   scale_or_null : fp32 [M], required exactly when there is a y of LF_E4M3; its values,
+ *              also for rows of zeros and NaN, as add_rms_norm's.
+ *   eps >= 0.  1 <= M, D < 2^31; ldx, ldr >= D (LF_ERR_SHAPE otherwise).
+ * Alignment as add_rms_norm (a gate of several rows is read element by element where D is
+ * odd).  h may be the buffer of x or of residual, and y in x's type that of the other,
+ * where that input's row pitch is D (LF_ERR_SHAPE for an e4m3 y over either, h and y in
+ * one buffer, or another pitch); other overlaps are not allowed.
+ * One launch; nothing is allocated.
+ */
+lf_status block_norm(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *post_or_null,
+                     const void *pre_or_null, const void *gate_or_null, int64_t gate_rows, int gate_dtype, void *h,
+                     void *y, float *scale_or_null, int dtype, int wdtype, int ydtype, float eps, float branch_scale,
+                     float residual_scale, int64_t M, int64_t D, cudaStream_t stream);
+
+/*
+ * block_norm_backward -- the gradient of block_norm from the x and h that it read and
+ * wrote (no statistics have to be kept).  With g = dy pre and r1, r2 as above:
+ *   H         = r2 (g - h r2^2 mean_d(g h)) + dh      the gradient at h (dh without pre)
+ *   dresidual = rn(residual_scale H)
+ *   c         = branch_scale H gate post,   dx = rn(r1 (c - x r1^2 mean_d(c x)))
+ *               (dx = rn(branch_scale H gate) without post)
+ *   dpre      = rn(sum_m dy h r2),   dpost = rn(branch_scale sum_m H gate x r1)
+ *   dgate     = rn(branch_scale sum H p) over the tokens of each gate row
+ * An e4m3 output is differentiated as if it had not been rounded.
+ *
+ *   dy, h  : dtype [M,D] contiguous, device; not read (NULL allowed) without pre.
+ *   x      : dtype [M,D] contiguous; not read (NULL allowed) without post and gate.
+ *   dh_or_null : dtype [M,D], the gradient that arrives at h by other ways (required
+ *            without pre).
+ *   dx, dresidual : dtype [M,D] contiguous, always written.
+ *   dpost_or_null, dpre_or_null : wdtype [D];  dgate_or_null : gate_dtype [gate_rows, D];
+ *            NULL where not wanted, and where the parameter itself is NULL.
+ *   scratch : block_norm_backward_scratch(M, D, dtype, gate_rows) bytes (gate_rows 0 without
+ *            a gate), 16-byte aligned, device, owned by the caller, contents arbitrary;
+ *            NULL allowed without parameter gradients.
+ * Sums in fp32 in a fixed order: two calls on the same inputs give the same bits.  dx and
+ * dresidual may each be the buffer of dy, x, h or dh (not the same one).  Two launches (one
+ * without parameter gradients); nothing is allocated.  Errors as block_norm.
+ */
+lf_status block_norm_backward(const void *dy, const void *x, const void *h, const void *post_or_null,
+                              const void *pre_or_null, const void *gate_or_null, int64_t gate_rows, int gate_dtype,
+                              const void *dh_or_null, void *dx, void *dresidual, void *dpost_or_null,
+                              void *dpre_or_null, void *dgate_or_null, void *scratch, int dtype, int wdtype, float eps,
+                              float branch_scale, float residual_scale, int64_t M, int64_t D, cudaStream_t stream);
+
+/* Bytes of scratch that block_norm_backward needs (0 for sizes or a type out of range). */
+int64_t block_norm_backward_scratch(int64_t M, int64_t D, int dtype, int64_t gate_rows);
+
+/*
  * gated_ffn -- the gated projections of a feed-forward block in one kernel:
  *   [g, u] = X . W^T,   out = act(g) * u
  * The two projections are two column blocks of one NT GEMM whose epilogue has

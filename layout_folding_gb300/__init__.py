@@ -18,6 +18,8 @@ Entry points (same names as the C ABI):
   gemm_batched(...) / bmm(a, b)                 -> batched a @ b over strided views (pitches, batch strides)
   add_rms_norm(x, weight, residual, fp8)        -> (y, h = x + residual, scale): y in x's type, or e4m3 + row scales
   add_rms_norm_backward(dy, h, weight, dh)      -> (dx, dweight)
+  block_norm(x, residual, post, pre, gate, ...) -> (y, h, scale): h = a residual + b gate norm(x) post, y = norm(h) pre
+  block_norm_backward(dy, x, h, post, pre, ...) -> (dx, dresidual, dpost, dpre, dgate)
   gated_ffn(x, w, act, x_scale, w_scale)        -> (act(x Wg^T) * (x Wu^T), [g, u] on request); bf16 or e4m3 operands
   gated_ffn_backward(dout, x, w, gu, act)       -> (dx, dw)
   linear(x, w, bias, act, residual, ...)        -> (act(x w^T + bias) + residual, x w^T + bias on request); bf16 or e4m3
@@ -129,6 +131,13 @@ def lib():
         L.linear_backward.restype = I32
         L.linear_backward_scratch.argtypes = [I64, I64, I64]
         L.linear_backward_scratch.restype = I64
+        L.block_norm.argtypes = [P, I64, P, I64, P, P, P, I64, I32, P, P, P, I32, I32, I32, F32, F32, F32, I64, I64, P]
+        L.block_norm.restype = I32
+        L.block_norm_backward.argtypes = ([P, P, P, P, P, P, I64, I32] + [P] * 7
+                                          + [I32, I32, F32, F32, F32, I64, I64, P])
+        L.block_norm_backward.restype = I32
+        L.block_norm_backward_scratch.argtypes = [I64, I64, I32, I64]
+        L.block_norm_backward_scratch.restype = I64
         _lib = L
         return L
 
@@ -510,4 +519,5 @@ def occupy_sms(ctas: int, duration_ns: int, stream=None):
 
 from .ffn import (ACTIVATIONS, LF_BF16, LF_E4M3, LF_FP16, LF_FP32, add_rms_norm,  # noqa: E402,F401
                   add_rms_norm_backward, gated_ffn, gated_ffn_backward)
+from .block_norms import block_norm, block_norm_backward  # noqa: E402,F401
 from .projections import linear, linear_backward  # noqa: E402,F401

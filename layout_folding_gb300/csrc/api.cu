@@ -1055,6 +1055,85 @@ static lf_status add_rms_norm_backward_call(const void *dy, const void *h, const
     return launched(lf::launch_rms_norm_bwd(p, dweight, dtype, wdtype, d->num_sms, stream), dweight ? 2 : 1);
 }
 
+// The arguments that block_norm and its gradient share.
+static bool block_norm_shape_ok(const void *gate, int64_t gate_rows, int gate_dtype, int dtype, int wdtype, float eps,
+                                int64_t M, int64_t D)
+{
+    if (!norm_types_ok(dtype, wdtype) || !(eps >= 0.f) || M <= 0 || D <= 0 || M > MAX_DIM || D > MAX_DIM)
+        return false;
+    return !gate || ((gate_dtype == dtype || gate_dtype == LF_FP32) && gate_rows > 0 && M % gate_rows == 0);
+}
+
+static lf_status block_norm_call(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *post,
+                                 const void *pre, const void *gate, int64_t gate_rows, int gate_dtype, void *h, void *y,
+                                 float *scale, int dtype, int wdtype, int ydtype, float eps, float branch_scale,
+                                 float residual_scale, int64_t M, int64_t D, cudaStream_t stream)
+{
+    const bool fp8 = pre && ydtype == LF_E4M3;
+    if (!x || !residual || !h || (pre && !y) || (fp8 && !scale))
+        return LF_ERR_NULL;
+    if (!block_norm_shape_ok(gate, gate_rows, gate_dtype, dtype, wdtype, eps, M, D) ||
+        (pre && ydtype != dtype && ydtype != LF_E4M3) || (!fp8 && scale) || ldx < D || ldr < D)
+        return LF_ERR_SHAPE;
+    if (!pre)
+        y = nullptr;
+    if (misaligned_for(x, dtype) || misaligned_for(residual, dtype) || misaligned_for(h, dtype) ||
+        misaligned_for(post, wdtype) || misaligned_for(pre, wdtype) || misaligned_for(gate, gate_dtype) ||
+        misaligned_for(y, ydtype) || !aligned4(scale))
+        return LF_ERR_ALIGN;
+    // Outputs over inputs go row by row: only where both lie in the same type and pitch.
+    const bool x_packed = M == 1 || ldx == D, r_packed = M == 1 || ldr == D;
+    if (h == y || (h == x && !x_packed) || (h == residual && !r_packed) ||
+        (y && ((y == x && (fp8 || !x_packed)) || (y == residual && (fp8 || !r_packed)))))
+        return LF_ERR_SHAPE;
+    DeviceState *d = nullptr;
+    lf_status st = current_device(&d);
+    if (st != LF_OK)
+        return st;
+    const lf::BlockNormParams p = {x, residual, post, pre, gate, h, y, scale, M, D, ldx, ldr, gate ? M / gate_rows : M,
+                                   eps, branch_scale, residual_scale, gate && gate_dtype == LF_FP32,
+                                   {d->err_word, g_timeout_ns.load(), g_inject.load()}};
+    return launched(lf::launch_block_norm(p, dtype, wdtype, fp8, d->num_sms, stream), 1);
+}
+
+// Floats of one of the two regions of block_norm_backward's scratch.
+static int64_t block_norm_part(int64_t rows, int64_t D) { return (rows * D + 3) / 4 * 4; }
+
+static lf_status block_norm_backward_call(const void *dy, const void *x, const void *h, const void *post, const void *pre,
+                                          const void *gate, int64_t gate_rows, int gate_dtype, const void *dh, void *dx,
+                                          void *dres, void *dpost, void *dpre, void *dgate, void *scratch, int dtype,
+                                          int wdtype, float eps, float branch_scale, float residual_scale, int64_t M,
+                                          int64_t D, cudaStream_t stream)
+{
+    if (!pre)
+        dy = h = nullptr;
+    if (!post && !gate)
+        x = nullptr;
+    const bool params = dpost || dpre || dgate;
+    if ((pre && (!dy || !h)) || ((post || gate) && !x) || (!pre && !dh) || !dx || !dres || (params && !scratch))
+        return LF_ERR_NULL;
+    if (!block_norm_shape_ok(gate, gate_rows, gate_dtype, dtype, wdtype, eps, M, D) || (dpost && !post) ||
+        (dpre && !pre) || (dgate && !gate) || dx == dres)
+        return LF_ERR_SHAPE;
+    if (misaligned_for(dy, dtype) || misaligned_for(x, dtype) || misaligned_for(h, dtype) || misaligned_for(dh, dtype) ||
+        misaligned_for(dx, dtype) || misaligned_for(dres, dtype) || misaligned_for(post, wdtype) ||
+        misaligned_for(pre, wdtype) || misaligned_for(dpost, wdtype) || misaligned_for(dpre, wdtype) ||
+        misaligned_for(gate, gate_dtype) || misaligned_for(dgate, gate_dtype) || (params && !aligned16(scratch)))
+        return LF_ERR_ALIGN;
+    DeviceState *d = nullptr;
+    lf_status st = current_device(&d);
+    if (st != LF_OK)
+        return st;
+    float *part_pre = static_cast<float *>(scratch);
+    float *part_sum = params ? part_pre + block_norm_part(lf::block_norm_bwd_lanes(M, D, dtype), D) : nullptr;
+    const lf::BlockNormBwdParams p = {dy, x, h, post, pre, gate, dh, dx, dres, dpre ? part_pre : nullptr,
+                                      dpost || dgate ? part_sum : nullptr, M, D, gate ? M / gate_rows : M,
+                                      gate ? gate_rows : 0, 0, eps, branch_scale, residual_scale,
+                                      gate && gate_dtype == LF_FP32,
+                                      {d->err_word, g_timeout_ns.load(), g_inject.load()}};
+    return launched(lf::launch_block_norm_bwd(p, dpost, dpre, dgate, dtype, wdtype, d->num_sms, stream), params ? 2 : 1);
+}
+
 static bool act_ok(int act) { return act >= LF_ACT_SILU && act <= LF_ACT_GELU_TANH; }
 
 static lf_status check_gated_shape(int64_t M, int64_t F, int64_t K, int act)
@@ -1589,6 +1668,40 @@ lf_status add_rms_norm_backward(const void *dy, const void *h, const void *weigh
     const lf::CallRange range("add_rms_norm_backward");
     return debug_sync(add_rms_norm_backward_call(dy, h, weight, dh_or_null, dx, dweight_or_null, scratch, dtype,
                                                  wdtype, eps, M, D, stream),
+                      stream);
+}
+
+lf_status block_norm(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *post_or_null,
+                     const void *pre_or_null, const void *gate_or_null, int64_t gate_rows, int gate_dtype, void *h,
+                     void *y, float *scale_or_null, int dtype, int wdtype, int ydtype, float eps, float branch_scale,
+                     float residual_scale, int64_t M, int64_t D, cudaStream_t stream)
+{
+    const lf::CallRange range("block_norm");
+    return debug_sync(block_norm_call(x, ldx, residual, ldr, post_or_null, pre_or_null, gate_or_null, gate_rows,
+                                      gate_dtype, h, y, scale_or_null, dtype, wdtype, ydtype, eps, branch_scale,
+                                      residual_scale, M, D, stream),
+                      stream);
+}
+
+int64_t block_norm_backward_scratch(int64_t M, int64_t D, int dtype, int64_t gate_rows)
+{
+    if (M <= 0 || D <= 0 || M > MAX_DIM || D > MAX_DIM || dtype < LF_BF16 || dtype > LF_FP32 || gate_rows < 0 ||
+        gate_rows > M)
+        return 0;
+    const int64_t lanes = lf::block_norm_bwd_lanes(M, D, dtype);
+    return (block_norm_part(lanes, D) + block_norm_part(lanes + gate_rows, D)) * static_cast<int64_t>(sizeof(float));
+}
+
+lf_status block_norm_backward(const void *dy, const void *x, const void *h, const void *post_or_null,
+                              const void *pre_or_null, const void *gate_or_null, int64_t gate_rows, int gate_dtype,
+                              const void *dh_or_null, void *dx, void *dresidual, void *dpost_or_null,
+                              void *dpre_or_null, void *dgate_or_null, void *scratch, int dtype, int wdtype, float eps,
+                              float branch_scale, float residual_scale, int64_t M, int64_t D, cudaStream_t stream)
+{
+    const lf::CallRange range("block_norm_backward");
+    return debug_sync(block_norm_backward_call(dy, x, h, post_or_null, pre_or_null, gate_or_null, gate_rows, gate_dtype,
+                                               dh_or_null, dx, dresidual, dpost_or_null, dpre_or_null, dgate_or_null,
+                                               scratch, dtype, wdtype, eps, branch_scale, residual_scale, M, D, stream),
                       stream);
 }
 

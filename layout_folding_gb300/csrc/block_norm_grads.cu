@@ -1,0 +1,642 @@
+// block_norm_grads.cu -- the gradient of block_norm.  With x, h, the gate row u and
+// g = dy pre, r1 and r2 recomputed from the x and h that were kept:
+//   H  = r2 (g - h r2^2 mean(g h)) + dh                       the gradient at h
+//   dresidual = alpha H,   dx = r1 (c' - x r1^2 mean(c' x)),  c' = beta H (post u)
+//                          (dx = c' without post)
+// mean(c' x) needs no second reduction: with c = x (post u),
+//   sum c' x = beta (r2 (sum g c - r2^2 mean(g h) sum h c) + sum dh c),
+// so one reduction of six sums serves the row.  The parameters' gradients are
+//   dpre = sum over rows of dy h r2,   S = sum over a gate row's tokens of H x r1,
+//   dpost = beta sum over gate rows of u S,   dgate = beta post S
+// (S of H x, and dgate = beta S, without post), so a thread keeps two sums for each of
+// its columns, not three.  Bound by memory: every element is read once.
+#include "block_norm_common.cuh"
+
+namespace lf {
+namespace {
+
+// A row's six sums over its columns (what a term has none of is 0).
+struct RowSums {
+    float v[6];  // h^2, g h, x^2, g c, h c, dh c
+    __device__ __forceinline__ explicit RowSums(const float2 (&s)[6])
+    {
+#pragma unroll
+        for (int i = 0; i < 6; ++i)
+            v[i] = s[i].x + s[i].y;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < 6; ++i)
+                v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    }
+    __device__ __forceinline__ void put(float *sh) const
+    {
+        *reinterpret_cast<float4 *>(sh) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float2 *>(sh + 4) = make_float2(v[4], v[5]);
+    }
+    __device__ __forceinline__ void add_all(const float *sh, int warps)
+    {
+#pragma unroll
+        for (int i = 0; i < 6; ++i)
+            v[i] = 0.f;
+        for (int w = 0; w < warps; ++w) {
+            const float4 a = *reinterpret_cast<const float4 *>(sh + 8 * w);
+            const float2 b = *reinterpret_cast<const float2 *>(sh + 8 * w + 4);
+            v[0] += a.x;
+            v[1] += a.y;
+            v[2] += a.z;
+            v[3] += a.w;
+            v[4] += b.x;
+            v[5] += b.y;
+        }
+    }
+};
+
+// A row's factors: H = r2 (g - h m2) + dh, dx = r1 (c' - x k1).
+struct RowFactors {
+    float r1, r2, m2, k1;
+    __device__ __forceinline__ RowFactors(const BlockNormBwdParams &p, const RowSums &s)
+    {
+        const float inv_d = 1.f / static_cast<float>(p.D);
+        r2 = p.pre ? rsqrtf(s.v[0] * inv_d + p.eps) : 0.f;
+        m2 = p.pre ? (s.v[1] * inv_d) * r2 * r2 : 0.f;
+        r1 = p.post ? rsqrtf(s.v[2] * inv_d + p.eps) : 1.f;
+        k1 = p.post ? p.branch_scale * (fmaf(r2, fmaf(-m2, s.v[4], s.v[3]), s.v[5]) * inv_d) * r1 * r1 : 0.f;
+    }
+};
+
+// VEC columns of a row; what the call has none of is 0, pre and the factors are 1.
+template <class T, class W, int VEC>
+struct Columns {
+    static constexpr int N = PAIRS<VEC>;
+    float2 dy[N], h[N], x[N], dh[N], pre[N], cf[N];
+    // at(k): the address of the columns in input k (h, dy, x, dh), w: that of pre's
+    template <class At>
+    __device__ __forceinline__ void load(const BlockNormBwdParams &p, const At &at, const W *w)
+    {
+        const auto get = [&](bool have, int k, float2 (&f)[N]) {
+            if (have) {
+                pairs_of<T, VEC>(at(k), f);
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    f[i] = both(0.f);
+            }
+        };
+        get(p.pre, 0, h);
+        get(p.pre, 1, dy);
+        get(p.x, 2, x);
+        get(p.dh, 3, dh);
+        if (p.pre) {
+            pairs_of<W, VEC>(load_pack<W, VEC>(w), pre);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                pre[i] = both(1.f);
+        }
+    }
+    __device__ __forceinline__ void add_to(const BlockNormBwdParams &p, float2 (&s)[6]) const
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float2 g = mul2(dy[i], pre[i]);
+            s[0] = fma2(h[i], h[i], s[0]);
+            s[1] = fma2(g, h[i], s[1]);
+            if (p.post) {
+                const float2 c = mul2(x[i], cf[i]);
+                s[2] = fma2(x[i], x[i], s[2]);
+                s[3] = fma2(g, c, s[3]);
+                s[4] = fma2(h[i], c, s[4]);
+                s[5] = fma2(dh[i], c, s[5]);
+            }
+        }
+    }
+    // dresidual, dx, and the two sums of the parameters' gradients
+    __device__ __forceinline__ void finish(const BlockNormBwdParams &p, const RowFactors &f, Pack<T, VEC> &dres,
+                                           Pack<T, VEC> &dx, float2 (&a_pre)[N], float2 (&a_sum)[N]) const
+    {
+        float2 o[N], q[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float2 at_h = p.pre ? fma2(both(f.r2), fma2(h[i], both(-f.m2), mul2(dy[i], pre[i])), dh[i]) : dh[i];
+            o[i] = mul2(at_h, both(p.residual_scale));
+            q[i] = mul2(mul2(at_h, both(p.branch_scale)), cf[i]);
+            if (p.post)
+                q[i] = mul2(fma2(x[i], both(-f.k1), q[i]), both(f.r1));
+            a_pre[i] = fma2(dy[i], mul2(h[i], both(f.r2)), a_pre[i]);
+            a_sum[i] = fma2(at_h, mul2(x[i], both(f.r1)), a_sum[i]);
+        }
+        from_pairs<T, VEC>(dres, o);
+        from_pairs<T, VEC>(dx, q);
+    }
+};
+
+template <int N>
+__device__ __forceinline__ void clear(float2 (&f)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        f[i] = both(0.f);
+}
+
+// Rows of a lane (a block, or a group of warps in the ring kernel).  With one gate row or
+// none they are strided; with several, lane l of `lanes` takes the rows M l / lanes ..
+// M (l + 1) / lanes - 1, so that it meets the gate rows one after another, and leaves S of
+// lane l and gate row g in row l + g of part_sum (a lane and a gate row that meet are on a
+// path on which one or both of them grow, so no two of them share a row).
+struct LaneRows {
+    int64_t first, end, step;
+    __device__ LaneRows(const BlockNormBwdParams &p, int64_t lane, int64_t strided_first, int64_t strided_step)
+    {
+        const bool several = p.gate_rows > 1;
+        first = several ? p.M * lane / p.lanes : strided_first;
+        end = several ? p.M * (lane + 1) / p.lanes : p.M;
+        step = several ? 1 : strided_step;
+    }
+};
+// After `row`: S of its gate row is complete for this lane.
+__device__ __forceinline__ bool gate_row_ends(const BlockNormBwdParams &p, const LaneRows &rows, int64_t row)
+{
+    return p.gate_rows > 1 && (row + 1 == rows.end || (row + 1) % p.gate_tokens == 0);
+}
+
+// One row per block and step, its sums of the parameters' gradients in registers.
+template <class T, class W, int VEC, int NV>
+__global__ void __launch_bounds__(512) k_block_norm_bwd(const __grid_constant__ BlockNormBwdParams p)
+{
+    wait_previous_kernel();
+    let_next_kernel_start();
+    constexpr int N = PAIRS<VEC>;
+    __shared__ __align__(16) float sh[2][MAX_WARPS * 8];
+    const int packs = static_cast<int>(p.D / VEC);
+    const T *const in[4] = {static_cast<const T *>(p.h), static_cast<const T *>(p.dy), static_cast<const T *>(p.x),
+                            static_cast<const T *>(p.dh)};
+    float2 a_pre[NV][N], a_sum[NV][N];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        clear(a_pre[j]);
+        clear(a_sum[j]);
+    }
+    int buf = 0;
+    const LaneRows rows(p, blockIdx.x, blockIdx.x, gridDim.x);
+    for (int64_t row = rows.first; row < rows.end; row += rows.step, buf ^= 1) {
+        const int64_t o = row * p.D, gate_row = p.gate ? row / p.gate_tokens * p.D : 0;
+        Pack<T, VEC> q[NV][4];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = threadIdx.x + j * blockDim.x;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (c < packs && in[k])
+                    q[j][k] = load_pack<T, VEC>(in[k] + o + static_cast<int64_t>(c) * VEC);
+        }
+        const auto columns = [&](int j, int64_t at) {
+            Columns<T, W, VEC> v;
+            v.load(p, [&](int k) { return q[j][k]; }, static_cast<const W *>(p.pre) + at);
+            column_factors<T, W, VEC>(p, gate_row, at, v.cf);
+            return v;
+        };
+        float2 s2[6];
+        clear(s2);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = threadIdx.x + j * blockDim.x;
+            if (c < packs)
+                columns(j, static_cast<int64_t>(c) * VEC).add_to(p, s2);
+        }
+        RowSums s(s2);
+        if ((threadIdx.x & 31) == 0)
+            s.put(&sh[buf][(threadIdx.x >> 5) * 8]);
+        __syncthreads();
+        s.add_all(sh[buf], blockDim.x >> 5);
+        const RowFactors f(p, s);
+        const bool ends = p.part_sum && gate_row_ends(p, rows, row);
+        float *seg = ends ? p.part_sum + (blockIdx.x + row / p.gate_tokens) * p.D : nullptr;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = threadIdx.x + j * blockDim.x;
+            if (c < packs) {
+                const int64_t at = static_cast<int64_t>(c) * VEC;
+                Pack<T, VEC> dres, dx;
+                columns(j, at).finish(p, f, dres, dx, a_pre[j], a_sum[j]);
+                dres.store(static_cast<T *>(p.dres) + o + at);
+                dx.store(static_cast<T *>(p.dx) + o + at);
+                if (ends) {
+                    Pack<float, VEC> a;
+                    from_pairs<float, VEC>(a, a_sum[j]);
+                    a.store(seg + at);
+                    clear(a_sum[j]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int c = threadIdx.x + j * blockDim.x;
+        if (c < packs) {
+            const int64_t at = static_cast<int64_t>(blockIdx.x) * p.D + static_cast<int64_t>(c) * VEC;
+            Pack<float, VEC> a;
+            from_pairs<float, VEC>(a, a_pre[j]);
+            if (p.part_pre)
+                a.store(p.part_pre + at);
+            from_pairs<float, VEC>(a, a_sum[j]);
+            if (p.part_sum && p.gate_rows <= 1)
+                a.store(p.part_sum + at);
+        }
+    }
+}
+
+// Rows too long for the registers: the row is read twice, and the sums are kept in
+// their rows of part_pre and part_sum (each thread updates its own columns only).
+template <class T, class W>
+__global__ void __launch_bounds__(1024) k_block_norm_bwd_long(const __grid_constant__ BlockNormBwdParams p)
+{
+    wait_previous_kernel();
+    let_next_kernel_start();
+    __shared__ __align__(16) float sh[2][MAX_WARPS * 8];
+    const T *const in[4] = {static_cast<const T *>(p.h), static_cast<const T *>(p.dy), static_cast<const T *>(p.x),
+                            static_cast<const T *>(p.dh)};
+    int buf = 0;
+    const LaneRows rows(p, blockIdx.x, blockIdx.x, gridDim.x);
+    const auto columns = [&](int64_t row, int64_t c) {
+        Columns<T, W, 1> v;
+        v.load(p, [&](int k) { return load_pack<T, 1>(in[k] + row * p.D + c); }, static_cast<const W *>(p.pre) + c);
+        column_factors<T, W, 1>(p, p.gate ? row / p.gate_tokens * p.D : 0, c, v.cf);
+        return v;
+    };
+    const bool several = p.gate_rows > 1;
+    for (int64_t row = rows.first; row < rows.end; row += rows.step, buf ^= 1) {
+        float2 s2[6];
+        clear(s2);
+        for (int64_t c = threadIdx.x; c < p.D; c += blockDim.x)
+            columns(row, c).add_to(p, s2);
+        RowSums s(s2);
+        if ((threadIdx.x & 31) == 0)
+            s.put(&sh[buf][(threadIdx.x >> 5) * 8]);
+        __syncthreads();
+        s.add_all(sh[buf], blockDim.x >> 5);
+        const RowFactors f(p, s);
+        float *pre_sum = p.part_pre ? p.part_pre + static_cast<int64_t>(blockIdx.x) * p.D : nullptr;
+        float *sum = p.part_sum ? p.part_sum + (blockIdx.x + (several ? row / p.gate_tokens : 0)) * p.D : nullptr;
+        const bool first = row == rows.first, first_of_gate = first || (several && row % p.gate_tokens == 0);
+        for (int64_t c = threadIdx.x; c < p.D; c += blockDim.x) {
+            float2 a[1] = {both(pre_sum && !first ? pre_sum[c] : 0.f)};
+            float2 b[1] = {both(sum && !first_of_gate ? sum[c] : 0.f)};
+            Pack<T, 1> dres, dx;
+            columns(row, c).finish(p, f, dres, dx, a, b);
+            dres.store(static_cast<T *>(p.dres) + row * p.D + c);
+            dx.store(static_cast<T *>(p.dx) + row * p.D + c);
+            if (pre_sum)
+                pre_sum[c] = a[0].x;
+            if (sum)
+                sum[c] = b[0].x;
+        }
+    }
+}
+
+constexpr int BLOCK_NORM_BWD_THREADS = 384;
+constexpr int BWD_RING_BUDGET = RING_BUDGET - 1024;  // the warps' sums take 768 bytes beside RingSync
+
+// In rings: a slot has the row of h, dy, x and dh (those that the call has, in this order).
+// The row stays in its slot until it is done -- with two sums for each column there are no
+// registers to keep it in -- so it is read from shared memory twice, and the slot is filled
+// again after a second barrier.
+template <class T, class W, bool PH>
+__global__ void __launch_bounds__(BLOCK_NORM_BWD_THREADS)
+    k_block_norm_bwd_ring(const __grid_constant__ BlockNormBwdParams p, const RingPlan r)
+{
+    constexpr int VEC = 16 / static_cast<int>(sizeof(T));
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ RingSync sy;
+    __shared__ __align__(16) float red[2][BLOCK_NORM_BWD_THREADS / 32][8];
+    const int group = threadIdx.x / r.group_threads, t = threadIdx.x % r.group_threads;
+    const int warps = r.group_threads >> 5, first_warp = group * warps;
+    const RowSpan<T, PH> span(p.M, p.D);
+    const int packs = span.packs;
+    const int64_t lane = static_cast<int64_t>(blockIdx.x) * r.groups + group;
+    // neighbouring rows go to neighbouring SMs
+    const LaneRows rows(p, lane, static_cast<int64_t>(group) * gridDim.x + blockIdx.x,
+                        static_cast<int64_t>(gridDim.x) * r.groups);
+    Ring ring(r, smem, sy, group);
+    const T *in[4] = {static_cast<const T *>(p.h), static_cast<const T *>(p.dy), static_cast<const T *>(p.x),
+                      static_cast<const T *>(p.dh)};
+    const int at_x = p.pre ? 2 : 0, at_dh = at_x + (p.x ? 1 : 0);
+    const auto fill = [&](int slot, int64_t row) { ring.fill_rows(span, slot, row, in, p.D); };
+    if (t == 0)
+        ring.init();
+    wait_previous_kernel();
+    let_next_kernel_start();
+    if (t == 0) {
+        // (test hook: the first block's first group never loads its first row)
+        for (int i = p.limit.inject && blockIdx.x == 0 && group == 0 ? 1 : 0;
+             i < r.slots && rows.first + i * rows.step < rows.end; ++i)
+            fill(i, rows.first + i * rows.step);
+    }
+    const RingParams<T, W, PH, BlockNormBwdParams> w(smem, r, span, p);
+    float2 a_pre[RING_NV][VEC / 2], a_sum[RING_NV][VEC / 2];
+#pragma unroll
+    for (int j = 0; j < RING_NV; ++j) {
+        clear(a_pre[j]);
+        clear(a_sum[j]);
+    }
+    bool ok = true;
+    int buf = 0;
+    for (int64_t row = rows.first; row < rows.end; row += rows.step, buf ^= 1) {
+        ok = ring_wait(ring.full_s + 8u * ring.slot, ring.phase, p.limit);
+        const auto columns = [&](int c) {
+            Columns<T, W, VEC> v;
+            const auto at = [&](int k) {
+                const int i = k < 2 ? k : k == 2 ? at_x : at_dh;
+                Pack<T, VEC> q = load_pack<T, VEC>(reinterpret_cast<const T *>(ring.input(i)) + c * VEC);
+                span.mask(q, c);
+                return q;
+            };
+            v.load(p, at, w.pre + c * VEC);
+            w.factors(p, span, row, c, v.cf);
+            return v;
+        };
+        float2 s2[6];
+        clear(s2);
+#pragma unroll
+        for (int j = 0; j < RING_NV; ++j) {
+            const int c = t + j * r.group_threads;
+            if (c < packs)
+                columns(c).add_to(p, s2);
+        }
+        RowSums s(s2);
+        ok = __all_sync(0xffffffffu, ok);
+        if ((t & 31) == 0) {
+            s.put(red[buf][threadIdx.x >> 5]);
+            sy.failed[buf][threadIdx.x >> 5] = ok ? 0 : 1;
+        }
+        group_barrier(1 + group, r.group_threads);
+        s.add_all(red[buf][first_warp], warps);
+        for (int i = 0; i < warps; ++i)
+            ok = ok && !sy.failed[buf][first_warp + i];
+        if (!ok)
+            break;
+        const RowFactors f(p, s);
+        const bool ends = p.part_sum && gate_row_ends(p, rows, row);
+        float *seg = ends ? p.part_sum + (lane + row / p.gate_tokens) * p.D : nullptr;
+#pragma unroll
+        for (int j = 0; j < RING_NV; ++j) {
+            const int c = t + j * r.group_threads;
+            if (c < packs) {
+                Pack<T, VEC> dres, dx;
+                columns(c).finish(p, f, dres, dx, a_pre[j], a_sum[j]);
+                span.store(static_cast<T *>(p.dres), row, c, dres);
+                span.store(static_cast<T *>(p.dx), row, c, dx);
+                if (ends) {  // (not with phased rows)
+                    Pack<float, VEC> a;
+                    from_pairs<float, VEC>(a, a_sum[j]);
+                    a.store(seg + c * VEC);
+                    clear(a_sum[j]);
+                }
+            }
+        }
+        group_barrier(1 + group, r.group_threads);
+        if (t == 0 && row + r.slots * rows.step < rows.end)
+            fill(ring.slot, row + r.slots * rows.step);  // every thread of the group has read the slot
+        ring.advance();
+    }
+    if (!ok) {  // copies of this group may still be in flight: give them time to land
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < RING_SETTLE_NS) {
+        }
+    }
+    // the rings are idle: the groups' sums are added there in turn, and written as the block's row
+    float *sums = reinterpret_cast<float *>(smem + r.slot_off);
+    const auto merge = [&](const float2 (&acc)[RING_NV][VEC / 2], float *out) {
+        for (int g = 0; g < r.groups; ++g) {
+            __syncthreads();
+            if (group != g)
+                continue;
+#pragma unroll
+            for (int j = 0; j < RING_NV; ++j) {
+                const int c = t + j * r.group_threads;
+                if (c < packs) {
+                    Pack<float, VEC> a;
+                    from_pairs<float, VEC>(a, acc[j]);
+                    if (g > 0)
+                        a.add(load_pack<float, VEC>(sums + c * VEC));
+                    a.store(sums + c * VEC);
+                }
+            }
+        }
+        __syncthreads();
+        for (int c = threadIdx.x; c < p.D; c += blockDim.x)
+            out[static_cast<int64_t>(blockIdx.x) * p.D + c] = sums[span.phase + c];
+    };
+    if (p.part_pre)
+        merge(a_pre, p.part_pre);
+    if (p.part_sum && p.gate_rows <= 1)
+        merge(a_sum, p.part_sum);
+}
+
+// The parameters' gradients from their sums.  A block has 32 columns and 32 rows of
+// threads; what it does goes by blockIdx.y: 0 dpre, 1 dpost, from 2 on dgate.  With one
+// gate row (or none) both sums have a row for each of `blocks` blocks; with several, S
+// lies as LaneRows says.
+constexpr int SUM_ROWS = 32;
+// S of many lanes to a gate row is added by all threads of a block, else a gate row each.
+__host__ __device__ constexpr bool many_lanes(int64_t lanes, int64_t gate_rows) { return lanes >= 16 * gate_rows; }
+
+template <class T, class W>
+__global__ void __launch_bounds__(32 * SUM_ROWS)
+    k_block_norm_sums(const __grid_constant__ BlockNormBwdParams p, int blocks, W *dpost, W *dpre, void *dgate)
+{
+    wait_previous_kernel();
+    __shared__ float sh[SUM_ROWS][33];
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x;
+    const bool several = p.gate_rows > 1;
+    const float post = p.post && c < p.D ? to_f(static_cast<const W *>(p.post)[c]) : 1.f;
+    const auto lane_of = [&](int64_t row) { return ((row + 1) * p.lanes - 1) / p.M; };
+    const auto put_gate = [&](int64_t i, float v) {
+        if (p.gate_f32)
+            static_cast<float *>(dgate)[i] = v;
+        else
+            static_cast<T *>(dgate)[i] = from_f<T>(v);
+    };
+    // the sum over the rows of threads, in a fixed tree; every column's in its first thread row
+    const auto over_rows = [&](float s) {
+        __syncthreads();
+        sh[threadIdx.y][threadIdx.x] = s;
+        __syncthreads();
+        s = sh[threadIdx.x][threadIdx.y];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            s += __shfl_xor_sync(0xffffffffu, s, o);
+        return s;  // of column threadIdx.y, in every thread of its warp
+    };
+    const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.y;
+    const bool writes = threadIdx.x == 0 && col < p.D;
+    if (blockIdx.y < 2 && (blockIdx.y == 0 || !several)) {
+        // rows of `blocks` blocks
+        const float *part = blockIdx.y == 0 ? p.part_pre : p.part_sum;
+        if (blockIdx.y == 0 ? !dpre : !dpost && !dgate)
+            return;
+        float s = 0.f;
+#pragma unroll 8
+        for (int b = threadIdx.y; b < blocks; b += SUM_ROWS)
+            s += c < p.D ? part[static_cast<int64_t>(b) * p.D + c] : 0.f;
+        s = over_rows(s);
+        if (!writes)
+            return;
+        if (blockIdx.y == 0) {
+            dpre[col] = from_f<W>(s);
+            return;
+        }
+        const float u = p.gate ? gate_one<T>(p.gate, p.gate_f32, col) : 1.f;
+        if (dpost)
+            dpost[col] = from_f<W>(p.branch_scale * u * s);
+        if (dgate)
+            put_gate(col, p.branch_scale * (p.post ? to_f(static_cast<const W *>(p.post)[col]) : 1.f) * s);
+        return;
+    }
+    if (blockIdx.y == 1) {
+        // dpost: every lane's gate rows
+        if (!dpost)
+            return;
+        float s = 0.f;
+        for (int64_t l = threadIdx.y; l < p.lanes; l += SUM_ROWS) {
+            const int64_t g0 = p.M * l / p.lanes / p.gate_tokens, g1 = (p.M * (l + 1) / p.lanes - 1) / p.gate_tokens;
+            for (int64_t g = g0; g <= g1 && c < p.D; ++g)
+                s = fmaf(gate_one<T>(p.gate, p.gate_f32, g * p.D + c), p.part_sum[(l + g) * p.D + c], s);
+        }
+        s = over_rows(s);
+        if (writes)
+            dpost[col] = from_f<W>(p.branch_scale * s);
+        return;
+    }
+    if (!dgate || !several)
+        return;
+    const int64_t step = gridDim.y - 2;
+    if (many_lanes(p.lanes, p.gate_rows)) {
+        for (int64_t g = blockIdx.y - 2; g < p.gate_rows; g += step) {
+            const int64_t l0 = lane_of(g * p.gate_tokens), l1 = lane_of((g + 1) * p.gate_tokens - 1);
+            float s = 0.f;
+#pragma unroll 4
+            for (int64_t l = l0 + threadIdx.y; l <= l1; l += SUM_ROWS)
+                s += c < p.D ? p.part_sum[(l + g) * p.D + c] : 0.f;
+            s = over_rows(s);
+            if (writes)
+                put_gate(g * p.D + col, p.branch_scale * (p.post ? to_f(static_cast<const W *>(p.post)[col]) : 1.f) * s);
+        }
+        return;
+    }
+    for (int64_t g = (blockIdx.y - 2) * SUM_ROWS + threadIdx.y; g < p.gate_rows; g += step * SUM_ROWS) {
+        const int64_t l0 = lane_of(g * p.gate_tokens), l1 = lane_of((g + 1) * p.gate_tokens - 1);
+        float s = 0.f;
+        for (int64_t l = l0; l <= l1 && c < p.D; ++l)
+            s += p.part_sum[(l + g) * p.D + c];
+        if (c < p.D)
+            put_gate(g * p.D + c, p.branch_scale * post * s);
+    }
+}
+
+// ---------------------------------------------------------------- launches
+template <class T, class W, int VEC>
+bool launch_block_bwd_regs(const BlockNormBwdParams &p, int grid, cudaStream_t s, cudaError_t *e)
+{
+    const int64_t packs = p.D / VEC;
+    int t;
+    if ((t = threads_for(packs, 8 / VEC)) && t <= 512) {  // eight columns per thread
+        *e = launch_overlapped(k_block_norm_bwd<T, W, VEC, 8 / VEC>, dim3(grid), dim3(t), 0, 1, s, p);
+        return true;
+    }
+    if ((t = threads_for(packs, 16 / VEC)) && t <= 512) {
+        *e = launch_overlapped(k_block_norm_bwd<T, W, VEC, 16 / VEC>, dim3(grid), dim3(t), 0, 1, s, p);
+        return true;
+    }
+    return false;
+}
+
+template <class T, class W, bool PH>
+cudaError_t launch_block_bwd_ring(const BlockNormBwdParams &p, const RingPlan &r, int blocks, cudaStream_t s)
+{
+    static std::atomic<unsigned long long> opted{0};
+    const cudaError_t e = ring_opt_in(k_block_norm_bwd_ring<T, W, PH>, opted, BWD_RING_BUDGET);
+    if (e != cudaSuccess)
+        return e;
+    return launch_overlapped(k_block_norm_bwd_ring<T, W, PH>, dim3(blocks), dim3(r.groups * r.group_threads), r.bytes, 1, s,
+                             p, r);
+}
+
+// Groups of warps in a block of the ring kernel at most.
+int64_t bwd_groups(int64_t M, int64_t D, int elem, int blocks)
+{
+    const int64_t packs = (D + 16 / elem - 1) / (16 / elem) + 1;
+    const int64_t gt = (packs + 32 * RING_NV - 1) / (32 * RING_NV) * 32;
+    int64_t groups = BLOCK_NORM_BWD_THREADS / gt;
+    groups = groups < RING_MAX_GROUPS ? groups : RING_MAX_GROUPS;
+    const int64_t rows = M / blocks;  // a row for each lane
+    groups = groups < rows ? groups : rows;
+    return groups < 1 ? 1 : groups;
+}
+
+template <class T, class W>
+cudaError_t launch_block_bwd_tw(BlockNormBwdParams p, Rows rows, void *dpost, void *dpre, void *dgate, int num_sms,
+                                cudaStream_t s)
+{
+    constexpr int V = 16 / static_cast<int>(sizeof(T));
+    const int inputs = (p.pre ? 2 : 0) + (p.x ? 1 : 0) + (p.dh ? 1 : 0);
+    const bool several = p.gate_rows > 1;
+    int blocks = static_cast<int>(p.M < RMS_BWD_BLOCKS ? p.M : RMS_BWD_BLOCKS);
+    cudaError_t e = cudaSuccess;
+    RingPlan r;
+    if (several && rows == ROWS_PHASED)
+        rows = ROWS_ANY;  // a lane's rows follow one another, so their phases differ
+    const int ring = ring_blocks(p.M, num_sms < BLOCK_NORM_BWD_BLOCKS ? num_sms : BLOCK_NORM_BWD_BLOCKS);
+    if (num_sms >= 8 && use_ring(rows, p.M, p.D) &&
+        plan_ring(&r, rows == ROWS_PHASED, p.D, sizeof(T), param_bytes<W>(p), inputs, BLOCK_NORM_BWD_THREADS,
+                  BWD_RING_BUDGET)) {
+        blocks = ring;
+        const int64_t most = bwd_groups(p.M, p.D, sizeof(T), blocks);
+        if (several && r.groups > most)
+            r.groups = static_cast<int>(most);
+        p.lanes = static_cast<int64_t>(blocks) * r.groups;
+        e = rows == ROWS_PHASED ? launch_block_bwd_ring<T, W, true>(p, r, blocks, s)
+                                : launch_block_bwd_ring<T, W, false>(p, r, blocks, s);
+    } else {
+        p.lanes = blocks;
+        if (!(rows == ROWS_VEC ? launch_block_bwd_regs<T, W, V>(p, blocks, s, &e)
+                               : launch_block_bwd_regs<T, W, 1>(p, blocks, s, &e)))
+            e = launch_overlapped(k_block_norm_bwd_long<T, W>, dim3(blocks), dim3(1024), 0, 1, s, p);
+    }
+    if (e != cudaSuccess || (!dpost && !dpre && !dgate))
+        return e;
+    int64_t jobs = 2;
+    if (several && dgate) {
+        const int64_t gate_blocks = many_lanes(p.lanes, p.gate_rows) ? p.gate_rows : (p.gate_rows + SUM_ROWS - 1) / SUM_ROWS;
+        jobs += gate_blocks < 65533 ? gate_blocks : 65533;
+    }
+    return launch_overlapped(k_block_norm_sums<T, W>, dim3(static_cast<unsigned>((p.D + 31) / 32), static_cast<unsigned>(jobs)),
+                             dim3(32, SUM_ROWS), 0, 1, s, p, blocks, static_cast<W *>(dpost), static_cast<W *>(dpre), dgate);
+}
+
+}  // namespace
+
+int64_t block_norm_bwd_lanes(int64_t M, int64_t D, int dtype)
+{
+    const int64_t ring = BLOCK_NORM_BWD_BLOCKS * bwd_groups(M, D, dtype == 2 ? 4 : 2, 1), lanes = M < ring ? M : ring;
+    const int64_t blocks = M < RMS_BWD_BLOCKS ? (M + 7) / 8 * 8 : RMS_BWD_BLOCKS;  // (304 is a multiple of eight)
+    return lanes > blocks ? lanes : blocks;
+}
+
+cudaError_t launch_block_norm_bwd(const BlockNormBwdParams &p, void *dpost, void *dpre, void *dgate, int dtype, int wdtype,
+                                  int num_sms, cudaStream_t s)
+{
+    const int64_t v = dtype == 2 ? 4 : 8;
+    const bool based = al16(p.dy) && al16(p.x) && al16(p.h) && al16(p.post) && al16(p.pre) && al16(p.gate) && al16(p.dh) &&
+                       al16(p.dx) && al16(p.dres) && al16(p.part_pre) && al16(p.part_sum);
+    const Rows rows = !based ? ROWS_ANY : p.D % v == 0 ? ROWS_VEC : p.D >= PHASED_MIN_D ? ROWS_PHASED : ROWS_ANY;
+    if (dtype == 0)
+        return wdtype == 0 ? launch_block_bwd_tw<__nv_bfloat16, __nv_bfloat16>(p, rows, dpost, dpre, dgate, num_sms, s)
+                           : launch_block_bwd_tw<__nv_bfloat16, float>(p, rows, dpost, dpre, dgate, num_sms, s);
+    if (dtype == 1)
+        return wdtype == 1 ? launch_block_bwd_tw<__half, __half>(p, rows, dpost, dpre, dgate, num_sms, s)
+                           : launch_block_bwd_tw<__half, float>(p, rows, dpost, dpre, dgate, num_sms, s);
+    return launch_block_bwd_tw<float, float>(p, rows, dpost, dpre, dgate, num_sms, s);
+}
+
+}  // namespace lf

@@ -119,6 +119,40 @@ int rms_norm_bwd_blocks(int64_t M);
 cudaError_t launch_rms_norm_bwd(const NormBwdParams &p, void *dweight, int dtype, int wdtype, int num_sms,
                                 cudaStream_t s);
 
+// The norms after and before a block with its gate and scales (block_norm.cu).  dtype /
+// wdtype as above; post, pre and gate may be null.  gate: [M / gate_tokens, D] of dtype or
+// (gate_f32) fp32; gate_tokens is M without a gate.  ldx, ldr: row pitches in elements; h
+// and y are [M,D].
+struct BlockNormParams {
+    const void *x, *residual, *post, *pre, *gate;
+    void *h, *y;   // y null without pre
+    float *scale;  // [M], the e4m3 form only
+    int64_t M, D, ldx, ldr, gate_tokens;
+    float eps, branch_scale, residual_scale;
+    int gate_f32;
+    WaitLimit limit;
+};
+cudaError_t launch_block_norm(const BlockNormParams &p, int dtype, int wdtype, bool fp8, int num_sms, cudaStream_t s);
+
+// Its gradient (block_norm_grads.cu).  dy and h are read with pre, x with post or a gate (null otherwise), dh may
+// be null with pre.  part_pre: fp32 [block_norm_bwd_lanes][D] or null with dpre null;
+// part_sum: fp32 [block_norm_bwd_lanes + gate_rows][D] or null with dpost and dgate null.
+// dpost and dpre have wdtype, dgate the gate's type.
+struct BlockNormBwdParams {
+    const void *dy, *x, *h, *post, *pre, *gate, *dh;
+    void *dx, *dres;
+    float *part_pre, *part_sum;
+    int64_t M, D, gate_tokens, gate_rows;  // gate_rows: M / gate_tokens, or 0 without a gate
+    int64_t lanes;                         // set by launch_block_norm_bwd
+    float eps, branch_scale, residual_scale;
+    int gate_f32;
+    WaitLimit limit;
+};
+constexpr int BLOCK_NORM_BWD_BLOCKS = 152;  // of the ring kernel at most
+int64_t block_norm_bwd_lanes(int64_t M, int64_t D, int dtype);
+cudaError_t launch_block_norm_bwd(const BlockNormBwdParams &p, void *dpost, void *dpre, void *dgate, int dtype, int wdtype,
+                                  int num_sms, cudaStream_t s);
+
 // Gated projections on CTA pairs (gated_ffn.cu): out = act(x Wg^T) * (x Wu^T).
 // g: M, N = F, K, block counts (256-row M blocks, N blocks of cols, 128-byte
 // K blocks), num_tiles, band_m, err, timeout_ns, inject.
