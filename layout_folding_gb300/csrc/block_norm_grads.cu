@@ -34,21 +34,24 @@ struct RowSums {
         *reinterpret_cast<float4 *>(sh) = make_float4(v[0], v[1], v[2], v[3]);
         *reinterpret_cast<float2 *>(sh + 4) = make_float2(v[4], v[5]);
     }
-    __device__ __forceinline__ void add_all(const float *sh, int warps)
+    // sh: [CTA of the cluster][warp][8]
+    template <int WARPS>
+    __device__ __forceinline__ void add_all(const float (*sh)[WARPS][8], int ctas, int first_warp, int warps)
     {
 #pragma unroll
         for (int i = 0; i < 6; ++i)
             v[i] = 0.f;
-        for (int w = 0; w < warps; ++w) {
-            const float4 a = *reinterpret_cast<const float4 *>(sh + 8 * w);
-            const float2 b = *reinterpret_cast<const float2 *>(sh + 8 * w + 4);
-            v[0] += a.x;
-            v[1] += a.y;
-            v[2] += a.z;
-            v[3] += a.w;
-            v[4] += b.x;
-            v[5] += b.y;
-        }
+        for (int c = 0; c < ctas; ++c)
+            for (int w = first_warp; w < first_warp + warps; ++w) {
+                const float4 a = *reinterpret_cast<const float4 *>(sh[c][w]);
+                const float2 b = *reinterpret_cast<const float2 *>(sh[c][w] + 4);
+                v[0] += a.x;
+                v[1] += a.y;
+                v[2] += a.z;
+                v[3] += a.w;
+                v[4] += b.x;
+                v[5] += b.y;
+            }
     }
 };
 
@@ -65,35 +68,21 @@ struct RowFactors {
     }
 };
 
-// VEC columns of a row; what the call has none of is 0, pre and the factors are 1.
+// VEC columns of a row.  What the call has none of is 0 (pre too, where it multiplies a
+// dy that is 0), the factors are 1.
 template <class T, class W, int VEC>
 struct Columns {
     static constexpr int N = PAIRS<VEC>;
     float2 dy[N], h[N], x[N], dh[N], pre[N], cf[N];
-    // at(k): the address of the columns in input k (h, dy, x, dh), w: that of pre's
+    // at(k): the columns in input k (h, dy, x, dh)
     template <class At>
-    __device__ __forceinline__ void load(const BlockNormBwdParams &p, const At &at, const W *w)
+    __device__ __forceinline__ void load(const At &at, const Pack<W, VEC> &w)
     {
-        const auto get = [&](bool have, int k, float2 (&f)[N]) {
-            if (have) {
-                pairs_of<T, VEC>(at(k), f);
-            } else {
-#pragma unroll
-                for (int i = 0; i < N; ++i)
-                    f[i] = both(0.f);
-            }
-        };
-        get(p.pre, 0, h);
-        get(p.pre, 1, dy);
-        get(p.x, 2, x);
-        get(p.dh, 3, dh);
-        if (p.pre) {
-            pairs_of<W, VEC>(load_pack<W, VEC>(w), pre);
-        } else {
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                pre[i] = both(1.f);
-        }
+        pairs_of<T, VEC>(at(0), h);
+        pairs_of<T, VEC>(at(1), dy);
+        pairs_of<T, VEC>(at(2), x);
+        pairs_of<T, VEC>(at(3), dh);
+        pairs_of<W, VEC>(w, pre);
     }
     __device__ __forceinline__ void add_to(const BlockNormBwdParams &p, float2 (&s)[6]) const
     {
@@ -102,13 +91,11 @@ struct Columns {
             const float2 g = mul2(dy[i], pre[i]);
             s[0] = fma2(h[i], h[i], s[0]);
             s[1] = fma2(g, h[i], s[1]);
-            if (p.post) {
-                const float2 c = mul2(x[i], cf[i]);
-                s[2] = fma2(x[i], x[i], s[2]);
-                s[3] = fma2(g, c, s[3]);
-                s[4] = fma2(h[i], c, s[4]);
-                s[5] = fma2(dh[i], c, s[5]);
-            }
+            const float2 c = mul2(x[i], cf[i]);  // (not used without post)
+            s[2] = fma2(x[i], x[i], s[2]);
+            s[3] = fma2(g, c, s[3]);
+            s[4] = fma2(h[i], c, s[4]);
+            s[5] = fma2(dh[i], c, s[5]);
         }
     }
     // dresidual, dx, and the two sums of the parameters' gradients
@@ -118,7 +105,7 @@ struct Columns {
         float2 o[N], q[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const float2 at_h = p.pre ? fma2(both(f.r2), fma2(h[i], both(-f.m2), mul2(dy[i], pre[i])), dh[i]) : dh[i];
+            const float2 at_h = fma2(both(f.r2), fma2(h[i], both(-f.m2), mul2(dy[i], pre[i])), dh[i]);
             o[i] = mul2(at_h, both(p.residual_scale));
             q[i] = mul2(mul2(at_h, both(p.branch_scale)), cf[i]);
             if (p.post)
@@ -130,6 +117,34 @@ struct Columns {
         from_pairs<T, VEC>(dx, q);
     }
 };
+
+// A pack, or zeros where there is nothing to read.
+template <class T, int VEC>
+__device__ __forceinline__ Pack<T, VEC> pack_or_zeros(const T *p, int64_t at)
+{
+    if (p)
+        return load_pack<T, VEC>(p + at);
+    Pack<T, VEC> z;
+    float f[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+        f[i] = 0.f;
+    z.set(f);
+    return z;
+}
+
+// VEC elements at a shared-memory address, 16 bytes a load.
+template <class T, int VEC>
+__device__ __forceinline__ Pack<T, VEC> lds_pack(uint32_t at)
+{
+    Pack<T, VEC> p;
+#pragma unroll
+    for (int i = 0; i < Pack<T, VEC>::WORDS; i += 4)
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(p.u[i]), "=r"(p.u[i + 1]), "=r"(p.u[i + 2]), "=r"(p.u[i + 3])
+                     : "r"(at + 4u * i));
+    return p;
+}
 
 template <int N>
 __device__ __forceinline__ void clear(float2 (&f)[N])
@@ -167,7 +182,7 @@ __global__ void __launch_bounds__(512) k_block_norm_bwd(const __grid_constant__ 
     wait_previous_kernel();
     let_next_kernel_start();
     constexpr int N = PAIRS<VEC>;
-    __shared__ __align__(16) float sh[2][MAX_WARPS * 8];
+    __shared__ __align__(16) float sh[2][1][MAX_WARPS][8];
     const int packs = static_cast<int>(p.D / VEC);
     const T *const in[4] = {static_cast<const T *>(p.h), static_cast<const T *>(p.dy), static_cast<const T *>(p.x),
                             static_cast<const T *>(p.dh)};
@@ -187,12 +202,12 @@ __global__ void __launch_bounds__(512) k_block_norm_bwd(const __grid_constant__ 
             const int c = threadIdx.x + j * blockDim.x;
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                if (c < packs && in[k])
-                    q[j][k] = load_pack<T, VEC>(in[k] + o + static_cast<int64_t>(c) * VEC);
+                if (c < packs)
+                    q[j][k] = pack_or_zeros<T, VEC>(in[k], o + static_cast<int64_t>(c) * VEC);
         }
         const auto columns = [&](int j, int64_t at) {
             Columns<T, W, VEC> v;
-            v.load(p, [&](int k) { return q[j][k]; }, static_cast<const W *>(p.pre) + at);
+            v.load([&](int k) { return q[j][k]; }, pack_or_zeros<W, VEC>(static_cast<const W *>(p.pre), at));
             column_factors<T, W, VEC>(p, gate_row, at, v.cf);
             return v;
         };
@@ -206,9 +221,9 @@ __global__ void __launch_bounds__(512) k_block_norm_bwd(const __grid_constant__ 
         }
         RowSums s(s2);
         if ((threadIdx.x & 31) == 0)
-            s.put(&sh[buf][(threadIdx.x >> 5) * 8]);
+            s.put(sh[buf][0][threadIdx.x >> 5]);
         __syncthreads();
-        s.add_all(sh[buf], blockDim.x >> 5);
+        s.add_all(sh[buf], 1, 0, blockDim.x >> 5);
         const RowFactors f(p, s);
         const bool ends = p.part_sum && gate_row_ends(p, rows, row);
         float *seg = ends ? p.part_sum + (blockIdx.x + row / p.gate_tokens) * p.D : nullptr;
@@ -253,14 +268,15 @@ __global__ void __launch_bounds__(1024) k_block_norm_bwd_long(const __grid_const
 {
     wait_previous_kernel();
     let_next_kernel_start();
-    __shared__ __align__(16) float sh[2][MAX_WARPS * 8];
+    __shared__ __align__(16) float sh[2][1][MAX_WARPS][8];
     const T *const in[4] = {static_cast<const T *>(p.h), static_cast<const T *>(p.dy), static_cast<const T *>(p.x),
                             static_cast<const T *>(p.dh)};
     int buf = 0;
     const LaneRows rows(p, blockIdx.x, blockIdx.x, gridDim.x);
     const auto columns = [&](int64_t row, int64_t c) {
         Columns<T, W, 1> v;
-        v.load(p, [&](int k) { return load_pack<T, 1>(in[k] + row * p.D + c); }, static_cast<const W *>(p.pre) + c);
+        v.load([&](int k) { return pack_or_zeros<T, 1>(in[k], row * p.D + c); },
+               pack_or_zeros<W, 1>(static_cast<const W *>(p.pre), c));
         column_factors<T, W, 1>(p, p.gate ? row / p.gate_tokens * p.D : 0, c, v.cf);
         return v;
     };
@@ -272,9 +288,9 @@ __global__ void __launch_bounds__(1024) k_block_norm_bwd_long(const __grid_const
             columns(row, c).add_to(p, s2);
         RowSums s(s2);
         if ((threadIdx.x & 31) == 0)
-            s.put(&sh[buf][(threadIdx.x >> 5) * 8]);
+            s.put(sh[buf][0][threadIdx.x >> 5]);
         __syncthreads();
-        s.add_all(sh[buf], blockDim.x >> 5);
+        s.add_all(sh[buf], 1, 0, blockDim.x >> 5);
         const RowFactors f(p, s);
         float *pre_sum = p.part_pre ? p.part_pre + static_cast<int64_t>(blockIdx.x) * p.D : nullptr;
         float *sum = p.part_sum ? p.part_sum + (blockIdx.x + (several ? row / p.gate_tokens : 0)) * p.D : nullptr;
@@ -294,36 +310,130 @@ __global__ void __launch_bounds__(1024) k_block_norm_bwd_long(const __grid_const
     }
 }
 
-constexpr int BLOCK_NORM_BWD_THREADS = 384;
-constexpr int BWD_RING_BUDGET = RING_BUDGET - 1024;  // the warps' sums take 768 bytes beside RingSync
+// ---------------------------------------------------------------- many rows
+// Rings of bulk copies as in rms_norm_common.cuh, with three differences.
+//
+// A row stays in its slot until it is done: with two sums for each column there are no
+// registers to keep it in, so it is read from shared memory twice.  Its warps count
+// themselves off on an mbarrier when they have, and the slot is filled again.
+//
+// A row may be shared by the two CTAs of a cluster, each with half of its columns: its slots
+// are half as large, so an SM has twice as many rows (and groups of warps) at hand, and rows
+// twice as long fit.  Every warp stores its six sums in both CTAs, in a place of its own,
+// and arrives on an mbarrier of the group there; all are added in the same order everywhere.
+//
+// What the call has none of is read as 16 bytes of zeros (factors of one), so that a pack's
+// loads stand in one straight line.
+constexpr int BWD_THREADS = 384;  // 168 registers a thread, 64 of them sums
+constexpr int BWD_WARPS = BWD_THREADS / 32;
+constexpr int BWD_CLUSTER = 2;
+constexpr int BWD_BUDGET = 223 * 1024;  // dynamic shared memory; BwdSync takes 3.6 KB more
 
-// In rings: a slot has the row of h, dy, x and dh (those that the call has, in this order).
-// The row stays in its slot until it is done -- with two sums for each column there are no
-// registers to keep it in -- so it is read from shared memory twice, and the slot is filled
-// again after a second barrier.
+struct BwdPlan {
+    int cluster, group_threads, groups, slots, packs;  // packs of a CTA's share of a row
+    uint32_t factor_off, factor_bytes;                 // factors: of the block, or of each group
+    uint32_t row_bytes, slot_off, slot_bytes, bytes;
+};
+
+struct BwdSync {
+    alignas(16) float sums[2][BWD_CLUSTER][BWD_WARPS][8];
+    alignas(16) float constants[2][8];  // zeros, ones
+    alignas(8) unsigned long long full[BWD_WARPS][RING_MAX_SLOTS], empty[BWD_WARPS][RING_MAX_SLOTS], landed[BWD_WARPS][2];
+};
+
+// ring_wait for what another CTA of the cluster wrote.
+__device__ __forceinline__ bool sums_wait(uint32_t bar, uint32_t parity, const WaitLimit &lim)
+{
+    const auto there = [&] {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        return ok != 0;
+    };
+    if (there())
+        return true;
+    const uint64_t t0 = global_timer_ns();
+    while (!there()) {
+        if (global_timer_ns() - t0 > lim.timeout_ns) {
+            atomicCAS(lim.err, 0, 0x108);
+            return false;
+        }
+    }
+    return true;
+}
+// Four floats into any CTA's shared memory (a shared::cluster address).
+__device__ __forceinline__ void st_cluster_f32x4(uint32_t addr, float4 v)
+{
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+                 : "memory");
+}
+
 template <class T, class W, bool PH>
-__global__ void __launch_bounds__(BLOCK_NORM_BWD_THREADS)
-    k_block_norm_bwd_ring(const __grid_constant__ BlockNormBwdParams p, const RingPlan r)
+__global__ void __launch_bounds__(BWD_THREADS)
+    k_block_norm_bwd_ring(const __grid_constant__ BlockNormBwdParams p, const BwdPlan r)
 {
     constexpr int VEC = 16 / static_cast<int>(sizeof(T));
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ RingSync sy;
-    __shared__ __align__(16) float red[2][BLOCK_NORM_BWD_THREADS / 32][8];
+    __shared__ BwdSync sy;
     const int group = threadIdx.x / r.group_threads, t = threadIdx.x % r.group_threads;
-    const int warps = r.group_threads >> 5, first_warp = group * warps;
-    const RowSpan<T, PH> span(p.M, p.D);
-    const int packs = span.packs;
-    const int64_t lane = static_cast<int64_t>(blockIdx.x) * r.groups + group;
+    const int warps = r.group_threads >> 5, first_warp = group * warps, warp = threadIdx.x >> 5, lane_id = threadIdx.x & 31;
+    const uint32_t clusters = PH ? 1u : r.cluster, rank = PH ? 0u : blockIdx.x % clusters;
+    const int unit = static_cast<int>(blockIdx.x / clusters), units = static_cast<int>(gridDim.x / clusters);
+    const RowSpan<T, PH> span(p.M, p.D);  // (phase: of a unit that is one block)
+    const int packs = min(r.packs, span.packs - static_cast<int>(rank) * r.packs);
+    const int64_t col0 = static_cast<int64_t>(rank) * r.packs * VEC - span.phase;  // of the share's first granule
+    const int64_t lane = static_cast<int64_t>(unit) * r.groups + group;
     // neighbouring rows go to neighbouring SMs
-    const LaneRows rows(p, lane, static_cast<int64_t>(group) * gridDim.x + blockIdx.x,
-                        static_cast<int64_t>(gridDim.x) * r.groups);
-    Ring ring(r, smem, sy, group);
+    const LaneRows rows(p, lane, static_cast<int64_t>(group) * units + unit, static_cast<int64_t>(units) * r.groups);
     const T *in[4] = {static_cast<const T *>(p.h), static_cast<const T *>(p.dy), static_cast<const T *>(p.x),
                       static_cast<const T *>(p.dh)};
-    const int at_x = p.pre ? 2 : 0, at_dh = at_x + (p.x ? 1 : 0);
-    const auto fill = [&](int slot, int64_t row) { ring.fill_rows(span, slot, row, in, p.D); };
-    if (t == 0)
-        ring.init();
+    const uint32_t slots = smem_u32(smem + r.slot_off) + static_cast<uint32_t>(group) * r.slots * r.slot_bytes;
+    const uint32_t full = smem_u32(sy.full[group]), empty = smem_u32(sy.empty[group]), landed = smem_u32(sy.landed[group]);
+    const auto fill = [&](int slot, int64_t row) {
+        const uint32_t bar = full + 8u * slot;
+        uint32_t n = 16u * packs, inputs = 0;
+        const int64_t at = row * p.D + col0;
+        if (PH && at + static_cast<int64_t>(packs) * VEC > p.M * p.D) {
+            // the granule that reaches past the last row's end: its elements one by one
+            n -= 16u;
+            T *s = reinterpret_cast<T *>(smem + r.slot_off + (static_cast<size_t>(group) * r.slots + slot) * r.slot_bytes);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (in[k]) {
+                    for (int64_t e = at + (packs - 1) * VEC; e < p.M * p.D; ++e)
+                        s[inputs * (r.row_bytes / sizeof(T)) + (e - at)] = in[k][e];
+                    ++inputs;
+                }
+            inputs = 0;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            inputs += in[k] ? 1u : 0u;
+        mbar_arrive_expect_tx(bar, n * inputs);
+        uint32_t dst = slots + slot * r.slot_bytes;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (in[k]) {
+                if (n)
+                    bulk_load_g2s(dst, in[k] + at, n, bar);
+                dst += r.row_bytes;
+            }
+    };
+    if (t == 0) {
+        for (int i = 0; i < r.slots; ++i) {
+            mbar_init(full + 8u * i, 1);
+            mbar_init(empty + 8u * i, warps);
+        }
+        mbar_init(landed, warps * clusters);
+        mbar_init(landed + 8u, warps * clusters);
+        fence_mbar_init();
+    }
+    if (threadIdx.x < 16)
+        sy.constants[threadIdx.x >> 3][threadIdx.x & 7] = threadIdx.x >> 3 ? 1.f : 0.f;
     wait_previous_kernel();
     let_next_kernel_start();
     if (t == 0) {
@@ -332,7 +442,38 @@ __global__ void __launch_bounds__(BLOCK_NORM_BWD_THREADS)
              i < r.slots && rows.first + i * rows.step < rows.end; ++i)
             fill(i, rows.first + i * rows.step);
     }
-    const RingParams<T, W, PH, BlockNormBwdParams> w(smem, r, span, p);
+    // pre, and post times a gate of one row (a gate of several rows: post times the group's)
+    const bool several = !PH && p.gate_rows > 1;
+    const T *const gate_t = several || !p.gate ? nullptr : static_cast<const T *>(p.gate);
+    {
+        W *const s_pre = reinterpret_cast<W *>(smem);
+        float *const s_f = reinterpret_cast<float *>(smem + r.factor_off);
+        const W *pre = static_cast<const W *>(p.pre), *post = static_cast<const W *>(p.post);
+        const bool factors = !several && (post || gate_t);
+#pragma unroll 4
+        for (int i = threadIdx.x; i < packs * VEC; i += blockDim.x) {
+            const int64_t k = i + col0;
+            const bool inside = !PH || (k >= 0 && k < p.D);
+            if (pre)
+                s_pre[i] = inside ? pre[k] : from_f<W>(0.f);
+            if (factors) {
+                float f = inside && post ? to_f(post[k]) : 1.f;
+                if (inside && gate_t)
+                    f *= gate_one<T>(p.gate, p.gate_f32, k);
+                s_f[i] = inside ? f : 0.f;
+            }
+        }
+    }
+    const uint32_t zeros = smem_u32(sy.constants[0]), ones = smem_u32(sy.constants[1]);
+    const uint32_t pre = p.pre ? smem_u32(smem) : zeros, pre_apart = p.pre ? VEC * sizeof(W) : 0u;
+    const bool has_factor = p.post || p.gate;
+    float *const group_factor =
+        reinterpret_cast<float *>(smem + r.factor_off + (several ? static_cast<uint32_t>(group) * r.factor_bytes : 0u));
+    const uint32_t factor = has_factor ? smem_u32(group_factor) : ones, factor_apart = has_factor ? VEC * sizeof(float) : 0u;
+    if (clusters > 1)
+        cluster_sync();  // both CTAs' barriers exist before any sum is sent
+    else
+        __syncthreads();
     float2 a_pre[RING_NV][VEC / 2], a_sum[RING_NV][VEC / 2];
 #pragma unroll
     for (int j = 0; j < RING_NV; ++j) {
@@ -340,19 +481,47 @@ __global__ void __launch_bounds__(BLOCK_NORM_BWD_THREADS)
         clear(a_sum[j]);
     }
     bool ok = true;
-    int buf = 0;
-    for (int64_t row = rows.first; row < rows.end; row += rows.step, buf ^= 1) {
-        ok = ring_wait(ring.full_s + 8u * ring.slot, ring.phase, p.limit);
+    int slot = 0;
+    uint32_t phase = 0, count = 0;
+    int64_t gate_row = -1;
+    for (int64_t row = rows.first; row < rows.end; row += rows.step, ++count) {
+        if (several && row / p.gate_tokens != gate_row) {
+            // the factors of the next gate row; every thread reads its own columns' only
+            gate_row = row / p.gate_tokens;
+#pragma unroll
+            for (int j = 0; j < RING_NV; ++j) {
+                const int c = t + j * r.group_threads;
+                if (c < packs) {
+                    float2 f[VEC / 2];
+                    column_factors<T, W, VEC>(p, gate_row * p.D, col0 + c * VEC, f);
+                    Pack<float, VEC> v;
+                    set2<float, VEC>(v, f);
+                    v.store(group_factor + c * VEC);
+                }
+            }
+        }
+        ok = ok && ring_wait(full + 8u * slot, phase, p.limit);
+        if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+        }
+        // an input's bytes in the slot, and how far apart its packs are
+        uint32_t base[4], apart[4], inputs = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            base[k] = in[k] ? slots + slot * r.slot_bytes + inputs * r.row_bytes : zeros;
+            apart[k] = in[k] ? 16u : 0u;
+            inputs += in[k] ? 1u : 0u;
+        }
         const auto columns = [&](int c) {
             Columns<T, W, VEC> v;
             const auto at = [&](int k) {
-                const int i = k < 2 ? k : k == 2 ? at_x : at_dh;
-                Pack<T, VEC> q = load_pack<T, VEC>(reinterpret_cast<const T *>(ring.input(i)) + c * VEC);
+                Pack<T, VEC> q = lds_pack<T, VEC>(base[k] + c * apart[k]);
                 span.mask(q, c);
                 return q;
             };
-            v.load(p, at, w.pre + c * VEC);
-            w.factors(p, span, row, c, v.cf);
+            v.load(at, lds_pack<W, VEC>(pre + c * pre_apart));
+            get2<float, VEC>(lds_pack<float, VEC>(factor + c * factor_apart), v.cf);
             return v;
         };
         float2 s2[6];
@@ -364,47 +533,68 @@ __global__ void __launch_bounds__(BLOCK_NORM_BWD_THREADS)
                 columns(c).add_to(p, s2);
         }
         RowSums s(s2);
-        ok = __all_sync(0xffffffffu, ok);
-        if ((t & 31) == 0) {
-            s.put(red[buf][threadIdx.x >> 5]);
-            sy.failed[buf][threadIdx.x >> 5] = ok ? 0 : 1;
+        const uint32_t buf = count & 1u, bar = landed + 8u * buf;
+        if (clusters == 1) {
+            if (lane_id == 0) {
+                s.put(sy.sums[buf][0][warp]);
+                mbar_arrive(bar);
+            }
+        } else if (static_cast<uint32_t>(lane_id) < clusters) {
+            const uint32_t to = mapa_shared(smem_u32(sy.sums[buf][rank][warp]), lane_id);
+            st_cluster_f32x4(to, make_float4(s.v[0], s.v[1], s.v[2], s.v[3]));
+            st_cluster_f32x4(to + 16u, make_float4(s.v[4], s.v[5], 0.f, 0.f));
+            mbar_arrive_cluster(mapa_shared(bar, lane_id));
         }
-        group_barrier(1 + group, r.group_threads);
-        s.add_all(red[buf][first_warp], warps);
-        for (int i = 0; i < warps; ++i)
-            ok = ok && !sy.failed[buf][first_warp + i];
-        if (!ok)
+        ok = sums_wait(bar, (count >> 1) & 1u, p.limit);
+        if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
             break;
+        }
+        s.add_all(sy.sums[buf], clusters, first_warp, warps);
         const RowFactors f(p, s);
         const bool ends = p.part_sum && gate_row_ends(p, rows, row);
-        float *seg = ends ? p.part_sum + (lane + row / p.gate_tokens) * p.D : nullptr;
+        float *seg = ends ? p.part_sum + (lane + row / p.gate_tokens) * p.D + col0 : nullptr;
 #pragma unroll
         for (int j = 0; j < RING_NV; ++j) {
             const int c = t + j * r.group_threads;
             if (c < packs) {
                 Pack<T, VEC> dres, dx;
                 columns(c).finish(p, f, dres, dx, a_pre[j], a_sum[j]);
-                span.store(static_cast<T *>(p.dres), row, c, dres);
-                span.store(static_cast<T *>(p.dx), row, c, dx);
+                if constexpr (PH) {
+                    span.store(static_cast<T *>(p.dres), row, c, dres);
+                    span.store(static_cast<T *>(p.dx), row, c, dx);
+                } else {
+                    const int64_t at = row * p.D + col0 + c * VEC;
+                    dres.store(static_cast<T *>(p.dres) + at);
+                    dx.store(static_cast<T *>(p.dx) + at);
+                }
                 if (ends) {  // (not with phased rows)
                     Pack<float, VEC> a;
-                    from_pairs<float, VEC>(a, a_sum[j]);
+                    set2<float, VEC>(a, a_sum[j]);
                     a.store(seg + c * VEC);
                     clear(a_sum[j]);
                 }
             }
         }
-        group_barrier(1 + group, r.group_threads);
-        if (t == 0 && row + r.slots * rows.step < rows.end)
-            fill(ring.slot, row + r.slots * rows.step);  // every thread of the group has read the slot
-        ring.advance();
+        __syncwarp();
+        if (lane_id == 0)
+            mbar_arrive(empty + 8u * slot);
+        if (t == 0 && row + r.slots * rows.step < rows.end) {
+            ok = ring_wait(empty + 8u * slot, phase, p.limit, 0x101);
+            if (ok)
+                fill(slot, row + r.slots * rows.step);
+        }
+        if (++slot == r.slots) {
+            slot = 0;
+            phase ^= 1u;
+        }
     }
     if (!ok) {  // copies of this group may still be in flight: give them time to land
         const uint64_t t0 = global_timer_ns();
         while (global_timer_ns() - t0 < RING_SETTLE_NS) {
         }
     }
-    // the rings are idle: the groups' sums are added there in turn, and written as the block's row
+    // the rings are idle: the groups' sums are added there in turn, and written as the unit's row
     float *sums = reinterpret_cast<float *>(smem + r.slot_off);
     const auto merge = [&](const float2 (&acc)[RING_NV][VEC / 2], float *out) {
         for (int g = 0; g < r.groups; ++g) {
@@ -416,7 +606,7 @@ __global__ void __launch_bounds__(BLOCK_NORM_BWD_THREADS)
                 const int c = t + j * r.group_threads;
                 if (c < packs) {
                     Pack<float, VEC> a;
-                    from_pairs<float, VEC>(a, acc[j]);
+                    set2<float, VEC>(a, acc[j]);
                     if (g > 0)
                         a.add(load_pack<float, VEC>(sums + c * VEC));
                     a.store(sums + c * VEC);
@@ -424,13 +614,17 @@ __global__ void __launch_bounds__(BLOCK_NORM_BWD_THREADS)
             }
         }
         __syncthreads();
-        for (int c = threadIdx.x; c < p.D; c += blockDim.x)
-            out[static_cast<int64_t>(blockIdx.x) * p.D + c] = sums[span.phase + c];
+        const int64_t to = static_cast<int64_t>(unit) * p.D + col0;
+        for (int c = threadIdx.x; c < packs * VEC; c += blockDim.x)
+            if (!PH || (c + col0 >= 0 && c + col0 < p.D))
+                out[to + c] = sums[c];
     };
     if (p.part_pre)
         merge(a_pre, p.part_pre);
     if (p.part_sum && p.gate_rows <= 1)
         merge(a_sum, p.part_sum);
+    if (clusters > 1)
+        cluster_sync();  // no CTA leaves while sums may still be sent to it
 }
 
 // The parameters' gradients from their sums.  A block has 32 columns and 32 rows of
@@ -552,26 +746,76 @@ bool launch_block_bwd_regs(const BlockNormBwdParams &p, int grid, cudaStream_t s
 }
 
 template <class T, class W, bool PH>
-cudaError_t launch_block_bwd_ring(const BlockNormBwdParams &p, const RingPlan &r, int blocks, cudaStream_t s)
+cudaError_t launch_block_bwd_ring(const BlockNormBwdParams &p, const BwdPlan &r, int units, cudaStream_t s)
 {
     static std::atomic<unsigned long long> opted{0};
-    const cudaError_t e = ring_opt_in(k_block_norm_bwd_ring<T, W, PH>, opted, BWD_RING_BUDGET);
+    const cudaError_t e = ring_opt_in(k_block_norm_bwd_ring<T, W, PH>, opted, BWD_BUDGET);
     if (e != cudaSuccess)
         return e;
-    return launch_overlapped(k_block_norm_bwd_ring<T, W, PH>, dim3(blocks), dim3(r.groups * r.group_threads), r.bytes, 1, s,
-                             p, r);
+    return launch_overlapped(k_block_norm_bwd_ring<T, W, PH>, dim3(units * r.cluster), dim3(r.groups * r.group_threads),
+                             r.bytes, r.cluster, s, p, r);
 }
 
-// Groups of warps in a block of the ring kernel at most.
-int64_t bwd_groups(int64_t M, int64_t D, int elem, int blocks)
+// Threads of a group for rows of D elements shared by `cluster` CTAs.
+int64_t bwd_group_threads(int64_t D, int elem, bool phased, int cluster, int64_t *packs)
 {
-    const int64_t packs = (D + 16 / elem - 1) / (16 / elem) + 1;
-    const int64_t gt = (packs + 32 * RING_NV - 1) / (32 * RING_NV) * 32;
-    int64_t groups = BLOCK_NORM_BWD_THREADS / gt;
-    groups = groups < RING_MAX_GROUPS ? groups : RING_MAX_GROUPS;
-    const int64_t rows = M / blocks;  // a row for each lane
-    groups = groups < rows ? groups : rows;
-    return groups < 1 ? 1 : groups;
+    const int64_t vec = 16 / elem, all = phased ? (D + 2 * vec - 2) / vec : D / vec;
+    *packs = all < cluster ? 1 : (all + cluster - 1) / cluster;
+    return (*packs + 32 * RING_NV - 1) / (32 * RING_NV) * 32;
+}
+// A plan with at most max_groups groups and two slots for each, or false where the rows are
+// too long for it.  groups_apart: each group has factors of its own.
+bool plan_bwd(BwdPlan *r, bool phased, int64_t D, int elem, int wbytes, bool factors, bool groups_apart, int inputs,
+              int cluster, int64_t max_groups)
+{
+    int64_t packs;
+    const int64_t gt = bwd_group_threads(D, elem, phased, cluster, &packs), vec = 16 / elem;
+    if (gt > BWD_THREADS || (cluster > 1 && packs * (cluster - 1) * vec >= D))
+        return false;
+    const int64_t pre = (packs * vec * wbytes + 127) / 128 * 128, f = factors ? packs * vec * 4 : 0;
+    const int64_t slot = packs * 16 * inputs;
+    int64_t groups = BWD_THREADS / gt;
+    groups = groups < max_groups ? groups : max_groups;
+    for (; groups > 0; --groups) {
+        const int64_t fixed = (pre + f * (groups_apart ? groups : 1) + 127) / 128 * 128;
+        int64_t n = (BWD_BUDGET - fixed) / (slot * groups);
+        n = n < RING_MAX_SLOTS ? n : RING_MAX_SLOTS;
+        if (n < 2)
+            continue;
+        r->cluster = cluster;
+        r->group_threads = static_cast<int>(gt);
+        r->groups = static_cast<int>(groups);
+        r->slots = static_cast<int>(n);
+        r->packs = static_cast<int>(packs);
+        r->factor_off = static_cast<uint32_t>(pre);
+        r->factor_bytes = static_cast<uint32_t>(f);
+        r->row_bytes = static_cast<uint32_t>(packs * 16);
+        r->slot_off = static_cast<uint32_t>(fixed);
+        r->slot_bytes = static_cast<uint32_t>(slot);
+        r->bytes = static_cast<uint32_t>(fixed + groups * n * slot);
+        return true;
+    }
+    return false;
+}
+
+// CTAs to a row: two where slots for four inputs and the parameters of a whole row would
+// leave room for one group of warps only, or not fit (us with one / two: 4096 x 8192 bf16
+// 102 / 97, 2048 x 16384 does not fit / 124; 8192 x 5120 109 / 121, 8192 x 4096 79 / 94, in
+// fp32 130 / 147).
+int bwd_cluster(bool phased, int64_t D, int elem) { return !phased && D * (8 * elem + 8) >= 24 * 8192 ? 2 : 1; }
+int64_t bwd_units(int64_t M, int num_sms, int cluster)
+{
+    const int sms = num_sms < BLOCK_NORM_BWD_BLOCKS ? num_sms : BLOCK_NORM_BWD_BLOCKS;
+    if (cluster == 1)
+        return ring_blocks(M, sms);
+    return M < sms / cluster ? M : sms / cluster;
+}
+// Groups of a block at most.
+int64_t bwd_groups(int64_t D, int elem, int cluster)
+{
+    int64_t packs;
+    const int64_t gt = bwd_group_threads(D, elem, false, cluster, &packs);
+    return gt > BWD_THREADS ? 1 : BWD_THREADS / gt;
 }
 
 template <class T, class W>
@@ -583,20 +827,19 @@ cudaError_t launch_block_bwd_tw(BlockNormBwdParams p, Rows rows, void *dpost, vo
     const bool several = p.gate_rows > 1;
     int blocks = static_cast<int>(p.M < RMS_BWD_BLOCKS ? p.M : RMS_BWD_BLOCKS);
     cudaError_t e = cudaSuccess;
-    RingPlan r;
+    BwdPlan r;
     if (several && rows == ROWS_PHASED)
         rows = ROWS_ANY;  // a lane's rows follow one another, so their phases differ
-    const int ring = ring_blocks(p.M, num_sms < BLOCK_NORM_BWD_BLOCKS ? num_sms : BLOCK_NORM_BWD_BLOCKS);
+    const bool phased = rows == ROWS_PHASED;
+    const int cluster = bwd_cluster(phased, p.D, sizeof(T));
+    const int64_t units = bwd_units(p.M, num_sms, cluster);
     if (num_sms >= 8 && use_ring(rows, p.M, p.D) &&
-        plan_ring(&r, rows == ROWS_PHASED, p.D, sizeof(T), param_bytes<W>(p), inputs, BLOCK_NORM_BWD_THREADS,
-                  BWD_RING_BUDGET)) {
-        blocks = ring;
-        const int64_t most = bwd_groups(p.M, p.D, sizeof(T), blocks);
-        if (several && r.groups > most)
-            r.groups = static_cast<int>(most);
-        p.lanes = static_cast<int64_t>(blocks) * r.groups;
-        e = rows == ROWS_PHASED ? launch_block_bwd_ring<T, W, true>(p, r, blocks, s)
-                                : launch_block_bwd_ring<T, W, false>(p, r, blocks, s);
+        plan_bwd(&r, phased, p.D, sizeof(T), p.pre ? sizeof(W) : 0, p.post || p.gate, several, inputs, cluster,
+                 several ? p.M / units : BWD_WARPS)) {  // (with several gate rows every lane has a row)
+        blocks = static_cast<int>(units);
+        p.lanes = units * r.groups;
+        e = phased ? launch_block_bwd_ring<T, W, true>(p, r, blocks, s)
+                   : launch_block_bwd_ring<T, W, false>(p, r, blocks, s);
     } else {
         p.lanes = blocks;
         if (!(rows == ROWS_VEC ? launch_block_bwd_regs<T, W, V>(p, blocks, s, &e)
@@ -618,9 +861,12 @@ cudaError_t launch_block_bwd_tw(BlockNormBwdParams p, Rows rows, void *dpost, vo
 
 int64_t block_norm_bwd_lanes(int64_t M, int64_t D, int dtype)
 {
-    const int64_t ring = BLOCK_NORM_BWD_BLOCKS * bwd_groups(M, D, dtype == 2 ? 4 : 2, 1), lanes = M < ring ? M : ring;
+    // as many lanes as the ring kernel can have, or one for every block
+    const int elem = dtype == 2 ? 4 : 2, cluster = bwd_cluster(false, D, elem);
+    const int64_t most = bwd_units(M, BLOCK_NORM_BWD_BLOCKS, cluster) * bwd_groups(D, elem, cluster);
+    const int64_t ring = M < most ? M : most;
     const int64_t blocks = M < RMS_BWD_BLOCKS ? (M + 7) / 8 * 8 : RMS_BWD_BLOCKS;  // (304 is a multiple of eight)
-    return lanes > blocks ? lanes : blocks;
+    return ring > blocks ? ring : blocks;
 }
 
 cudaError_t launch_block_norm_bwd(const BlockNormBwdParams &p, void *dpost, void *dpre, void *dgate, int dtype, int wdtype,

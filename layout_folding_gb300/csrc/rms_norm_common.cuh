@@ -374,14 +374,14 @@ struct RingSync {
 };
 
 // Bounded wait for a slot; on a timeout the code goes to the device error word.
-__device__ __forceinline__ bool ring_wait(uint32_t bar, uint32_t parity, const WaitLimit &lim)
+__device__ __forceinline__ bool ring_wait(uint32_t bar, uint32_t parity, const WaitLimit &lim, int code = 0x102)
 {
     if (mbar_try_wait(bar, parity))
         return true;
     const uint64_t t0 = global_timer_ns();
     while (!mbar_try_wait(bar, parity)) {
         if (global_timer_ns() - t0 > lim.timeout_ns) {
-            atomicCAS(lim.err, 0, 0x102);
+            atomicCAS(lim.err, 0, code);
             return false;
         }
     }
@@ -549,31 +549,6 @@ struct Ring {
         if (c)
             bulk_load_g2s(dst + 2 * row_bytes, c + (PH ? span.first(row) : row * ldc), n, bar);
     }
-    // The same for up to four contiguous inputs of pitch D; those that are null are left out
-    // of the slot.
-    template <class T, bool PH>
-    __device__ void fill_rows(const RowSpan<T, PH> &span, int s, int64_t row, const T *const (&in)[4], int64_t D) const
-    {
-        const uint32_t bar = full_s + 8u * s, n = span.bytes(row);
-        uint32_t inputs = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (PH && in[i])
-                span.copy_tail(reinterpret_cast<T *>(const_cast<uint8_t *>(slots) + s * slot_bytes + inputs * row_bytes),
-                               in[i], row);
-            inputs += in[i] ? 1u : 0u;
-        }
-        mbar_arrive_expect_tx(bar, n * inputs);
-        if (n == 0)
-            return;
-        uint32_t dst = slots_s + s * slot_bytes;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (in[i]) {
-                bulk_load_g2s(dst, in[i] + (PH ? span.first(row) : row * D), n, bar);
-                dst += row_bytes;
-            }
-    }
     __device__ const uint8_t *input(int i) const { return slots + slot * slot_bytes + i * row_bytes; }
     __device__ void advance()
     {
@@ -623,26 +598,25 @@ __device__ __forceinline__ const W *ring_weights(uint8_t *smem, const RingPlan &
 // A ring of `inputs` rows of D elements per slot, or false where a row is too
 // long for two slots.  At least two slots per group, then as many groups as the
 // threads and the shared memory allow, then more slots.
-bool plan_ring(RingPlan *r, bool phased, int64_t D, int elem, int welem, int inputs, int max_threads,
-               int64_t budget = RING_BUDGET)
+bool plan_ring(RingPlan *r, bool phased, int64_t D, int elem, int welem, int inputs, int max_threads)
 {
     const int64_t vec = 16 / elem;
     const int64_t packs = phased ? (D + 2 * vec - 2) / vec : D / vec;  // at most
     const int64_t row_bytes = packs * 16, slot = row_bytes * inputs;
     int64_t wbytes = (packs * vec * welem + 127) / 128 * 128;
     r->w_shared = 1;
-    if (!phased && wbytes + 2 * slot > budget && 2 * slot <= budget) {
+    if (!phased && wbytes + 2 * slot > RING_BUDGET && 2 * slot <= RING_BUDGET) {
         wbytes = 0;
         r->w_shared = 0;
     }
     const int64_t gt = (packs + 32 * RING_NV - 1) / (32 * RING_NV) * 32;
-    if (gt > max_threads || wbytes + 2 * slot > budget)
+    if (gt > max_threads || wbytes + 2 * slot > RING_BUDGET)
         return false;
     int64_t groups = max_threads / gt;
     groups = groups < RING_MAX_GROUPS ? groups : RING_MAX_GROUPS;
-    const int64_t fit = (budget - wbytes) / (2 * slot);
+    const int64_t fit = (RING_BUDGET - wbytes) / (2 * slot);
     groups = groups < fit ? groups : fit;
-    int64_t slots = (budget - wbytes) / (slot * groups);
+    int64_t slots = (RING_BUDGET - wbytes) / (slot * groups);
     slots = slots < RING_MAX_SLOTS ? slots : RING_MAX_SLOTS;
     r->group_threads = static_cast<int>(gt);
     r->groups = static_cast<int>(groups);
