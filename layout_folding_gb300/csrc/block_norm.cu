@@ -203,15 +203,30 @@ __global__ void __launch_bounds__(1024) k_block_norm_long(const __grid_constant_
 }
 
 // ---------------------------------------------------------------- many rows
-constexpr int BLOCK_NORM_THREADS = 640;
+// Where a ring kernel has the parameters.
+enum Params { PARAMS_GLOBAL, PARAMS_SHARED, PARAMS_SHARED_GATES };
+__host__ __device__ constexpr int block_norm_threads(bool fp8) { return fp8 ? 640 : 512; }
 
-template <class T, class W, bool FP8, bool PH>
-__global__ void __launch_bounds__(BLOCK_NORM_THREADS)
+// In rings of bulk copies (rms_norm_common.cuh).  The parameters lie in shared memory where
+// they fit: beta post (times a gate of one row) in fp32, then pre, in fp32 too (in its own
+// type for e4m3, which reads it twice), so that a pack takes no conversions and one product
+// for them.  A gate of several rows is read where it is, before the wait for the row if it is
+// of the stream's type.  Between its two reductions a row is kept in fp32, in its type where
+// the gate or the codes need the registers.
+// 8192 x 5120 bf16 takes 58.5 us (335 MB: 5.7 TB/s, 85 % of the copy rate), as much with
+// one gate or four, without pre 44.7; with 640 threads, and so spills, 82.  Into e4m3 at 640
+// threads 52.2, four gates 59.5.
+template <class T, class W, bool FP8, bool PH, Params PARAMS>
+__global__ void __launch_bounds__(block_norm_threads(FP8))
     k_block_norm_ring(const __grid_constant__ BlockNormParams p, const RingPlan r)
 {
-    constexpr int VEC = 16 / static_cast<int>(sizeof(T));
+    constexpr int VEC = 16 / static_cast<int>(sizeof(T)), N = VEC / 2;
+    constexpr bool SHARED = PARAMS != PARAMS_GLOBAL, EARLY_GATE = PARAMS == PARAMS_SHARED_GATES;
+    constexpr bool KEEP_F32 = !FP8 && !EARLY_GATE;
+    using Pre = typename std::conditional<FP8, W, float>::type;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ RingSync sy;
+    __shared__ __align__(16) float scales[8];  // beta
     const int group = threadIdx.x / r.group_threads, t = threadIdx.x % r.group_threads;
     const int warps = r.group_threads >> 5, first_warp = group * warps;
     const RowSpan<T, PH> span(p.M, p.D);
@@ -235,7 +250,36 @@ __global__ void __launch_bounds__(BLOCK_NORM_THREADS)
         for (int i = p.limit.inject && blockIdx.x == 0 && group == 0 ? 1 : 0; i < r.slots && row0 + i * step < p.M; ++i)
             fill(i, row0 + i * step);
     }
-    const RingParams<T, W, PH, BlockNormParams> w(smem, r, span, p);
+    const bool one_gate = p.gate && p.gate_tokens == p.M, gates = p.gate && !one_gate, factors = p.post || one_gate;
+    const W *const post = static_cast<const W *>(p.post), *const pre = static_cast<const W *>(p.pre);
+    if (threadIdx.x < 8)
+        scales[threadIdx.x] = p.branch_scale;
+    float *const s_factor = reinterpret_cast<float *>(smem + r.w_off);
+    Pre *const s_pre = reinterpret_cast<Pre *>(s_factor + (factors ? packs * VEC : 0));
+    if (SHARED) {
+#pragma unroll 4
+        for (int i = threadIdx.x; i < packs * VEC; i += blockDim.x) {
+            const int k = i - span.phase;
+            const bool inside = !PH || (k >= 0 && k < span.D);
+            if (factors) {
+                float f = inside && post ? to_f(post[k]) : 1.f;
+                if (inside && one_gate)
+                    f *= gate_one<T>(p.gate, p.gate_f32, k);
+                s_factor[i] = inside ? f * p.branch_scale : 0.f;
+            }
+            if (pre)
+                s_pre[i] = from_f<Pre>(inside ? to_f(pre[k]) : 0.f);
+        }
+    }
+    __syncthreads();
+    const uint32_t factor = factors ? smem_u32(s_factor) : smem_u32(scales), factor_apart = factors ? 4u * VEC : 0u;
+    const uint32_t pre_at = smem_u32(s_pre);
+    const auto second_weights = [&](int c, float2 (&w)[N]) {
+        if constexpr (SHARED)
+            get2<Pre, VEC>(lds_pack<Pre, VEC>(pre_at + c * static_cast<uint32_t>(VEC * sizeof(Pre))), w);
+        else
+            get2<W, VEC>(load_pack<W, VEC>(pre + c * VEC), w);
+    };
     bool ok = true;
     for (int64_t row = row0; row < p.M; row += step) {
         // every thread of the group has read the slot: it takes the row `slots` steps ahead
@@ -244,26 +288,69 @@ __global__ void __launch_bounds__(BLOCK_NORM_THREADS)
                 fill(ring.slot, row + r.slots * step);
             ring.advance();
         };
+        const int64_t gate_row = gates ? row / p.gate_tokens * p.D : 0;
+        Pack<T, VEC> u[RING_NV];
+        if (EARLY_GATE) {
+#pragma unroll
+            for (int j = 0; j < RING_NV; ++j) {
+                const int c = t + j * r.group_threads;
+                if (c < packs)
+                    u[j] = load_pack<T, VEC>(static_cast<const T *>(p.gate) + gate_row + c * VEC);
+            }
+        }
+        // post times the gate times beta
+        const auto first_weights = [&](int j, int c, float2 (&w)[N]) {
+            if constexpr (!SHARED) {
+                column_factors<T, W, VEC>(p, gate_row, c * VEC, w);
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    w[i] = mul2(w[i], both(p.branch_scale));
+                return;
+            }
+            get2<float, VEC>(lds_pack<float, VEC>(factor + c * factor_apart), w);
+            if (!gates)
+                return;
+            float2 g[N];
+            if constexpr (PH) {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    const float v = span.inside(c, i) ? gate_one<T>(p.gate, p.gate_f32, gate_row + c * VEC + i - span.phase) : 0.f;
+                    (i % 2 ? g[i / 2].y : g[i / 2].x) = v;
+                }
+            } else if (!EARLY_GATE) {
+                gate_at<T, VEC>(p.gate, p.gate_f32, gate_row + c * VEC, g);
+            } else {
+                get2<T, VEC>(u[j], g);
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                w[i] = mul2(w[i], g[i]);
+        };
         ok = ring_wait(ring.full_s + 8u * ring.slot, ring.phase, p.limit);
-        Pack<T, VEC> h[RING_NV], rs[RING_NV];
+        const uint32_t in = ring.slots_s + ring.slot * ring.slot_bytes;
+        Pack<T, VEC> xs[RING_NV], rs[RING_NV];
         float2 ss = both(0.f);
 #pragma unroll
         for (int j = 0; j < RING_NV; ++j) {
             const int c = t + j * r.group_threads;
             if (c < packs) {
-                h[j] = load_pack<T, VEC>(reinterpret_cast<const T *>(ring.input(0)) + c * VEC);
-                rs[j] = load_pack<T, VEC>(reinterpret_cast<const T *>(ring.input(1)) + c * VEC);
-                span.mask(h[j], c);
+                xs[j] = lds_pack<T, VEC>(in + c * 16u);
+                rs[j] = lds_pack<T, VEC>(in + ring.row_bytes + c * 16u);
+                span.mask(xs[j], c);
                 span.mask(rs[j], c);
-                float2 f[VEC / 2];
-                get2<T, VEC>(h[j], f);
+                float2 f[N];
+                get2<T, VEC>(xs[j], f);
 #pragma unroll
-                for (int i = 0; i < VEC / 2; ++i)
+                for (int i = 0; i < N; ++i)
                     ss = fma2(f[i], f[i], ss);
             }
         }
         float r1 = 1.f;
-        if (p.post || !p.pre) {  // (a barrier has to free the slot in any case)
+        if (!p.post && p.pre) {
+            group_barrier(1 + group, r.group_threads);
+            if (ok)
+                refill();
+        } else {
             const float2 sums = group_reduce<false>(ss.x + ss.y, 0u, ok, sy, 0, first_warp, warps, 1 + group);
             if (!ok)
                 break;
@@ -271,29 +358,40 @@ __global__ void __launch_bounds__(BLOCK_NORM_THREADS)
             if (p.post)
                 r1 = rsqrtf(sums.x / static_cast<float>(p.D) + p.eps);
         }
+        float2 h[KEEP_F32 ? RING_NV : 1][N];  // the stream as it is kept, in fp32 (else in xs)
         ss = both(0.f);
         float mx = 0.f;
 #pragma unroll
         for (int j = 0; j < RING_NV; ++j) {
             const int c = t + j * r.group_threads;
             if (c < packs) {
-                float2 cf[VEC / 2], f[VEC / 2];
-                w.factors(p, span, row, c, cf);
-                enter_stream<T, VEC>(p, h[j], rs[j], r1, cf, h[j]);
-                span.store(static_cast<T *>(p.h), row, c, h[j]);
-                get2<T, VEC>(h[j], f);
-                if (FP8) {
-                    float2 wv[VEC / 2];
-                    get2<W, VEC>(load_pack<W, VEC>(w.pre + c * VEC), wv);
+                float2 w[N], f[N], v[N];
+                first_weights(j, c, w);
+                get2<T, VEC>(xs[j], f);
+                get2<T, VEC>(rs[j], v);
 #pragma unroll
-                    for (int i = 0; i < VEC / 2; ++i) {
-                        const float2 m = mul2(f[i], wv[i]);
+                for (int i = 0; i < N; ++i) {
+                    f[i] = mul2(mul2(f[i], both(r1)), w[i]);
+                    f[i] = make_float2(fmaf(v[i].x, p.residual_scale, f[i].x), fmaf(v[i].y, p.residual_scale, f[i].y));
+                }
+                Pack<T, VEC> kept;
+                set2<T, VEC>(kept, f);
+                span.store(static_cast<T *>(p.h), row, c, kept);
+                float2 (&k)[N] = h[KEEP_F32 ? j : 0];
+                get2<T, VEC>(kept, k);
+                if (!KEEP_F32)
+                    xs[j] = kept;
+                if (FP8) {
+                    second_weights(c, w);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        const float2 m = mul2(k[i], w[i]);
                         mx = max_mag3(mx, m.x, m.y);
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < VEC / 2; ++i)
-                    ss = fma2(f[i], f[i], ss);
+                for (int i = 0; i < N; ++i)
+                    ss = fma2(k[i], k[i], ss);
             }
         }
         if (!p.pre) {
@@ -303,8 +401,6 @@ __global__ void __launch_bounds__(BLOCK_NORM_THREADS)
         const float2 sums = group_reduce<true>(ss.x + ss.y, mag_bits(mx), ok, sy, 1, first_warp, warps, 1 + group);
         if (!ok)
             break;
-        if (!p.post)
-            refill();
         const float r2 = rsqrtf(sums.x / static_cast<float>(p.D) + p.eps);
         const RowScale scale(sums.y, sums.x, r2);
         if (FP8 && t == 0)
@@ -315,23 +411,26 @@ __global__ void __launch_bounds__(BLOCK_NORM_THREADS)
         for (int j = 0; j < RING_NV; ++j) {
             const int c = t + j * r.group_threads;
             if (c < packs) {
-                float2 f[VEC / 2], wv[VEC / 2];
-                get2<T, VEC>(h[j], f);
-                get2<W, VEC>(load_pack<W, VEC>(w.pre + c * VEC), wv);
+                float2 w[N];
+                second_weights(c, w);
+                float2 (&k)[N] = h[KEEP_F32 ? j : 0];
+                if (!KEEP_F32)
+                    get2<T, VEC>(xs[j], k);
                 if (FP8) {
                     float q[VEC];
 #pragma unroll
-                    for (int i = 0; i < VEC / 2; ++i) {
-                        const float2 m = mul2(f[i], wv[i]);
+                    for (int i = 0; i < N; ++i) {
+                        const float2 m = mul2(k[i], w[i]);
                         q[2 * i] = m.x;
                         q[2 * i + 1] = m.y;
                     }
                     scale.apply(q);
                     span.store_codes(static_cast<uint8_t *>(p.y), row, c, q);
                 } else {
+                    float2 f[N];
 #pragma unroll
-                    for (int i = 0; i < VEC / 2; ++i)
-                        f[i] = mul2(mul2(f[i], both(r2)), wv[i]);
+                    for (int i = 0; i < N; ++i)
+                        f[i] = mul2(mul2(k[i], both(r2)), w[i]);
                     Pack<T, VEC> y;
                     set2<T, VEC>(y, f);
                     span.store(static_cast<T *>(p.y), row, c, y);
@@ -369,14 +468,14 @@ bool launch_block_regs(const BlockNormParams &p, cudaStream_t s, cudaError_t *e)
     return true;
 }
 
-template <class T, class W, bool FP8, bool PH>
+template <class T, class W, bool FP8, bool PH, Params PARAMS>
 cudaError_t launch_block_ring(const BlockNormParams &p, const RingPlan &r, int num_sms, cudaStream_t s)
 {
     static std::atomic<unsigned long long> opted{0};
-    const cudaError_t e = ring_opt_in(k_block_norm_ring<T, W, FP8, PH>, opted);
+    const cudaError_t e = ring_opt_in(k_block_norm_ring<T, W, FP8, PH, PARAMS>, opted);
     if (e != cudaSuccess)
         return e;
-    return launch_overlapped(k_block_norm_ring<T, W, FP8, PH>, dim3(ring_blocks(p.M, num_sms)),
+    return launch_overlapped(k_block_norm_ring<T, W, FP8, PH, PARAMS>, dim3(ring_blocks(p.M, num_sms)),
                              dim3(r.groups * r.group_threads), r.bytes, 1, s, p, r);
 }
 
@@ -385,10 +484,15 @@ cudaError_t launch_block_t(const BlockNormParams &p, Rows rows, int num_sms, cud
 {
     constexpr int V = 16 / static_cast<int>(sizeof(T));
     RingPlan r;
+    const bool one_gate = p.gate && p.gate_tokens == p.M;
+    const int param_bytes = (p.pre ? static_cast<int>(FP8 ? sizeof(W) : sizeof(float)) : 0) + (p.post || one_gate ? 4 : 0);
     if (num_sms >= 8 && use_ring(rows, p.M, p.D) &&
-        plan_ring(&r, rows == ROWS_PHASED, p.D, sizeof(T), param_bytes<W>(p), 2, BLOCK_NORM_THREADS))
-        return rows == ROWS_PHASED ? launch_block_ring<T, W, FP8, true>(p, r, num_sms, s)
-                                   : launch_block_ring<T, W, FP8, false>(p, r, num_sms, s);
+        plan_ring(&r, rows == ROWS_PHASED, p.D, sizeof(T), param_bytes, 2, block_norm_threads(FP8)))
+        return rows == ROWS_PHASED ? launch_block_ring<T, W, FP8, true, PARAMS_SHARED>(p, r, num_sms, s)
+               : !r.w_shared       ? launch_block_ring<T, W, FP8, false, PARAMS_GLOBAL>(p, r, num_sms, s)
+               : p.gate && !one_gate && (!p.gate_f32 || sizeof(T) == sizeof(float))
+                   ? launch_block_ring<T, W, FP8, false, PARAMS_SHARED_GATES>(p, r, num_sms, s)
+                   : launch_block_ring<T, W, FP8, false, PARAMS_SHARED>(p, r, num_sms, s);
     cudaError_t e = cudaSuccess;
     if (rows == ROWS_VEC ? launch_block_regs<T, W, V, FP8>(p, s, &e) : launch_block_regs<T, W, 1, FP8>(p, s, &e))
         return e;

@@ -1,5 +1,4 @@
-// block_norm_common.cuh -- what block_norm and its gradient share: the gate, and the
-// parameters of the ring kernels in shared memory.
+// block_norm_common.cuh -- what block_norm and its gradient share.
 #pragma once
 #include "rms_norm_common.cuh"
 
@@ -71,79 +70,17 @@ __device__ __forceinline__ void column_factors(const P &p, int64_t gate_row, int
     }
 }
 
-// The parameters of a ring kernel: pre in its type, then post times a gate of one row in
-// fp32 (one load and one product less for a column than the two of them apart), both in
-// shared memory where they fit, shifted by the block's phase.  A gate of several rows is
-// read where it is: the tokens of a row of it follow one another.
-template <class T, class W, bool PH, class P>
-struct RingParams {
-    using Span = RowSpan<T, PH>;
-    static constexpr int VEC = Span::VEC;
-    const W *pre;
-    const float *factor;  // null: none, or not in shared memory
-    bool gate_apart;
-    __device__ __forceinline__ RingParams(uint8_t *smem, const RingPlan &r, const Span &span, const P &p)
-        : pre(static_cast<const W *>(p.pre)), factor(nullptr), gate_apart(p.gate && p.gate_tokens != p.M)
-    {
-        RingPlan at = r;
-        if (pre) {
-            pre = ring_weights<W, PH>(smem, at, pre, span);
-            at.w_off += r.row_bytes / static_cast<uint32_t>(sizeof(T)) * static_cast<uint32_t>(sizeof(W));
-        }
-        const bool one_gate = p.gate && !gate_apart;
-        if ((p.post || one_gate) && (PH || r.w_shared)) {
-            float *f = reinterpret_cast<float *>(smem + at.w_off);
-            for (int i = threadIdx.x; i < span.packs * VEC; i += blockDim.x) {
-                const int k = i - span.phase;
-                const bool in = k >= 0 && k < span.D;
-                float v = in ? 1.f : 0.f;
-                if (in && p.post)
-                    v = to_f(static_cast<const W *>(p.post)[k]);
-                if (in && one_gate)
-                    v *= gate_one<T>(p.gate, p.gate_f32, k);
-                f[i] = v;
-            }
-            factor = f;
-        }
-        __syncthreads();
-    }
-    // the factors of pack c of row `row`
-    __device__ __forceinline__ void factors(const P &p, const Span &span, int64_t row, int c, float2 (&cf)[VEC / 2]) const
-    {
-        const int64_t gate_row = gate_apart ? row / p.gate_tokens * p.D : 0;
-        if (!PH && !factor) {
-            column_factors<T, W, VEC>(p, gate_row, c * VEC, cf);
-            return;
-        }
-        if (factor) {
-            get2<float, VEC>(load_pack<float, VEC>(factor + c * VEC), cf);
-        } else {
-#pragma unroll
-            for (int i = 0; i < VEC / 2; ++i)
-                cf[i] = both(1.f);
-        }
-        if (!gate_apart)
-            return;
-        float2 u[VEC / 2];
-        if constexpr (PH) {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const float v = span.inside(c, i) ? gate_one<T>(p.gate, p.gate_f32, gate_row + c * VEC + i - span.phase) : 0.f;
-                (i % 2 ? u[i / 2].y : u[i / 2].x) = v;
-            }
-        } else {
-            gate_at<T, VEC>(p.gate, p.gate_f32, gate_row + c * VEC, u);
-        }
-#pragma unroll
-        for (int i = 0; i < VEC / 2; ++i)
-            cf[i] = mul2(cf[i], u[i]);
-    }
-};
-// Bytes of them for each column.
-template <class W, class P>
-int param_bytes(const P &p)
+// VEC elements at a shared-memory address, 16 bytes a load.
+template <class T, int VEC>
+__device__ __forceinline__ Pack<T, VEC> lds_pack(uint32_t at)
 {
-    return static_cast<int>((p.pre ? sizeof(W) : 0) + (p.post || (p.gate && p.gate_tokens == p.M) ? sizeof(float) : 0));
+    Pack<T, VEC> p;
+#pragma unroll
+    for (int i = 0; i < Pack<T, VEC>::WORDS; i += 4)
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(p.u[i]), "=r"(p.u[i + 1]), "=r"(p.u[i + 2]), "=r"(p.u[i + 3])
+                     : "r"(at + 4u * i));
+    return p;
 }
 
 }  // namespace

@@ -133,19 +133,6 @@ __device__ __forceinline__ Pack<T, VEC> pack_or_zeros(const T *p, int64_t at)
     return z;
 }
 
-// VEC elements at a shared-memory address, 16 bytes a load.
-template <class T, int VEC>
-__device__ __forceinline__ Pack<T, VEC> lds_pack(uint32_t at)
-{
-    Pack<T, VEC> p;
-#pragma unroll
-    for (int i = 0; i < Pack<T, VEC>::WORDS; i += 4)
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(p.u[i]), "=r"(p.u[i + 1]), "=r"(p.u[i + 2]), "=r"(p.u[i + 3])
-                     : "r"(at + 4u * i));
-    return p;
-}
-
 template <int N>
 __device__ __forceinline__ void clear(float2 (&f)[N])
 {
