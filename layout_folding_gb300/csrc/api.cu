@@ -1096,9 +1096,6 @@ static lf_status block_norm_call(const void *x, int64_t ldx, const void *residua
     return launched(lf::launch_block_norm(p, dtype, wdtype, fp8, d->num_sms, stream), 1);
 }
 
-// Floats of one of the two regions of block_norm_backward's scratch.
-static int64_t block_norm_part(int64_t rows, int64_t D) { return (rows * D + 3) / 4 * 4; }
-
 static lf_status block_norm_backward_call(const void *dy, const void *x, const void *h, const void *post, const void *pre,
                                           const void *gate, int64_t gate_rows, int gate_dtype, const void *dh, void *dx,
                                           void *dres, void *dpost, void *dpre, void *dgate, void *scratch, int dtype,
@@ -1124,12 +1121,17 @@ static lf_status block_norm_backward_call(const void *dy, const void *x, const v
     lf_status st = current_device(&d);
     if (st != LF_OK)
         return st;
-    float *part_pre = static_cast<float *>(scratch);
-    float *part_sum = params ? part_pre + block_norm_part(lf::block_norm_bwd_lanes(M, D, dtype), D) : nullptr;
+    float *part_pre = static_cast<float *>(scratch), *part_sum = nullptr;
+    unsigned *counters = nullptr;
+    if (params) {
+        const lf::BlockNormScratch parts = lf::block_norm_bwd_scratch(M, D, dtype, gate ? gate_rows : 0);
+        part_sum = part_pre + parts.pre_floats;
+        counters = reinterpret_cast<unsigned *>(part_sum + parts.sum_floats);
+    }
     const lf::BlockNormBwdParams p = {dy, x, h, post, pre, gate, dh, dx, dres, dpre ? part_pre : nullptr,
-                                      dpost || dgate ? part_sum : nullptr, M, D, gate ? M / gate_rows : M,
-                                      gate ? gate_rows : 0, 0, eps, branch_scale, residual_scale,
-                                      gate && gate_dtype == LF_FP32,
+                                      dpost || dgate ? part_sum : nullptr, dpost ? counters : nullptr, M, D,
+                                      gate ? M / gate_rows : M, gate ? gate_rows : 0, 0, 0, eps, branch_scale,
+                                      residual_scale, gate && gate_dtype == LF_FP32,
                                       {d->err_word, g_timeout_ns.load(), g_inject.load()}};
     return launched(lf::launch_block_norm_bwd(p, dpost, dpre, dgate, dtype, wdtype, d->num_sms, stream), params ? 2 : 1);
 }
@@ -1688,8 +1690,8 @@ int64_t block_norm_backward_scratch(int64_t M, int64_t D, int dtype, int64_t gat
     if (M <= 0 || D <= 0 || M > MAX_DIM || D > MAX_DIM || dtype < LF_BF16 || dtype > LF_FP32 || gate_rows < 0 ||
         gate_rows > M)
         return 0;
-    const int64_t lanes = lf::block_norm_bwd_lanes(M, D, dtype);
-    return (block_norm_part(lanes, D) + block_norm_part(lanes + gate_rows, D)) * static_cast<int64_t>(sizeof(float));
+    const lf::BlockNormScratch s = lf::block_norm_bwd_scratch(M, D, dtype, gate_rows);
+    return (s.pre_floats + s.sum_floats + s.counters) * 4;
 }
 
 lf_status block_norm_backward(const void *dy, const void *x, const void *h, const void *post_or_null,

@@ -160,11 +160,13 @@ __global__ void __launch_bounds__(1024) k_block_norm_long(const __grid_constant_
         const int64_t gate_row = p.gate ? row / p.gate_tokens * p.D : 0;
         float r1 = 1.f, ss = 0.f, mx = 0.f;
         if (p.post) {
+#pragma unroll 4
             for (int64_t c = threadIdx.x; c < p.D; c += blockDim.x)
                 ss = fmaf(to_f(x[c]), to_f(x[c]), ss);
             r1 = rsqrtf(block_reduce<false>(ss, 0u, sh[0]).x / static_cast<float>(p.D) + p.eps);
         }
         ss = 0.f;
+#pragma unroll 4
         for (int64_t c = threadIdx.x; c < p.D; c += blockDim.x) {
             Pack<T, 1> k;
             float2 cf[1];
@@ -336,8 +338,11 @@ __global__ void __launch_bounds__(block_norm_threads(FP8))
             if (c < packs) {
                 xs[j] = lds_pack<T, VEC>(in + c * 16u);
                 rs[j] = lds_pack<T, VEC>(in + ring.row_bytes + c * 16u);
-                span.mask(xs[j], c);
-                span.mask(rs[j], c);
+                if (PH) {
+                    const uint4 keep = span.words(c);
+                    xs[j].keep(keep);
+                    rs[j].keep(keep);
+                }
                 float2 f[N];
                 get2<T, VEC>(xs[j], f);
 #pragma unroll

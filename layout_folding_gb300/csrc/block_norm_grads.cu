@@ -142,24 +142,36 @@ __device__ __forceinline__ void clear(float2 (&f)[N])
 }
 
 // Rows of a lane (a block, or a group of warps in the ring kernel).  With one gate row or
-// none they are strided; with several, lane l of `lanes` takes the rows M l / lanes ..
+// none they are strided.  With several, lane l of `lanes` takes the rows M l / lanes ..
 // M (l + 1) / lanes - 1, so that it meets the gate rows one after another, and leaves S of
-// lane l and gate row g in row l + g of part_sum (a lane and a gate row that meet are on a
-// path on which one or both of them grow, so no two of them share a row).
+// lane l and gate row g in row l + g of part_sum: a lane and a gate row that meet are on a
+// path on which one or both of them grow, so no two of them share a row.  (Phased rows: the
+// lane's rows are shared out over `residues` units, each with those of one phase, and row
+// (l + g) residues + r is unit r's, which has no such row where none of its phase is there.)
 struct LaneRows {
     int64_t first, end, step;
-    __device__ LaneRows(const BlockNormBwdParams &p, int64_t lane, int64_t strided_first, int64_t strided_step)
+    __device__ LaneRows(const BlockNormBwdParams &p, int64_t lane, int residue, int64_t strided_first, int64_t strided_step)
     {
         const bool several = p.gate_rows > 1;
         first = several ? p.M * lane / p.lanes : strided_first;
         end = several ? p.M * (lane + 1) / p.lanes : p.M;
-        step = several ? 1 : strided_step;
+        step = several ? p.residues : strided_step;
+        if (several && p.residues > 1)
+            first += (residue - first % p.residues + p.residues) % p.residues;
     }
 };
 // After `row`: S of its gate row is complete for this lane.
 __device__ __forceinline__ bool gate_row_ends(const BlockNormBwdParams &p, const LaneRows &rows, int64_t row)
 {
-    return p.gate_rows > 1 && (row + 1 == rows.end || (row + 1) % p.gate_tokens == 0);
+    return p.gate_rows > 1 &&
+           (row + rows.step >= rows.end || (row + rows.step) / p.gate_tokens != row / p.gate_tokens);
+}
+// The last kernel of a call counts its blocks in words that the first one clears.
+__device__ __forceinline__ void clear_counters(const BlockNormBwdParams &p)
+{
+    if (p.counters && blockIdx.x == 0)
+        for (int64_t i = threadIdx.x; i < (p.D + 31) / 32; i += blockDim.x)
+            p.counters[i] = 0u;
 }
 
 // One row per block and step, its sums of the parameters' gradients in registers.
@@ -180,7 +192,8 @@ __global__ void __launch_bounds__(512) k_block_norm_bwd(const __grid_constant__ 
         clear(a_sum[j]);
     }
     int buf = 0;
-    const LaneRows rows(p, blockIdx.x, blockIdx.x, gridDim.x);
+    const LaneRows rows(p, blockIdx.x, 0, blockIdx.x, gridDim.x);
+    clear_counters(p);
     for (int64_t row = rows.first; row < rows.end; row += rows.step, buf ^= 1) {
         const int64_t o = row * p.D, gate_row = p.gate ? row / p.gate_tokens * p.D : 0;
         Pack<T, VEC> q[NV][4];
@@ -259,7 +272,8 @@ __global__ void __launch_bounds__(1024) k_block_norm_bwd_long(const __grid_const
     const T *const in[4] = {static_cast<const T *>(p.h), static_cast<const T *>(p.dy), static_cast<const T *>(p.x),
                             static_cast<const T *>(p.dh)};
     int buf = 0;
-    const LaneRows rows(p, blockIdx.x, blockIdx.x, gridDim.x);
+    const LaneRows rows(p, blockIdx.x, 0, blockIdx.x, gridDim.x);
+    clear_counters(p);
     const auto columns = [&](int64_t row, int64_t c) {
         Columns<T, W, 1> v;
         v.load([&](int k) { return pack_or_zeros<T, 1>(in[k], row * p.D + c); },
@@ -271,6 +285,7 @@ __global__ void __launch_bounds__(1024) k_block_norm_bwd_long(const __grid_const
     for (int64_t row = rows.first; row < rows.end; row += rows.step, buf ^= 1) {
         float2 s2[6];
         clear(s2);
+#pragma unroll 4
         for (int64_t c = threadIdx.x; c < p.D; c += blockDim.x)
             columns(row, c).add_to(p, s2);
         RowSums s(s2);
@@ -304,17 +319,17 @@ __global__ void __launch_bounds__(1024) k_block_norm_bwd_long(const __grid_const
 // registers to keep it in, so it is read from shared memory twice.  Its warps count
 // themselves off on an mbarrier when they have, and the slot is filled again.
 //
-// A row may be shared by the two CTAs of a cluster, each with half of its columns: its slots
-// are half as large, so an SM has twice as many rows (and groups of warps) at hand, and rows
-// twice as long fit.  Every warp stores its six sums in both CTAs, in a place of its own,
-// and arrives on an mbarrier of the group there; all are added in the same order everywhere.
+// A row may be shared by the two or four CTAs of a cluster, each with a part of its columns,
+// so that longer rows fit.  Every warp stores its six sums in all CTAs, in a place of its
+// own, and arrives on an mbarrier of the group there; all are added in the same order
+// everywhere.
 //
 // What the call has none of is read as 16 bytes of zeros (factors of one), so that a pack's
 // loads stand in one straight line.
 constexpr int BWD_THREADS = 384;  // 168 registers a thread, 64 of them sums
 constexpr int BWD_WARPS = BWD_THREADS / 32;
-constexpr int BWD_CLUSTER = 2;
-constexpr int BWD_BUDGET = 223 * 1024;  // dynamic shared memory; BwdSync takes 3.6 KB more
+constexpr int BWD_CLUSTER = 4;
+constexpr int BWD_BUDGET = 222 * 1024;  // dynamic shared memory; BwdSync takes 4.8 KB more
 
 struct BwdPlan {
     int cluster, group_threads, groups, slots, packs;  // packs of a CTA's share of a row
@@ -368,14 +383,15 @@ __global__ void __launch_bounds__(BWD_THREADS)
     __shared__ BwdSync sy;
     const int group = threadIdx.x / r.group_threads, t = threadIdx.x % r.group_threads;
     const int warps = r.group_threads >> 5, first_warp = group * warps, warp = threadIdx.x >> 5, lane_id = threadIdx.x & 31;
-    const uint32_t clusters = PH ? 1u : r.cluster, rank = PH ? 0u : blockIdx.x % clusters;
+    const uint32_t clusters = r.cluster, rank = blockIdx.x % clusters;
     const int unit = static_cast<int>(blockIdx.x / clusters), units = static_cast<int>(gridDim.x / clusters);
-    const RowSpan<T, PH> span(p.M, p.D);  // (phase: of a unit that is one block)
-    const int packs = min(r.packs, span.packs - static_cast<int>(rank) * r.packs);
-    const int64_t col0 = static_cast<int64_t>(rank) * r.packs * VEC - span.phase;  // of the share's first granule
-    const int64_t lane = static_cast<int64_t>(unit) * r.groups + group;
+    const RowSpan<T, PH> span(p.M, p.D, unit);
+    const int pack0 = static_cast<int>(rank) * r.packs, packs = min(r.packs, span.packs - pack0);
+    const int64_t col0 = static_cast<int64_t>(pack0) * VEC - span.phase;  // of the share's first granule
+    const int residues = PH && p.gate_rows > 1 ? VEC : 1, residue = unit % residues;
+    const int64_t lane = static_cast<int64_t>(unit / residues) * r.groups + group;
     // neighbouring rows go to neighbouring SMs
-    const LaneRows rows(p, lane, static_cast<int64_t>(group) * units + unit, static_cast<int64_t>(units) * r.groups);
+    const LaneRows rows(p, lane, residue, static_cast<int64_t>(group) * units + unit, static_cast<int64_t>(units) * r.groups);
     const T *in[4] = {static_cast<const T *>(p.h), static_cast<const T *>(p.dy), static_cast<const T *>(p.x),
                       static_cast<const T *>(p.dh)};
     const uint32_t slots = smem_u32(smem + r.slot_off) + static_cast<uint32_t>(group) * r.slots * r.slot_bytes;
@@ -423,6 +439,7 @@ __global__ void __launch_bounds__(BWD_THREADS)
         sy.constants[threadIdx.x >> 3][threadIdx.x & 7] = threadIdx.x >> 3 ? 1.f : 0.f;
     wait_previous_kernel();
     let_next_kernel_start();
+    clear_counters(p);
     if (t == 0) {
         // (test hook: the first block's first group never loads its first row)
         for (int i = p.limit.inject && blockIdx.x == 0 && group == 0 ? 1 : 0;
@@ -430,7 +447,7 @@ __global__ void __launch_bounds__(BWD_THREADS)
             fill(i, rows.first + i * rows.step);
     }
     // pre, and post times a gate of one row (a gate of several rows: post times the group's)
-    const bool several = !PH && p.gate_rows > 1;
+    const bool several = p.gate_rows > 1;
     const T *const gate_t = several || !p.gate ? nullptr : static_cast<const T *>(p.gate);
     {
         W *const s_pre = reinterpret_cast<W *>(smem);
@@ -478,7 +495,18 @@ __global__ void __launch_bounds__(BWD_THREADS)
 #pragma unroll
             for (int j = 0; j < RING_NV; ++j) {
                 const int c = t + j * r.group_threads;
-                if (c < packs) {
+                if (c >= packs)
+                    continue;
+                if constexpr (PH) {
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) {
+                        const int64_t k = col0 + c * VEC + i;
+                        float2 f[1] = {both(0.f)};
+                        if (k >= 0 && k < p.D)
+                            column_factors<T, W, 1>(p, gate_row * p.D, k, f);
+                        group_factor[c * VEC + i] = f[0].x;
+                    }
+                } else {
                     float2 f[VEC / 2];
                     column_factors<T, W, VEC>(p, gate_row * p.D, col0 + c * VEC, f);
                     Pack<float, VEC> v;
@@ -500,11 +528,14 @@ __global__ void __launch_bounds__(BWD_THREADS)
             apart[k] = in[k] ? 16u : 0u;
             inputs += in[k] ? 1u : 0u;
         }
-        const auto columns = [&](int c) {
+        // (what lies beside a phased row is cut off for the sums; its results go nowhere)
+        const auto columns = [&](int c, bool cut) {
             Columns<T, W, VEC> v;
+            const uint4 keep = PH && cut ? span.words(pack0 + c) : make_uint4(0u, 0u, 0u, 0u);
             const auto at = [&](int k) {
                 Pack<T, VEC> q = lds_pack<T, VEC>(base[k] + c * apart[k]);
-                span.mask(q, c);
+                if (PH && cut)
+                    q.keep(keep);
                 return q;
             };
             v.load(at, lds_pack<W, VEC>(pre + c * pre_apart));
@@ -517,48 +548,57 @@ __global__ void __launch_bounds__(BWD_THREADS)
         for (int j = 0; j < RING_NV; ++j) {
             const int c = t + j * r.group_threads;
             if (c < packs)
-                columns(c).add_to(p, s2);
+                columns(c, true).add_to(p, s2);
         }
         RowSums s(s2);
         const uint32_t buf = count & 1u, bar = landed + 8u * buf;
-        if (clusters == 1) {
-            if (lane_id == 0) {
-                s.put(sy.sums[buf][0][warp]);
-                mbar_arrive(bar);
+        if (clusters * warps > 1) {
+            if (clusters == 1) {
+                if (lane_id == 0) {
+                    s.put(sy.sums[buf][0][warp]);
+                    mbar_arrive(bar);
+                }
+            } else if (static_cast<uint32_t>(lane_id) < clusters) {
+                const uint32_t to = mapa_shared(smem_u32(sy.sums[buf][rank][warp]), lane_id);
+                st_cluster_f32x4(to, make_float4(s.v[0], s.v[1], s.v[2], s.v[3]));
+                st_cluster_f32x4(to + 16u, make_float4(s.v[4], s.v[5], 0.f, 0.f));
+                mbar_arrive_cluster(mapa_shared(bar, lane_id));
             }
-        } else if (static_cast<uint32_t>(lane_id) < clusters) {
-            const uint32_t to = mapa_shared(smem_u32(sy.sums[buf][rank][warp]), lane_id);
-            st_cluster_f32x4(to, make_float4(s.v[0], s.v[1], s.v[2], s.v[3]));
-            st_cluster_f32x4(to + 16u, make_float4(s.v[4], s.v[5], 0.f, 0.f));
-            mbar_arrive_cluster(mapa_shared(bar, lane_id));
+            ok = sums_wait(bar, (count >> 1) & 1u, p.limit);
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+            }
+            s.add_all(sy.sums[buf], clusters, first_warp, warps);
         }
-        ok = sums_wait(bar, (count >> 1) & 1u, p.limit);
-        if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            break;
-        }
-        s.add_all(sy.sums[buf], clusters, first_warp, warps);
         const RowFactors f(p, s);
         const bool ends = p.part_sum && gate_row_ends(p, rows, row);
-        float *seg = ends ? p.part_sum + (lane + row / p.gate_tokens) * p.D + col0 : nullptr;
+        float *seg = ends ? p.part_sum + ((lane + row / p.gate_tokens) * residues + residue) * p.D + col0 : nullptr;
 #pragma unroll
         for (int j = 0; j < RING_NV; ++j) {
             const int c = t + j * r.group_threads;
             if (c < packs) {
                 Pack<T, VEC> dres, dx;
-                columns(c).finish(p, f, dres, dx, a_pre[j], a_sum[j]);
+                columns(c, false).finish(p, f, dres, dx, a_pre[j], a_sum[j]);
                 if constexpr (PH) {
-                    span.store(static_cast<T *>(p.dres), row, c, dres);
-                    span.store(static_cast<T *>(p.dx), row, c, dx);
+                    span.store(static_cast<T *>(p.dres), row, pack0 + c, dres);
+                    span.store(static_cast<T *>(p.dx), row, pack0 + c, dx);
                 } else {
                     const int64_t at = row * p.D + col0 + c * VEC;
                     dres.store(static_cast<T *>(p.dres) + at);
                     dx.store(static_cast<T *>(p.dx) + at);
                 }
-                if (ends) {  // (not with phased rows)
-                    Pack<float, VEC> a;
-                    set2<float, VEC>(a, a_sum[j]);
-                    a.store(seg + c * VEC);
+                if (ends) {
+                    if constexpr (PH) {
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i)
+                            if (span.inside(pack0 + c, i))
+                                seg[c * VEC + i] = i % 2 ? a_sum[j][i / 2].y : a_sum[j][i / 2].x;
+                    } else {
+                        Pack<float, VEC> a;
+                        set2<float, VEC>(a, a_sum[j]);
+                        a.store(seg + c * VEC);
+                    }
                     clear(a_sum[j]);
                 }
             }
@@ -581,30 +621,28 @@ __global__ void __launch_bounds__(BWD_THREADS)
         while (global_timer_ns() - t0 < RING_SETTLE_NS) {
         }
     }
-    // the rings are idle: the groups' sums are added there in turn, and written as the unit's row
+    // the rings are idle: the groups' sums go there, are added in order and written as the unit's row
     float *sums = reinterpret_cast<float *>(smem + r.slot_off);
     const auto merge = [&](const float2 (&acc)[RING_NV][VEC / 2], float *out) {
-        for (int g = 0; g < r.groups; ++g) {
-            __syncthreads();
-            if (group != g)
-                continue;
+        __syncthreads();
 #pragma unroll
-            for (int j = 0; j < RING_NV; ++j) {
-                const int c = t + j * r.group_threads;
-                if (c < packs) {
-                    Pack<float, VEC> a;
-                    set2<float, VEC>(a, acc[j]);
-                    if (g > 0)
-                        a.add(load_pack<float, VEC>(sums + c * VEC));
-                    a.store(sums + c * VEC);
-                }
+        for (int j = 0; j < RING_NV; ++j) {
+            const int c = t + j * r.group_threads;
+            if (c < packs) {
+                Pack<float, VEC> a;
+                set2<float, VEC>(a, acc[j]);
+                a.store(sums + (static_cast<size_t>(group) * r.packs + c) * VEC);
             }
         }
         __syncthreads();
         const int64_t to = static_cast<int64_t>(unit) * p.D + col0;
         for (int c = threadIdx.x; c < packs * VEC; c += blockDim.x)
-            if (!PH || (c + col0 >= 0 && c + col0 < p.D))
-                out[to + c] = sums[c];
+            if (!PH || (c + col0 >= 0 && c + col0 < p.D)) {
+                float s = sums[c];
+                for (int g = 1; g < r.groups; ++g)
+                    s += sums[static_cast<size_t>(g) * r.packs * VEC + c];
+                out[to + c] = s;
+            }
     };
     if (p.part_pre)
         merge(a_pre, p.part_pre);
@@ -614,105 +652,141 @@ __global__ void __launch_bounds__(BWD_THREADS)
         cluster_sync();  // no CTA leaves while sums may still be sent to it
 }
 
-// The parameters' gradients from their sums.  A block has 32 columns and 32 rows of
-// threads; what it does goes by blockIdx.y: 0 dpre, 1 dpost, from 2 on dgate.  With one
-// gate row (or none) both sums have a row for each of `blocks` blocks; with several, S
-// lies as LaneRows says.
-constexpr int SUM_ROWS = 32;
+// The parameters' gradients from their sums.  A block has 32 columns and SUM_ROWS rows of
+// threads, whose sums the first warp adds up; what it does goes by blockIdx.y: 0 dpre; 1
+// dpost and dgate of one gate row (or none), whose sums, like dpre's, have a row for each of
+// `blocks` blocks.  With several gate rows S lies as LaneRows says and the blocks from 1 on
+// share the gate rows: each adds up its rows' S, writes their dgate and leaves its part of
+// dpost (the sum of u S) in the first row of S that only it reads; the last of a column's
+// blocks to do so adds those up, in their order.
+constexpr int SUM_ROWS = 16;
 // S of many lanes to a gate row is added by all threads of a block, else a gate row each.
-__host__ __device__ constexpr bool many_lanes(int64_t lanes, int64_t gate_rows) { return lanes >= 16 * gate_rows; }
+__host__ __device__ constexpr bool many_lanes(int64_t lanes, int64_t gate_rows) { return lanes >= SUM_ROWS / 2 * gate_rows; }
 
 template <class T, class W>
 __global__ void __launch_bounds__(32 * SUM_ROWS)
     k_block_norm_sums(const __grid_constant__ BlockNormBwdParams p, int blocks, W *dpost, W *dpre, void *dgate)
 {
     wait_previous_kernel();
-    __shared__ float sh[SUM_ROWS][33];
+    __shared__ float sh[SUM_ROWS][32];
+    __shared__ bool last;
+    const int ty = threadIdx.y;
     const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x;
-    const bool several = p.gate_rows > 1;
-    const float post = p.post && c < p.D ? to_f(static_cast<const W *>(p.post)[c]) : 1.f;
-    const auto lane_of = [&](int64_t row) { return ((row + 1) * p.lanes - 1) / p.M; };
+    const bool in = c < p.D, writes = in && ty == 0;
+    const float post = p.post && in ? to_f(static_cast<const W *>(p.post)[c]) : 1.f;
     const auto put_gate = [&](int64_t i, float v) {
         if (p.gate_f32)
             static_cast<float *>(dgate)[i] = v;
         else
             static_cast<T *>(dgate)[i] = from_f<T>(v);
     };
-    // the sum over the rows of threads, in a fixed tree; every column's in its first thread row
+    // the sum over the rows of threads, in their order, in the first of them
     const auto over_rows = [&](float s) {
         __syncthreads();
-        sh[threadIdx.y][threadIdx.x] = s;
+        sh[ty][threadIdx.x] = s;
         __syncthreads();
-        s = sh[threadIdx.x][threadIdx.y];
+        if (ty == 0) {
+            s = sh[0][threadIdx.x];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            s += __shfl_xor_sync(0xffffffffu, s, o);
-        return s;  // of column threadIdx.y, in every thread of its warp
+            for (int r = 1; r < SUM_ROWS; ++r)
+                s += sh[r][threadIdx.x];
+        }
+        return s;
     };
-    const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.y;
-    const bool writes = threadIdx.x == 0 && col < p.D;
-    if (blockIdx.y < 2 && (blockIdx.y == 0 || !several)) {
-        // rows of `blocks` blocks
+    if (blockIdx.y == 0 || p.gate_rows <= 1) {
         const float *part = blockIdx.y == 0 ? p.part_pre : p.part_sum;
         if (blockIdx.y == 0 ? !dpre : !dpost && !dgate)
             return;
         float s = 0.f;
 #pragma unroll 8
-        for (int b = threadIdx.y; b < blocks; b += SUM_ROWS)
-            s += c < p.D ? part[static_cast<int64_t>(b) * p.D + c] : 0.f;
+        for (int b = ty; b < blocks; b += SUM_ROWS)
+            s += in ? part[static_cast<int64_t>(b) * p.D + c] : 0.f;
         s = over_rows(s);
         if (!writes)
             return;
         if (blockIdx.y == 0) {
-            dpre[col] = from_f<W>(s);
+            dpre[c] = from_f<W>(s);
             return;
         }
-        const float u = p.gate ? gate_one<T>(p.gate, p.gate_f32, col) : 1.f;
+        const float u = p.gate ? gate_one<T>(p.gate, p.gate_f32, c) : 1.f;
         if (dpost)
-            dpost[col] = from_f<W>(p.branch_scale * u * s);
+            dpost[c] = from_f<W>(p.branch_scale * u * s);
         if (dgate)
-            put_gate(col, p.branch_scale * (p.post ? to_f(static_cast<const W *>(p.post)[col]) : 1.f) * s);
+            put_gate(c, p.branch_scale * post * s);
         return;
     }
-    if (blockIdx.y == 1) {
-        // dpost: every lane's gate rows
-        if (!dpost)
-            return;
+    if (!dpost && !dgate)
+        return;
+    const int sets = gridDim.y - 1, set = blockIdx.y - 1;
+    const bool many = many_lanes(p.lanes * p.residues, p.gate_rows);
+    const auto first_lane = [&](int64_t g) { return ((g * p.gate_tokens + 1) * p.lanes - 1) / p.M; };
+    const auto last_lane = [&](int64_t g) { return ((g + 1) * p.gate_tokens * p.lanes - 1) / p.M; };
+    // the row of part_sum where a set of blocks leaves its part of dpost
+    const auto place = [&](int64_t set_of) {
+        const int64_t g = set_of * (many ? 1 : SUM_ROWS);
+        return (first_lane(g) + g) * p.residues;
+    };
+    // whether unit r of lane l has rows of gate row g
+    const auto there = [&](int64_t l, int64_t g, int r) {
+        const int64_t a = max(p.M * l / p.lanes, g * p.gate_tokens);
+        const int64_t b = min(p.M * (l + 1) / p.lanes, (g + 1) * p.gate_tokens);
+        return b - a >= p.residues || a + (r - a % p.residues + p.residues) % p.residues < b;
+    };
+    // this thread's share (i0, i0 + step, ..) of gate row g's S
+    const auto share = [&](int64_t g, int64_t i0, int64_t step) {
+        const int64_t l0 = first_lane(g), n = (last_lane(g) - l0 + 1) * p.residues;
+        const float *part = p.part_sum + (l0 + g) * p.residues * p.D + c;
         float s = 0.f;
-        for (int64_t l = threadIdx.y; l < p.lanes; l += SUM_ROWS) {
-            const int64_t g0 = p.M * l / p.lanes / p.gate_tokens, g1 = (p.M * (l + 1) / p.lanes - 1) / p.gate_tokens;
-            for (int64_t g = g0; g <= g1 && c < p.D; ++g)
-                s = fmaf(gate_one<T>(p.gate, p.gate_f32, g * p.D + c), p.part_sum[(l + g) * p.D + c], s);
+        if (p.residues == 1) {
+#pragma unroll 8
+            for (int64_t i = i0; i < n; i += step)
+                s += in ? part[i * p.D] : 0.f;
+        } else {
+            for (int64_t i = i0; i < n; i += step)
+                if (in && there(l0 + i / p.residues, g, static_cast<int>(i % p.residues)))
+                    s += part[i * p.D];
         }
-        s = over_rows(s);
-        if (writes)
-            dpost[col] = from_f<W>(p.branch_scale * s);
-        return;
-    }
-    if (!dgate || !several)
-        return;
-    const int64_t step = gridDim.y - 2;
-    if (many_lanes(p.lanes, p.gate_rows)) {
-        for (int64_t g = blockIdx.y - 2; g < p.gate_rows; g += step) {
-            const int64_t l0 = lane_of(g * p.gate_tokens), l1 = lane_of((g + 1) * p.gate_tokens - 1);
-            float s = 0.f;
-#pragma unroll 4
-            for (int64_t l = l0 + threadIdx.y; l <= l1; l += SUM_ROWS)
-                s += c < p.D ? p.part_sum[(l + g) * p.D + c] : 0.f;
+        return s;
+    };
+    float acc = 0.f;  // of dpost
+    const int64_t g0 = many ? set : static_cast<int64_t>(set) * SUM_ROWS + ty;
+    for (int64_t g = g0; g < p.gate_rows; g += static_cast<int64_t>(sets) * (many ? 1 : SUM_ROWS)) {
+        float s = share(g, many ? ty : 0, many ? SUM_ROWS : 1);
+        if (many)
             s = over_rows(s);
-            if (writes)
-                put_gate(g * p.D + col, p.branch_scale * (p.post ? to_f(static_cast<const W *>(p.post)[col]) : 1.f) * s);
+        if (in && (ty == 0 || !many)) {
+            if (dgate)
+                put_gate(g * p.D + c, p.branch_scale * post * s);
+            if (dpost)
+                acc = fmaf(gate_one<T>(p.gate, p.gate_f32, g * p.D + c), s, acc);
         }
+    }
+    if (!dpost)
         return;
+    if (!many)
+        acc = over_rows(acc);
+    if (sets > 1) {
+        // (the rows that the set's first thread row writes over have been read by all of them)
+        if (ty == 0) {
+            if (in)
+                p.part_sum[place(set) * p.D + c] = acc;
+            __threadfence();
+            __syncwarp();
+            if (threadIdx.x == 0)
+                last = atomicAdd(p.counters + blockIdx.x, 1u) == static_cast<unsigned>(sets) - 1u;
+        }
+        __syncthreads();
+        if (!last)
+            return;
+        __threadfence();
+        acc = 0.f;
+#pragma unroll 4
+        for (int i = ty; i < sets; i += SUM_ROWS)
+            acc += in ? __ldcg(p.part_sum + place(i) * p.D + c) : 0.f;
+        acc = over_rows(acc);
     }
-    for (int64_t g = (blockIdx.y - 2) * SUM_ROWS + threadIdx.y; g < p.gate_rows; g += step * SUM_ROWS) {
-        const int64_t l0 = lane_of(g * p.gate_tokens), l1 = lane_of((g + 1) * p.gate_tokens - 1);
-        float s = 0.f;
-        for (int64_t l = l0; l <= l1 && c < p.D; ++l)
-            s += p.part_sum[(l + g) * p.D + c];
-        if (c < p.D)
-            put_gate(g * p.D + c, p.branch_scale * post * s);
-    }
+    if (writes)
+        dpost[c] = from_f<W>(p.branch_scale * acc);
 }
 
 // ---------------------------------------------------------------- launches
@@ -757,7 +831,7 @@ bool plan_bwd(BwdPlan *r, bool phased, int64_t D, int elem, int wbytes, bool fac
 {
     int64_t packs;
     const int64_t gt = bwd_group_threads(D, elem, phased, cluster, &packs), vec = 16 / elem;
-    if (gt > BWD_THREADS || (cluster > 1 && packs * (cluster - 1) * vec >= D))
+    if (gt > BWD_THREADS || packs * (cluster - 1) * vec >= D)
         return false;
     const int64_t pre = (packs * vec * wbytes + 127) / 128 * 128, f = factors ? packs * vec * 4 : 0;
     const int64_t slot = packs * 16 * inputs;
@@ -786,16 +860,30 @@ bool plan_bwd(BwdPlan *r, bool phased, int64_t D, int elem, int wbytes, bool fac
 }
 
 // CTAs to a row: two where slots for four inputs and the parameters of a whole row would
-// leave room for one group of warps only, or not fit (us with one / two: 4096 x 8192 bf16
-// 102 / 97, 2048 x 16384 does not fit / 124; 8192 x 5120 109 / 121, 8192 x 4096 79 / 94, in
-// fp32 130 / 147).
-int bwd_cluster(bool phased, int64_t D, int elem) { return !phased && D * (8 * elem + 8) >= 24 * 8192 ? 2 : 1; }
-int64_t bwd_units(int64_t M, int num_sms, int cluster)
+// leave room for one group of warps only (us with one / two: 4096 x 8192 bf16 102 / 97, 8192 x
+// 5120 109 / 121, 8192 x 4096 79 / 94, in fp32 130 / 147), four where half a row does not fit
+// (2048 x 16384 bf16 element by element 483, on two CTAs 124; 1024 x 16384 fp32 217, on four 195).
+int bwd_cluster(int64_t D, int elem)
+{
+    if (D * (8 * elem + 8) < 24 * 8192)
+        return 1;
+    const int64_t half = (D / 2 / (16 / elem) + 2) * (16 / elem);
+    return half * (8 * elem + 8) <= BWD_BUDGET - 256 && half <= BWD_THREADS * RING_NV * (16 / elem) ? 2 : 4;
+}
+// Clusters, a multiple of eight where the rows of each have one phase.
+int64_t bwd_units(int64_t M, int num_sms, int cluster, bool phased)
 {
     const int sms = num_sms < BLOCK_NORM_BWD_BLOCKS ? num_sms : BLOCK_NORM_BWD_BLOCKS;
-    if (cluster == 1)
-        return ring_blocks(M, sms);
+    if (cluster == 1 || phased)
+        return ring_blocks(M, sms / cluster);
     return M < sms / cluster ? M : sms / cluster;
+}
+// Phased rows with several gate rows take the ring where each phase meets each gate row
+// several times; else their parts would be most of the traffic.
+bool bwd_phased_gates(int64_t M, int64_t D, int elem, int64_t gate_rows)
+{
+    const int64_t vec = 16 / elem;
+    return gate_rows > 1 && D % vec != 0 && D >= PHASED_MIN_D && M / gate_rows >= 4 * vec;
 }
 // Groups of a block at most.
 int64_t bwd_groups(int64_t D, int elem, int cluster)
@@ -815,16 +903,19 @@ cudaError_t launch_block_bwd_tw(BlockNormBwdParams p, Rows rows, void *dpost, vo
     int blocks = static_cast<int>(p.M < RMS_BWD_BLOCKS ? p.M : RMS_BWD_BLOCKS);
     cudaError_t e = cudaSuccess;
     BwdPlan r;
-    if (several && rows == ROWS_PHASED)
-        rows = ROWS_ANY;  // a lane's rows follow one another, so their phases differ
+    p.residues = 1;
+    if (several && rows == ROWS_PHASED && !bwd_phased_gates(p.M, p.D, sizeof(T), p.gate_rows))
+        rows = ROWS_ANY;
     const bool phased = rows == ROWS_PHASED;
-    const int cluster = bwd_cluster(phased, p.D, sizeof(T));
-    const int64_t units = bwd_units(p.M, num_sms, cluster);
-    if (num_sms >= 8 && use_ring(rows, p.M, p.D) &&
-        plan_bwd(&r, phased, p.D, sizeof(T), p.pre ? sizeof(W) : 0, p.post || p.gate, several, inputs, cluster,
-                 several ? p.M / units : BWD_WARPS)) {  // (with several gate rows every lane has a row)
+    const int cluster = bwd_cluster(p.D, sizeof(T));
+    const int64_t units = num_sms >= 64 ? bwd_units(p.M, num_sms, cluster, phased) : 0;
+    // (rows of more than 16 columns for each of 512 threads: always)
+    const bool ring = units > 0 && (use_ring(rows, p.M, p.D) || (rows != ROWS_ANY && p.D > 8192));
+    if (ring && plan_bwd(&r, phased, p.D, sizeof(T), p.pre ? sizeof(W) : 0, p.post || p.gate, several, inputs, cluster,
+                         several ? p.M / units : BWD_WARPS)) {  // (with several gate rows every lane has a row)
+        p.residues = several && phased ? V : 1;
         blocks = static_cast<int>(units);
-        p.lanes = units * r.groups;
+        p.lanes = units / p.residues * r.groups;
         e = phased ? launch_block_bwd_ring<T, W, true>(p, r, blocks, s)
                    : launch_block_bwd_ring<T, W, false>(p, r, blocks, s);
     } else {
@@ -836,9 +927,9 @@ cudaError_t launch_block_bwd_tw(BlockNormBwdParams p, Rows rows, void *dpost, vo
     if (e != cudaSuccess || (!dpost && !dpre && !dgate))
         return e;
     int64_t jobs = 2;
-    if (several && dgate) {
-        const int64_t gate_blocks = many_lanes(p.lanes, p.gate_rows) ? p.gate_rows : (p.gate_rows + SUM_ROWS - 1) / SUM_ROWS;
-        jobs += gate_blocks < 65533 ? gate_blocks : 65533;
+    if (several) {
+        const int64_t sets = many_lanes(p.lanes * p.residues, p.gate_rows) ? p.gate_rows : (p.gate_rows + SUM_ROWS - 1) / SUM_ROWS;
+        jobs = 1 + (sets < 65534 ? sets : 65534);
     }
     return launch_overlapped(k_block_norm_sums<T, W>, dim3(static_cast<unsigned>((p.D + 31) / 32), static_cast<unsigned>(jobs)),
                              dim3(32, SUM_ROWS), 0, 1, s, p, blocks, static_cast<W *>(dpost), static_cast<W *>(dpre), dgate);
@@ -846,14 +937,17 @@ cudaError_t launch_block_bwd_tw(BlockNormBwdParams p, Rows rows, void *dpost, vo
 
 }  // namespace
 
-int64_t block_norm_bwd_lanes(int64_t M, int64_t D, int dtype)
+BlockNormScratch block_norm_bwd_scratch(int64_t M, int64_t D, int dtype, int64_t gate_rows)
 {
-    // as many lanes as the ring kernel can have, or one for every block
-    const int elem = dtype == 2 ? 4 : 2, cluster = bwd_cluster(false, D, elem);
-    const int64_t most = bwd_units(M, BLOCK_NORM_BWD_BLOCKS, cluster) * bwd_groups(D, elem, cluster);
+    // a row for as many lanes as the ring kernel can have, or for every block
+    const int elem = dtype == 2 ? 4 : 2, cluster = bwd_cluster(D, elem);
+    const int64_t most = bwd_units(M, BLOCK_NORM_BWD_BLOCKS, cluster, false) * bwd_groups(D, elem, cluster);
     const int64_t ring = M < most ? M : most;
     const int64_t blocks = M < RMS_BWD_BLOCKS ? (M + 7) / 8 * 8 : RMS_BWD_BLOCKS;  // (304 is a multiple of eight)
-    return ring > blocks ? ring : blocks;
+    const int64_t lanes = ring > blocks ? ring : blocks;
+    const int64_t residues = bwd_phased_gates(M, D, elem, gate_rows) ? 16 / elem : 1;
+    const auto floats = [](int64_t n) { return (n + 3) / 4 * 4; };
+    return {floats(lanes * D), floats((lanes + gate_rows * residues) * D), (D + 31) / 32};
 }
 
 cudaError_t launch_block_norm_bwd(const BlockNormBwdParams &p, void *dpost, void *dpre, void *dgate, int dtype, int wdtype,

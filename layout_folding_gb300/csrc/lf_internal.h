@@ -135,21 +135,25 @@ struct BlockNormParams {
 cudaError_t launch_block_norm(const BlockNormParams &p, int dtype, int wdtype, bool fp8, int num_sms, cudaStream_t s);
 
 // Its gradient (block_norm_grads.cu).  dy and h are read with pre, x with post or a gate (null otherwise), dh may
-// be null with pre.  part_pre: fp32 [block_norm_bwd_lanes][D] or null with dpre null;
-// part_sum: fp32 [block_norm_bwd_lanes + gate_rows][D] or null with dpost and dgate null.
-// dpost and dpre have wdtype, dgate the gate's type.
+// be null with pre.  part_pre, part_sum and counters: the three parts of the scratch, in
+// this order; part_pre is null with dpre, part_sum with dpost and dgate, and counters with
+// dpost.  dpost and dpre have wdtype, dgate the gate's type.
 struct BlockNormBwdParams {
     const void *dy, *x, *h, *post, *pre, *gate, *dh;
     void *dx, *dres;
     float *part_pre, *part_sum;
+    unsigned *counters;
     int64_t M, D, gate_tokens, gate_rows;  // gate_rows: M / gate_tokens, or 0 without a gate
-    int64_t lanes;                         // set by launch_block_norm_bwd
+    int64_t lanes, residues;               // set by launch_block_norm_bwd
     float eps, branch_scale, residual_scale;
     int gate_f32;
     WaitLimit limit;
 };
 constexpr int BLOCK_NORM_BWD_BLOCKS = 152;  // of the ring kernel at most
-int64_t block_norm_bwd_lanes(int64_t M, int64_t D, int dtype);
+struct BlockNormScratch {
+    int64_t pre_floats, sum_floats, counters;  // (words of four bytes, the first two multiples of four)
+};
+BlockNormScratch block_norm_bwd_scratch(int64_t M, int64_t D, int dtype, int64_t gate_rows);
 cudaError_t launch_block_norm_bwd(const BlockNormBwdParams &p, void *dpost, void *dpre, void *dgate, int dtype, int wdtype,
                                   int num_sms, cudaStream_t s);
 

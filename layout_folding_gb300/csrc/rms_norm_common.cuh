@@ -74,6 +74,14 @@ struct Pack {
             }
         }
     }
+    // The bits of w only (16 bytes).
+    __device__ __forceinline__ void keep(const uint4 &w)
+    {
+        u[0] &= w.x;
+        u[1] &= w.y;
+        u[2] &= w.z;
+        u[3] &= w.w;
+    }
     // this += o, each sum rounded once to T.  (For the 16-bit types that is also
     // what an fp32 addition rounded to T gives: fp32 has more than twice their
     // digits, so its own rounding cannot move a sum across one of theirs.)
@@ -436,8 +444,9 @@ struct RowSpan {
     static constexpr int VEC = 16 / static_cast<int>(sizeof(T));
     int phase, packs;
     const int64_t &M, &D;  // the kernel's parameters, which need no registers
-    __device__ RowSpan(const int64_t &m, const int64_t &d)
-        : phase(PH ? static_cast<int>((blockIdx.x % VEC) * (d % VEC) % VEC) : 0),
+    // unit: the block, or the cluster that shares its rows
+    __device__ RowSpan(const int64_t &m, const int64_t &d, uint32_t unit = blockIdx.x)
+        : phase(PH ? static_cast<int>((unit % VEC) * (d % VEC) % VEC) : 0),
           packs(static_cast<int>((phase + d + VEC - 1) / VEC)), M(m), D(d)
     {
     }
@@ -460,6 +469,19 @@ struct RowSpan {
                 f[i] = inside(c, i) ? f[i] : 0.f;
             v.set(f);
         }
+    }
+    // The bits of granule c that belong to the row, a word at a time (mask() for several packs).
+    __device__ __forceinline__ uint4 words(int c) const
+    {
+        uint32_t w[4] = {~0u, ~0u, ~0u, ~0u};
+        if (ragged(c)) {
+            const int lo = phase - c * VEC, hi = lo + static_cast<int>(D);  // elements lo .. hi - 1
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                if (i < lo || i >= hi)
+                    w[i * static_cast<int>(sizeof(T)) / 4] &= sizeof(T) == 4 ? 0u : i % 2 ? 0xffffu : 0xffff0000u;
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
     }
     __device__ void store(T *rows, int64_t row, int c, const Pack<T, VEC> &v) const
     {

@@ -227,7 +227,9 @@ def test_few_rows(M, D, dtype, wdtype):
 # group only, rows too long; rows that are not a multiple of 16 bytes; few of those
 MANY = [(610, 8), (1000, 136), (2500, 264), (700, 1032), (1300, 2056), (640, 5120), (612, 12296), (610, 20000),
         (700, 33), (612, 37), (900, 250), (1332, 1027), (777, 1530), (650, 5121), (609, 9999), (608, 12301),
-        (620, 16384), (609, 16383), (100, 1027), (153, 515), (303, 2050), (1, 5121), (4, 10303), (33, 13611)]
+        (620, 16384), (609, 16383), (100, 1027), (153, 515), (303, 2050), (1, 5121), (4, 10303), (33, 13611),
+        # rows on two and four CTAs
+        (40, 12288), (160, 16383), (310, 11416), (78, 22000), (90, 14337), (620, 9000)]
 
 
 @pytest.mark.parametrize("M,D", MANY)
