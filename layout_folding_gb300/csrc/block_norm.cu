@@ -207,25 +207,26 @@ __global__ void __launch_bounds__(1024) k_block_norm_long(const __grid_constant_
 // ---------------------------------------------------------------- many rows
 // Where a ring kernel has the parameters.
 enum Params { PARAMS_GLOBAL, PARAMS_SHARED, PARAMS_SHARED_GATES };
-__host__ __device__ constexpr int block_norm_threads(bool fp8) { return fp8 ? 640 : 512; }
+__host__ __device__ constexpr int block_norm_threads(bool fp8, bool phased) { return fp8 || phased ? 640 : 512; }
 
 // In rings of bulk copies (rms_norm_common.cuh).  The parameters lie in shared memory where
 // they fit: beta post (times a gate of one row) in fp32, then pre, in fp32 too (in its own
-// type for e4m3, which reads it twice), so that a pack takes no conversions and one product
-// for them.  A gate of several rows is read where it is, before the wait for the row if it is
-// of the stream's type.  Between its two reductions a row is kept in fp32, in its type where
-// the gate or the codes need the registers.
-// 8192 x 5120 bf16 takes 58.5 us (335 MB: 5.7 TB/s, 85 % of the copy rate), as much with
-// one gate or four, without pre 44.7; with 640 threads, and so spills, 82.  Into e4m3 at 640
-// threads 52.2, four gates 59.5.
+// type for e4m3, which reads it twice, and for phased rows, which leave less room), so that a
+// pack takes few conversions and one product for them.  A gate of several rows is read where
+// it is, before the wait for the row if it is of the stream's type.  Between its two
+// reductions a row is kept in fp32, in its type where the gate or the codes need the
+// registers.
+// 8192 x 5120 bf16 takes 58 to 60 us (335 MB: 5.7 TB/s, 84 % of the copy rate), with no gate,
+// one or four; without pre 44.7; with 640 threads, and so spills, 82.  Into e4m3, at 640
+// threads, 52.2, with four gates 59.5.  8188 x 4097 55.4, at 512 threads 63.
 template <class T, class W, bool FP8, bool PH, Params PARAMS>
-__global__ void __launch_bounds__(block_norm_threads(FP8))
+__global__ void __launch_bounds__(block_norm_threads(FP8, PH))
     k_block_norm_ring(const __grid_constant__ BlockNormParams p, const RingPlan r)
 {
     constexpr int VEC = 16 / static_cast<int>(sizeof(T)), N = VEC / 2;
     constexpr bool SHARED = PARAMS != PARAMS_GLOBAL, EARLY_GATE = PARAMS == PARAMS_SHARED_GATES;
-    constexpr bool KEEP_F32 = !FP8 && !EARLY_GATE;
-    using Pre = typename std::conditional<FP8, W, float>::type;
+    constexpr bool KEEP_F32 = !FP8 && !EARLY_GATE && !PH;
+    using Pre = typename std::conditional<FP8 || PH, W, float>::type;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ RingSync sy;
     __shared__ __align__(16) float scales[8];  // beta
@@ -490,9 +491,9 @@ cudaError_t launch_block_t(const BlockNormParams &p, Rows rows, int num_sms, cud
     constexpr int V = 16 / static_cast<int>(sizeof(T));
     RingPlan r;
     const bool one_gate = p.gate && p.gate_tokens == p.M;
-    const int param_bytes = (p.pre ? static_cast<int>(FP8 ? sizeof(W) : sizeof(float)) : 0) + (p.post || one_gate ? 4 : 0);
+    const int param_bytes = (p.pre ? static_cast<int>(FP8 || rows == ROWS_PHASED ? sizeof(W) : sizeof(float)) : 0) + (p.post || one_gate ? 4 : 0);
     if (num_sms >= 8 && use_ring(rows, p.M, p.D) &&
-        plan_ring(&r, rows == ROWS_PHASED, p.D, sizeof(T), param_bytes, 2, block_norm_threads(FP8)))
+        plan_ring(&r, rows == ROWS_PHASED, p.D, sizeof(T), param_bytes, 2, block_norm_threads(FP8, rows == ROWS_PHASED)))
         return rows == ROWS_PHASED ? launch_block_ring<T, W, FP8, true, PARAMS_SHARED>(p, r, num_sms, s)
                : !r.w_shared       ? launch_block_ring<T, W, FP8, false, PARAMS_GLOBAL>(p, r, num_sms, s)
                : p.gate && !one_gate && (!p.gate_f32 || sizeof(T) == sizeof(float))
