@@ -55,21 +55,23 @@ struct RowSums {
     }
 };
 
-// A row's factors: H = r2 (g - h m2) + dh, dx = r1 (c' - x k1).
+// A row's factors: H = r2 dy pre - h m + dh, dx = r1 H cf - x k, where cf has beta in it
+// (and so have the sums of c).
 struct RowFactors {
-    float r1, r2, m2, k1;
+    float r1, r2, m, k;
     __device__ __forceinline__ RowFactors(const BlockNormBwdParams &p, const RowSums &s)
     {
         const float inv_d = 1.f / static_cast<float>(p.D);
         r2 = p.pre ? rsqrtf(s.v[0] * inv_d + p.eps) : 0.f;
-        m2 = p.pre ? (s.v[1] * inv_d) * r2 * r2 : 0.f;
+        const float m2 = p.pre ? (s.v[1] * inv_d) * r2 * r2 : 0.f;
+        m = m2 * r2;
         r1 = p.post ? rsqrtf(s.v[2] * inv_d + p.eps) : 1.f;
-        k1 = p.post ? p.branch_scale * (fmaf(r2, fmaf(-m2, s.v[4], s.v[3]), s.v[5]) * inv_d) * r1 * r1 : 0.f;
+        k = p.post ? (fmaf(r2, fmaf(-m2, s.v[4], s.v[3]), s.v[5]) * inv_d) * r1 * r1 * r1 : 0.f;
     }
 };
 
 // VEC columns of a row.  What the call has none of is 0 (pre too, where it multiplies a
-// dy that is 0), the factors are 1.
+// dy that is 0), the factors are beta.
 template <class T, class W, int VEC>
 struct Columns {
     static constexpr int N = PAIRS<VEC>;
@@ -105,13 +107,15 @@ struct Columns {
         float2 o[N], q[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const float2 at_h = fma2(both(f.r2), fma2(h[i], both(-f.m2), mul2(dy[i], pre[i])), dh[i]);
+            const float2 dyr = mul2(dy[i], both(f.r2));
+            const float2 at_h = fma2(h[i], both(-f.m), fma2(dyr, pre[i], dh[i]));
+            const float2 at_x = mul2(at_h, both(f.r1));
             o[i] = mul2(at_h, both(p.residual_scale));
-            q[i] = mul2(mul2(at_h, both(p.branch_scale)), cf[i]);
+            q[i] = mul2(at_x, cf[i]);
             if (p.post)
-                q[i] = mul2(fma2(x[i], both(-f.k1), q[i]), both(f.r1));
-            a_pre[i] = fma2(dy[i], mul2(h[i], both(f.r2)), a_pre[i]);
-            a_sum[i] = fma2(at_h, mul2(x[i], both(f.r1)), a_sum[i]);
+                q[i] = fma2(x[i], both(-f.k), q[i]);
+            a_pre[i] = fma2(dyr, h[i], a_pre[i]);
+            a_sum[i] = fma2(at_x, x[i], a_sum[i]);
         }
         from_pairs<T, VEC>(dres, o);
         from_pairs<T, VEC>(dx, q);
@@ -131,6 +135,17 @@ __device__ __forceinline__ Pack<T, VEC> pack_or_zeros(const T *p, int64_t at)
         f[i] = 0.f;
     z.set(f);
     return z;
+}
+
+// The columns' factors times beta.
+template <class T, class W, int VEC>
+__device__ __forceinline__ void scaled_factors(const BlockNormBwdParams &p, int64_t gate_row, int64_t at,
+                                               float2 (&cf)[PAIRS<VEC>])
+{
+    column_factors<T, W, VEC>(p, gate_row, at, cf);
+#pragma unroll
+    for (int i = 0; i < PAIRS<VEC>; ++i)
+        cf[i] = mul2(cf[i], both(p.branch_scale));
 }
 
 template <int N>
@@ -208,7 +223,7 @@ __global__ void __launch_bounds__(512) k_block_norm_bwd(const __grid_constant__ 
         const auto columns = [&](int j, int64_t at) {
             Columns<T, W, VEC> v;
             v.load([&](int k) { return q[j][k]; }, pack_or_zeros<W, VEC>(static_cast<const W *>(p.pre), at));
-            column_factors<T, W, VEC>(p, gate_row, at, v.cf);
+            scaled_factors<T, W, VEC>(p, gate_row, at, v.cf);
             return v;
         };
         float2 s2[6];
@@ -278,7 +293,7 @@ __global__ void __launch_bounds__(1024) k_block_norm_bwd_long(const __grid_const
         Columns<T, W, 1> v;
         v.load([&](int k) { return pack_or_zeros<T, 1>(in[k], row * p.D + c); },
                pack_or_zeros<W, 1>(static_cast<const W *>(p.pre), c));
-        column_factors<T, W, 1>(p, p.gate ? row / p.gate_tokens * p.D : 0, c, v.cf);
+        scaled_factors<T, W, 1>(p, p.gate ? row / p.gate_tokens * p.D : 0, c, v.cf);
         return v;
     };
     const bool several = p.gate_rows > 1;
@@ -324,7 +339,7 @@ __global__ void __launch_bounds__(1024) k_block_norm_bwd_long(const __grid_const
 // own, and arrives on an mbarrier of the group there; all are added in the same order
 // everywhere.
 //
-// What the call has none of is read as 16 bytes of zeros (factors of one), so that a pack's
+// What the call has none of is read as 16 bytes of zeros (factors of beta), so that a pack's
 // loads stand in one straight line.
 constexpr int BWD_THREADS = 384;  // 168 registers a thread, 64 of them sums
 constexpr int BWD_WARPS = BWD_THREADS / 32;
@@ -339,7 +354,7 @@ struct BwdPlan {
 
 struct BwdSync {
     alignas(16) float sums[2][BWD_CLUSTER][BWD_WARPS][8];
-    alignas(16) float constants[2][8];  // zeros, ones
+    alignas(16) float constants[2][8];  // zeros, beta
     alignas(8) unsigned long long full[BWD_WARPS][RING_MAX_SLOTS], empty[BWD_WARPS][RING_MAX_SLOTS], landed[BWD_WARPS][2];
 };
 
@@ -436,7 +451,7 @@ __global__ void __launch_bounds__(BWD_THREADS)
         fence_mbar_init();
     }
     if (threadIdx.x < 16)
-        sy.constants[threadIdx.x >> 3][threadIdx.x & 7] = threadIdx.x >> 3 ? 1.f : 0.f;
+        sy.constants[threadIdx.x >> 3][threadIdx.x & 7] = threadIdx.x >> 3 ? p.branch_scale : 0.f;
     wait_previous_kernel();
     let_next_kernel_start();
     clear_counters(p);
@@ -464,16 +479,16 @@ __global__ void __launch_bounds__(BWD_THREADS)
                 float f = inside && post ? to_f(post[k]) : 1.f;
                 if (inside && gate_t)
                     f *= gate_one<T>(p.gate, p.gate_f32, k);
-                s_f[i] = inside ? f : 0.f;
+                s_f[i] = inside ? f * p.branch_scale : 0.f;
             }
         }
     }
-    const uint32_t zeros = smem_u32(sy.constants[0]), ones = smem_u32(sy.constants[1]);
+    const uint32_t zeros = smem_u32(sy.constants[0]), betas = smem_u32(sy.constants[1]);
     const uint32_t pre = p.pre ? smem_u32(smem) : zeros, pre_apart = p.pre ? VEC * sizeof(W) : 0u;
     const bool has_factor = p.post || p.gate;
     float *const group_factor =
         reinterpret_cast<float *>(smem + r.factor_off + (several ? static_cast<uint32_t>(group) * r.factor_bytes : 0u));
-    const uint32_t factor = has_factor ? smem_u32(group_factor) : ones, factor_apart = has_factor ? VEC * sizeof(float) : 0u;
+    const uint32_t factor = has_factor ? smem_u32(group_factor) : betas, factor_apart = has_factor ? VEC * sizeof(float) : 0u;
     if (clusters > 1)
         cluster_sync();  // both CTAs' barriers exist before any sum is sent
     else
@@ -503,12 +518,12 @@ __global__ void __launch_bounds__(BWD_THREADS)
                         const int64_t k = col0 + c * VEC + i;
                         float2 f[1] = {both(0.f)};
                         if (k >= 0 && k < p.D)
-                            column_factors<T, W, 1>(p, gate_row * p.D, k, f);
+                            scaled_factors<T, W, 1>(p, gate_row * p.D, k, f);
                         group_factor[c * VEC + i] = f[0].x;
                     }
                 } else {
                     float2 f[VEC / 2];
-                    column_factors<T, W, VEC>(p, gate_row * p.D, col0 + c * VEC, f);
+                    scaled_factors<T, W, VEC>(p, gate_row * p.D, col0 + c * VEC, f);
                     Pack<float, VEC> v;
                     set2<float, VEC>(v, f);
                     v.store(group_factor + c * VEC);
