@@ -255,7 +255,7 @@ LinearSkinny plan_linear_skinny(int64_t M, int64_t N, int num_k_blocks, int num_
 cudaError_t launch_linear_skinny(bool e4m3, int act, const LinearMaps &m, const LinearParams &p,
                                  const LinearSkinny &plan, const void *residual, void *pre, cudaStream_t s);
 // dz = dout act'(pre) (not written without an activation) and its column sums: to
-// dbias, or to `partial` (fp32 [linear_dz_blocks][N]) where that is more than one row,
+// dbias, or to `partial` (fp32 [linear_dz_blocks][N]) where that is more than one row (of blocks that no cluster holds),
 // and from there by launch_linear_dbias.  dbias may be null.  N % 8 == 0, 16-byte aligned.
 int linear_dz_blocks(int64_t M, int64_t N);
 cudaError_t launch_linear_dz(int act, const void *dout, const void *pre, void *dz, float *partial, void *dbias,

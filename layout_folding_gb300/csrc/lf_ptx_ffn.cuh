@@ -26,6 +26,13 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr)
     return v;
 }
 
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
 // ---------------------------------------------------------------- tcgen05
 // umma_f16 with e4m3 operands (kind::f8f6f4, K = 32).
 __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
