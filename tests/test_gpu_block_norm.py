@@ -443,9 +443,9 @@ def test_repeatable_parts_alone_and_on_two_streams(M, D, form):
     assert torch.equal(bits(none[0]), bits(grads[0])) and torch.equal(bits(none[1]), bits(grads[1]))
 
 
-@pytest.mark.parametrize("M,D", [(33, 520), (700, 520), (150, 1027)])
-def test_on_a_side_stream_and_captured(M, D):
-    c = Case(M, D, gates=1)
+@pytest.mark.parametrize("M,D,gates", [(33, 520, 1), (700, 520, 1), (150, 1027, 1), (700, 520, 7), (330, 1027, 5), (60, 264, 60)])
+def test_on_a_side_stream_and_captured(M, D, gates):
+    c = Case(M, D, gates=gates)
     x, res, dy, h, dh = (dev(t) for t in (c.x, c.res, c.dy, c.h, c.dh))
     kw = c.kw()
     side = torch.cuda.Stream()
@@ -487,13 +487,16 @@ def test_new_tensors_of_a_side_stream():
         torch.cuda.synchronize()
 
 
-def test_stalled_wait_times_out_and_context_survives():
-    c = Case(1000, 1024, gates=4)
+@pytest.mark.parametrize("M,D,gates", [(1000, 1024, 4), (616, 4096, 1), (300, 1027, 1), (80, 12288, 2)])
+def test_stalled_wait_times_out_and_context_survives(M, D, gates):
+    """Rows of one warp, of several, phased, and on two CTAs."""
+    c = Case(M, D, gates=gates)
+    forward = M >= 300
     for call, check in ((lambda: lf.block_norm(dev(c.x), dev(c.res), **c.kw()), c.check_forward),
                         (lambda: lf.block_norm(dev(c.x), dev(c.res), fp8=True, **c.kw()),
                          lambda out: c.check_forward(out, fp8=True)),
                         (lambda: lf.block_norm_backward(dev(c.dy), dev(c.x), dev(c.h), dh=dev(c.dh), **c.kw()),
-                         c.check_backward)):
+                         c.check_backward))[0 if forward else 2:]:
         lf.check_device_error()
         lf.set_test_hooks(True, 100_000_000)   # the first group's first row never lands; 100 ms per wait
         try:
