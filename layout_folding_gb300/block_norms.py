@@ -9,6 +9,7 @@ import torch
 
 import layout_folding_gb300 as _lf
 
+from . import compiled as _compiled
 from . import ffn as _f
 from .ffn import LF_BF16, LF_E4M3, LF_FP32
 
@@ -76,6 +77,12 @@ def block_norm(x, residual, post=None, pre=None, gate=None, branch_scale=1.0, re
     the next M / G of x's M rows in order), or x's shape with 1 in place of its last
     dimensions but D.  h may be passed as residual or x, to update a contiguous stream in
     place."""
+    if stream is None and h is None and y is None and scale is None:
+        made = _compiled.block_norm(x, residual, post, pre, gate, branch_scale, residual_scale, eps, fp8)
+        if made.__class__ is tuple:
+            return made
+        if made is not None:
+            _lf._check(made, "block_norm")
     dtype = getattr(x, "dtype", None)
     code = _f._CODES.get(dtype, -1)
     dev = x.get_device() if code >= 0 else -1
@@ -128,6 +135,12 @@ def block_norm_backward(dy, x, h, post=None, pre=None, gate=None, dh=None, branc
     parameter's type and shape, None for a parameter that is None, and with want_dparams
     False for those that are not given a tensor.  dx and dresidual may each be passed as
     dy, x, h or dh, to reuse its memory."""
+    if stream is None and dx is None and dresidual is None and dpost is None and dpre is None and dgate is None:
+        made = _compiled.block_norm_backward(dy, x, h, post, pre, gate, dh, branch_scale, residual_scale, eps, want_dparams)
+        if made.__class__ is tuple:
+            return made
+        if made is not None:
+            _lf._check(made, "block_norm_backward")
     dtype = getattr(x, "dtype", None)
     code = _f._CODES.get(dtype, -1)
     dev = x.get_device() if code >= 0 else -1

@@ -1,11 +1,14 @@
 """Build liblayoutfold.so in-tree with nvcc for sm_103a (no torch extension
-machinery: the library is a plain C-ABI shared object)."""
+machinery: the library is a plain C-ABI shared object), and the compiled part of
+its Python binding with g++."""
 from __future__ import annotations
 
 import glob
 import os
+import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -14,6 +17,8 @@ INCLUDE = os.path.join(ROOT, "include")
 OBJ_DIR = os.path.join(PKG, "_build")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "liblayoutfold.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING_PATH = os.path.join(LIB_DIR, "_binding.so")
 
 NVCC = os.environ.get("NVCC", "nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -27,13 +32,37 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def _binding_command(out):
+    """g++ for the compiled part of the Python binding, or None without the headers of
+    PyTorch or Python (the ctypes part does every call then)."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    base = os.path.join(os.path.dirname(os.path.abspath(torch.__file__)))
+    python = sysconfig.get_paths()["include"]
+    nvcc = shutil.which(NVCC)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include") if nvcc else ""
+    if not (os.path.exists(os.path.join(base, "include", "torch", "csrc", "autograd", "python_variable.h"))
+            and os.path.exists(os.path.join(python, "Python.h"))
+            and os.path.exists(os.path.join(cuda, "cuda_runtime_api.h"))):
+        return None
+    return [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-shared",
+            "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI), "-I", INCLUDE, "-I",
+            os.path.join(base, "include"), "-I", os.path.join(base, "include", "torch", "csrc", "api", "include"), "-I",
+            python, "-I", cuda, BINDING_SRC, "-o", out, "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch",
+            "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+
+
 def _deps():
-    return (_sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))
+    return (_sources() + [BINDING_SRC] + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))
             + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)])
 
 
 def up_to_date() -> bool:
     if not os.path.exists(LIB_PATH):
+        return False
+    if not os.path.exists(BINDING_PATH) and _binding_command(BINDING_PATH):
         return False
     t = os.path.getmtime(LIB_PATH)
     return all(os.path.getmtime(d) <= t for d in _deps())
@@ -48,6 +77,14 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     extra = ["-Xptxas", "-v"] if ptxas_info else []
     procs = []
     objs = []
+    binding_tmp = BINDING_PATH + ".tmp%d" % os.getpid()
+    binding = _binding_command(binding_tmp)
+    if binding is None:
+        print("no headers of PyTorch or Python: the compiled part of the binding is not built", file=sys.stderr)
+    else:
+        if verbose:
+            print(" ".join(binding), file=sys.stderr)
+        procs.append((BINDING_SRC, subprocess.Popen(binding, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     for src in _sources():
         obj = os.path.join(OBJ_DIR, os.path.splitext(os.path.basename(src))[0] + ".o")
         objs.append(obj)
@@ -67,6 +104,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     tmp = LIB_PATH + ".tmp%d" % os.getpid()
     cmd = [NVCC, *ARCH, "-shared", "-o", tmp, *objs]
     subprocess.run(cmd, check=True)
+    if binding is not None:
+        os.replace(binding_tmp, BINDING_PATH)
     os.replace(tmp, LIB_PATH)
     return LIB_PATH
 

@@ -9,6 +9,7 @@ import torch
 
 import layout_folding_gb300 as _lf
 
+from . import compiled as _compiled
 from . import ffn as _f
 from .ffn import ACTIVATIONS, LF_BF16, LF_FP32
 
@@ -65,6 +66,12 @@ def linear(x, w, bias=None, act=None, residual=None, x_scale=None, w_scale=None,
     x @ w.T + bias in bf16, which linear_backward takes where there is an activation,
     when want_pre (bf16 operands only), else None.  out may be the residual itself."""
     code = _act_code(act)
+    if stream is None and out is None and pre is None:
+        made = _compiled.linear(x, w, bias, code, residual, x_scale, w_scale, want_pre)
+        if made.__class__ is tuple:
+            return made
+        if made is not None:
+            _lf._check(made, "linear" if x_scale is None else "linear_e4m3")
     scaled = x_scale is not None or w_scale is not None
     M, N, K, dev = _dims(x, w, _FP8 if scaled else _BF16, stream)
     shape = (*x.shape[:-1], N)
@@ -106,6 +113,12 @@ def linear_backward(dout, x, w, pre=None, act=None, bias=None, want_dx=True, wan
     receives the gradient of x @ w.T + bias (pass pre or dout to reuse its memory; a
     new tensor by default)."""
     code = _act_code(act)
+    if stream is None and dx is None and dw is None and dbias is None and dz is None:
+        made = _compiled.linear_backward(dout, x, w, pre, code, bias, want_dx, want_dw)
+        if made.__class__ is tuple:
+            return made
+        if made is not None:
+            _lf._check(made, "linear_backward")
     M, N, K, dev = _dims(x, w, _BF16, stream)
     shape = (*x.shape[:-1], N)
     _f._output(dout, _BF16, shape, dev, "dout")
