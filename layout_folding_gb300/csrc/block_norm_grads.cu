@@ -749,7 +749,7 @@ __global__ void __launch_bounds__(32 * SUM_ROWS)
     };
     // this thread's share (i0, i0 + step, ..) of gate row g's S
     const auto share = [&](int64_t g, int64_t i0, int64_t step) {
-        const int64_t l0 = first_lane(g), n = (last_lane(g) - l0 + 1) * p.residues;
+        const int64_t l0 = first_lane(g), last = last_lane(g) - l0, n = (last + 1) * p.residues;
         const float *part = p.part_sum + (l0 + g) * p.residues * p.D + c;
         float s = 0.f;
         if (p.residues == 1) {
@@ -757,9 +757,14 @@ __global__ void __launch_bounds__(32 * SUM_ROWS)
             for (int64_t i = i0; i < n; i += step)
                 s += in ? part[i * p.D] : 0.f;
         } else {
-            for (int64_t i = i0; i < n; i += step)
-                if (in && there(l0 + i / p.residues, g, static_cast<int>(i % p.residues)))
-                    s += part[i * p.D];
+            // (a lane has `residues` rows or more, so only those at the gate row's ends can lack one)
+            const int bits = p.residues == 4 ? 2 : 3;
+#pragma unroll 4
+            for (int64_t i = i0; i < n; i += step) {
+                const int64_t l = i >> bits;
+                const bool inner = l > 0 && l < last;
+                s += in && (inner || there(l0 + l, g, static_cast<int>(i - (l << bits)))) ? part[i * p.D] : 0.f;
+            }
         }
         return s;
     };
@@ -894,11 +899,14 @@ int64_t bwd_units(int64_t M, int num_sms, int cluster, bool phased)
     return M < sms / cluster ? M : sms / cluster;
 }
 // Phased rows with several gate rows take the ring where each phase meets each gate row
-// several times; else their parts would be most of the traffic.
+// once at least (else their parts would be most of the traffic) and a block has more than
+// one row, or a row is too long for its registers (us by blocks, element by element, / in
+// rings, four gates of bf16: 100 x 1027 12.9 / 13.3, 100 x 4097 38 / 41, 2048 x 65 30 / 24, 1020 x 4097
+// 195 / 62, 256 x 16383 120 / 87).
 bool bwd_phased_gates(int64_t M, int64_t D, int elem, int64_t gate_rows)
 {
     const int64_t vec = 16 / elem;
-    return gate_rows > 1 && D % vec != 0 && D >= PHASED_MIN_D && M / gate_rows >= 4 * vec;
+    return gate_rows > 1 && D % vec != 0 && D >= PHASED_MIN_D && M / gate_rows >= vec && (M > RMS_BWD_BLOCKS || D > 8192);
 }
 // Groups of a block at most.
 int64_t bwd_groups(int64_t D, int elem, int cluster)
