@@ -5,7 +5,7 @@
 // has to be refused -- is not taken (None), and the Python function does it or says what
 // is wrong with it.  A call that is taken returns its outputs, or the library's status.
 //
-// One call's share of the host with two outputs, on the GPU machine: block_norm 12.3 us in
+// One call's share of the host with two outputs (Grace): block_norm 12.3 us in
 // Python, 4.6 here; its gradient 22 and 10.6; linear 10 and 4.0.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>

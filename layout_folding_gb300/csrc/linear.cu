@@ -1017,7 +1017,12 @@ LinearSkinny plan_linear_skinny(int64_t M, int64_t N, int num_k_blocks, int num_
         if (tiles <= linear_clusters(split, num_sms))
             g.split = split;
     const int stage = LS_W_BYTES + g.n * G_ROW;
-    const int fit = ((two ? LS_SMEM_TWO : LS_SMEM_ONE) - LS_MISC) / stage;
+    // Half the ring for few tokens and short shares of K, too: the next call's CTAs can start
+    // beside this one's (us with all / half of it, K to N [K blocks of a CTA], one token: 5120 to
+    // 5120 [27] 13.1 / 12.5, 4096 to 4096 [16] 10.0 / 9.3, 2048 to 5632 [11] 8.6 / 8.1, e4m3 5120 to 13824 [40]
+    // 15.9 / 15.4; longer ones 13824 to 5120 [72] 26.0 / 26.7; 64 tokens 5120 to 5120 14.1 / 15.4).
+    const bool lean = g.n <= 32 && (num_k_blocks + g.split - 1) / g.split <= 40;
+    const int fit = ((two || lean ? LS_SMEM_TWO : LS_SMEM_ONE) - LS_MISC) / stage;
     g.stages = fit < LS_MAX_STAGES ? fit : LS_MAX_STAGES;
     g.smem = LS_MISC + g.stages * stage;
     // The choice between this kernel and the pair kernel (us, this one / the pair kernel,
