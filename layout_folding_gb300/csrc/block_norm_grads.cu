@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(1024) k_block_norm_bwd_long(const __grid_const
 constexpr int BWD_THREADS = 384;  // 168 registers a thread, 64 of them sums
 constexpr int BWD_WARPS = BWD_THREADS / 32;
 constexpr int BWD_CLUSTER = 4;
-constexpr int BWD_BUDGET = 222 * 1024;  // dynamic shared memory; BwdSync takes 4.8 KB more
+constexpr int BWD_BUDGET = 221 * 1024;  // dynamic shared memory; BwdSync and the ragged granules take 5.5 KB more
 
 struct BwdPlan {
     int cluster, group_threads, groups, slots, packs;  // packs of a CTA's share of a row
@@ -396,6 +396,10 @@ __global__ void __launch_bounds__(BWD_THREADS)
     constexpr int VEC = 16 / static_cast<int>(sizeof(T));
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ BwdSync sy;
+    // The two ragged granules of each group's row, dresidual's and dx's: stored element by element
+    // after the others, by one loop.  (Unrolled into every pack's code the kernel does not fit the
+    // instruction cache: 8192 x 4081 116 us, so 101, 16384 x 1015 68 and 53.)
+    __shared__ uint4 edges[PH ? BWD_WARPS : 1][2][2];
     const int group = threadIdx.x / r.group_threads, t = threadIdx.x % r.group_threads;
     const int warps = r.group_threads >> 5, first_warp = group * warps, warp = threadIdx.x >> 5, lane_id = threadIdx.x & 31;
     const uint32_t clusters = r.cluster, rank = blockIdx.x % clusters;
@@ -499,6 +503,20 @@ __global__ void __launch_bounds__(BWD_THREADS)
         clear(a_pre[j]);
         clear(a_sum[j]);
     }
+    // What belongs to the row of its two ragged granules, where they are this thread's (chosen
+    // without a branch in the loop, which would keep the packs' loads apart: 8192 x 4081 117.5
+    // us with one, 115.7 without)
+    uint4 head = make_uint4(~0u, ~0u, ~0u, ~0u), tail = head;
+    int j_tail = -1;
+    if constexpr (PH) {
+        if (t == 0 && pack0 == 0)
+            head = span.words(0);
+        const int c = span.packs - 1 - pack0;
+        if (c >= 0 && c < packs && c % r.group_threads == t) {
+            tail = span.words(span.packs - 1);
+            j_tail = c / r.group_threads;
+        }
+    }
     bool ok = true;
     int slot = 0;
     uint32_t phase = 0, count = 0;
@@ -507,7 +525,7 @@ __global__ void __launch_bounds__(BWD_THREADS)
         if (several && row / p.gate_tokens != gate_row) {
             // the factors of the next gate row; every thread reads its own columns' only
             gate_row = row / p.gate_tokens;
-#pragma unroll
+#pragma unroll(PH ? 1 : RING_NV)
             for (int j = 0; j < RING_NV; ++j) {
                 const int c = t + j * r.group_threads;
                 if (c >= packs)
@@ -544,9 +562,15 @@ __global__ void __launch_bounds__(BWD_THREADS)
             inputs += in[k] ? 1u : 0u;
         }
         // (what lies beside a phased row is cut off for the sums; its results go nowhere)
-        const auto columns = [&](int c, bool cut) {
+        const auto columns = [&](int j, int c, bool cut) {
             Columns<T, W, VEC> v;
-            const uint4 keep = PH && cut ? span.words(pack0 + c) : make_uint4(0u, 0u, 0u, 0u);
+            uint4 keep = make_uint4(~0u, ~0u, ~0u, ~0u);
+            if (PH && cut) {
+                if (j == 0)
+                    keep = head;
+                if (j == j_tail)
+                    keep = make_uint4(keep.x & tail.x, keep.y & tail.y, keep.z & tail.z, keep.w & tail.w);
+            }
             const auto at = [&](int k) {
                 Pack<T, VEC> q = lds_pack<T, VEC>(base[k] + c * apart[k]);
                 if (PH && cut)
@@ -563,7 +587,7 @@ __global__ void __launch_bounds__(BWD_THREADS)
         for (int j = 0; j < RING_NV; ++j) {
             const int c = t + j * r.group_threads;
             if (c < packs)
-                columns(c, true).add_to(p, s2);
+                columns(j, c, true).add_to(p, s2);
         }
         RowSums s(s2);
         const uint32_t buf = count & 1u, bar = landed + 8u * buf;
@@ -594,14 +618,15 @@ __global__ void __launch_bounds__(BWD_THREADS)
             const int c = t + j * r.group_threads;
             if (c < packs) {
                 Pack<T, VEC> dres, dx;
-                columns(c, false).finish(p, f, dres, dx, a_pre[j], a_sum[j]);
-                if constexpr (PH) {
-                    span.store(static_cast<T *>(p.dres), row, pack0 + c, dres);
-                    span.store(static_cast<T *>(p.dx), row, pack0 + c, dx);
-                } else {
-                    const int64_t at = row * p.D + col0 + c * VEC;
+                columns(j, c, false).finish(p, f, dres, dx, a_pre[j], a_sum[j]);
+                const int64_t at = row * p.D + col0 + c * VEC;
+                if (!span.ragged(pack0 + c)) {
                     dres.store(static_cast<T *>(p.dres) + at);
                     dx.store(static_cast<T *>(p.dx) + at);
+                } else {
+                    uint4 *e = edges[group][pack0 + c > 0];
+                    dres.store(reinterpret_cast<T *>(e));
+                    dx.store(reinterpret_cast<T *>(e + 1));
                 }
                 if (ends) {
                     if constexpr (PH) {
@@ -617,6 +642,23 @@ __global__ void __launch_bounds__(BWD_THREADS)
                     clear(a_sum[j]);
                 }
             }
+        }
+        if constexpr (PH) {
+            const auto finish_edge = [&](int edge, int c) {
+                const T *e = reinterpret_cast<const T *>(edges[group][edge]);
+                const int64_t at = row * p.D + static_cast<int64_t>(c) * VEC - span.phase;
+#pragma unroll
+                for (int i = 0; i < VEC; ++i)
+                    if (span.inside(c, i)) {
+                        static_cast<T *>(p.dres)[at + i] = e[i];
+                        static_cast<T *>(p.dx)[at + i] = e[VEC + i];
+                    }
+            };
+            // (one copy of the code: a thread with both goes round twice)
+            const bool first = t == 0 && pack0 == 0, last = j_tail >= 0 && span.packs > 1;
+#pragma unroll 1
+            for (int e = first ? 0 : 1; e < (last ? 2 : 1); ++e)
+                finish_edge(e, e ? span.packs - 1 : 0);
         }
         __syncwarp();
         if (lane_id == 0)
@@ -678,7 +720,9 @@ constexpr int SUM_ROWS = 16;
 // S of many lanes to a gate row is added by all threads of a block, else a gate row each.
 __host__ __device__ constexpr bool many_lanes(int64_t lanes, int64_t gate_rows) { return lanes >= SUM_ROWS / 2 * gate_rows; }
 
-template <class T, class W>
+// RESIDUES: of phased rows with several gate rows, else 1 (a kernel of its own: its searches
+// would cost the other one half of its blocks on an SM, 64 x 5120 9.0 -> 10.7 us).
+template <class T, class W, int RESIDUES>
 __global__ void __launch_bounds__(32 * SUM_ROWS)
     k_block_norm_sums(const __grid_constant__ BlockNormBwdParams p, int blocks, W *dpost, W *dpre, void *dgate)
 {
@@ -733,32 +777,32 @@ __global__ void __launch_bounds__(32 * SUM_ROWS)
     if (!dpost && !dgate)
         return;
     const int sets = gridDim.y - 1, set = blockIdx.y - 1;
-    const bool many = many_lanes(p.lanes * p.residues, p.gate_rows);
+    const bool many = many_lanes(p.lanes * RESIDUES, p.gate_rows);
     const auto first_lane = [&](int64_t g) { return ((g * p.gate_tokens + 1) * p.lanes - 1) / p.M; };
     const auto last_lane = [&](int64_t g) { return ((g + 1) * p.gate_tokens * p.lanes - 1) / p.M; };
     // the row of part_sum where a set of blocks leaves its part of dpost
     const auto place = [&](int64_t set_of) {
         const int64_t g = set_of * (many ? 1 : SUM_ROWS);
-        return (first_lane(g) + g) * p.residues;
+        return (first_lane(g) + g) * RESIDUES;
     };
     // whether unit r of lane l has rows of gate row g
     const auto there = [&](int64_t l, int64_t g, int r) {
         const int64_t a = max(p.M * l / p.lanes, g * p.gate_tokens);
         const int64_t b = min(p.M * (l + 1) / p.lanes, (g + 1) * p.gate_tokens);
-        return b - a >= p.residues || a + (r - a % p.residues + p.residues) % p.residues < b;
+        return b - a >= RESIDUES || a + (r - a % RESIDUES + RESIDUES) % RESIDUES < b;
     };
     // this thread's share (i0, i0 + step, ..) of gate row g's S
     const auto share = [&](int64_t g, int64_t i0, int64_t step) {
-        const int64_t l0 = first_lane(g), last = last_lane(g) - l0, n = (last + 1) * p.residues;
-        const float *part = p.part_sum + (l0 + g) * p.residues * p.D + c;
+        const int64_t l0 = first_lane(g), last = last_lane(g) - l0, n = (last + 1) * RESIDUES;
+        const float *part = p.part_sum + (l0 + g) * RESIDUES * p.D + c;
         float s = 0.f;
-        if (p.residues == 1) {
+        if (RESIDUES == 1) {
 #pragma unroll 8
             for (int64_t i = i0; i < n; i += step)
                 s += in ? part[i * p.D] : 0.f;
         } else {
             // (a lane has `residues` rows or more, so only those at the gate row's ends can lack one)
-            const int bits = p.residues == 4 ? 2 : 3;
+            constexpr int bits = RESIDUES == 4 ? 2 : 3;
 #pragma unroll 4
             for (int64_t i = i0; i < n; i += step) {
                 const int64_t l = i >> bits;
@@ -954,7 +998,8 @@ cudaError_t launch_block_bwd_tw(BlockNormBwdParams p, Rows rows, void *dpost, vo
         const int64_t sets = many_lanes(p.lanes * p.residues, p.gate_rows) ? p.gate_rows : (p.gate_rows + SUM_ROWS - 1) / SUM_ROWS;
         jobs = 1 + (sets < 65534 ? sets : 65534);
     }
-    return launch_overlapped(k_block_norm_sums<T, W>, dim3(static_cast<unsigned>((p.D + 31) / 32), static_cast<unsigned>(jobs)),
+    const auto sums = p.residues > 1 ? k_block_norm_sums<T, W, V> : k_block_norm_sums<T, W, 1>;
+    return launch_overlapped(sums, dim3(static_cast<unsigned>((p.D + 31) / 32), static_cast<unsigned>(jobs)),
                              dim3(32, SUM_ROWS), 0, 1, s, p, blocks, static_cast<W *>(dpost), static_cast<W *>(dpre), dgate);
 }
 
