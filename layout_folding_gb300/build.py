@@ -1,6 +1,7 @@
 """Build liblayoutfold.so in-tree with nvcc for sm_103a (no torch extension
 machinery: the library is a plain C-ABI shared object), and the compiled part of
-its Python binding with g++."""
+its Python binding with g++.  The binding is optional: what keeps it from being built
+is said and the library is built without it."""
 from __future__ import annotations
 
 import glob
@@ -54,37 +55,63 @@ def _binding_command(out):
             "-ltorch_cpu", "-lc10_cuda", "-lc10"]
 
 
-def _deps():
-    return (_sources() + [BINDING_SRC] + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))
-            + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)])
+def _older(path, deps):
+    """Whether `path` is missing or older than one of deps."""
+    return not os.path.exists(path) or any(os.path.getmtime(d) > os.path.getmtime(path) for d in deps)
+
+
+def _headers():
+    return glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
+
+
+def _library_up_to_date() -> bool:
+    return not _older(LIB_PATH, _sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))
+                      + _headers())
+
+
+def _binding_up_to_date() -> bool:
+    return not _older(BINDING_PATH, [BINDING_SRC] + _headers()) or _binding_command(BINDING_PATH) is None
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
-        return False
-    if not os.path.exists(BINDING_PATH) and _binding_command(BINDING_PATH):
-        return False
-    t = os.path.getmtime(LIB_PATH)
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    return _library_up_to_date() and _binding_up_to_date()
 
 
-def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile every .cu in csrc/ (in parallel) and link liblayoutfold.so."""
-    if not force and up_to_date():
-        return LIB_PATH
-    os.makedirs(OBJ_DIR, exist_ok=True)
-    os.makedirs(LIB_DIR, exist_ok=True)
+def _start_binding(out, verbose):
+    """g++ at work on the compiled part of the binding, or None where there is none: the
+    Python functions do every call then, and the library is built all the same."""
+    cmd = _binding_command(out)
+    if cmd is None:
+        print("no headers of PyTorch or Python: the compiled part of the binding is not built", file=sys.stderr)
+        return None
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    try:
+        return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    except OSError as e:
+        print("%s: the compiled part of the binding is not built" % e, file=sys.stderr)
+        return None
+
+
+def _finish_binding(p, out, verbose):
+    """Puts the binding in its place, or takes away one that is out of date."""
+    text = p.communicate()[0] if p else b""
+    if p and (verbose or p.returncode != 0):
+        sys.stderr.write(text.decode(errors="replace"))
+    if p and p.returncode == 0:
+        os.replace(out, BINDING_PATH)
+        return
+    if p:
+        print("%s failed: the compiled part of the binding is not built" % p.args[0], file=sys.stderr)
+    for path in (out, BINDING_PATH):
+        if os.path.exists(path):
+            os.remove(path)
+
+
+def _build_library(verbose, ptxas_info):
     extra = ["-Xptxas", "-v"] if ptxas_info else []
     procs = []
     objs = []
-    binding_tmp = BINDING_PATH + ".tmp%d" % os.getpid()
-    binding = _binding_command(binding_tmp)
-    if binding is None:
-        print("no headers of PyTorch or Python: the compiled part of the binding is not built", file=sys.stderr)
-    else:
-        if verbose:
-            print(" ".join(binding), file=sys.stderr)
-        procs.append((BINDING_SRC, subprocess.Popen(binding, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     for src in _sources():
         obj = os.path.join(OBJ_DIR, os.path.splitext(os.path.basename(src))[0] + ".o")
         objs.append(obj)
@@ -102,11 +129,24 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     if failed:
         raise RuntimeError("nvcc failed for: " + ", ".join(failed))
     tmp = LIB_PATH + ".tmp%d" % os.getpid()
-    cmd = [NVCC, *ARCH, "-shared", "-o", tmp, *objs]
-    subprocess.run(cmd, check=True)
-    if binding is not None:
-        os.replace(binding_tmp, BINDING_PATH)
+    subprocess.run([NVCC, *ARCH, "-shared", "-o", tmp, *objs], check=True)
     os.replace(tmp, LIB_PATH)
+
+
+def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
+    """Compile every .cu in csrc/ (in parallel) and link liblayoutfold.so; beside it the
+    compiled part of the Python binding, where this machine can build it."""
+    library, binding = force or not _library_up_to_date(), force or not _binding_up_to_date()
+    os.makedirs(OBJ_DIR, exist_ok=True)
+    os.makedirs(LIB_DIR, exist_ok=True)
+    tmp = BINDING_PATH + ".tmp%d" % os.getpid()
+    p = _start_binding(tmp, verbose) if binding else None
+    try:
+        if library:
+            _build_library(verbose, ptxas_info)
+    finally:
+        if binding:
+            _finish_binding(p, tmp, verbose)
     return LIB_PATH
 
 
