@@ -11,6 +11,8 @@ import subprocess
 import sys
 import sysconfig
 
+from .compiled import PATH as BINDING_PATH
+
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
@@ -19,7 +21,6 @@ OBJ_DIR = os.path.join(PKG, "_build")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "liblayoutfold.so")
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
-BINDING_PATH = os.path.join(LIB_DIR, "_binding.so")
 
 NVCC = os.environ.get("NVCC", "nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -94,18 +95,19 @@ def _start_binding(out, verbose):
 
 
 def _finish_binding(p, out, verbose):
-    """Puts the binding in its place, or takes away one that is out of date."""
+    """Puts the binding in its place, and takes away those that are out of date (for
+    another PyTorch or Python among them: the library may have changed under them)."""
     text = p.communicate()[0] if p else b""
     if p and (verbose or p.returncode != 0):
         sys.stderr.write(text.decode(errors="replace"))
+    for path in glob.glob(os.path.join(LIB_DIR, "_binding*.so")):
+        os.remove(path)
     if p and p.returncode == 0:
         os.replace(out, BINDING_PATH)
-        return
-    if p:
+    elif p:
         print("%s failed: the compiled part of the binding is not built" % p.args[0], file=sys.stderr)
-    for path in (out, BINDING_PATH):
-        if os.path.exists(path):
-            os.remove(path)
+        if os.path.exists(out):
+            os.remove(out)
 
 
 def _build_library(verbose, ptxas_info):

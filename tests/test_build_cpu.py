@@ -5,6 +5,7 @@ import shutil
 import stat
 
 import pytest
+import torch
 
 from layout_folding_gb300 import build as lfbuild
 
@@ -66,6 +67,16 @@ def test_only_what_is_out_of_date_is_built(place, monkeypatch):
     assert not lfbuild.up_to_date()
     lfbuild.build()
     assert len(files(place)) == 2 and lfbuild.up_to_date() and os.stat(lfbuild.LIB_PATH).st_mtime_ns == before
+
+
+def test_a_binding_for_another_torch_or_python_is_not_taken(place, monkeypatch):
+    monkeypatch.setenv("CXX", compiler(place, 'while [ $# -gt 1 ]; do [ "$1" = -o ] && echo new > "$2"; shift; done\n'))
+    lfbuild.build()
+    other = os.path.basename(lfbuild.BINDING_PATH).replace(torch.__version__, "0.0.1")
+    os.rename(lfbuild.BINDING_PATH, place / "lib" / other)
+    assert other in files(place) and not lfbuild.up_to_date()
+    lfbuild.build()
+    assert lfbuild.up_to_date() and os.path.exists(lfbuild.BINDING_PATH) and other not in files(place)
 
 
 def test_a_library_that_does_not_build_is_an_error(place, monkeypatch):
