@@ -3,7 +3,8 @@
 // of the Python modules (projections.py, block_norms.py) ask here first.  A call that is
 // not of the plain kind -- given outputs, a stream, sliced rows, no rows, anything that
 // has to be refused -- is not taken (None), and the Python function does it or says what
-// is wrong with it.  A call that is taken returns its outputs, or the library's status.
+// is wrong with it.  A call that is taken returns its outputs, or the library's status;
+// other Python threads run while it allocates and launches.
 //
 // One call's share of the host with two outputs (Grace): block_norm 12.3 us in
 // Python, 4.6 here; its gradient 22 and 10.6; linear 10 and 4.0.
@@ -98,6 +99,15 @@ PyObject *outputs(const T &...t)
         Py_CLEAR(tuple);
     return tuple;
 }
+// The interpreter is left to other threads in its scope: an allocation may wait for the
+// device, a launch for room in its queue, and what runs before it there may be a host
+// function that needs the interpreter.
+struct WithoutInterpreter {
+    PyThreadState *state = PyEval_SaveThread();
+    WithoutInterpreter() = default;
+    WithoutInterpreter(const WithoutInterpreter &) = delete;
+    ~WithoutInterpreter() { PyEval_RestoreThread(state); }
+};
 PyObject *status(lf_status s) { return PyLong_FromLong(s); }
 
 bool number(PyObject *o, float *v)
@@ -164,16 +174,20 @@ PyObject *py_block_norm(PyObject *, PyObject *const *a, Py_ssize_t n)
     if (n != 9 || !lib.norm || !c.read(a[0], a[2], a[3], a[4], a[5], a[6], a[7]) || !boolean(a[8], &fp8) ||
         !required(a[1], c.device, &residual) || !is_rows(residual, *c.x) || (fp8 && !c.pre))
         Py_RETURN_NONE;
-    const Tensor h = new_like(*c.x, c.x->sizes(), c.x->scalar_type());
-    Tensor y, scale;
-    if (c.pre) {
-        y = new_like(*c.x, c.x->sizes(), fp8 ? at::kFloat8_e4m3fn : c.x->scalar_type());
-        if (fp8)
-            scale = new_like(*c.x, c.x->sizes().slice(0, c.x->dim() - 1), at::kFloat);
-    }
-    const lf_status s = lib.norm(at_of(c.x), c.D, at_of(residual), c.D, at_of(c.post), at_of(c.pre), at_of(c.gate),
-                                 c.gate_rows, c.gate_code, out_of(h), out_of(y), static_cast<float *>(out_of(scale)), c.code,
-                                 c.wcode, fp8 ? LF_E4M3 : c.code, c.eps, c.branch, c.residual, c.M, c.D, c.stream());
+    Tensor h, y, scale;
+    const auto call = [&] {
+        const WithoutInterpreter others_run;
+        h = new_like(*c.x, c.x->sizes(), c.x->scalar_type());
+        if (c.pre) {
+            y = new_like(*c.x, c.x->sizes(), fp8 ? at::kFloat8_e4m3fn : c.x->scalar_type());
+            if (fp8)
+                scale = new_like(*c.x, c.x->sizes().slice(0, c.x->dim() - 1), at::kFloat);
+        }
+        return lib.norm(at_of(c.x), c.D, at_of(residual), c.D, at_of(c.post), at_of(c.pre), at_of(c.gate), c.gate_rows,
+                        c.gate_code, out_of(h), out_of(y), static_cast<float *>(out_of(scale)), c.code, c.wcode,
+                        fp8 ? LF_E4M3 : c.code, c.eps, c.branch, c.residual, c.M, c.D, c.stream());
+    };
+    const lf_status s = call();
     return s == LF_OK ? outputs(y, h, scale) : status(s);
     END_HANDLE_TH_ERRORS
 }
@@ -190,16 +204,24 @@ PyObject *py_block_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n)
         !plain(a[0], c.device, &dy) || !plain(a[2], c.device, &h) || !plain(a[6], c.device, &dh) ||
         (c.pre ? !dy || !h : !dh) || (dy && !is_rows(dy, *c.x)) || (h && !is_rows(h, *c.x)) || (dh && !is_rows(dh, *c.x)))
         Py_RETURN_NONE;
-    const Tensor dx = new_like(*c.x, c.x->sizes(), c.x->scalar_type()), dres = new_like(*c.x, c.x->sizes(), c.x->scalar_type());
-    const auto gradient = [&](const Tensor *p) { return p && params ? new_like(*p, p->sizes(), p->scalar_type()) : Tensor(); };
-    const Tensor dpost = gradient(c.post), dpre = gradient(c.pre), dgate = gradient(c.gate);
-    Tensor scratch;
-    if (dpost.defined() || dpre.defined() || dgate.defined())
-        scratch = scratch_of(*c.x, lib.norm_scratch(c.M, c.D, c.code, c.gate_rows));
-    const lf_status s =
-        lib.norm_backward(at_of(dy), at_of(c.x), at_of(h), at_of(c.post), at_of(c.pre), at_of(c.gate), c.gate_rows,
-                          c.gate_code, at_of(dh), out_of(dx), out_of(dres), out_of(dpost), out_of(dpre), out_of(dgate),
-                          out_of(scratch), c.code, c.wcode, c.eps, c.branch, c.residual, c.M, c.D, c.stream());
+    Tensor dx, dres, dpost, dpre, dgate;
+    const auto call = [&] {
+        const WithoutInterpreter others_run;
+        const auto gradient = [&](const Tensor *p) { return p && params ? new_like(*p, p->sizes(), p->scalar_type()) : Tensor(); };
+        dx = new_like(*c.x, c.x->sizes(), c.x->scalar_type());
+        dres = new_like(*c.x, c.x->sizes(), c.x->scalar_type());
+        dpost = gradient(c.post);
+        dpre = gradient(c.pre);
+        dgate = gradient(c.gate);
+        Tensor scratch;
+        if (dpost.defined() || dpre.defined() || dgate.defined())
+            scratch = scratch_of(*c.x, lib.norm_scratch(c.M, c.D, c.code, c.gate_rows));
+        return lib.norm_backward(at_of(dy), at_of(c.x), at_of(h), at_of(c.post), at_of(c.pre), at_of(c.gate), c.gate_rows,
+                                 c.gate_code, at_of(dh), out_of(dx), out_of(dres), out_of(dpost), out_of(dpre),
+                                 out_of(dgate), out_of(scratch), c.code, c.wcode, c.eps, c.branch, c.residual, c.M, c.D,
+                                 c.stream());
+    };
+    const lf_status s = call();
     return s == LF_OK ? outputs(dx, dres, dpost, dpre, dgate) : status(s);
     END_HANDLE_TH_ERRORS
 }
@@ -254,16 +276,19 @@ PyObject *py_linear(PyObject *, PyObject *const *a, Py_ssize_t n)
     if (e4m3 && (want_pre || xs->scalar_type() != at::kFloat || ws->scalar_type() != at::kFloat || xs->numel() != c.M ||
                  ws->numel() != c.N))
         Py_RETURN_NONE;
-    const Tensor out = new_like(*c.x, c.out, at::kBFloat16);
-    Tensor pre;
-    if (want_pre)
-        pre = new_like(*c.x, c.out, at::kBFloat16);
-    const lf_status s =
-        e4m3 ? lib.lin_e4m3(at_of(c.x), static_cast<const float *>(at_of(xs)), at_of(c.w),
-                            static_cast<const float *>(at_of(ws)), at_of(c.bias), c.bias_code, static_cast<int>(c.act),
-                            at_of(residual), out_of(out), c.M, c.N, c.K, c.stream())
-             : lib.lin(at_of(c.x), at_of(c.w), at_of(c.bias), c.bias_code, static_cast<int>(c.act), at_of(residual),
-                       out_of(out), out_of(pre), c.M, c.N, c.K, c.stream());
+    Tensor out, pre;
+    const auto call = [&] {
+        const WithoutInterpreter others_run;
+        out = new_like(*c.x, c.out, at::kBFloat16);
+        if (want_pre)
+            pre = new_like(*c.x, c.out, at::kBFloat16);
+        return e4m3 ? lib.lin_e4m3(at_of(c.x), static_cast<const float *>(at_of(xs)), at_of(c.w),
+                                   static_cast<const float *>(at_of(ws)), at_of(c.bias), c.bias_code,
+                                   static_cast<int>(c.act), at_of(residual), out_of(out), c.M, c.N, c.K, c.stream())
+                    : lib.lin(at_of(c.x), at_of(c.w), at_of(c.bias), c.bias_code, static_cast<int>(c.act), at_of(residual),
+                              out_of(out), out_of(pre), c.M, c.N, c.K, c.stream());
+    };
+    const lf_status s = call();
     return s == LF_OK ? outputs(out, pre) : status(s);
     END_HANDLE_TH_ERRORS
 }
@@ -278,22 +303,27 @@ PyObject *py_linear_backward(PyObject *, PyObject *const *a, Py_ssize_t n)
     if (n != 8 || !lib.lin_backward || !c.read(a[1], a[2], a[5], a[4], at::kBFloat16) || !required(a[0], c.device, &dout) ||
         !plain(a[3], c.device, &pre) || !boolean(a[6], &want_dx) || !boolean(a[7], &want_dw) || !c.is_output(dout))
         Py_RETURN_NONE;
-    Tensor dz, dx, dw, db;
-    if (c.act != LF_ACT_NONE) {
-        if (!pre || !c.is_output(pre))
-            Py_RETURN_NONE;
-        dz = new_like(*c.x, c.out, at::kBFloat16);
-    }
-    if (want_dx)
-        dx = new_like(*c.x, c.x->sizes(), at::kBFloat16);
-    if (want_dw)
-        dw = new_like(*c.w, c.w->sizes(), at::kBFloat16);
-    if (c.bias)
-        db = new_like(*c.bias, c.bias->sizes(), c.bias->scalar_type());
-    const Tensor scratch = scratch_of(*c.x, lib.lin_scratch(c.M, c.N, c.K));
-    const lf_status s = lib.lin_backward(at_of(dout), at_of(c.x), at_of(c.w), c.act == LF_ACT_NONE ? nullptr : at_of(pre),
-                                         static_cast<int>(c.act), out_of(dz), out_of(dx), out_of(dw), out_of(db), c.bias_code,
-                                         out_of(scratch), c.M, c.N, c.K, c.stream());
+    const bool activated = c.act != LF_ACT_NONE;
+    if (activated && (!pre || !c.is_output(pre)))
+        Py_RETURN_NONE;
+    Tensor dx, dw, db;
+    const auto call = [&] {
+        const WithoutInterpreter others_run;
+        Tensor dz;
+        if (activated)
+            dz = new_like(*c.x, c.out, at::kBFloat16);
+        if (want_dx)
+            dx = new_like(*c.x, c.x->sizes(), at::kBFloat16);
+        if (want_dw)
+            dw = new_like(*c.w, c.w->sizes(), at::kBFloat16);
+        if (c.bias)
+            db = new_like(*c.bias, c.bias->sizes(), c.bias->scalar_type());
+        const Tensor scratch = scratch_of(*c.x, lib.lin_scratch(c.M, c.N, c.K));
+        return lib.lin_backward(at_of(dout), at_of(c.x), at_of(c.w), activated ? at_of(pre) : nullptr,
+                                static_cast<int>(c.act), out_of(dz), out_of(dx), out_of(dw), out_of(db), c.bias_code,
+                                out_of(scratch), c.M, c.N, c.K, c.stream());
+    };
+    const lf_status s = call();
     return s == LF_OK ? outputs(dx, dw, db) : status(s);
     END_HANDLE_TH_ERRORS
 }
