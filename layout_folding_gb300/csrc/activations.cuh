@@ -65,6 +65,8 @@ __device__ __forceinline__ float act_dphi(float v, float p)
         return p * (1.f - p);
     if (ACT == ACT_GELU)
         return 0.3989422804014327f * ex2_approx(-0.5f * LOG2E * v * v);
+    // (p (1 - p) is 0 long before v^2 would pass fp32's range, and 0 times infinity no number)
+    v = fminf(fabsf(v), 0x1p60f);
     return p * (1.f - p) * GELU_C2 * fmaf(3.f * GELU_A * v, v, 1.f);
 }
 
