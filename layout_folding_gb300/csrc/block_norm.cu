@@ -46,7 +46,7 @@ __device__ __forceinline__ NormParams second_norm(const BlockNormParams &p)
     return n;
 }
 
-// One row per block and step; thread t holds the row's packs t, t + threads, ...
+// One row per block; thread t holds the row's packs t, t + threads, ...
 template <class T, class W, int VEC, int NV, bool FP8>
 __global__ void __launch_bounds__(NV <= 2 ? 512 : 1024) k_block_norm(const __grid_constant__ BlockNormParams p)
 {
@@ -57,151 +57,148 @@ __global__ void __launch_bounds__(NV <= 2 ? 512 : 1024) k_block_norm(const __gri
     const int packs = static_cast<int>(p.D / VEC);
     const T *x = static_cast<const T *>(p.x), *res = static_cast<const T *>(p.residual);
     const W *pre = static_cast<const W *>(p.pre);
-    bool wide = false;
-    for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x) {
-        Pack<T, VEC> h[NV], rs[NV];
-        float ss = 0.f;
+    const int64_t row = blockIdx.x;
+    Pack<T, VEC> h[NV], rs[NV];
+    float ss = 0.f;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = threadIdx.x + j * blockDim.x;
-            if (c < packs) {
-                h[j] = load_pack<T, VEC>(x + row * p.ldx + static_cast<int64_t>(c) * VEC);
-                rs[j] = load_pack<T, VEC>(res + row * p.ldr + static_cast<int64_t>(c) * VEC);
-                float v[VEC];
-                h[j].get(v);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i)
-                    ss = fmaf(v[i], v[i], ss);
-            }
+    for (int j = 0; j < NV; ++j) {
+        const int c = threadIdx.x + j * blockDim.x;
+        if (c < packs) {
+            h[j] = load_pack<T, VEC>(x + row * p.ldx + static_cast<int64_t>(c) * VEC);
+            rs[j] = load_pack<T, VEC>(res + row * p.ldr + static_cast<int64_t>(c) * VEC);
         }
-        float r1 = 1.f;
-        if (p.post)
-            r1 = rsqrtf(block_reduce<false>(ss, 0u, sh[0]).x / static_cast<float>(p.D) + p.eps);
-        const int64_t gate_row = p.gate ? row / p.gate_tokens * p.D : 0;
-        ss = 0.f;
-        float mx = 0.f;
+    }
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = threadIdx.x + j * blockDim.x;
-            if (c < packs) {
-                const int64_t at = static_cast<int64_t>(c) * VEC;
-                float2 cf[PAIRS<VEC>];
-                float v[VEC];
-                column_factors<T, W, VEC>(p, gate_row, at, cf);
-                enter_stream<T, VEC>(p, h[j], rs[j], r1, cf, h[j]);
-                h[j].store(static_cast<T *>(p.h) + row * p.D + at);
-                h[j].get(v);
-                if (FP8) {
-                    float w[VEC];
-                    load_pack<W, VEC>(pre + at).get(w);
+    for (int j = 0; j < NV; ++j) {
+        const int c = threadIdx.x + j * blockDim.x;
+        if (c < packs) {
+            float v[VEC];
+            h[j].get(v);
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i)
-                        mx = max_mag(mx, v[i] * w[i]);
-                }
-#pragma unroll
-                for (int i = 0; i < VEC; ++i)
-                    ss = fmaf(v[i], v[i], ss);
-            }
+            for (int i = 0; i < VEC; ++i)
+                ss = fmaf(v[i], v[i], ss);
         }
-        if (!pre) {
-            __syncthreads();  // sh[0] is written again
-            continue;
-        }
-        const float2 sums = block_reduce<true>(ss, mag_bits(mx), sh[1]);
-        const float r2 = rsqrtf(sums.x / static_cast<float>(p.D) + p.eps);
-        const RowScale scale(sums.y, sums.x, r2);
-        if (FP8 && threadIdx.x == 0)
-            p.scale[row] = scale.scale;
-        wide |= FP8 && scale.wide;
+    }
+    float r1 = 1.f;
+    if (p.post)
+        r1 = rsqrtf(block_reduce<false>(ss, 0u, sh[0]).x / static_cast<float>(p.D) + p.eps);
+    const int64_t gate_row = p.gate ? row / p.gate_tokens * p.D : 0;
+    ss = 0.f;
+    float mx = 0.f;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = threadIdx.x + j * blockDim.x;
-            if (c < packs) {
-                const int64_t at = static_cast<int64_t>(c) * VEC;
-                float f[VEC], w[VEC];
-                h[j].get(f);
+    for (int j = 0; j < NV; ++j) {
+        const int c = threadIdx.x + j * blockDim.x;
+        if (c < packs) {
+            const int64_t at = static_cast<int64_t>(c) * VEC;
+            float2 cf[PAIRS<VEC>];
+            float v[VEC];
+            column_factors<T, W, VEC>(p, gate_row, at, cf);
+            enter_stream<T, VEC>(p, h[j], rs[j], r1, cf, h[j]);
+            h[j].store(static_cast<T *>(p.h) + row * p.D + at);
+            h[j].get(v);
+            if (FP8) {
+                float w[VEC];
                 load_pack<W, VEC>(pre + at).get(w);
-                if (FP8) {
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i)
-                        f[i] *= w[i];
-                    scale.apply(f);
-                    store_e4m3<VEC>(static_cast<uint8_t *>(p.y) + row * p.D + at, f);
-                } else {
+                for (int i = 0; i < VEC; ++i)
+                    mx = max_mag(mx, v[i] * w[i]);
+            }
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i)
-                        f[i] = f[i] * r2 * w[i];
-                    Pack<T, VEC> y;
-                    y.set(f);
-                    y.store(static_cast<T *>(p.y) + row * p.D + at);
-                }
+            for (int i = 0; i < VEC; ++i)
+                ss = fmaf(v[i], v[i], ss);
+        }
+    }
+    if (!pre)
+        return;
+    const float2 sums = block_reduce<true>(ss, mag_bits(mx), sh[1]);
+    const float r2 = rsqrtf(sums.x / static_cast<float>(p.D) + p.eps);
+    const RowScale scale(sums.y, sums.x, r2);
+    if (FP8 && threadIdx.x == 0)
+        p.scale[row] = scale.scale;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int c = threadIdx.x + j * blockDim.x;
+        if (c < packs) {
+            const int64_t at = static_cast<int64_t>(c) * VEC;
+            float f[VEC], w[VEC];
+            h[j].get(f);
+            load_pack<W, VEC>(pre + at).get(w);
+            if (FP8) {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i)
+                    f[i] *= w[i];
+                scale.apply(f);
+                store_e4m3<VEC>(static_cast<uint8_t *>(p.y) + row * p.D + at, f);
+            } else {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i)
+                    f[i] = f[i] * r2 * w[i];
+                Pack<T, VEC> y;
+                y.set(f);
+                y.store(static_cast<T *>(p.y) + row * p.D + at);
             }
         }
     }
     if constexpr (FP8)
-        if (wide)  // the same for every thread
+        if (scale.wide)  // the same for every thread
             wide_rows<T, W>(second_norm(p), wide_sh, blockDim.x, 1);
 }
 
 // Rows that do not fit the registers of a block: x is read twice, and h, which each
 // thread wrote itself, once more.
+constexpr int LONG_THREADS = 1024;
 template <class T, class W, bool FP8>
-__global__ void __launch_bounds__(1024) k_block_norm_long(const __grid_constant__ BlockNormParams p)
+__global__ void __launch_bounds__(LONG_THREADS) k_block_norm_long(const __grid_constant__ BlockNormParams p)
 {
     wait_previous_kernel();
     let_next_kernel_start();
     __shared__ float2 sh[2][MAX_WARPS];
     __shared__ uint32_t wide_sh[MAX_WARPS];
     const W *pre = static_cast<const W *>(p.pre);
-    bool wide = false;
-    for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x) {
-        const T *x = static_cast<const T *>(p.x) + row * p.ldx, *res = static_cast<const T *>(p.residual) + row * p.ldr;
-        T *h = static_cast<T *>(p.h) + row * p.D;
-        const int64_t gate_row = p.gate ? row / p.gate_tokens * p.D : 0;
-        float r1 = 1.f, ss = 0.f, mx = 0.f;
-        if (p.post) {
+    const int64_t row = blockIdx.x;
+    const T *x = static_cast<const T *>(p.x) + row * p.ldx, *res = static_cast<const T *>(p.residual) + row * p.ldr;
+    T *h = static_cast<T *>(p.h) + row * p.D;
+    const int64_t gate_row = p.gate ? row / p.gate_tokens * p.D : 0;
+    float r1 = 1.f, ss = 0.f, mx = 0.f;
+    if (p.post) {
 #pragma unroll 4
-            for (int64_t c = threadIdx.x; c < p.D; c += blockDim.x)
-                ss = fmaf(to_f(x[c]), to_f(x[c]), ss);
-            r1 = rsqrtf(block_reduce<false>(ss, 0u, sh[0]).x / static_cast<float>(p.D) + p.eps);
-        }
-        ss = 0.f;
+        for (int64_t c = threadIdx.x; c < p.D; c += LONG_THREADS)
+            ss = fmaf(to_f(x[c]), to_f(x[c]), ss);
+        r1 = rsqrtf(block_reduce<false>(ss, 0u, sh[0]).x / static_cast<float>(p.D) + p.eps);
+    }
+    ss = 0.f;
 #pragma unroll 4
-        for (int64_t c = threadIdx.x; c < p.D; c += blockDim.x) {
-            Pack<T, 1> k;
-            float2 cf[1];
-            column_factors<T, W, 1>(p, gate_row, c, cf);
-            enter_stream<T, 1>(p, load_pack<T, 1>(x + c), load_pack<T, 1>(res + c), r1, cf, k);
-            h[c] = k.v;
-            const float v = to_f(k.v);
-            ss = fmaf(v, v, ss);
-            if (FP8)
-                mx = max_mag(mx, v * to_f(pre[c]));
-        }
-        if (!pre) {
-            __syncthreads();  // sh[0] is written again
-            continue;
-        }
-        const float2 sums = block_reduce<true>(ss, mag_bits(mx), sh[1]);
-        const float r2 = rsqrtf(sums.x / static_cast<float>(p.D) + p.eps);
-        const RowScale scale(sums.y, sums.x, r2);
-        if (FP8 && threadIdx.x == 0)
-            p.scale[row] = scale.scale;
-        wide |= FP8 && scale.wide;
-        for (int64_t c = threadIdx.x; c < p.D; c += blockDim.x) {
-            const float v = to_f(h[c]);
-            if (FP8) {
-                float f[1] = {v * to_f(pre[c])};
-                scale.apply(f);
-                store_e4m3<1>(static_cast<uint8_t *>(p.y) + row * p.D + c, f);
-            } else {
-                static_cast<T *>(p.y)[row * p.D + c] = from_f<T>(v * r2 * to_f(pre[c]));
-            }
+    for (int64_t c = threadIdx.x; c < p.D; c += LONG_THREADS) {
+        Pack<T, 1> k;
+        float2 cf[1];
+        column_factors<T, W, 1>(p, gate_row, c, cf);
+        enter_stream<T, 1>(p, load_pack<T, 1>(x + c), load_pack<T, 1>(res + c), r1, cf, k);
+        h[c] = k.v;
+        const float v = to_f(k.v);
+        ss = fmaf(v, v, ss);
+        if (FP8)
+            mx = max_mag(mx, v * to_f(pre[c]));
+    }
+    if (!pre)
+        return;
+    const float2 sums = block_reduce<true>(ss, mag_bits(mx), sh[1]);
+    const float r2 = rsqrtf(sums.x / static_cast<float>(p.D) + p.eps);
+    const RowScale scale(sums.y, sums.x, r2);
+    if (FP8 && threadIdx.x == 0)
+        p.scale[row] = scale.scale;
+    for (int64_t c = threadIdx.x; c < p.D; c += LONG_THREADS) {
+        const float v = to_f(h[c]);
+        if (FP8) {
+            float f[1] = {v * to_f(pre[c])};
+            scale.apply(f);
+            store_e4m3<1>(static_cast<uint8_t *>(p.y) + row * p.D + c, f);
+        } else {
+            static_cast<T *>(p.y)[row * p.D + c] = from_f<T>(v * r2 * to_f(pre[c]));
         }
     }
     if constexpr (FP8)
-        if (wide)  // the same for every thread
-            wide_rows<T, W>(second_norm(p), wide_sh, blockDim.x, 1);
+        if (scale.wide)  // the same for every thread
+            wide_rows<T, W>(second_norm(p), wide_sh, LONG_THREADS, 1);
 }
 
 // ---------------------------------------------------------------- many rows
@@ -502,7 +499,8 @@ cudaError_t launch_block_t(const BlockNormParams &p, Rows rows, int num_sms, cud
     cudaError_t e = cudaSuccess;
     if (rows == ROWS_VEC ? launch_block_regs<T, W, V, FP8>(p, s, &e) : launch_block_regs<T, W, 1, FP8>(p, s, &e))
         return e;
-    return launch_overlapped(k_block_norm_long<T, W, FP8>, dim3(static_cast<unsigned>(p.M)), dim3(1024), 0, 1, s, p);
+    return launch_overlapped(k_block_norm_long<T, W, FP8>, dim3(static_cast<unsigned>(p.M)), dim3(LONG_THREADS), 0, 1,
+                            s, p);
 }
 
 template <class T, class W>
