@@ -667,6 +667,15 @@ uint64_t lf_launch_count(void);
 void lf_last_gemm_plan(int *grid, int *cta_pairs, int *stream_k, int *tile_n);
 
 /*
+ * How the last linear or linear_e4m3 call of this process ran: on the kernel for few
+ * tokens (1) or on CTA pairs (0), the MMA's N (few tokens: the tokens of a CTA, rounded up
+ * to 16; pairs: the columns of a tile), how many CTAs or pairs of a cluster share a
+ * tile's K blocks, and the stages of a few-token CTA's ring (0 on pairs).  All zero before
+ * the first such call.  Any pointer may be NULL; otherwise as lf_last_gemm_plan.
+ */
+void lf_last_linear_plan(int *few_tokens, int *tile_n, int *split, int *stages);
+
+/*
  * Sets up the current device if needed and reports its SM count and how many
  * CTA pairs of the pair GEMM kernel can be resident at once (either pointer
  * may be NULL).  LF_ERR_ARCH on a device that is not sm_103.

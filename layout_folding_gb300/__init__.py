@@ -86,6 +86,8 @@ def lib():
         L.lf_launch_count.restype = ctypes.c_uint64
         L.lf_last_gemm_plan.argtypes = [ctypes.POINTER(ctypes.c_int)] * 4
         L.lf_last_gemm_plan.restype = None
+        L.lf_last_linear_plan.argtypes = [ctypes.POINTER(ctypes.c_int)] * 4
+        L.lf_last_linear_plan.restype = None
         L.lf_last_device_wait_code.argtypes = []
         L.lf_last_device_wait_code.restype = ctypes.c_int
         L.lf_device_query.argtypes = [P, P]
@@ -462,6 +464,15 @@ def last_gemm_plan():
     v = [ctypes.c_int(0) for _ in range(4)]
     lib().lf_last_gemm_plan(*[ctypes.byref(x) for x in v])
     return {"grid": v[0].value, "cta_pairs": bool(v[1].value), "stream_k": bool(v[2].value), "tile_n": v[3].value}
+
+
+def last_linear_plan():
+    """How the last linear in this process ran: few_tokens (bool; else on CTA pairs), tile_n
+    (the MMA's N), split (CTAs or pairs that share a tile's K blocks) and stages (of a
+    few-token CTA's ring, 0 on pairs)."""
+    v = [ctypes.c_int(0) for _ in range(4)]
+    lib().lf_last_linear_plan(*[ctypes.byref(x) for x in v])
+    return {"few_tokens": bool(v[0].value), "tile_n": v[1].value, "split": v[2].value, "stages": v[3].value}
 
 
 def device_query():

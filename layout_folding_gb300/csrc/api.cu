@@ -45,6 +45,8 @@ std::atomic<uint64_t> g_launches{0};
 // the schedule of the last tensor-core GEMM launch:
 // grid | (0 single CTA, 1 CTA pairs) << 20 | stream-K << 23 | N-tile width << 24
 std::atomic<uint64_t> g_last_plan{0};
+// how the last linear ran: few tokens (1 or 0) | ring stages << 8 | split << 16 | the MMA's N / 8 << 24
+std::atomic<uint32_t> g_last_linear{0};
 // the code of the last device-side wait that gave up, as lf_check_device_error read it
 std::atomic<int> g_last_wait_code{0};
 std::atomic<int> g_inject{0};
@@ -1372,7 +1374,12 @@ static lf_status linear_launch(const void *x, const float *x_scale, const void *
                     : make_tmap(&m.x, x, M, K, x_rows) && make_tmap(&m.w, w, N, K, w_rows);
     };
     const lf::LinearSkinny plan = lf::plan_linear_skinny(M, N, p.num_k_blocks, d->num_sms);
+    const auto ran = [](bool few, int stages, int split, int n) {
+        g_last_linear.store((few ? 1u : 0u) | static_cast<uint32_t>(stages) << 8 | static_cast<uint32_t>(split) << 16 |
+                            static_cast<uint32_t>(n / 8) << 24);
+    };
     if (plan.preferred) {
+        ran(true, plan.stages, plan.split, plan.n);
         p.num_n_blocks = static_cast<int>((N + lf::BM - 1) / lf::BM);
         if (!operands(static_cast<uint32_t>(plan.n), lf::BM))
             return LF_ERR_LAUNCH;
@@ -1380,6 +1387,7 @@ static lf_status linear_launch(const void *x, const float *x_scale, const void *
     }
     p.num_m_blocks = static_cast<int>((M + 2 * lf::BM - 1) / (2 * lf::BM));
     lf::plan_linear_pair(p.num_m_blocks, N, p.num_k_blocks, d->pair_clusters, &lp.cols, &lp.split);
+    ran(false, 0, lp.split, lp.cols);
     p.num_n_blocks = static_cast<int>((N + lp.cols - 1) / lp.cols);
     p.num_tiles = p.num_m_blocks * p.num_n_blocks;
     if (!operands(lf::BM, static_cast<uint32_t>(lp.cols / 2)) || !make_tmap_out64(&m.out, out, M, N, N))
@@ -1530,6 +1538,19 @@ void lf_last_gemm_plan(int *grid, int *cta_pairs, int *stream_k, int *tile_n)
         *stream_k = static_cast<int>((v >> 23) & 1u);
     if (tile_n)
         *tile_n = static_cast<int>(v >> 24);
+}
+
+void lf_last_linear_plan(int *few_tokens, int *tile_n, int *split, int *stages)
+{
+    const uint32_t v = g_last_linear.load();
+    if (few_tokens)
+        *few_tokens = static_cast<int>(v & 0xffu);
+    if (stages)
+        *stages = static_cast<int>(v >> 8 & 0xffu);
+    if (split)
+        *split = static_cast<int>(v >> 16 & 0xffu);
+    if (tile_n)
+        *tile_n = static_cast<int>(v >> 24) * 8;
 }
 
 lf_status lf_device_query(int *num_sms, int *pair_clusters)
