@@ -450,7 +450,8 @@ int64_t add_rms_norm_backward_scratch(int64_t M, int64_t D);
  * Alignment as add_rms_norm (a gate of several rows is read element by element where D is
  * odd).  h may be the buffer of x or of residual, and y in x's type that of the other,
  * where that input's row pitch is D (LF_ERR_SHAPE for an e4m3 y over either, h and y in
- * one buffer, or another pitch); other overlaps are not allowed.
+ * one buffer, or another pitch); other overlaps are not allowed (LF_ERR_SHAPE, but for
+ * those with an input of wider rows, which are not looked for).
  * One launch; nothing is allocated.
  */
 lf_status block_norm(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *post_or_null,
@@ -480,7 +481,8 @@ lf_status block_norm(const void *x, int64_t ldx, const void *residual, int64_t l
  *            a gate), 16-byte aligned, device, owned by the caller, contents arbitrary;
  *            NULL allowed without parameter gradients.
  * Sums in fp32 in a fixed order: two calls on the same inputs give the same bits.  dx and
- * dresidual may each be the buffer of dy, x, h or dh (not the same one).  Two launches (one
+ * dresidual may each be the buffer of dy, x, h or dh (not the same one); an output that
+ * meets another one or what is read after it is written is LF_ERR_SHAPE.  Two launches (one
  * without parameter gradients); nothing is allocated.  Errors as block_norm.
  */
 lf_status block_norm_backward(const void *dy, const void *x, const void *h, const void *post_or_null,
@@ -574,8 +576,8 @@ int64_t gated_ffn_backward_scratch(int64_t M, int64_t F, int64_t K);
  *          stream updated in place).
  *   pre_or_null : NULL, or bf16 [M,N]: bf16_rn(z), which linear_backward takes.
  *   K % 8 == 0, N % 8 == 0 (16-byte row pitches), 1 <= M, N, K < 2^31; all pointers
- *   16-byte aligned; outputs otherwise overlap nothing (a pre that is out's or the
- *   residual's buffer is LF_ERR_SHAPE).  One launch; nothing is allocated.
+ *   16-byte aligned; outputs otherwise overlap nothing (LF_ERR_SHAPE).  One launch;
+ *   nothing is allocated.
  */
 lf_status linear(const void *x, const void *w, const void *bias_or_null, int bias_dtype, int act,
                  const void *residual_or_null, void *out, void *pre_or_null, int64_t M, int64_t N, int64_t K,
@@ -611,7 +613,8 @@ lf_status linear_e4m3(const void *x, const float *x_scale, const void *w, const 
  *          dz in fp32, or NULL.
  *   scratch : linear_backward_scratch(M, N, K) bytes, 16-byte aligned, device, owned by
  *          the caller, contents arbitrary; NULL is allowed when that is 0.
- * Sizes and alignment as linear; outputs otherwise overlap nothing.  One launch for dz
+ * Sizes and alignment as linear; outputs otherwise overlap nothing (LF_ERR_SHAPE where one
+ * meets another one or what is read after it is written).  One launch for dz
  * and dbias's sums, one that adds those up where many rows are shared out over blocks,
  * one for both products and one for their parts where a sum was split (see
  * gated_ffn_backward).  Two calls on the same inputs give the same bits, and one

@@ -5,6 +5,7 @@
 #include <atomic>
 #include <cstdlib>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include "layoutfold.h"
@@ -1057,6 +1058,41 @@ static lf_status add_rms_norm_backward_call(const void *dy, const void *h, const
     return launched(lf::launch_rms_norm_bwd(p, dweight, dtype, wdtype, d->num_sms, stream), dweight ? 2 : 1);
 }
 
+// Memory of a call, for what may not lie in one another (a null pointer lies nowhere).
+struct Span {
+    const void *p;
+    uint64_t bytes;
+    Span(const void *at, int64_t n, int size = 1) : p(at), bytes(static_cast<uint64_t>(n) * static_cast<uint64_t>(size)) {}
+    bool meets(const Span &o) const
+    {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(o.p);
+        return p && o.p && (a <= b ? b - a < bytes : a - b < o.bytes);
+    }
+};
+// None of `outs` meets another of them or one of `others`.
+static bool apart(std::initializer_list<Span> outs, std::initializer_list<Span> others)
+{
+    for (const Span *a = outs.begin(); a != outs.end(); ++a) {
+        for (const Span *b = a + 1; b != outs.end(); ++b)
+            if (a->meets(*b))
+                return false;
+        for (const Span &b : others)
+            if (a->meets(b))
+                return false;
+    }
+    return true;
+}
+// Each of `outs` is one of `ins` (of its size) or meets none of them.
+static bool over_or_apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins)
+{
+    for (const Span &a : outs)
+        for (const Span &b : ins)
+            if (a.p != b.p && a.meets(b))
+                return false;
+    return true;
+}
+static int size_of(int dtype) { return dtype == LF_FP32 ? 4 : dtype == LF_E4M3 ? 1 : 2; }
+
 // The arguments that block_norm and its gradient share.
 static bool block_norm_shape_ok(const void *gate, int64_t gate_rows, int gate_dtype, int dtype, int wdtype, float eps,
                                 int64_t M, int64_t D)
@@ -1087,6 +1123,13 @@ static lf_status block_norm_call(const void *x, int64_t ldx, const void *residua
     const bool x_packed = M == 1 || ldx == D, r_packed = M == 1 || ldr == D;
     if (h == y || (h == x && !x_packed) || (h == residual && !r_packed) ||
         (y && ((y == x && (fp8 || !x_packed)) || (y == residual && (fp8 || !r_packed)))))
+        return LF_ERR_SHAPE;
+    // (an input of wider rows may have an output between its rows)
+    const int size = size_of(dtype), w_size = size_of(wdtype);
+    const Span hs(h, M * D, size), ys(y, M * D, size_of(ydtype)), ss(scale, M, 4), xs(x_packed ? x : nullptr, M * D, size),
+        rs(r_packed ? residual : nullptr, M * D, size), gs(gate, gate ? gate_rows * D : 0, size_of(gate_dtype));
+    if (!apart({hs, ys, ss}, {{post, D, w_size}, {pre, D, w_size}, gs}) || !over_or_apart({hs, ys}, {xs, rs}) ||
+        !apart({ss}, {xs, rs}))
         return LF_ERR_SHAPE;
     DeviceState *d = nullptr;
     lf_status st = current_device(&d);
@@ -1119,6 +1162,14 @@ static lf_status block_norm_backward_call(const void *dy, const void *x, const v
         misaligned_for(pre, wdtype) || misaligned_for(dpost, wdtype) || misaligned_for(dpre, wdtype) ||
         misaligned_for(gate, gate_dtype) || misaligned_for(dgate, gate_dtype) || (params && !aligned16(scratch)))
         return LF_ERR_ALIGN;
+    // (the parameters' gradients are written by the second launch, which reads post and the gate)
+    const int64_t n = M * D, gn = gate ? gate_rows * D : 0;
+    const int size = size_of(dtype), w_size = size_of(wdtype), g_size = size_of(gate_dtype);
+    const Span dxs(dx, n, size), drs(dres, n, size);
+    if (!apart({dxs, drs, {dpost, D, w_size}, {dpre, D, w_size}, {dgate, gn, g_size}}, {{post, D, w_size}, {gate, gn, g_size}}) ||
+        !apart({dxs, drs}, {{pre, D, w_size}}) ||
+        !over_or_apart({dxs, drs}, {{dy, n, size}, {x, n, size}, {h, n, size}, {dh, n, size}}))
+        return LF_ERR_SHAPE;
     DeviceState *d = nullptr;
     lf_status st = current_device(&d);
     if (st != LF_OK)
@@ -1413,7 +1464,8 @@ static lf_status linear_call(const void *x, const void *w, const void *bias, int
     if (!aligned16(x) || !aligned16(w) || !aligned16(out) || !aligned16(bias) || !aligned16(residual) ||
         !aligned16(pre) || N % 8 != 0 || K % 8 != 0)
         return LF_ERR_ALIGN;
-    if (pre && (pre == out || pre == residual))
+    const Span xs(x, M * K, 2), ws(w, N * K, 2), bs(bias, N, size_of(bias_dtype)), rs(residual, M * N, 2), os(out, M * N, 2);
+    if (!apart({os, {pre, M * N, 2}}, {xs, ws, bs}) || !apart({{pre, M * N, 2}}, {rs}) || !over_or_apart({os}, {rs}))
         return LF_ERR_SHAPE;
     return linear_launch(x, nullptr, w, nullptr, bias, bias_dtype, act, residual, out, pre, M, N, K, stream);
 }
@@ -1430,6 +1482,10 @@ static lf_status linear_e4m3_call(const void *x, const float *x_scale, const voi
     if (!aligned16(x) || !aligned16(w) || !aligned16(out) || !aligned16(w_scale) || !aligned4(x_scale) ||
         !aligned16(bias) || !aligned16(residual) || N % 8 != 0 || K % 16 != 0)
         return LF_ERR_ALIGN;
+    const Span os(out, M * N, 2);
+    if (!apart({os}, {{x, M * K}, {w, N * K}, {x_scale, M, 4}, {w_scale, N, 4}, {bias, N, size_of(bias_dtype)}}) ||
+        !over_or_apart({os}, {{residual, M * N, 2}}))
+        return LF_ERR_SHAPE;
     return linear_launch(x, x_scale, w, w_scale, bias, bias_dtype, act, residual, out, nullptr, M, N, K, stream);
 }
 
@@ -1462,12 +1518,19 @@ static lf_status linear_backward_call(const void *dout, const void *x, const voi
     const bool summed = dbias && linear_bias_floats(M, N) > 0;  // by a second kernel
     if ((p.part_floats > 0 || summed) && !scratch)
         return LF_ERR_NULL;
+    // dz is written first, from dout and pre, the rest by products of dz, x and w: dx reads
+    // w, dw reads x.
+    const void *grad = act == LF_ACT_NONE ? dout : dz;
+    const Span ds(grad, M * N, 2), xs(dw ? x : nullptr, M * K, 2), ws(dx ? w : nullptr, N * K, 2), dos(dout, M * N, 2),
+        zs(act == LF_ACT_NONE ? nullptr : pre, M * N, 2), dbs(dbias, N, size_of(bias_dtype));
+    if (!apart({{dx, M * K, 2}, {dw, N * K, 2}, dbs}, {ds, xs, ws}) || !apart({dbs}, {dos, zs}) ||
+        (act != LF_ACT_NONE && (!apart({ds}, {xs, ws}) || !over_or_apart({ds}, {dos, zs}))))
+        return LF_ERR_SHAPE;
     DeviceState *d = nullptr;
     if ((st = current_device(&d)) != LF_OK)
         return st;
     if (d->pair_clusters <= 0)
         return LF_ERR_LAUNCH;
-    const void *grad = act == LF_ACT_NONE ? dout : dz;
     float *parts = static_cast<float *>(scratch), *sums = parts + p.part_floats;
     lf::GradMaps maps;
     if (!grad_maps(&maps, &p, grad, x, w, dx, dw, parts, M, N, K))
