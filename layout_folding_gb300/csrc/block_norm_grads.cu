@@ -923,10 +923,13 @@ bool plan_bwd(BwdPlan *r, bool phased, int64_t D, int elem, int wbytes, bool fac
     return false;
 }
 
-// CTAs to a row: two where slots for four inputs and the parameters of a whole row would
-// leave room for one group of warps only (us with one / two: 4096 x 8192 bf16 102 / 97, 8192 x
-// 5120 109 / 121, 8192 x 4096 79 / 94, in fp32 130 / 147), four where half a row does not fit
-// (2048 x 16384 bf16 element by element 483, on two CTAs 124; 1024 x 16384 fp32 217, on four 195).
+// CTAs to a row: two from 8192 elements of 16 bits (4916 of 32) on (us with one / two: 4096 x
+// 8192 bf16 102 / 97, 8192 x 5120 109 / 121, 8192 x 4096 79 / 94, in fp32 130 / 147), four where
+// half a row does not fit (2048 x 16384 bf16 element by element 483, on two CTAs 124; 1024 x
+// 16384 fp32 217, on four 195).  One CTA has room for slots of four inputs and the parameters
+// of one group of warps only from 5960 elements of 16 bits on (5664 with fp32 parameters), and
+// two would be faster from there: 4096 x 5632 63 / 74, but 4096 x 6144 94 / 77, 4096 x 7168 95 / 90,
+// 1133 x 6373 69 / 52, 4096 x 8184 97 / 97 (with fp32 parameters 101 / 114).
 int bwd_cluster(int64_t D, int elem)
 {
     if (D * (8 * elem + 8) < 24 * 8192)
