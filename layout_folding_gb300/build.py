@@ -71,7 +71,10 @@ def _library_up_to_date() -> bool:
 
 
 def _binding_up_to_date() -> bool:
-    return not _older(BINDING_PATH, [BINDING_SRC] + _headers()) or _binding_command(BINDING_PATH) is None
+    """None is up to date where none can be built; one that is there is not, for that."""
+    if not _older(BINDING_PATH, [BINDING_SRC] + _headers()):
+        return True
+    return not glob.glob(os.path.join(LIB_DIR, "_binding*.so")) and _binding_command(BINDING_PATH) is None
 
 
 def up_to_date() -> bool:

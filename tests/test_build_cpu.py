@@ -79,6 +79,18 @@ def test_a_binding_for_another_torch_or_python_is_not_taken(place, monkeypatch):
     assert lfbuild.up_to_date() and os.path.exists(lfbuild.BINDING_PATH) and other not in files(place)
 
 
+def test_one_that_is_out_of_date_goes_where_none_can_be_built(place, monkeypatch):
+    monkeypatch.setattr(lfbuild, "_binding_command", lambda out: None)  # (no headers)
+    lfbuild.build()
+    assert len(files(place)) == 1 and lfbuild.up_to_date()
+    binding = place / "lib" / os.path.basename(lfbuild.BINDING_PATH)
+    binding.write_text("old")
+    os.utime(binding, (1, 1))
+    assert not lfbuild.up_to_date()
+    lfbuild.build()
+    assert len(files(place)) == 1 and lfbuild.up_to_date()
+
+
 def test_a_library_that_does_not_build_is_an_error(place, monkeypatch):
     monkeypatch.setenv("CXX", "/nonexistent/g++")
     script = place / "cuda" / "bin" / "nvcc"
