@@ -46,7 +46,10 @@ __device__ __forceinline__ NormParams second_norm(const BlockNormParams &p)
     return n;
 }
 
-// One row per block; thread t holds the row's packs t, t + threads, ...
+// One row per block; thread t holds the row's packs t, t + threads, ...  Latency bounds it: two
+// reductions, one after the other (one token of 5120 2.8 us, 100 x 4096 2.5, both in L2; 600 x
+// 5120 6.6 of 3.6).  Without a loop over rows it needs ten registers fewer (600 x 5120 9.5 us with
+// one); the loads stand in a loop of their own, before the sums (one token 2.9 us, so 2.8).
 template <class T, class W, int VEC, int NV, bool FP8>
 __global__ void __launch_bounds__(NV <= 2 ? 512 : 1024) k_block_norm(const __grid_constant__ BlockNormParams p)
 {
@@ -145,7 +148,8 @@ __global__ void __launch_bounds__(NV <= 2 ? 512 : 1024) k_block_norm(const __gri
 }
 
 // Rows that do not fit the registers of a block: x is read twice, and h, which each
-// thread wrote itself, once more.
+// thread wrote itself, once more (element by element, 16 x 40000 fp32 18.4 us, 4 x 70000 bf16 30.2;
+// with blockDim.x for the step of the loops 20.3 and 31.2).
 constexpr int LONG_THREADS = 1024;
 template <class T, class W, bool FP8>
 __global__ void __launch_bounds__(LONG_THREADS) k_block_norm_long(const __grid_constant__ BlockNormParams p)
