@@ -49,7 +49,7 @@ __device__ __forceinline__ NormParams second_norm(const BlockNormParams &p)
 // One row per block; thread t holds the row's packs t, t + threads, ...  Latency bounds it: two
 // reductions, one after the other (one token of 5120 2.8 us, 100 x 4096 2.5, both in L2; 600 x
 // 5120 6.6 of 3.6).  Without a loop over rows it needs ten registers fewer (600 x 5120 9.5 us with
-// one); the loads stand in a loop of their own, before the sums (one token 2.9 us, so 2.8).
+// one); the loads stand in a loop of their own, before the sums (one token 3.04 us, so 2.91).
 template <class T, class W, int VEC, int NV, bool FP8>
 __global__ void __launch_bounds__(NV <= 2 ? 512 : 1024) k_block_norm(const __grid_constant__ BlockNormParams p)
 {
